@@ -539,6 +539,179 @@ int fp8_linear_autocast_noalloc(const void *x, const void *w, int in_dtype,
                                 fp8q_amax_history *hist_w, void *y,
                                 int out_dtype, cudaStream_t stream);
 
+/* ------------------------------------------------ 4-bit formats: the types */
+
+/* Microscaled 4-bit floating point.  An element is E2M1 (sign, 2 exponent
+ * bits, 1 fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6; no NaN or infinity);
+ * consecutive elements along the contraction dimension K share a scale:
+ *   MXFP4: 32 elements, E8M0 scale X = 2^(code - 127) (0xFF = NaN), with
+ *     code = floor(log2 max|x|) - 2 + 127 clamped to [0, 254] (OCP
+ *     Microscaling Formats v1.0; an all-zero block has code 0);
+ *     element = RNE_e2m1(x / X), saturating at 6.
+ *   NVFP4 ([te_blog] compares it with MXFP8): 16 elements, an E4M3 scale s,
+ *     and one fp32 scale g for the whole tensor:
+ *     g = max(fl32(amax / 2688), 1e-12)               (2688 = 6 * 448)
+ *     s = RNE_e4m3(fl32(fl32(max|x| / 6) / g)) within [2^-9, 448]
+ *     element = RNE_e2m1(fl32(x / fl32(s g))), saturating at 6.
+ *   A block that holds a NaN or an infinity gets the scale's NaN code (0xFF,
+ *   0x7F) and zero elements: it stands for NaN.  An amax that is NaN or
+ *   infinite makes every NVFP4 block so.  Elements keep their sign, zeros
+ *   included.
+ * An operand [rows, K] (any rows, any K) in device memory:
+ *   data     two codes to a byte, the lower k in the low half; a row takes
+ *            16 * ceil(K / 32) bytes, zero past K; 16-byte aligned
+ *   scales   fp4q_scale_bytes(kind, rows, K) bytes, 16-byte aligned, in the
+ *            512-byte atoms the tensor cores read: one atom per 128 rows x 4
+ *            scales along K; the scale of row r, block b is byte
+ *            (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of atom
+ *            (r / 128) * ceil(blocks / 4) + b / 4, blocks = ceil(K / 32) or
+ *            ceil(K / 16).  Scales of rows or blocks past the matrix are in
+ *            the atoms too and must not be NaN codes (the quantize calls
+ *            write 0).
+ *   global_scale  NVFP4: device float holding g, 4-byte aligned; MXFP4: NULL
+ */
+typedef enum fp4q_kind {
+  FP4Q_MXFP4 = 0,
+  FP4Q_NVFP4 = 1
+} fp4q_kind;
+
+typedef struct fp4q_operand {
+  const uint8_t *data;
+  const uint8_t *scales;
+  const float *global_scale;
+  int32_t kind;       /* fp4q_kind */
+  int32_t reserved;   /* 0 */
+} fp4q_operand;
+
+/* Bytes of the scale atoms of an [rows, K] operand: ceil(rows/128) *
+ * ceil(K/128) * 512 (MXFP4) or ceil(rows/128) * ceil(K/64) * 512 (NVFP4); 0
+ * for negative sizes or a bad kind. */
+size_t fp4q_scale_bytes(int kind, int64_t rows, int64_t K);
+
+/* ------------------------------------------------- 4-bit formats: casting */
+
+/* Quantises x [rows, cols] (device, in_dtype; element (r, c) at r * ld + c,
+ * ld >= cols, aligned to its type) from one read into either or both of
+ *   q, q_scales:   the operand [rows, cols], blocks along each row of x
+ *   qt, qt_scales: the operand [cols, rows], i.e. x^T, blocks down each
+ *                  column of x (what Dgrad and Wgrad contract over)
+ * Each pair is both-or-neither; at least one.  Rows that start on 16-byte
+ * boundaries (base and ld) are read 16 bytes at a time.
+ *   amax          NVFP4: device float, the tensor's amax as the caller knows
+ *                 it (a calibrated value may be smaller than max|x|: elements
+ *                 then saturate).  MXFP4: ignored, may be NULL.
+ *   global_scale  NVFP4: device float that receives g, required; MXFP4: NULL
+ * rows == 0 or cols == 0: only global_scale is written.
+ * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
+int fp4_quantize(const void *x, int in_dtype, int64_t rows, int64_t cols,
+                 int64_t ld, int kind, const float *amax, uint8_t *q,
+                 uint8_t *q_scales, uint8_t *qt, uint8_t *qt_scales,
+                 float *global_scale, cudaStream_t stream);
+
+/* *amax = max |x| of a matrix as fp4_quantize reads it (fp8_amax for rows
+ * that lie apart); a NaN anywhere makes it NaN.  amax: device float.
+ * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
+int fp4_amax(const void *x, int in_dtype, int64_t rows, int64_t cols,
+             int64_t ld, float *amax, cudaStream_t stream);
+
+/* y [rows, K] (dense, out_dtype) = the values the operand stands for: code *
+ * X (MXFP4), fl32(code * fl32(s g)) (NVFP4), rounded once more to bf16 if
+ * that is out_dtype (MXFP4 values are exact in bf16).
+ * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
+int fp4_dequantize(const fp4q_operand *op, int64_t rows, int64_t K, void *y,
+                   int out_dtype, cudaStream_t stream);
+
+/* ------------------------------------------------ 4-bit formats: products */
+
+/* C [M, N] (dense, out_dtype) = A [M, K] . B [N, K]^T of two operands of one
+ * kind, accumulated in fp32 on the tensor cores, which apply the block
+ * scales; NVFP4 results are multiplied by fl32(g_A g_B).  Any M, N, K; M or
+ * N == 0: nothing to do, K == 0: C is zero.  C is 16-byte aligned.
+ * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
+int fp4_gemm(const fp4q_operand *A, const fp4q_operand *B, void *C,
+             int out_dtype, int64_t M, int64_t N, int64_t K,
+             cudaStream_t stream);
+
+/* Bytes of device workspace fp4_linear needs (the 4-bit copy of x, its scales
+ * and amax); 0 for invalid sizes or kind. */
+size_t fp4q_linear_workspace_size(int kind, int64_t M, int64_t N, int64_t K);
+
+/* y [M, N] = x w^T of a linear layer whose weight [N, K] is held in 4 bits:
+ * x [M, K] (device, in_dtype, rows ldx elements apart) is quantised to w's
+ * kind as fp4_quantize does and multiplied as fp4_gemm does, in this call.
+ *   x_amax     NVFP4: device float, a calibrated amax of x, or NULL: the call
+ *              finds max|x| itself.  MXFP4: ignored.
+ *   workspace  device, >= fp4q_linear_workspace_size, 256-byte aligned
+ * Errors: INVALID_ARG, MISALIGNED, WORKSPACE, ARCH, CUDA. */
+int fp4_linear(const void *x, int in_dtype, int64_t ldx,
+               const fp4q_operand *w, int64_t M, int64_t N, int64_t K,
+               const float *x_amax, void *y, int out_dtype, void *workspace,
+               size_t ws_bytes, cudaStream_t stream);
+
+/* Bytes of device workspace fp4_linear_train needs; 0 for invalid sizes or
+ * kind. */
+size_t fp4q_linear_train_workspace_size(int kind, int64_t M, int64_t N,
+                                        int64_t K);
+
+/* fp8_linear_train in 4 bits: x [M, K], w [N, K] and g [M, N] (dense,
+ * in_dtype) are each quantised in both orientations, then
+ *   y  [M, N] = x . w^T,   dx [M, K] = g . w,   dw [N, K] = g^T . x
+ * (dense, out_dtype).  Any M, N, K.
+ *   workspace: device, >= fp4q_linear_train_workspace_size, 256-byte aligned
+ * Errors: INVALID_ARG, MISALIGNED, WORKSPACE, ARCH, CUDA. */
+int fp4_linear_train(const void *x, const void *w, const void *g, int in_dtype,
+                     int64_t M, int64_t N, int64_t K, int kind, void *y,
+                     void *dx, void *dw, int out_dtype, void *workspace,
+                     size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------- activation functions with 8-bit checkpoints */
+
+/* What a feed-forward block keeps between its forward and backward pass is
+ * the input of its activation function, one or two [T, F] matrices.  These
+ * calls keep it in E4M3 under 1x128 tile scales: the bytes and scales that
+ * fp8_quantize_tile1x128 (saturate 0) gives for the same matrix, for any F;
+ * scales [ceil(F/128), T].
+ *   f: SILU u / (1 + e^-u); GELU u (1 + erf(u / sqrt 2)) / 2; GELU_TANH
+ *   u (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))) / 2.
+ * All arithmetic is fp32, with one rounding to the output's type. */
+typedef enum fp8q_act {
+  FP8Q_ACT_SILU = 0,
+  FP8Q_ACT_GELU = 1,
+  FP8Q_ACT_GELU_TANH = 2
+} fp8q_act;
+
+/* a = f(u), or f(u) * v (elementwise) when v is given, from u, v as they are;
+ * in the same pass the checkpoint of u (and v).
+ *   u, v      device [T, F] of `dtype`, rows ldu / ldv elements apart (two
+ *             halves of one matrix, say), aligned to their type; v NULL for an
+ *             ungated activation
+ *   a         device [T, F] of `dtype`, rows lda elements apart, not
+ *             overlapping an input (or exactly u or v, with its ld)
+ *   u8, u_scales, v8, v_scales
+ *             device: bytes [T, F] dense, fp32 [ceil(F/128), T]; the v pair
+ *             exactly when v is given.  Bytes and matrices whose rows start
+ *             on 16-byte boundaries and F % 16 == 0 are moved in vectors.
+ * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
+int fp8_act_forward(int act, int dtype, int64_t T, int64_t F, const void *u,
+                    int64_t ldu, const void *v, int64_t ldv, void *a,
+                    int64_t lda, uint8_t *u8, float *u_scales, uint8_t *v8,
+                    float *v_scales, cudaStream_t stream);
+
+/* The backward pass from the checkpoint: with u, v the values it stands for
+ * and da the gradient of a,
+ *   du = da f'(u) v,   dv = da f(u)        (gated)
+ *   du = da f'(u)                          (v8 NULL; dv NULL)
+ * and, when `a` is given, a = f(u) (v) again: what the next weight gradient
+ * contracts with.
+ *   da, du, dv, a  device [T, F] of `dtype`, rows ldda, lddu, lddv, lda
+ *                  elements apart; an output may be exactly da, with its ld
+ * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
+int fp8_act_backward(int act, int dtype, int64_t T, int64_t F,
+                     const uint8_t *u8, const float *u_scales,
+                     const uint8_t *v8, const float *v_scales, const void *da,
+                     int64_t ldda, void *du, int64_t lddu, void *dv,
+                     int64_t lddv, void *a, int64_t lda, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,9 @@ The names follow the C ABI: ``fp8_amax``, ``fp8_quantize_tensor``,
 ``fp8_quantize_delayed``, ``fp8_quantize_tile1x128``,
 ``fp8_quantize_block128x128``, ``fp8_gemm`` and the role wrappers
 ``fp8_gemm_fprop`` / ``fp8_gemm_dgrad`` / ``fp8_gemm_wgrad``, and
-``fp8_linear_autocast``.
+``fp8_linear_autocast``; the 4-bit ``fp4_quantize``, ``fp4_dequantize``,
+``fp4_gemm``, ``fp4_linear`` and ``fp4_linear_train``; and ``fp8_act_forward`` /
+``fp8_act_backward``, activation functions with 8-bit checkpoints.
 """
 from __future__ import annotations
 
@@ -34,6 +36,11 @@ RECIPE_TENSOR_DELAYED = 1
 RECIPE_BLOCK = 2
 RECIPE_MXFP8 = 3
 MX_BLOCK = 32
+MXFP4 = 0
+NVFP4 = 1
+ACT_SILU = 0
+ACT_GELU = 1
+ACT_GELU_TANH = 2
 HISTORY_LEN = 16
 HISTORY_BYTES = 80
 
@@ -57,6 +64,10 @@ EXPORTS = (
     "fp8_linear_autocast",
     "fp8_linear_autocast_noalloc", "fp8q_linear_train_workspace_size", "fp8_linear_train",
     "fp8q_linear_train_host_workspace_size", "fp8_linear_train_host",
+    "fp4q_scale_bytes", "fp4_quantize", "fp4_amax", "fp4_dequantize", "fp4_gemm",
+    "fp4q_linear_workspace_size", "fp4_linear",
+    "fp4q_linear_train_workspace_size", "fp4_linear_train",
+    "fp8_act_forward", "fp8_act_backward",
 )
 
 
@@ -110,6 +121,18 @@ def signatures() -> dict:
         "fp8q_linear_train_host_workspace_size": (SZ, [I32, I32, I32, I64, I64, I64]),
         "fp8_linear_train_host": (I32, [P, P, P, I32, I64, I64, I64, I32, P, P, P, P, P, P,
                                         I32, P, SZ, P]),
+        "fp4q_scale_bytes": (SZ, [I32, I64, I64]),
+        "fp4_quantize": (I32, [P, I32, I64, I64, I64, I32, P, P, P, P, P, P, P]),
+        "fp4_amax": (I32, [P, I32, I64, I64, I64, P, P]),
+        "fp4_dequantize": (I32, [P, I64, I64, P, I32, P]),
+        "fp4_gemm": (I32, [P, P, P, I32, I64, I64, I64, P]),
+        "fp4q_linear_workspace_size": (SZ, [I32, I64, I64, I64]),
+        "fp4_linear": (I32, [P, I32, I64, P, I64, I64, I64, P, P, I32, P, SZ, P]),
+        "fp4q_linear_train_workspace_size": (SZ, [I32, I64, I64, I64]),
+        "fp4_linear_train": (I32, [P, P, P, I32, I64, I64, I64, I32, P, P, P, I32, P, SZ, P]),
+        "fp8_act_forward": (I32, [I32, I32, I64, I64, P, I64, P, I64, P, I64, P, P, P, P, P]),
+        "fp8_act_backward": (I32, [I32, I32, I64, I64, P, P, P, P, P, I64, P, I64, P, I64, P,
+                                   I64, P]),
     }
 
 
@@ -580,6 +603,267 @@ def fp8_linear_autocast_noalloc(x, w, recipe=RECIPE_TENSOR_CURRENT, out_dtype=to
         _ptr(hist_x.buf) if hist_x else None, _ptr(hist_w.buf) if hist_w else None,
         _ptr(out), _out_dtype(out.dtype), _stream(stream)), "fp8_linear_autocast_noalloc")
     return out
+
+
+# ------------------------------------------------------------ 4-bit formats
+
+class _Fp4Struct(ctypes.Structure):
+    """fp4q_operand."""
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("global_scale", ctypes.c_void_p), ("kind", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+def _ptr_rows(t: torch.Tensor):
+    """(pointer, row stride in elements) of a 2-D matrix whose rows are dense;
+    the rows may lie apart (a slice of a wider matrix)."""
+    if not t.is_cuda:
+        raise ValueError("fp8q needs CUDA tensors")
+    rows, cols = _rows_cols(t)
+    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError("fp8q needs matrices whose rows are dense and do not overlap")
+    return ctypes.c_void_p(t.data_ptr()), ld
+
+
+def _new(shape, dtype, device, stream):
+    """Storage a call writes on ``stream``: allocated there, so that the
+    caching allocator orders its reuse after that stream's work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _like(t: torch.Tensor, shape, dtype, what: str):
+    """Checks a caller's tensor against what a call is about to write or read."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of shape "
+                         f"{tuple(t.shape)}")
+    return t
+
+
+def fp4_scale_bytes(kind: int, rows: int, K: int) -> int:
+    """Bytes of the scale atoms of an [rows, K] 4-bit operand."""
+    return int(lib().fp4q_scale_bytes(kind, rows, K))
+
+
+class Fp4Operand:
+    """A 4-bit operand [rows, K] (MXFP4 or NVFP4): packed codes [rows, 16
+    ceil(K/32)] and scale atoms, both uint8 device tensors, and for NVFP4 the
+    one-element fp32 tensor scale; see fp4q_operand in include/fp8q.h."""
+
+    def __init__(self, data: torch.Tensor, scales: torch.Tensor, kind: int, K: int,
+                 global_scale: torch.Tensor | None = None):
+        if data.dim() != 2 or data.dtype != torch.uint8 or data.shape[1] != (K + 31) // 32 * 16:
+            raise ValueError("4-bit data must be uint8 [rows, 16 ceil(K/32)]")
+        self.rows, self.K, self.kind = data.shape[0], K, kind
+        need = fp4_scale_bytes(kind, self.rows, K)
+        if scales.dtype != torch.uint8 or scales.numel() != need:
+            raise ValueError(f"4-bit scales must be {need} uint8 values")
+        if (kind == NVFP4) != (global_scale is not None):
+            raise ValueError("NVFP4 operands, and only they, have a global scale")
+        if global_scale is not None and (global_scale.dtype != torch.float32
+                                         or global_scale.numel() != 1):
+            raise ValueError("a global scale is one fp32 value")
+        self.data, self.scales, self.global_scale = data, scales, global_scale
+        self.struct = _Fp4Struct(_ptr(data), _ptr(scales), _ptr(global_scale), kind, 0)
+
+    @classmethod
+    def empty(cls, kind: int, rows: int, K: int, device, global_scale=None, stream=None):
+        """Uninitialised storage for an operand."""
+        data = _new((rows, (K + 31) // 32 * 16), torch.uint8, device, stream)
+        scales = _new((fp4_scale_bytes(kind, rows, K),), torch.uint8, device, stream)
+        return cls(data, scales, kind, K, global_scale)
+
+
+def fp4_amax(x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """max |x| of a matrix whose rows may lie apart, as a one-element fp32 tensor."""
+    p, ld = _ptr_rows(x)
+    out = out if out is not None else _new((1,), torch.float32, x.device, stream)
+    _check(lib().fp4_amax(p, _in_dtype(x), x.shape[0], x.shape[1], ld, _ptr(out),
+                          _stream(stream)), "fp4_amax")
+    return out
+
+
+def fp4_quantize(x: torch.Tensor, kind: int, rows=True, cols=False,
+                 amax: torch.Tensor | None = None, q: Fp4Operand | None = None,
+                 q_t: Fp4Operand | None = None, stream=None):
+    """x [R, C] (rows may lie apart) -> (operand [R, C] | None, operand [C, R]
+    of x^T | None).  NVFP4 takes the tensor's amax from ``amax`` (one fp32
+    device value) or finds it first."""
+    p, ld = _ptr_rows(x)
+    R, C = x.shape
+    g = None
+    if kind == NVFP4:
+        amax = amax if amax is not None else fp4_amax(x, stream=stream)
+        _like(amax.reshape(-1), (1,), torch.float32, "amax")
+        given = q if q is not None else q_t
+        g = given.global_scale if given is not None else _new((1,), torch.float32, x.device,
+                                                                             stream)
+    if rows:
+        q = q if q is not None else Fp4Operand.empty(kind, R, C, x.device, g, stream)
+    if cols:
+        q_t = q_t if q_t is not None else Fp4Operand.empty(kind, C, R, x.device, g, stream)
+    for op, shape in ((q if rows else None, (kind, R, C)), (q_t if cols else None, (kind, C, R))):
+        if op is not None and (op.kind, op.rows, op.K) != shape:
+            raise ValueError(f"an operand of kind, rows, K {shape} is needed")
+    if rows and cols and kind == NVFP4 and q.global_scale.data_ptr() != q_t.global_scale.data_ptr():
+        raise ValueError("both orientations share one global scale")
+    _check(lib().fp4_quantize(
+        p, _in_dtype(x), R, C, ld, kind, _ptr(amax) if kind == NVFP4 else None,
+        _ptr(q.data) if rows else None, _ptr(q.scales) if rows else None,
+        _ptr(q_t.data) if cols else None, _ptr(q_t.scales) if cols else None, _ptr(g),
+        _stream(stream)), "fp4_quantize")
+    return (q if rows else None), (q_t if cols else None)
+
+
+def fp4_dequantize(op: Fp4Operand, out_dtype=torch.bfloat16, out=None, stream=None):
+    """The values [rows, K] an operand stands for."""
+    out = out if out is not None else _new((op.rows, op.K), out_dtype, op.data.device, stream)
+    _like(out, (op.rows, op.K), out.dtype, "out")
+    _check(lib().fp4_dequantize(ctypes.byref(op.struct), op.rows, op.K, _ptr(out),
+                                _out_dtype(out.dtype), _stream(stream)), "fp4_dequantize")
+    return out
+
+
+def fp4_gemm(A: Fp4Operand, B: Fp4Operand, out_dtype=torch.bfloat16, out=None, stream=None):
+    """C [M, N] = A [M, K] . B [N, K]^T of two operands of one kind."""
+    if A.K != B.K:
+        raise ValueError(f"operands contract over {A.K} and {B.K}")
+    out = out if out is not None else _new((A.rows, B.rows), out_dtype, A.data.device, stream)
+    _like(out, (A.rows, B.rows), out.dtype, "out")
+    _check(lib().fp4_gemm(ctypes.byref(A.struct), ctypes.byref(B.struct), _ptr(out),
+                          _out_dtype(out.dtype), A.rows, B.rows, A.K, _stream(stream)),
+           "fp4_gemm")
+    return out
+
+
+def fp4_linear_workspace_size(kind: int, M: int, N: int, K: int) -> int:
+    return int(lib().fp4q_linear_workspace_size(kind, M, N, K))
+
+
+def fp4_linear(x: torch.Tensor, w: Fp4Operand, x_amax: torch.Tensor | None = None,
+               out_dtype=torch.bfloat16, workspace=None, out=None, stream=None):
+    """y [M, N] = x w^T with w [N, K] held in 4 bits: x [M, K] (rows may lie
+    apart) is quantised to w's kind in the call.  ``x_amax``: a calibrated
+    amax of x for NVFP4 (one fp32 device value); without it the call finds
+    max |x|."""
+    p, ld = _ptr_rows(x)
+    M, K = x.shape
+    if K != w.K:
+        raise ValueError(f"x has {K} columns, w contracts over {w.K}")
+    if x_amax is not None:
+        _like(x_amax.reshape(-1), (1,), torch.float32, "x_amax")
+    if workspace is None:
+        workspace = _new((max(1, fp4_linear_workspace_size(w.kind, M, w.rows, K)),), torch.uint8,
+                         x.device, stream)
+    out = out if out is not None else _new((M, w.rows), out_dtype, x.device, stream)
+    _like(out, (M, w.rows), out.dtype, "out")
+    _check(lib().fp4_linear(
+        p, _in_dtype(x), ld, ctypes.byref(w.struct), M, w.rows, K, _ptr(x_amax), _ptr(out),
+        _out_dtype(out.dtype), _ptr(workspace), workspace.numel(), _stream(stream)), "fp4_linear")
+    return out
+
+
+def fp4_linear_train_workspace_size(kind: int, M: int, N: int, K: int) -> int:
+    return int(lib().fp4q_linear_train_workspace_size(kind, M, N, K))
+
+
+def fp4_linear_train(x, w, g, kind: int, out_dtype=torch.bfloat16, workspace=None, y=None,
+                     dx=None, dw=None, stream=None):
+    """One linear layer's Fprop, Dgrad and Wgrad in 4 bits, every operand
+    quantised in the call (device tensors).  Returns (y, dx, dw)."""
+    M, K = _rows_cols(x)
+    N = w.shape[0]
+    _like(w, (N, K), x.dtype, "w")
+    _like(g, (M, N), x.dtype, "g")
+    if workspace is None:
+        workspace = _new((max(1, fp4_linear_train_workspace_size(kind, M, N, K)),), torch.uint8,
+                         x.device, stream)
+    y = y if y is not None else _new((M, N), out_dtype, x.device, stream)
+    dx = dx if dx is not None else _new((M, K), out_dtype, x.device, stream)
+    dw = dw if dw is not None else _new((N, K), out_dtype, x.device, stream)
+    for t, shape, what in ((y, (M, N), "y"), (dx, (M, K), "dx"), (dw, (N, K), "dw")):
+        _like(t, shape, y.dtype, what)
+    _check(lib().fp4_linear_train(
+        _ptr(x), _ptr(w), _ptr(g), _in_dtype(x), M, N, K, kind, _ptr(y), _ptr(dx), _ptr(dw),
+        _out_dtype(y.dtype), _ptr(workspace), workspace.numel(), _stream(stream)),
+        "fp4_linear_train")
+    return y, dx, dw
+
+
+# ------------------------------- activation functions with 8-bit checkpoints
+
+class ActCheckpoint:
+    """What fp8_act_forward keeps for the backward pass: E4M3 bytes [T, F]
+    (uint8) of u, and of v for a gated activation, under 1x128 tile scales
+    (fp32 [ceil(F/128), T])."""
+
+    def __init__(self, u: torch.Tensor, u_scales: torch.Tensor, v: torch.Tensor | None = None,
+                 v_scales: torch.Tensor | None = None):
+        self.T, self.F = _rows_cols(u)
+        if (v is None) != (v_scales is None):
+            raise ValueError("v and v_scales come together")
+        for q, s in ((u, u_scales), (v, v_scales)):
+            if q is not None:
+                _like(q, (self.T, self.F), torch.uint8, "checkpoint bytes")
+                _like(s, ((self.F + 127) // 128, self.T), torch.float32, "checkpoint scales")
+        self.u, self.u_scales, self.v, self.v_scales = u, u_scales, v, v_scales
+
+    @classmethod
+    def empty(cls, T: int, F: int, gated: bool, device, stream=None):
+        """Uninitialised storage for a checkpoint."""
+        def pair():
+            return (_new((T, F), torch.uint8, device, stream),
+                    _new(((F + 127) // 128, T), torch.float32, device, stream))
+        return cls(*pair(), *(pair() if gated else ()))
+
+
+def fp8_act_forward(act: int, u: torch.Tensor, v: torch.Tensor | None = None, out=None,
+                    ckpt: ActCheckpoint | None = None, stream=None):
+    """(a, checkpoint) with a = f(u), or f(u) * v.  u and v are [T, F] of one
+    type; their rows may lie apart (the two halves of one matrix)."""
+    T, F = _rows_cols(u)
+    if v is not None:
+        _like(v, (T, F), u.dtype, "v")
+    out = out if out is not None else _new((T, F), u.dtype, u.device, stream)
+    _like(out, (T, F), u.dtype, "out")
+    ckpt = ckpt if ckpt is not None else ActCheckpoint.empty(T, F, v is not None, u.device, stream)
+    if (ckpt.T, ckpt.F, ckpt.v is None) != (T, F, v is None):
+        raise ValueError("the checkpoint's shape is another")
+    (pu, ldu), (pa, lda) = _ptr_rows(u), _ptr_rows(out)
+    pv, ldv = _ptr_rows(v) if v is not None else (None, 0)
+    _check(lib().fp8_act_forward(
+        act, _in_dtype(u), T, F, pu, ldu, pv, ldv, pa, lda, _ptr(ckpt.u), _ptr(ckpt.u_scales),
+        _ptr(ckpt.v), _ptr(ckpt.v_scales), _stream(stream)), "fp8_act_forward")
+    return out, ckpt
+
+
+def fp8_act_backward(act: int, ckpt: ActCheckpoint, da: torch.Tensor, want_a=False, du=None,
+                     dv=None, a=None, stream=None):
+    """(du, dv | None, a | None) from the checkpoint and the gradient of a;
+    ``want_a`` (or a given ``a``) asks for the activation again."""
+    T, F = ckpt.T, ckpt.F
+    _like(da, (T, F), da.dtype, "da")
+    gated = ckpt.v is not None
+    new = lambda: _new((T, F), da.dtype, da.device, stream)
+    du = du if du is not None else new()
+    if gated:
+        dv = dv if dv is not None else new()
+    elif dv is not None:
+        raise ValueError("an ungated activation has no dv")
+    if want_a and a is None:
+        a = new()
+    for t, what in ((du, "du"), (dv, "dv"), (a, "a")):
+        if t is not None:
+            _like(t, (T, F), da.dtype, what)
+    rows = lambda t: _ptr_rows(t) if t is not None else (None, 0)
+    _check(lib().fp8_act_backward(
+        act, _in_dtype(da), T, F, _ptr(ckpt.u), _ptr(ckpt.u_scales), _ptr(ckpt.v),
+        _ptr(ckpt.v_scales), *rows(da), *rows(du), *rows(dv), *rows(a), _stream(stream)),
+        "fp8_act_backward")
+    return du, dv, a
 
 
 # ------------------------------------------------------------- diagnostics

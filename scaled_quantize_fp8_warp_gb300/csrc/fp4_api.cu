@@ -1,0 +1,359 @@
+// The extern "C" boundary of the 4-bit operators and of the activation
+// functions with 8-bit checkpoints (include/fp8q.h): argument checks, device
+// check, workspace layout and dispatch.  No call allocates or synchronises.
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include "fp4_common.cuh"
+#include "fp4_internal.h"
+#include "fp8_act.h"
+
+namespace fp8q {
+namespace {
+
+bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+bool valid_dtype(int d) { return d == FP8Q_DT_F32 || d == FP8Q_DT_BF16; }
+bool valid_kind(int k) { return k == FP4Q_MXFP4 || k == FP4Q_NVFP4; }
+int64_t dtype_size(int d) { return d == FP8Q_DT_BF16 ? 2 : 4; }
+int from_cuda(cudaError_t e) { return e == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA; }
+
+int check_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FP8Q_ERR_CUDA;
+  return fp8q_device_supported() == 1 ? FP8Q_OK : FP8Q_ERR_ARCH;
+}
+
+// A rows x cols matrix whose padded byte counts (4-byte elements, rows and
+// columns rounded up to 128) fit in int64.
+bool dims_ok(int64_t rows, int64_t cols) {
+  constexpr int64_t kLim = INT64_MAX / 32;
+  if (rows < 0 || cols < 0 || rows > kLim || cols > kLim) return false;
+  return cols == 0 || rows + 128 <= kLim / (cols + 128);
+}
+
+// Matrix argument [rows, cols] with rows ld elements apart; `align` in bytes.
+int check_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t align) {
+  if (rows == 0 || cols == 0) return FP8Q_OK;
+  if (p == nullptr || ld < cols) return FP8Q_ERR_INVALID_ARG;
+  if (rows > 1 && !dims_ok(rows, ld)) return FP8Q_ERR_INVALID_ARG;
+  return aligned(p, (uintptr_t)align) ? FP8Q_OK : FP8Q_ERR_MISALIGNED;
+}
+
+int check_operand(const fp4q_operand *op, int64_t rows, int64_t K) {
+  if (op == nullptr || !valid_kind(op->kind) || op->reserved != 0) return FP8Q_ERR_INVALID_ARG;
+  if ((op->kind == FP4Q_NVFP4) != (op->global_scale != nullptr)) return FP8Q_ERR_INVALID_ARG;
+  if (!aligned(op->global_scale, 4)) return FP8Q_ERR_MISALIGNED;
+  if (rows > 0 && K > 0) {
+    if (op->data == nullptr || op->scales == nullptr) return FP8Q_ERR_INVALID_ARG;
+    if (!aligned(op->data, 16) || !aligned(op->scales, 16)) return FP8Q_ERR_MISALIGNED;
+  }
+  return FP8Q_OK;
+}
+
+bool linear_ok(int64_t M, int64_t N, int64_t K) {
+  return dims_ok(M, K) && dims_ok(N, K) && dims_ok(M, N);
+}
+
+size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+size_t data_bytes(int64_t rows, int64_t K) { return (size_t)(rows * fp4::row_bytes(K)); }
+
+// A piece-by-piece workspace: take() hands out 256-byte aligned pieces.
+struct Pieces {
+  uint8_t *base;
+  size_t used = 0;
+  uint8_t *take(size_t bytes) {
+    uint8_t *p = base == nullptr ? nullptr : base + used;
+    used += round256(bytes);
+    return p;
+  }
+};
+
+// One matrix quantised in both orientations, in a workspace.
+struct Both {
+  fp4q_operand rows, cols;
+  float *amax, *global;
+  void lay_out(Pieces &ws, int kind, int64_t R, int64_t C) {
+    uint8_t *words = ws.take(8);   // amax and g
+    amax = reinterpret_cast<float *>(words);
+    global = amax == nullptr ? nullptr : amax + 1;
+    const float *g = kind == FP4Q_NVFP4 ? global : nullptr;
+    uint8_t *q = ws.take(data_bytes(R, C)), *qs = ws.take(fp4q_scale_bytes(kind, R, C));
+    uint8_t *t = ws.take(data_bytes(C, R)), *ts = ws.take(fp4q_scale_bytes(kind, C, R));
+    rows = fp4q_operand{q, qs, g, kind, 0};
+    cols = fp4q_operand{t, ts, g, kind, 0};
+  }
+};
+
+int quantize_into(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_t ld, int kind,
+                  const float *amax, float *amax_ws, const fp4q_operand *q,
+                  const fp4q_operand *qt, float *global, cudaStream_t stream) {
+  if (rows == 0 || cols == 0) return FP8Q_OK;
+  if (kind == FP4Q_NVFP4 && amax == nullptr) {
+    const cudaError_t e = fp4::launch_amax_ld(x, in_dtype, rows, cols, ld, amax_ws, stream);
+    if (e != cudaSuccess) return FP8Q_ERR_CUDA;
+    amax = amax_ws;
+  }
+  fp4::QuantArgs a{};
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ld;
+  a.amax = amax;
+  a.q = q == nullptr ? nullptr : const_cast<uint8_t *>(q->data);
+  a.q_scales = q == nullptr ? nullptr : const_cast<uint8_t *>(q->scales);
+  a.qt = qt == nullptr ? nullptr : const_cast<uint8_t *>(qt->data);
+  a.qt_scales = qt == nullptr ? nullptr : const_cast<uint8_t *>(qt->scales);
+  a.global_scale = kind == FP4Q_NVFP4 ? global : nullptr;
+  return from_cuda(fp4::launch_quantize(kind, in_dtype, a, stream));
+}
+
+// C = A . B^T for checked operands of one kind, any sizes.
+int product(const fp4q_operand &A, const fp4q_operand &B, void *C, int out_dtype, int64_t M,
+            int64_t N, int64_t K, cudaStream_t stream) {
+  if (M == 0 || N == 0) return FP8Q_OK;
+  if (K == 0)
+    return from_cuda(cudaMemsetAsync(C, 0, (size_t)(M * N * dtype_size(out_dtype)), stream));
+  return fp4::launch_gemm(A.kind, A, B, out_dtype, C, M, N, K, stream);
+}
+
+}  // namespace
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" {
+
+size_t fp4q_scale_bytes(int kind, int64_t rows, int64_t K) {
+  if (!valid_kind(kind) || !dims_ok(rows, K)) return 0;
+  return (size_t)((rows + 127) / 128 * fp4::num_atoms_k(kind, K) * 512);
+}
+
+int fp4_quantize(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_t ld, int kind,
+                 const float *amax, uint8_t *q, uint8_t *q_scales, uint8_t *qt,
+                 uint8_t *qt_scales, float *global_scale, cudaStream_t stream) {
+  if (!valid_dtype(in_dtype) || !valid_kind(kind) || !dims_ok(rows, cols))
+    return FP8Q_ERR_INVALID_ARG;
+  int rc = check_matrix(x, rows, cols, ld, dtype_size(in_dtype));
+  if (rc != FP8Q_OK) return rc;
+  const bool empty = rows == 0 || cols == 0;
+  if ((q == nullptr) != (q_scales == nullptr) || (qt == nullptr) != (qt_scales == nullptr) ||
+      (!empty && q == nullptr && qt == nullptr))
+    return FP8Q_ERR_INVALID_ARG;
+  if (kind == FP4Q_NVFP4 ? (amax == nullptr || global_scale == nullptr) : global_scale != nullptr)
+    return FP8Q_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(q_scales, 16) || !aligned(qt, 16) || !aligned(qt_scales, 16) ||
+      !aligned(amax, 4) || !aligned(global_scale, 4))
+    return FP8Q_ERR_MISALIGNED;
+  if ((rc = check_device()) != FP8Q_OK) return rc;
+  if (log_enabled())
+    fprintf(stderr, "[fp8q] fp4_quantize %lldx%lld kind=%d q=%d qt=%d\n", (long long)rows,
+            (long long)cols, kind, q != nullptr, qt != nullptr);
+  if (empty)
+    return kind == FP4Q_NVFP4 ? from_cuda(fp4::launch_global(amax, global_scale, stream)) : FP8Q_OK;
+  const fp4q_operand a{q, q_scales, nullptr, kind, 0}, b{qt, qt_scales, nullptr, kind, 0};
+  return quantize_into(x, in_dtype, rows, cols, ld, kind, amax, nullptr, q ? &a : nullptr,
+                       qt ? &b : nullptr, global_scale, stream);
+}
+
+int fp4_amax(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_t ld, float *amax,
+             cudaStream_t stream) {
+  if (!valid_dtype(in_dtype) || !dims_ok(rows, cols) || amax == nullptr)
+    return FP8Q_ERR_INVALID_ARG;
+  int rc = check_matrix(x, rows, cols, ld, dtype_size(in_dtype));
+  if (rc != FP8Q_OK) return rc;
+  if (!aligned(amax, 4)) return FP8Q_ERR_MISALIGNED;
+  if ((rc = check_device()) != FP8Q_OK) return rc;
+  return from_cuda(fp4::launch_amax_ld(x, in_dtype, rows, cols, ld, amax, stream));
+}
+
+int fp4_dequantize(const fp4q_operand *op, int64_t rows, int64_t K, void *y, int out_dtype,
+                   cudaStream_t stream) {
+  if (!valid_dtype(out_dtype) || !dims_ok(rows, K)) return FP8Q_ERR_INVALID_ARG;
+  int rc = check_operand(op, rows, K);
+  if (rc != FP8Q_OK) return rc;
+  if ((rc = check_matrix(y, rows, K, K, 16)) != FP8Q_OK) return rc;
+  if ((rc = check_device()) != FP8Q_OK) return rc;
+  if (rows == 0 || K == 0) return FP8Q_OK;
+  return from_cuda(fp4::launch_dequantize(op->kind, *op, rows, K, out_dtype, y, stream));
+}
+
+int fp4_gemm(const fp4q_operand *A, const fp4q_operand *B, void *C, int out_dtype, int64_t M,
+             int64_t N, int64_t K, cudaStream_t stream) {
+  if (!valid_dtype(out_dtype) || !linear_ok(M, N, K)) return FP8Q_ERR_INVALID_ARG;
+  int rc = check_operand(A, M, K);
+  if (rc != FP8Q_OK) return rc;
+  if ((rc = check_operand(B, N, K)) != FP8Q_OK) return rc;
+  if (A->kind != B->kind) return FP8Q_ERR_INVALID_ARG;
+  if ((rc = check_matrix(C, M, N, N, 16)) != FP8Q_OK) return rc;
+  if ((rc = check_device()) != FP8Q_OK) return rc;
+  return product(*A, *B, C, out_dtype, M, N, K, stream);
+}
+
+size_t fp4q_linear_workspace_size(int kind, int64_t M, int64_t N, int64_t K) {
+  if (!valid_kind(kind) || !linear_ok(M, N, K)) return 0;
+  Pieces ws{nullptr};
+  ws.take(8);
+  ws.take(data_bytes(M, K));
+  ws.take(fp4q_scale_bytes(kind, M, K));
+  return ws.used;
+}
+
+int fp4_linear(const void *x, int in_dtype, int64_t ldx, const fp4q_operand *w, int64_t M,
+               int64_t N, int64_t K, const float *x_amax, void *y, int out_dtype,
+               void *workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype) || !linear_ok(M, N, K))
+    return FP8Q_ERR_INVALID_ARG;
+  int rc = check_operand(w, N, K);
+  if (rc != FP8Q_OK) return rc;
+  if ((rc = check_matrix(x, M, K, ldx, dtype_size(in_dtype))) != FP8Q_OK) return rc;
+  if ((rc = check_matrix(y, M, N, N, 16)) != FP8Q_OK) return rc;
+  if (!aligned(x_amax, 4)) return FP8Q_ERR_MISALIGNED;
+  if (workspace == nullptr || ws_bytes < fp4q_linear_workspace_size(w->kind, M, N, K))
+    return FP8Q_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FP8Q_ERR_MISALIGNED;
+  if ((rc = check_device()) != FP8Q_OK) return rc;
+  if (M == 0 || N == 0) return FP8Q_OK;
+  Pieces ws{static_cast<uint8_t *>(workspace)};
+  float *words = reinterpret_cast<float *>(ws.take(8));
+  fp4q_operand q{};
+  q.kind = w->kind;
+  q.data = ws.take(data_bytes(M, K));
+  q.scales = ws.take(fp4q_scale_bytes(w->kind, M, K));
+  q.global_scale = w->kind == FP4Q_NVFP4 ? words + 1 : nullptr;
+  rc = quantize_into(x, in_dtype, M, K, ldx, w->kind, x_amax, words, &q, nullptr, words + 1,
+                     stream);
+  if (rc != FP8Q_OK) return rc;
+  return product(q, *w, y, out_dtype, M, N, K, stream);
+}
+
+size_t fp4q_linear_train_workspace_size(int kind, int64_t M, int64_t N, int64_t K) {
+  if (!valid_kind(kind) || !linear_ok(M, N, K)) return 0;
+  Pieces ws{nullptr};
+  Both b;
+  b.lay_out(ws, kind, M, K);
+  b.lay_out(ws, kind, N, K);
+  b.lay_out(ws, kind, M, N);
+  return ws.used;
+}
+
+int fp4_linear_train(const void *x, const void *w, const void *g, int in_dtype, int64_t M,
+                     int64_t N, int64_t K, int kind, void *y, void *dx, void *dw, int out_dtype,
+                     void *workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype) || !valid_kind(kind) ||
+      !linear_ok(M, N, K))
+    return FP8Q_ERR_INVALID_ARG;
+  const int64_t in = dtype_size(in_dtype);
+  int rc;
+  if ((rc = check_matrix(x, M, K, K, in)) != FP8Q_OK ||
+      (rc = check_matrix(w, N, K, K, in)) != FP8Q_OK ||
+      (rc = check_matrix(g, M, N, N, in)) != FP8Q_OK ||
+      (rc = check_matrix(y, M, N, N, 16)) != FP8Q_OK ||
+      (rc = check_matrix(dx, M, K, K, 16)) != FP8Q_OK ||
+      (rc = check_matrix(dw, N, K, K, 16)) != FP8Q_OK)
+    return rc;
+  if (workspace == nullptr || ws_bytes < fp4q_linear_train_workspace_size(kind, M, N, K))
+    return FP8Q_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FP8Q_ERR_MISALIGNED;
+  if ((rc = check_device()) != FP8Q_OK) return rc;
+  Pieces ws{static_cast<uint8_t *>(workspace)};
+  Both bx, bw, bg;
+  bx.lay_out(ws, kind, M, K);
+  bw.lay_out(ws, kind, N, K);
+  bg.lay_out(ws, kind, M, N);
+  const struct {
+    const void *p;
+    int64_t rows, cols;
+    const Both *to;
+  } in_m[3] = {{x, M, K, &bx}, {w, N, K, &bw}, {g, M, N, &bg}};
+  for (const auto &m : in_m) {
+    rc = quantize_into(m.p, in_dtype, m.rows, m.cols, m.cols, kind, nullptr, m.to->amax,
+                       &m.to->rows, &m.to->cols, m.to->global, stream);
+    if (rc != FP8Q_OK) return rc;
+  }
+  if ((rc = product(bx.rows, bw.rows, y, out_dtype, M, N, K, stream)) != FP8Q_OK ||
+      (rc = product(bg.rows, bw.cols, dx, out_dtype, M, K, N, stream)) != FP8Q_OK)
+    return rc;
+  return product(bg.cols, bx.cols, dw, out_dtype, N, K, M, stream);
+}
+
+int fp8_act_forward(int act, int dtype, int64_t T, int64_t F, const void *u, int64_t ldu,
+                    const void *v, int64_t ldv, void *a, int64_t lda, uint8_t *u8,
+                    float *u_scales, uint8_t *v8, float *v_scales, cudaStream_t stream) {
+  if (act < FP8Q_ACT_SILU || act > FP8Q_ACT_GELU_TANH || !valid_dtype(dtype) || !dims_ok(T, F))
+    return FP8Q_ERR_INVALID_ARG;
+  const int64_t size = dtype_size(dtype);
+  const bool gated = v != nullptr;
+  if (gated != (v8 != nullptr) || gated != (v_scales != nullptr)) return FP8Q_ERR_INVALID_ARG;
+  int rc;
+  if ((rc = check_matrix(u, T, F, ldu, size)) != FP8Q_OK ||
+      (gated && (rc = check_matrix(v, T, F, ldv, size)) != FP8Q_OK) ||
+      (rc = check_matrix(a, T, F, lda, size)) != FP8Q_OK ||
+      (rc = check_matrix(u8, T, F, F, 1)) != FP8Q_OK ||
+      (rc = check_matrix(u_scales, T, F, F, 4)) != FP8Q_OK)
+    return rc;
+  if (!aligned(v_scales, 4)) return FP8Q_ERR_MISALIGNED;
+  if ((rc = check_device()) != FP8Q_OK) return rc;
+  if (T == 0 || F == 0) return FP8Q_OK;
+  if (log_enabled())
+    fprintf(stderr, "[fp8q] fp8_act_forward act=%d %lldx%lld gated=%d\n", act, (long long)T,
+            (long long)F, gated);
+  act::ForwardArgs p{};
+  p.T = T;
+  p.F = F;
+  p.u = u;
+  p.v = v;
+  p.ldu = ldu;
+  p.ldv = ldv;
+  p.a = a;
+  p.lda = lda;
+  p.u8 = u8;
+  p.v8 = v8;
+  p.u_scales = u_scales;
+  p.v_scales = v_scales;
+  return from_cuda(act::launch_forward(act, dtype, p, stream));
+}
+
+int fp8_act_backward(int act, int dtype, int64_t T, int64_t F, const uint8_t *u8,
+                     const float *u_scales, const uint8_t *v8, const float *v_scales,
+                     const void *da, int64_t ldda, void *du, int64_t lddu, void *dv,
+                     int64_t lddv, void *a, int64_t lda, cudaStream_t stream) {
+  if (act < FP8Q_ACT_SILU || act > FP8Q_ACT_GELU_TANH || !valid_dtype(dtype) || !dims_ok(T, F))
+    return FP8Q_ERR_INVALID_ARG;
+  const int64_t size = dtype_size(dtype);
+  const bool gated = v8 != nullptr;
+  if (gated != (v_scales != nullptr) || gated != (dv != nullptr)) return FP8Q_ERR_INVALID_ARG;
+  int rc;
+  if ((rc = check_matrix(u8, T, F, F, 1)) != FP8Q_OK ||
+      (rc = check_matrix(u_scales, T, F, F, 4)) != FP8Q_OK ||
+      (rc = check_matrix(da, T, F, ldda, size)) != FP8Q_OK ||
+      (rc = check_matrix(du, T, F, lddu, size)) != FP8Q_OK ||
+      (gated && (rc = check_matrix(dv, T, F, lddv, size)) != FP8Q_OK) ||
+      (a != nullptr && (rc = check_matrix(a, T, F, lda, size)) != FP8Q_OK))
+    return rc;
+  if (!aligned(v_scales, 4)) return FP8Q_ERR_MISALIGNED;
+  if ((rc = check_device()) != FP8Q_OK) return rc;
+  if (T == 0 || F == 0) return FP8Q_OK;
+  if (log_enabled())
+    fprintf(stderr, "[fp8q] fp8_act_backward act=%d %lldx%lld gated=%d a=%d\n", act, (long long)T,
+            (long long)F, gated, a != nullptr);
+  act::BackwardArgs p{};
+  p.T = T;
+  p.F = F;
+  p.u8 = u8;
+  p.v8 = v8;
+  p.u_scales = u_scales;
+  p.v_scales = v_scales;
+  p.da = da;
+  p.ldda = ldda;
+  p.du = du;
+  p.lddu = lddu;
+  p.dv = dv;
+  p.lddv = lddv;
+  p.a = a;
+  p.lda = lda;
+  return from_cuda(act::launch_backward(act, dtype, p, stream));
+}
+
+}  // extern "C"

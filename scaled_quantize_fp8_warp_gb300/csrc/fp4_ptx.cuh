@@ -1,0 +1,49 @@
+// Inline-PTX wrappers for the 4-bit block-scaled MMA (tcgen05.mma
+// kind::mxf4nvf4), written from the public PTX ISA description.
+#pragma once
+
+#include <stdint.h>
+
+#include "../../include/fp8q.h"
+#include "fp8q_ptx.cuh"
+
+namespace fp8q {
+namespace ptx {
+
+// Instruction descriptor for kind::mxf4nvf4, both operands E2M1 and K-major,
+// K = 64 per instruction: scale-word half of B in [4,6) and of A in [29,31)
+// (0 or 2: which two bytes of the 32-bit word, for one scale per 32), A / B
+// formats in [7,10) / [10,12) (1 = E2M1), N >> 3 in [17,23), scale type in
+// bit 23 (0 = UE4M3, 1 = UE8M0), M >> 7 in [27,29).
+__host__ __device__ constexpr uint32_t idesc_fp4(int kind, uint32_t m, uint32_t n) {
+  return (1u << 7) | (1u << 10) | ((n >> 3) << 17) |
+         ((kind == FP4Q_MXFP4 ? 1u : 0u) << 23) | ((m >> 7) << 27);
+}
+
+// D[tmem] (+)= (A . SFA) . (B . SFB)^T over 64 K, scales read from tensor
+// memory: two bytes a row for MXFP4 (one scale per 32), four for NVFP4 (one
+// per 16).
+template <int KIND>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                        uint32_t accumulate) {
+  if (KIND == FP4Q_MXFP4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+}  // namespace ptx
+}  // namespace fp8q
