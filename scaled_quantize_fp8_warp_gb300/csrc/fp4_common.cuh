@@ -54,67 +54,97 @@ __device__ __forceinline__ float nv_global(float amax) {
   return g < 1e-12f ? 1e-12f : g;
 }
 
+// NVFP4's 127 block scales of one tensor: d = fl32(s g) and RN(1 / d) by
+// scale byte, so that no block needs a division of its own.
+struct ScaleTable {
+  float2 d_r[128];
+  __device__ __forceinline__ void fill(float g) {   // by 128 threads or more, then a barrier
+    if (threadIdx.x < 128) {
+      const __half_raw h =
+          __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)min(threadIdx.x, 126u), __NV_E4M3);
+      const float d = __fmul_rn(__half2float(__half(h)), g);
+      d_r[threadIdx.x] = make_float2(d, threadIdx.x == 0 ? 0.0f : __frcp_rn(d));
+    }
+  }
+};
+
+// RN(RN(amax / 6) / g) with rg = RN(1 / g), each quotient by Markstein's
+// correction.  Past 512 the scale saturates, below 2^-10 it is the smallest:
+// there the quotient need not be exact (and the correction may overflow).
+__device__ __forceinline__ float nv_ratio(float amax, float g, float rg) {
+  const float r6 = 1.0f / 6.0f;
+  const float a0 = __fmul_rn(amax, r6);
+  const float a = __fmaf_rn(__fmaf_rn(a0, -6.0f, amax), r6, a0);
+  const float t0 = __fmul_rn(a, rg);
+  return t0 > 512.0f ? t0 : __fmaf_rn(__fmaf_rn(t0, -g, a), rg, t0);
+}
+
 // A block's scale byte and what dividing by the scale takes.
 struct BlockScale {
   uint32_t byte;
-  float d;   // NVFP4: the divisor; unused for MXFP4
-  float r;   // MXFP4: 1 / d, exact; NVFP4: RN(1 / d); 0 where the block is not finite
-  bool over; // NVFP4: the block's scale saturated, so quotients may pass 6 by any factor
+  float d;     // NVFP4: the divisor; unused for MXFP4
+  float r;     // MXFP4: 1 / d, exact; NVFP4: RN(1 / d)
+  bool nan;    // the block stands for NaN
+  bool over;   // NVFP4: the scale saturated, so quotients may pass 6 by any factor
 };
 
 template <int KIND>
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g) {
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g, float rg,
+                                                  const ScaleTable *table) {
   BlockScale b;
-  const bool finite = amax_bits < 0x7F800000u;
+  b.nan = amax_bits >= 0x7F800000u;
   if (KIND == FP4Q_MXFP4) {
     // the biased exponent of amax is floor(log2 amax) + 127; zero, subnormal
-    // and tiny maxima clamp to 2^-127
-    const int e = (int)(amax_bits >> 23);
-    b.byte = finite ? (uint32_t)max(e - 2, 0) : 0xFFu;
+    // and tiny maxima clamp to 2^-127, whose reciprocal is a normal number
+    const uint32_t code = (uint32_t)max((int)(amax_bits >> 23) - 2, 0);
+    b.byte = b.nan ? 0xFFu : code;
     b.d = 0.0f;
+    b.r = __uint_as_float((254u - code) << 23);
     b.over = false;
-    // 2^(127 - byte), a normal number for every finite byte (at most 252)
-    b.r = finite ? __uint_as_float((254u - b.byte) << 23) : 0.0f;
   } else {
-    const float t = __fdiv_rn(__fdiv_rn(__uint_as_float(amax_bits), 6.0f), g);
-    uint32_t s = (uint32_t)__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
-    s = s == 0u ? 1u : s;                       // at least 2^-9
-    const bool nan = !finite || !(t == t) || !(g < __uint_as_float(0x7F800000u));
-    b.byte = nan ? 0x7Fu : s;
-    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s, __NV_E4M3);
-    b.d = __fmul_rn(__half2float(__half(h)), g);
-    b.r = nan ? 0.0f : __frcp_rn(b.d);
+    const float t = nv_ratio(__uint_as_float(amax_bits), g, rg);
+    uint32_t s = (uint32_t)__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3) & 0x7Fu;
+    s = min(max(s, 1u), 126u);                   // at least 2^-9
+    b.nan = b.nan || !(g < __uint_as_float(0x7F800000u));
+    b.byte = b.nan ? 0x7Fu : s;
+    const float2 dr = table->d_r[s];
+    b.d = dr.x;
+    b.r = dr.y;
     b.over = t > 448.0f;
   }
   return b;
 }
 
-// Codes of two elements of a block (the first in the low four bits).
+// Codes of two elements of a block, given negated (the first in the low four
+// bits).  NVFP4: RN(x / d) by Markstein's correction, signs arranged so that a
+// zero quotient keeps x's sign: q0 = x r, e = q0 d - x, q = q0 - e r.
 template <int KIND>
-__device__ __forceinline__ uint32_t encode2(float lo, float hi, const BlockScale &b) {
-  if (KIND == FP4Q_MXFP4) return e2m1x2(__fmul_rn(lo, b.r), __fmul_rn(hi, b.r));
-  if (b.over) {   // keep the correction finite: everything past 6 d has the code of 6 d
-    lo = fminf(fmaxf(lo, -6.5f * b.d), 6.5f * b.d);
-    hi = fminf(fmaxf(hi, -6.5f * b.d), 6.5f * b.d);
+__device__ __forceinline__ uint32_t encode2(float2 y, const BlockScale &b) {
+  const float2 nr = make_float2(-b.r, -b.r);
+  if (KIND == FP4Q_NVFP4 && b.over) {   // keep the correction finite: past 6 d the code is 6's
+    const float lim = 6.5f * b.d;
+    y.x = fminf(fmaxf(y.x, -lim), lim);
+    y.y = fminf(fmaxf(y.y, -lim), lim);
   }
-  const float2 x = make_float2(lo, hi), r = make_float2(b.r, b.r), nd = make_float2(-b.d, -b.d);
-  const float2 q0 = __fmul2_rn(x, r);
-  const float2 q = __ffma2_rn(__ffma2_rn(q0, nd, x), r, q0);
-  return e2m1x2(copysignf(q.x, lo), copysignf(q.y, hi));   // a zero quotient keeps its sign
+  float2 q = __fmul2_rn(y, nr);
+  if (KIND == FP4Q_NVFP4) q = __ffma2_rn(__ffma2_rn(q, make_float2(b.d, b.d), y), nr, q);
+  return e2m1x2(q.x, q.y);
 }
 
-// Codes of eight elements, element j in bits [4j, 4j + 4).
+// Codes of eight elements given as negated pairs, element j in bits
+// [4j, 4j + 4).
 template <int KIND>
-__device__ __forceinline__ uint32_t encode8(const float (&v)[8], const BlockScale &b) {
-  const uint32_t w = encode2<KIND>(v[0], v[1], b) | (encode2<KIND>(v[2], v[3], b) << 8) |
-                     (encode2<KIND>(v[4], v[5], b) << 16) | (encode2<KIND>(v[6], v[7], b) << 24);
-  return b.r == 0.0f ? 0u : w;   // NaN or infinity in the block
+__device__ __forceinline__ uint32_t encode8(float2 y0, float2 y1, float2 y2, float2 y3,
+                                            const BlockScale &b) {
+  const uint32_t lo = __byte_perm(encode2<KIND>(y0, b), encode2<KIND>(y1, b), 0x0040);
+  const uint32_t hi = __byte_perm(encode2<KIND>(y2, b), encode2<KIND>(y3, b), 0x0040);
+  return b.nan ? 0u : __byte_perm(lo, hi, 0x5410);
 }
 
-// Value of one E2M1 code: exact in fp32.
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-  const __half_raw h = __nv_cvt_fp4_to_halfraw((__nv_fp4_storage_t)(code & 15u), __NV_E2M1);
-  return __half2float(__half(h));
+// Values of the two codes in a byte, the low one first: exact in fp32.
+__device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(byte & 0xFFu), __NV_E2M1);
+  return __half22float2(__half2(h));
 }
 
 // Value of a scale byte.

@@ -17,40 +17,78 @@
 
 #include "fp4_common.cuh"
 #include "fp4_internal.h"
+#include "fp8_pack8.cuh"
 
 namespace fp8q {
 namespace fp4 {
 namespace {
 
+using pack8::Pack8;
+using pack8::load;
+
 constexpr int kTile = 128;
 constexpr int kThreads = 256;
 
-// Eight consecutive elements of a row as fp32.  VEC: 16-byte loads (the base
-// and every row are 16-byte aligned); elements at or past `valid` read as 0.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *p, int valid, float (&v)[8]) {
-  if (VEC && valid >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Maxima (fp32 bit patterns) of the blocks that this thread's 8 rows (m) and
+// 8 columns of an 8 x 8 patch belong to: `lanes` neighbouring lanes share a
+// block of a row, `lanes` lanes eight apart one of a column.  bf16 works on
+// two 16-bit magnitudes to a register.
+template <int LANES>
+__device__ __forceinline__ void block_max_rows(const Pack8<__nv_bfloat16> (&x)[8], uint32_t (&m)[8]) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(u[k] << 16);
-        v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-      }
-    } else {
-      const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-      const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-    return;
+  for (int i = 0; i < 8; i += 2) {
+    // high halves: rows i and i + 1
+    uint32_t t = __byte_perm(x[i].amax_bits(), x[i + 1].amax_bits(), 0x7632);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) t = __vmaxu2(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+    m[i] = t << 16;
+    m[i + 1] = t & 0xFFFF0000u;
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = j < valid ? (float)p[j] : 0.0f;
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+template <int LANES>
+__device__ __forceinline__ void block_max_rows(const Pack8<float> (&x)[8], uint32_t (&m)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m[i] = x[i].amax_bits();
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) m[i] = max(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+  }
+}
+
+template <int LANES>
+__device__ __forceinline__ void block_max_cols(const Pack8<__nv_bfloat16> (&x)[8], uint32_t (&m)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = __vmaxu2(t, x[i].w[k] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) t = __vmaxu2(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8 * o));
+    m[2 * k] = t << 16;
+    m[2 * k + 1] = t & 0xFFFF0000u;
+  }
+}
+
+template <int LANES>
+__device__ __forceinline__ void block_max_cols(const Pack8<float> (&x)[8], uint32_t (&m)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    m[j] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[j] = max(m[j], __float_as_uint(x[i].v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 8 * o));
+  }
+}
+
+// The transposed codes of a tile in shared memory: word w (8 rows) of column
+// c.  Sixteen-byte chunks are permuted by the column and every 32 columns
+// shift by 16 words, so that a warp's stores (8 columns eight apart x 4 words)
+// fall into 32 banks.
+__device__ __forceinline__ int t_word(int c, int w) {
+  return (c + (c >> 5)) * 16 + ((((w >> 2) ^ (c >> 3)) & 3) << 2 | (w & 3));
+}
 
 template <int KIND, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs p) {
@@ -58,7 +96,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs p) {
   constexpr int kAtoms = kTile / Kind<KIND>::kAtomK;   // atoms along K per tile: 1 or 2
   constexpr int kLanes = kBlock / 8;                   // lanes that share a block: 4 or 2
   __shared__ __align__(16) uint8_t s_scale[kAtoms * 512], t_scale[kAtoms * 512];
-  __shared__ __align__(16) uint32_t t_code[kTile][kTile / 8 + 4];   // [column][8 rows a word]
+  __shared__ __align__(16) uint32_t t_code[(kTile + kTile / 32) * 16];
+  __shared__ ScaleTable table;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tr = (warp >> 1) * 32 + (lane >> 3) * 8;   // this thread's first row in the tile
@@ -67,56 +106,59 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs p) {
   const unsigned by = blockIdx.x / tiles_c, bx = blockIdx.x - by * tiles_c;
   const int64_t r0 = (int64_t)by * kTile, c0 = (int64_t)bx * kTile;
   const int64_t row = r0 + tr, col = c0 + tc;
-  const T *x = static_cast<const T *>(p.x);
 
-  float v[8][8];
-  const int valid = (int)max((int64_t)0, min((int64_t)8, p.cols - col));
+  Pack8<T> y[8];
+  const int rows_in = (int)max((int64_t)0, min((int64_t)8, p.rows - row));
+  const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.cols - col));
+  {
+    const T *x = static_cast<const T *>(p.x) + (rows_in > 0 && cols_in > 0 ? row * p.ld + col : 0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool in = row + i < p.rows && valid > 0;
-    load8<T, VEC>(x + (in ? (row + i) * p.ld + col : 0), in ? valid : 0, v[i]);
+    for (int i = 0; i < 8; ++i) load<VEC>(y[i], i < rows_in ? x + i * p.ld : x, i < rows_in ? cols_in : 0);
   }
-  const float g = KIND == FP4Q_NVFP4 ? nv_global(*p.amax) : 1.0f;
-  if (KIND == FP4Q_NVFP4 && p.global_scale != nullptr && blockIdx.x == 0 && threadIdx.x == 0)
-    *p.global_scale = g;
+  float g = 1.0f, rg = 1.0f;
+  if (KIND == FP4Q_NVFP4) {
+    g = nv_global(*p.amax);
+    rg = __frcp_rn(g);
+    table.fill(g);
+    if (p.global_scale != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.global_scale = g;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i].negate();   // encode8 takes the negated elements
 
   if (p.q != nullptr) {
     const int64_t ldq = row_bytes(p.cols);
+    uint8_t *q = p.q + row * ldq + col / 2;
+    const bool in = col / 2 < ldq;
+    uint32_t m[8];
+    block_max_rows<kLanes>(y, m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const BlockScale b = block_scale<KIND>(m, g);
-      const uint32_t w = encode8<KIND>(v[i], b);
-      if (row + i < p.rows && col / 2 < ldq)
-        *reinterpret_cast<uint32_t *>(p.q + (row + i) * ldq + col / 2) = w;
+      const BlockScale b = block_scale<KIND>(m[i], g, rg, &table);
+      const uint32_t w = encode8<KIND>(y[i].pair(0), y[i].pair(1), y[i].pair(2), y[i].pair(3), b);
+      if (i < rows_in && in) *reinterpret_cast<uint32_t *>(q + i * ldq) = w;
       if ((lane & (kLanes - 1)) == 0)
         s_scale[atom_byte(tr + i, tc / kBlock, kAtoms)] =
-            (uint8_t)(row + i < p.rows && col < p.cols ? b.byte : 0u);
+            (uint8_t)(i < rows_in && cols_in > 0 ? b.byte : 0u);
     }
   }
   if (p.qt != nullptr) {
+    uint32_t m[8];
+    block_max_cols<kLanes>(y, m);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i][j]));
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8 * o));
-      const BlockScale b = block_scale<KIND>(m, g);
-      const float t[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
-      t_code[tc + j][tr / 8] = encode8<KIND>(t, b);
+      const BlockScale b = block_scale<KIND>(m[j], g, rg, &table);
+      t_code[t_word(tc + j, tr / 8)] =
+          encode8<KIND>(make_float2(y[0].at(j), y[1].at(j)), make_float2(y[2].at(j), y[3].at(j)),
+                        make_float2(y[4].at(j), y[5].at(j)), make_float2(y[6].at(j), y[7].at(j)), b);
       if (((lane >> 3) & (kLanes - 1)) == 0)
         t_scale[atom_byte(tc + j, tr / kBlock, kAtoms)] =
-            (uint8_t)(row < p.rows && col + j < p.cols ? b.byte : 0u);
+            (uint8_t)(rows_in > 0 && j < cols_in ? b.byte : 0u);
     }
   }
   __syncthreads();
-  // Atoms of this tile: kAtoms consecutive ones of row block `by` (or
-  // of the transpose's row block `bx`); the last tile may have fewer.
+  // Atoms of this tile: kAtoms consecutive ones of row block `by` (or of the
+  // transpose's row block `bx`); the last tile may have fewer.
   if (threadIdx.x < kAtoms * 32) {
     const int a = threadIdx.x >> 5;
     if (p.q != nullptr) {
@@ -140,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs p) {
       const int64_t at = r0 / 2 + piece * 16;
       if (c0 + c < p.cols && at < ldt)
         *reinterpret_cast<uint4 *>(p.qt + (c0 + c) * ldt + at) =
-            *reinterpret_cast<const uint4 *>(&t_code[c][piece * 4]);
+            *reinterpret_cast<const uint4 *>(&t_code[t_word(c, piece * 4)]);
     }
   }
 }
@@ -152,6 +194,8 @@ __global__ void global_kernel(const float *amax, float *global_scale) {
 // max |x| for matrices whose rows lie apart or are not 16-byte aligned.  The
 // maximum of bit patterns does not depend on the order of the atomics; NaN
 // patterns sort above infinity.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
 template <typename T>
 __global__ void __launch_bounds__(256)
     amax_ld_kernel(const T *x, int64_t rows, int64_t cols, int64_t ld, unsigned int *amax) {
@@ -169,22 +213,39 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Values of an operand: one thread per 8 codes (one 32-bit word) of a row.
-template <int KIND, typename T>
-__global__ void __launch_bounds__(256)
+// Values of an operand: one thread per 8 codes (one 32-bit word) of four rows
+// at a time, whose reads are in flight together.  VEC: every row of y starts on
+// a 16-byte boundary.
+template <int KIND, typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const fp4q_operand op, int64_t rows, int64_t K, T *y) {
-  const int64_t ldq = row_bytes(K), words = (K + 7) / 8, nk = num_atoms_k(KIND, K);
-  const int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (w >= words) return;
+  constexpr int kRows = 4;
+  const int64_t ldq = row_bytes(K), nk = num_atoms_k(KIND, K);
+  const int64_t w = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int valid = (int)min((int64_t)8, K - w * 8);
+  if (valid <= 0) return;
   const float g = KIND == FP4Q_NVFP4 ? *op.global_scale : 1.0f;
-  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-    const uint32_t code = *reinterpret_cast<const uint32_t *>(op.data + r * ldq + w * 4);
-    const float s =
-        scale_value<KIND>(op.scales[atom_byte(r, w * 8 / Kind<KIND>::kBlock, nk)], g);
-    T *out = y + r * K + w * 8;
+  for (int64_t r0 = (int64_t)blockIdx.y * kRows; r0 < rows; r0 += (int64_t)gridDim.y * kRows) {
+    uint32_t code[kRows], byte[kRows];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (w * 8 + j < K) out[j] = (T)__fmul_rn(e2m1_value(code >> (4 * j)), s);
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t r = min(r0 + i, rows - 1);
+      code[i] = *reinterpret_cast<const uint32_t *>(op.data + r * ldq + w * 4);
+      byte[i] = op.scales[atom_byte(r, w * 8 / Kind<KIND>::kBlock, nk)];
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (r0 + i >= rows) break;
+      const float s = scale_value<KIND>(byte[i], g);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = e2m1x2_values(code[i] >> (8 * j));
+        v[2 * j] = __fmul_rn(f.x, s);
+        v[2 * j + 1] = __fmul_rn(f.y, s);
+      }
+      pack8::store<VEC>(y + (r0 + i) * K + w * 8, valid, v);
+    }
   }
 }
 
@@ -233,21 +294,28 @@ cudaError_t launch_amax_ld(const void *x, int in_dtype, int64_t rows, int64_t co
   return cudaGetLastError();
 }
 
+template <int KIND, typename T>
+static cudaError_t run_dequantize(const fp4q_operand &op, int64_t rows, int64_t K, void *y,
+                                  cudaStream_t stream) {
+  const int64_t gx = (K + 8 * kThreads - 1) / (8 * kThreads);
+  if (gx > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>((rows + 3) / 4, 65535));
+  if (K * (int64_t)sizeof(T) % 16 == 0)
+    dequantize_kernel<KIND, T, true><<<grid, kThreads, 0, stream>>>(op, rows, K, static_cast<T *>(y));
+  else
+    dequantize_kernel<KIND, T, false><<<grid, kThreads, 0, stream>>>(op, rows, K, static_cast<T *>(y));
+  return cudaGetLastError();
+}
+
 cudaError_t launch_dequantize(int kind, const fp4q_operand &op, int64_t rows, int64_t K,
                               int out_dtype, void *y, cudaStream_t stream) {
-  const dim3 grid((unsigned)(((K + 7) / 8 + 255) / 256), (unsigned)std::min<int64_t>(rows, 65535));
-  if (kind == FP4Q_MXFP4) {
-    if (out_dtype == FP8Q_DT_BF16)
-      dequantize_kernel<FP4Q_MXFP4><<<grid, 256, 0, stream>>>(op, rows, K, (__nv_bfloat16 *)y);
-    else
-      dequantize_kernel<FP4Q_MXFP4><<<grid, 256, 0, stream>>>(op, rows, K, (float *)y);
-  } else {
-    if (out_dtype == FP8Q_DT_BF16)
-      dequantize_kernel<FP4Q_NVFP4><<<grid, 256, 0, stream>>>(op, rows, K, (__nv_bfloat16 *)y);
-    else
-      dequantize_kernel<FP4Q_NVFP4><<<grid, 256, 0, stream>>>(op, rows, K, (float *)y);
-  }
-  return cudaGetLastError();
+  if (kind == FP4Q_MXFP4)
+    return out_dtype == FP8Q_DT_BF16
+               ? run_dequantize<FP4Q_MXFP4, __nv_bfloat16>(op, rows, K, y, stream)
+               : run_dequantize<FP4Q_MXFP4, float>(op, rows, K, y, stream);
+  return out_dtype == FP8Q_DT_BF16
+             ? run_dequantize<FP4Q_NVFP4, __nv_bfloat16>(op, rows, K, y, stream)
+             : run_dequantize<FP4Q_NVFP4, float>(op, rows, K, y, stream);
 }
 
 }  // namespace fp4

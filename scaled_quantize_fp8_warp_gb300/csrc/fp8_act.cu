@@ -14,82 +14,54 @@
 #include <algorithm>
 
 #include "fp8_act.h"
+#include "fp8_pack8.cuh"
 
 namespace fp8q {
 namespace act {
 namespace {
 
+using pack8::Pack8;
+using pack8::divide2;
+using pack8::load;
+using pack8::store;
+
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// 2^x and 1 / x of the hardware, about 2 units in the last place; tiny results
+// are zero, which no sum with 1 below notices.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
-// f(u), and f'(u) where it is wanted.  exp is the hardware's base-2
-// exponential (about 2 units in the last place); large |u| stay finite: e^-u
-// may overflow to infinity, whose reciprocal is 0.
+// f(u), and f'(u) where it is wanted.  Large |u| stay finite: e^-u may
+// overflow to infinity, whose reciprocal is 0.
 template <int ACT, bool GRAD>
 __device__ __forceinline__ void activation(float u, float &f, float &df) {
   if (ACT == FP8Q_ACT_SILU) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-u));
+    const float s = rcp_fast(1.0f + exp2_fast(-1.44269504f * u));
     f = u * s;
     if (GRAD) df = s * (1.0f + u * (1.0f - s));
   } else if (ACT == FP8Q_ACT_GELU) {
     const float p = 0.5f + 0.5f * erff(u * 0.70710678f);
     f = u * p;
-    if (GRAD) df = p + u * (0.39894228f * __expf(-0.5f * u * u));
+    if (GRAD) df = p + u * (0.39894228f * exp2_fast(-0.72134752f * u * u));
   } else {
-    // (1 + tanh z) / 2 = 1 / (1 + e^-2z)
-    const float p = __fdividef(1.0f, 1.0f + __expf(-1.5957691f * u * (1.0f + 0.044715f * u * u)));
+    // (1 + tanh z) / 2 = 1 / (1 + e^-2z), 2 z log2(e) = u (2.302208 + 0.1029432 u^2)
+    const float uu = u * u;
+    const float p = rcp_fast(1.0f + exp2_fast(-u * (2.30220819f + 0.10294324f * uu)));
     f = u * p;
     if (GRAD) {
       const float q = p * (1.0f - p);
-      df = p + (q == 0.0f ? 0.0f : u * q * 1.5957691f * (1.0f + 0.134145f * u * u));
+      df = p + (q == 0.0f ? 0.0f : u * q * (1.5957691f + 0.21406671f * uu));
     }
   }
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *p, int valid, float (&v)[8]) {
-  if (VEC && valid >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 w = *reinterpret_cast<const uint4 *>(p);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(u[k] << 16);
-        v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-      }
-    } else {
-      const float4 a = *reinterpret_cast<const float4 *>(p);
-      const float4 b = *(reinterpret_cast<const float4 *>(p) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = j < valid ? (float)p[j] : 0.0f;
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T *p, int valid, const float (&v)[8]) {
-  if (VEC && valid >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-        w[k] = *reinterpret_cast<const uint32_t *>(&b);
-      }
-      *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      *(reinterpret_cast<float4 *>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < valid) p[j] = (T)v[j];
 }
 
 // One element where the tile is not finite: a NaN keeps its sign, a NaN that
@@ -102,13 +74,10 @@ __device__ __forceinline__ uint32_t cast1_slow(float x, float s) {
   return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
-// The eight E4M3 bytes of this lane's part of a tile, and the tile's scale.
-__device__ __forceinline__ uint2 cast_tile(const float (&v)[8], float &scale) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+// The eight E4M3 bytes of this lane's part of a tile whose max |x| is m, and
+// the tile's scale.
+template <typename T>
+__device__ __forceinline__ uint2 cast_tile(const Pack8<T> &x, uint32_t m, float &scale) {
   const float q = __fdiv_rn(__uint_as_float(m), 448.0f);
   const float s = q < 1e-12f ? 1e-12f : q;
   scale = s;
@@ -116,19 +85,13 @@ __device__ __forceinline__ uint2 cast_tile(const float (&v)[8], float &scale) {
   if (m < 0x7F800000u) {
     const float r = __frcp_rn(s);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const float2 x = make_float2(v[j], v[j + 1]), r2 = make_float2(r, r);
-      const float2 q0 = __fmul2_rn(x, r2);
-      const float2 e = __ffma2_rn(q0, make_float2(-s, -s), x);
-      float2 t = __ffma2_rn(e, r2, q0);
-      t.x = copysignf(t.x, x.x);
-      t.y = copysignf(t.y, x.y);
-      b[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3);
-    }
-    return make_uint2(b[0] | (b[2] << 16), b[4] | (b[6] << 16));
+    for (int k = 0; k < 4; ++k)
+      b[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(divide2(x.pair(k), s, r), __NV_SATFINITE,
+                                                __NV_E4M3);
+    return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = cast1_slow(v[j], s);
+  for (int j = 0; j < 8; ++j) b[j] = cast1_slow(x.at(j), s);
   return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
                     b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
 }
@@ -144,83 +107,162 @@ __device__ __forceinline__ void store_bytes(uint8_t *p, int valid, uint2 w) {
     if (j < valid) p[j] = (uint8_t)((j < 4 ? w.x >> (8 * j) : w.y >> (8 * (j - 4))) & 0xFFu);
 }
 
-// The values of this lane's eight bytes under scale s.
 template <bool VEC>
-__device__ __forceinline__ void load_saved(const uint8_t *p, int valid, float s, float (&v)[8]) {
+__device__ __forceinline__ uint2 load_bytes(const uint8_t *p, int valid) {
+  if (VEC && valid >= 8) return *reinterpret_cast<const uint2 *>(p);
   uint32_t w[2] = {0u, 0u};
-  if (VEC && valid >= 8) {
-    const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
-    w[0] = t.x, w[1] = t.y;
-  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < valid) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
-  }
+  for (int j = 0; j < 8; ++j)
+    if (j < valid) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+// The values of eight bytes under scale s.
+__device__ __forceinline__ void saved(uint2 w, float s, float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-        (__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+        (__nv_fp8x2_storage_t)((j < 2 ? w.x : w.y) >> (16 * (j & 1))), __NV_E4M3);
     const float2 f = __half22float2(__half2(h));
     v[2 * j] = __fmul_rn(f.x, s);
     v[2 * j + 1] = __fmul_rn(f.y, s);
   }
 }
 
+// The pieces (2 rows x 128 columns) of a [T, F] matrix that one warp visits:
+// numbered row pair after row pair, `step` apart, kept as (pair, tile)
+// without a division per piece.
+struct Walk {
+  int64_t pair, pairs;
+  int tile, tiles;
+  int64_t step_pair;
+  int step_tile;
+  __device__ __forceinline__ Walk(int64_t T, int64_t F) {
+    const int64_t first = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
+    tiles = (int)((F + 127) / 128);
+    pairs = (T + 1) / 2;
+    pair = first / tiles;
+    tile = (int)(first - pair * tiles);
+    step_pair = step / tiles;
+    step_tile = (int)(step - step_pair * tiles);
+  }
+  __device__ __forceinline__ bool in() const { return pair < pairs; }
+  __device__ __forceinline__ void next() {
+    pair += step_pair;
+    tile += step_tile;
+    if (tile >= tiles) {
+      tile -= tiles;
+      ++pair;
+    }
+  }
+};
+
+// This lane's 8 elements of a piece: row, first column, how many exist.
+struct Place {
+  int64_t row;
+  int64_t col;
+  int tile, valid;
+  __device__ __forceinline__ Place(const Walk &w, int64_t T, int64_t F) {
+    const int lane = threadIdx.x & 31;
+    row = 2 * w.pair + (lane >> 4);
+    tile = w.tile;
+    col = (int64_t)tile * 128 + (lane & 15) * 8;
+    valid = w.in() && row < T ? (int)max((int64_t)0, min((int64_t)8, F - col)) : 0;
+  }
+};
+
 template <int ACT, typename T, bool GATED, bool VEC>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const ForwardArgs p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tiles = (p.F + 127) / 128, pairs = (p.T + 1) / 2;
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t n = (int64_t)blockIdx.x * (kThreads / 32) + warp; n < tiles * pairs; n += step) {
-    const int64_t pair = n / tiles, tile = n - pair * tiles;
-    const int64_t row = 2 * pair + (lane >> 4), col = tile * 128 + (lane & 15) * 8;
-    const int valid = row < p.T ? (int)max((int64_t)0, min((int64_t)8, p.F - col)) : 0;
-    const int64_t at = valid > 0 ? 1 : 0;   // nothing is addressed where nothing is valid
-    float u[8], v[8], a[8], s, unused;
-    load8<T, VEC>(static_cast<const T *>(p.u) + at * (row * p.ldu + col), valid, u);
-    if (GATED) load8<T, VEC>(static_cast<const T *>(p.v) + at * (row * p.ldv + col), valid, v);
-    const uint2 bu = cast_tile(u, s);
-    store_bytes<VEC>(p.u8 + at * (row * p.F + col), valid, bu);
-    if ((lane & 15) == 0 && row < p.T) p.u_scales[tile * p.T + row] = s;
-    if (GATED) {
-      const uint2 bv = cast_tile(v, s);
-      store_bytes<VEC>(p.v8 + at * (row * p.F + col), valid, bv);
-      if ((lane & 15) == 0 && row < p.T) p.v_scales[tile * p.T + row] = s;
+  const int lane = threadIdx.x & 31;
+  Walk walk(p.T, p.F);
+  while (walk.in()) {
+    // two pieces at a time: their loads are in flight together
+    Place at[2] = {Place(walk, p.T, p.F), (walk.next(), Place(walk, p.T, p.F))};
+    walk.next();
+    Pack8<T> u[2], v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // nothing is addressed where nothing is valid
+      const int64_t on = at[i].valid > 0 ? 1 : 0;
+      load<VEC>(u[i], static_cast<const T *>(p.u) + on * (at[i].row * p.ldu + at[i].col), at[i].valid);
+      if (GATED)
+        load<VEC>(v[i], static_cast<const T *>(p.v) + on * (at[i].row * p.ldv + at[i].col), at[i].valid);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      activation<ACT, false>(u[j], a[j], unused);
-      if (GATED) a[j] *= v[j];
+    for (int i = 0; i < 2; ++i) {
+      const Place &a = at[i];
+      uint32_t mu = u[i].amax_bits(), mv = GATED ? v[i].amax_bits() : 0u;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        mu = max(mu, __shfl_xor_sync(0xFFFFFFFFu, mu, o));
+        if (GATED) mv = max(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, o));
+      }
+      float su, sv = 0.0f;
+      const uint2 bu = cast_tile(u[i], mu, su);
+      uint2 bv = make_uint2(0u, 0u);
+      if (GATED) bv = cast_tile(v[i], mv, sv);
+      if (a.valid > 0) {
+        store_bytes<VEC>(p.u8 + a.row * p.F + a.col, a.valid, bu);
+        if (GATED) store_bytes<VEC>(p.v8 + a.row * p.F + a.col, a.valid, bv);
+        if ((lane & 15) == 0) {
+          p.u_scales[a.tile * p.T + a.row] = su;
+          if (GATED) p.v_scales[a.tile * p.T + a.row] = sv;
+        }
+        float out[8], unused;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          activation<ACT, false>(u[i].at(j), out[j], unused);
+          if (GATED) out[j] *= v[i].at(j);
+        }
+        store<VEC>(static_cast<T *>(p.a) + a.row * p.lda + a.col, a.valid, out);
+      }
     }
-    store8<T, VEC>(static_cast<T *>(p.a) + at * (row * p.lda + col), valid, a);
   }
 }
 
 template <int ACT, typename T, bool GATED, bool VEC>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const BackwardArgs p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tiles = (p.F + 127) / 128, pairs = (p.T + 1) / 2;
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t n = (int64_t)blockIdx.x * (kThreads / 32) + warp; n < tiles * pairs; n += step) {
-    const int64_t pair = n / tiles, tile = n - pair * tiles;
-    const int64_t row = 2 * pair + (lane >> 4), col = tile * 128 + (lane & 15) * 8;
-    const int valid = row < p.T ? (int)max((int64_t)0, min((int64_t)8, p.F - col)) : 0;
-    if (valid == 0) continue;
-    float u[8], v[8], da[8], du[8], dv[8], a[8];
-    load_saved<VEC>(p.u8 + row * p.F + col, valid, p.u_scales[tile * p.T + row], u);
-    if (GATED) load_saved<VEC>(p.v8 + row * p.F + col, valid, p.v_scales[tile * p.T + row], v);
-    load8<T, VEC>(static_cast<const T *>(p.da) + row * p.ldda + col, valid, da);
+  Walk walk(p.T, p.F);
+  while (walk.in()) {
+    Place at[2] = {Place(walk, p.T, p.F), (walk.next(), Place(walk, p.T, p.F))};
+    walk.next();
+    Pack8<T> d[2];
+    uint2 bu[2], bv[2];
+    float su[2], sv[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float f, df;
-      activation<ACT, true>(u[j], f, df);
-      du[j] = GATED ? da[j] * v[j] * df : da[j] * df;
-      dv[j] = da[j] * f;
-      a[j] = GATED ? f * v[j] : f;
+    for (int i = 0; i < 2; ++i) {
+      const Place &a = at[i];
+      if (a.valid > 0) {
+        bu[i] = load_bytes<VEC>(p.u8 + a.row * p.F + a.col, a.valid);
+        su[i] = p.u_scales[a.tile * p.T + a.row];
+        if (GATED) {
+          bv[i] = load_bytes<VEC>(p.v8 + a.row * p.F + a.col, a.valid);
+          sv[i] = p.v_scales[a.tile * p.T + a.row];
+        }
+        load<VEC>(d[i], static_cast<const T *>(p.da) + a.row * p.ldda + a.col, a.valid);
+      }
     }
-    store8<T, VEC>(static_cast<T *>(p.du) + row * p.lddu + col, valid, du);
-    if (GATED) store8<T, VEC>(static_cast<T *>(p.dv) + row * p.lddv + col, valid, dv);
-    if (p.a != nullptr) store8<T, VEC>(static_cast<T *>(p.a) + row * p.lda + col, valid, a);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const Place &a = at[i];
+      if (a.valid == 0) continue;
+      float u[8], v[8], du[8], dv[8], out[8];
+      saved(bu[i], su[i], u);
+      if (GATED) saved(bv[i], sv[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float f, df;
+        const float da = d[i].at(j);
+        activation<ACT, true>(u[j], f, df);
+        du[j] = GATED ? da * v[j] * df : da * df;
+        dv[j] = da * f;
+        out[j] = GATED ? f * v[j] : f;
+      }
+      store<VEC>(static_cast<T *>(p.du) + a.row * p.lddu + a.col, a.valid, du);
+      if (GATED) store<VEC>(static_cast<T *>(p.dv) + a.row * p.lddv + a.col, a.valid, dv);
+      if (p.a != nullptr) store<VEC>(static_cast<T *>(p.a) + a.row * p.lda + a.col, a.valid, out);
+    }
   }
 }
 

@@ -1,0 +1,120 @@
+// Eight consecutive elements of a row in their storage type, as the casting
+// kernels of the 4-bit and activation-checkpoint operators hold them: bf16
+// stays packed two to a register.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fp8q {
+namespace pack8 {
+
+template <typename T>
+struct Pack8;
+
+template <>
+struct Pack8<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load_vec(const __nv_bfloat16 *p) {
+    const uint4 t = *reinterpret_cast<const uint4 *>(p);
+    w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+  }
+  __device__ __forceinline__ void load_some(const __nv_bfloat16 *p, int valid) {
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = (2 * k < valid ? (uint32_t)q[2 * k] : 0u) |
+             (2 * k + 1 < valid ? (uint32_t)q[2 * k + 1] << 16 : 0u);
+  }
+  __device__ __forceinline__ float2 pair(int k) const {
+    return make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ float at(int j) const {
+    return __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
+  }
+  __device__ __forceinline__ void negate() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] ^= 0x80008000u;
+  }
+  // max |element| as an fp32 bit pattern (NaN sorts above infinity)
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    const uint32_t k = 0x7FFF7FFFu;
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & k, w[1] & k), __vmaxu2(w[2] & k, w[3] & k));
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+};
+
+template <>
+struct Pack8<float> {
+  float v[8];
+  __device__ __forceinline__ void load_vec(const float *p) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    const float4 b = *(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void load_some(const float *p, int valid) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < valid ? p[j] : 0.0f;
+  }
+  __device__ __forceinline__ float2 pair(int k) const { return make_float2(v[2 * k], v[2 * k + 1]); }
+  __device__ __forceinline__ float at(int j) const { return v[j]; }
+  __device__ __forceinline__ void negate() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = -v[j];
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    return m;
+  }
+};
+
+// Elements [0, valid) of a row from p, zeros after; VEC: p is 16-byte aligned.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load(Pack8<T> &x, const T *p, int valid) {
+  if (VEC && valid >= 8)
+    x.load_vec(p);
+  else
+    x.load_some(p, valid);
+}
+
+// Two values to two elements of T.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store(T *p, int valid, const float (&v)[8]) {
+  if (VEC && valid >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]),
+                                                 bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+    } else {
+      *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      *(reinterpret_cast<float4 *>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < valid) p[j] = (T)v[j];
+}
+
+// RN(x / d) for a pair, by Markstein's correction of x r with r = RN(1 / d)
+// (P. Markstein, IBM J. Res. Dev. 34(1), 1990), written with the negated
+// reciprocal so that a zero quotient keeps x's sign: q0 = x r, e = q0 d - x,
+// q = q0 - e r.  Exact unless the remainder underflows, where the narrow
+// formats' codes are zeros either way.
+__device__ __forceinline__ float2 divide2(float2 x, float d, float r) {
+  const float2 q0 = __fmul2_rn(x, make_float2(r, r));
+  const float2 e = __ffma2_rn(q0, make_float2(d, d), make_float2(-x.x, -x.y));
+  return __ffma2_rn(e, make_float2(-r, -r), q0);
+}
+
+}  // namespace pack8
+}  // namespace fp8q
