@@ -54,16 +54,16 @@ __device__ __forceinline__ float nv_global(float amax) {
   return g < 1e-12f ? 1e-12f : g;
 }
 
-// NVFP4's 127 block scales of one tensor: d = fl32(s g) and RN(1 / d) by
+// NVFP4's 126 block scales of one tensor: d = fl32(s g) and RN(1 / d) by
 // scale byte, so that no block needs a division of its own.
 struct ScaleTable {
   float2 d_r[128];
   __device__ __forceinline__ void fill(float g) {   // by 128 threads or more, then a barrier
     if (threadIdx.x < 128) {
-      const __half_raw h =
-          __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)min(threadIdx.x, 126u), __NV_E4M3);
+      const __half_raw h = __nv_cvt_fp8_to_halfraw(
+          (__nv_fp8_storage_t)min(max(threadIdx.x, 1u), 126u), __NV_E4M3);
       const float d = __fmul_rn(__half2float(__half(h)), g);
-      d_r[threadIdx.x] = make_float2(d, threadIdx.x == 0 ? 0.0f : __frcp_rn(d));
+      d_r[threadIdx.x] = make_float2(d, __frcp_rn(d));
     }
   }
 };
@@ -79,66 +79,71 @@ __device__ __forceinline__ float nv_ratio(float amax, float g, float rg) {
   return t0 > 512.0f ? t0 : __fmaf_rn(__fmaf_rn(t0, -g, a), rg, t0);
 }
 
-// A block's scale byte and what dividing by the scale takes.
-struct BlockScale {
-  uint32_t byte;
-  float d;     // NVFP4: the divisor; unused for MXFP4
-  float r;     // MXFP4: 1 / d, exact; NVFP4: RN(1 / d)
-  bool nan;    // the block stands for NaN
-  bool over;   // NVFP4: the scale saturated, so quotients may pass 6 by any factor
-};
-
-template <int KIND>
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g, float rg,
-                                                  const ScaleTable *table) {
-  BlockScale b;
-  b.nan = amax_bits >= 0x7F800000u;
-  if (KIND == FP4Q_MXFP4) {
-    // the biased exponent of amax is floor(log2 amax) + 127; zero, subnormal
-    // and tiny maxima clamp to 2^-127, whose reciprocal is a normal number
-    const uint32_t code = (uint32_t)max((int)(amax_bits >> 23) - 2, 0);
-    b.byte = b.nan ? 0xFFu : code;
-    b.d = 0.0f;
-    b.r = __uint_as_float((254u - code) << 23);
-    b.over = false;
-  } else {
-    const float t = nv_ratio(__uint_as_float(amax_bits), g, rg);
-    uint32_t s = (uint32_t)__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3) & 0x7Fu;
-    s = min(max(s, 1u), 126u);                   // at least 2^-9
-    b.nan = b.nan || !(g < __uint_as_float(0x7F800000u));
-    b.byte = b.nan ? 0x7Fu : s;
-    const float2 dr = table->d_r[s];
-    b.d = dr.x;
-    b.r = dr.y;
-    b.over = t > 448.0f;
-  }
-  return b;
-}
+// Block maxima from here on take the careful path: NaN and infinity, and
+// magnitudes so large that x / d may overflow where a calibrated amax is far
+// too small (d >= 448e-12 > 2^-32 wherever the quotient is past 6).
+constexpr uint32_t kCarefulBits = 0x6F800000u;   // 2^96
 
 // Codes of two elements of a block, given negated (the first in the low four
-// bits).  NVFP4: RN(x / d) by Markstein's correction, signs arranged so that a
-// zero quotient keeps x's sign: q0 = x r, e = q0 d - x, q = q0 - e r.
+// bits); r = RN(1 / d).  MXFP4: d is a power of two and the product exact.
+// NVFP4: RN(x / d) by Markstein's correction, signs arranged so that a zero
+// quotient keeps x's sign: q0 = x r, e = q0 d - x, q = q0 - e r.
 template <int KIND>
-__device__ __forceinline__ uint32_t encode2(float2 y, const BlockScale &b) {
-  const float2 nr = make_float2(-b.r, -b.r);
-  if (KIND == FP4Q_NVFP4 && b.over) {   // keep the correction finite: past 6 d the code is 6's
-    const float lim = 6.5f * b.d;
-    y.x = fminf(fmaxf(y.x, -lim), lim);
-    y.y = fminf(fmaxf(y.y, -lim), lim);
-  }
+__device__ __forceinline__ uint32_t encode2(float2 y, float d, float r) {
+  const float2 nr = make_float2(-r, -r);
   float2 q = __fmul2_rn(y, nr);
-  if (KIND == FP4Q_NVFP4) q = __ffma2_rn(__ffma2_rn(q, make_float2(b.d, b.d), y), nr, q);
+  if (KIND == FP4Q_NVFP4) q = __ffma2_rn(__ffma2_rn(q, make_float2(d, d), y), nr, q);
   return e2m1x2(q.x, q.y);
 }
 
 // Codes of eight elements given as negated pairs, element j in bits
 // [4j, 4j + 4).
 template <int KIND>
-__device__ __forceinline__ uint32_t encode8(float2 y0, float2 y1, float2 y2, float2 y3,
-                                            const BlockScale &b) {
-  const uint32_t lo = __byte_perm(encode2<KIND>(y0, b), encode2<KIND>(y1, b), 0x0040);
-  const uint32_t hi = __byte_perm(encode2<KIND>(y2, b), encode2<KIND>(y3, b), 0x0040);
-  return b.nan ? 0u : __byte_perm(lo, hi, 0x5410);
+__device__ __forceinline__ uint32_t encode8(const float2 (&y)[4], float d, float r) {
+  const uint32_t lo = __byte_perm(encode2<KIND>(y[0], d, r), encode2<KIND>(y[1], d, r), 0x0040);
+  const uint32_t hi = __byte_perm(encode2<KIND>(y[2], d, r), encode2<KIND>(y[3], d, r), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// 1 / d of an MXFP4 block by scale byte: d = 2^(byte - 127) and the byte is
+// at most 252, so the reciprocal is a normal number.
+__device__ __forceinline__ float mx_reciprocal(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+
+// Scale byte of a block with a finite maximum below 2^96.
+__device__ __forceinline__ uint32_t mx_byte(uint32_t amax_bits) {
+  // the biased exponent of amax is floor(log2 amax) + 127; zero, subnormal
+  // and tiny maxima clamp to 2^-127
+  return (uint32_t)max((int)(amax_bits >> 23) - 2, 0);
+}
+
+// The careful path: scale byte and codes of eight elements for any maximum
+// and any tensor scale.
+template <int KIND>
+__device__ __noinline__ uint32_t encode8_careful(float2 y0, float2 y1, float2 y2, float2 y3,
+                                                 uint32_t amax_bits, float g, uint32_t *byte) {
+  bool nan = amax_bits >= 0x7F800000u;
+  float2 y[4] = {y0, y1, y2, y3};
+  float d = 0.0f, r;
+  if (KIND == FP4Q_MXFP4) {
+    *byte = nan ? 0xFFu : mx_byte(amax_bits);
+    r = nan ? 0.0f : mx_reciprocal(*byte);
+  } else {
+    nan = nan || !(g < __uint_as_float(0x7F800000u));
+    const float t = __fdiv_rn(__fdiv_rn(__uint_as_float(amax_bits), 6.0f), g);
+    const uint32_t s =
+        (uint32_t)__nv_cvt_float_to_fp8(fmaxf(t, 0x1p-9f), __NV_SATFINITE, __NV_E4M3);
+    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s, __NV_E4M3);
+    *byte = nan ? 0x7Fu : s;
+    d = __fmul_rn(__half2float(__half(h)), g);
+    r = __frcp_rn(d);
+    const float lim = 6.5f * d;   // past 6 d the code is 6's
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      y[k] = make_float2(fminf(fmaxf(y[k].x, -lim), lim), fminf(fmaxf(y[k].y, -lim), lim));
+  }
+  return nan ? 0u : encode8<KIND>(y, d, r);
 }
 
 // Values of the two codes in a byte, the low one first: exact in fp32.

@@ -90,6 +90,40 @@ __device__ __forceinline__ int t_word(int c, int w) {
   return (c + (c >> 5)) * 16 + ((((w >> 2) ^ (c >> 3)) & 3) << 2 | (w & 3));
 }
 
+// Scale bytes of eight blocks of one thread, rows (or columns) 0-3 in the low
+// word.  MXFP4: from the exponents.  NVFP4: the two lanes that share the
+// blocks (`mate` apart; `second` is the one with the bit set) find four each
+// and swap them.
+template <int KIND>
+__device__ __forceinline__ void scale_bytes(const uint32_t (&m)[8], float g, float rg, int mate,
+                                            bool second, uint32_t (&byte)[2]) {
+  if (KIND == FP4Q_MXFP4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      byte[h] = __byte_perm(__byte_perm(mx_byte(m[4 * h]), mx_byte(m[4 * h + 1]), 0x0040),
+                            __byte_perm(mx_byte(m[4 * h + 2]), mx_byte(m[4 * h + 3]), 0x0040), 0x5410);
+  } else {
+    float t[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      t[k] = fmaxf(nv_ratio(__uint_as_float(second ? m[k + 4] : m[k]), g, rg), 0x1p-9f);
+    const uint32_t mine =
+        (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(t[0], t[1]), __NV_SATFINITE, __NV_E4M3) |
+        (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(t[2], t[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, mine, mate);
+    byte[0] = second ? other : mine;
+    byte[1] = second ? mine : other;
+  }
+}
+
+template <int KIND>
+__device__ __forceinline__ uint32_t encode_block(const float2 (&y)[4], uint32_t byte,
+                                                 const ScaleTable &table) {
+  if (KIND == FP4Q_MXFP4) return encode8<KIND>(y, 0.0f, mx_reciprocal(byte));
+  const float2 dr = table.d_r[byte];
+  return encode8<KIND>(y, dr.x, dr.y);
+}
+
 template <int KIND, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs p) {
   constexpr int kBlock = Kind<KIND>::kBlock;
@@ -129,31 +163,62 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs p) {
   if (p.q != nullptr) {
     const int64_t ldq = row_bytes(p.cols);
     uint8_t *q = p.q + row * ldq + col / 2;
-    const bool in = col / 2 < ldq;
-    uint32_t m[8];
+    if (col / 2 >= ldq) q = nullptr;
+    uint8_t *scale = s_scale + atom_byte(tr, tc / kBlock, kAtoms);
+    const bool first = (lane & (kLanes - 1)) == 0;
+    uint32_t m[8], top = 0;
     block_max_rows<kLanes>(y, m);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const BlockScale b = block_scale<KIND>(m[i], g, rg, &table);
-      const uint32_t w = encode8<KIND>(y[i].pair(0), y[i].pair(1), y[i].pair(2), y[i].pair(3), b);
-      if (i < rows_in && in) *reinterpret_cast<uint32_t *>(q + i * ldq) = w;
-      if ((lane & (kLanes - 1)) == 0)
-        s_scale[atom_byte(tr + i, tc / kBlock, kAtoms)] =
-            (uint8_t)(i < rows_in && cols_in > 0 ? b.byte : 0u);
+    for (int i = 0; i < 8; ++i) top = max(top, m[i]);
+    if (!__any_sync(0xFFFFFFFFu, top >= kCarefulBits || !(g < __uint_as_float(0x7F800000u)))) {
+      uint32_t byte[2];
+      scale_bytes<KIND>(m, g, rg, 1, lane & 1, byte);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = (byte[i >> 2] >> (8 * (i & 3))) & 0xFFu;
+        const float2 v[4] = {y[i].pair(0), y[i].pair(1), y[i].pair(2), y[i].pair(3)};
+        const uint32_t w = encode_block<KIND>(v, b, table);
+        if (i < rows_in && q != nullptr) *reinterpret_cast<uint32_t *>(q + i * ldq) = w;
+        if (first) scale[16 * i] = (uint8_t)(i < rows_in && cols_in > 0 ? b : 0u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t b;
+        const uint32_t w = encode8_careful<KIND>(y[i].pair(0), y[i].pair(1), y[i].pair(2),
+                                                 y[i].pair(3), m[i], g, &b);
+        if (i < rows_in && q != nullptr) *reinterpret_cast<uint32_t *>(q + i * ldq) = w;
+        if (first) scale[16 * i] = (uint8_t)(i < rows_in && cols_in > 0 ? b : 0u);
+      }
     }
   }
   if (p.qt != nullptr) {
-    uint32_t m[8];
+    uint8_t *scale = t_scale + atom_byte(tc, tr / kBlock, kAtoms);
+    const bool first = ((lane >> 3) & (kLanes - 1)) == 0;
+    uint32_t m[8], top = 0;
     block_max_cols<kLanes>(y, m);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const BlockScale b = block_scale<KIND>(m[j], g, rg, &table);
-      t_code[t_word(tc + j, tr / 8)] =
-          encode8<KIND>(make_float2(y[0].at(j), y[1].at(j)), make_float2(y[2].at(j), y[3].at(j)),
-                        make_float2(y[4].at(j), y[5].at(j)), make_float2(y[6].at(j), y[7].at(j)), b);
-      if (((lane >> 3) & (kLanes - 1)) == 0)
-        t_scale[atom_byte(tc + j, tr / kBlock, kAtoms)] =
-            (uint8_t)(rows_in > 0 && j < cols_in ? b.byte : 0u);
+    for (int j = 0; j < 8; ++j) top = max(top, m[j]);
+    if (!__any_sync(0xFFFFFFFFu, top >= kCarefulBits || !(g < __uint_as_float(0x7F800000u)))) {
+      uint32_t byte[2];
+      scale_bytes<KIND>(m, g, rg, 8, lane & 8, byte);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = (byte[j >> 2] >> (8 * (j & 3))) & 0xFFu;
+        const float2 v[4] = {make_float2(y[0].at(j), y[1].at(j)), make_float2(y[2].at(j), y[3].at(j)),
+                             make_float2(y[4].at(j), y[5].at(j)), make_float2(y[6].at(j), y[7].at(j))};
+        t_code[t_word(tc + j, tr / 8)] = encode_block<KIND>(v, b, table);
+        if (first) scale[16 * j] = (uint8_t)(rows_in > 0 && j < cols_in ? b : 0u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t b;
+        t_code[t_word(tc + j, tr / 8)] = encode8_careful<KIND>(
+            make_float2(y[0].at(j), y[1].at(j)), make_float2(y[2].at(j), y[3].at(j)),
+            make_float2(y[4].at(j), y[5].at(j)), make_float2(y[6].at(j), y[7].at(j)), m[j], g, &b);
+        if (first) scale[16 * j] = (uint8_t)(rows_in > 0 && j < cols_in ? b : 0u);
+      }
     }
   }
   __syncthreads();

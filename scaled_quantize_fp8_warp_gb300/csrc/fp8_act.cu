@@ -4,8 +4,8 @@
 // 1e-12), RNE of the correctly rounded quotient x / s, reached by one
 // reciprocal per tile and Markstein's correction).
 //
-// One warp owns 2 rows x 128 columns at a time: 16 lanes of 8 columns each a
-// tile, whose maximum is a 4-step butterfly.
+// A warp works on pieces of 2 rows x 128 columns, 16 lanes of 8 columns to a
+// tile, two pieces at a time.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
@@ -21,7 +21,6 @@ namespace act {
 namespace {
 
 using pack8::Pack8;
-using pack8::divide2;
 using pack8::load;
 using pack8::store;
 
@@ -74,24 +73,30 @@ __device__ __forceinline__ uint32_t cast1_slow(float x, float s) {
   return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
-// The eight E4M3 bytes of this lane's part of a tile whose max |x| is m, and
-// the tile's scale.
+// A tile's scale from its max |x|.
+__device__ __forceinline__ float tile_scale(uint32_t amax_bits) {
+  const float s = __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
+  return s < 1e-12f ? 1e-12f : s;
+}
+
+// E4M3 bytes of eight elements, given negated, under scale s with r = RN(1/s).
+// r is 0 where s is not finite.
 template <typename T>
-__device__ __forceinline__ uint2 cast_tile(const Pack8<T> &x, uint32_t m, float &scale) {
-  const float q = __fdiv_rn(__uint_as_float(m), 448.0f);
-  const float s = q < 1e-12f ? 1e-12f : q;
-  scale = s;
+__device__ __forceinline__ uint2 cast8(const Pack8<T> &y, float s, float r) {
   uint32_t b[8];
-  if (m < 0x7F800000u) {
-    const float r = __frcp_rn(s);
+  if (r != 0.0f) {
+    const float2 nr = make_float2(-r, -r), s2 = make_float2(s, s);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      b[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(divide2(x.pair(k), s, r), __NV_SATFINITE,
-                                                __NV_E4M3);
+    for (int k = 0; k < 4; ++k) {
+      // RN(x / s) by Markstein's correction, a zero keeping x's sign
+      const float2 v = y.pair(k), q = __fmul2_rn(v, nr);
+      b[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(__ffma2_rn(__ffma2_rn(q, s2, v), nr, q),
+                                                __NV_SATFINITE, __NV_E4M3);
+    }
     return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = cast1_slow(x.at(j), s);
+  for (int j = 0; j < 8; ++j) b[j] = cast1_slow(-y.at(j), s);
   return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
                     b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
 }
@@ -129,139 +134,198 @@ __device__ __forceinline__ void saved(uint2 w, float s, float (&v)[8]) {
   }
 }
 
-// The pieces (2 rows x 128 columns) of a [T, F] matrix that one warp visits:
-// numbered row pair after row pair, `step` apart, kept as (pair, tile)
-// without a division per piece.
+// One warp keeps to one tile column and walks down the rows, two row pairs at
+// a time (`step` pairs apart, so that four rows' loads are in flight), with
+// pointers that advance by constants.  Lanes 0-15 have a pair's first row.
 struct Walk {
-  int64_t pair, pairs;
-  int tile, tiles;
-  int64_t step_pair;
-  int step_tile;
+  int64_t tile, tile_step, tiles;   // tile columns this warp serves
+  int64_t pair0, pairs, step;
   __device__ __forceinline__ Walk(int64_t T, int64_t F) {
-    const int64_t first = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-    tiles = (int)((F + 127) / 128);
+    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t all = (int64_t)gridDim.x * (kThreads / 32);
+    tiles = (F + 127) / 128;
     pairs = (T + 1) / 2;
-    pair = first / tiles;
-    tile = (int)(first - pair * tiles);
-    step_pair = step / tiles;
-    step_tile = (int)(step - step_pair * tiles);
-  }
-  __device__ __forceinline__ bool in() const { return pair < pairs; }
-  __device__ __forceinline__ void next() {
-    pair += step_pair;
-    tile += step_tile;
-    if (tile >= tiles) {
-      tile -= tiles;
-      ++pair;
-    }
+    step = max(all / tiles, (int64_t)1);              // warps per tile column
+    tile_step = all < tiles ? all : tiles;
+    pair0 = w / tiles;
+    tile = pair0 < step ? w - pair0 * tiles : tiles;  // the warps left over have none
   }
 };
 
-// This lane's 8 elements of a piece: row, first column, how many exist.
-struct Place {
-  int64_t row;
-  int64_t col;
-  int tile, valid;
-  __device__ __forceinline__ Place(const Walk &w, int64_t T, int64_t F) {
-    const int lane = threadIdx.x & 31;
-    row = 2 * w.pair + (lane >> 4);
-    tile = w.tile;
-    col = (int64_t)tile * 128 + (lane & 15) * 8;
-    valid = w.in() && row < T ? (int)max((int64_t)0, min((int64_t)8, F - col)) : 0;
-  }
+// Scales and reciprocals of the four tiles (two pieces of u, v) of a half warp
+// from the lanes' maxima: the halving steps leave piece 0's maxima in even
+// lanes and piece 1's in odd ones, each lane finds one tile's scale (lane bit
+// 1: u or v), and the results are handed round.
+struct Scales {
+  float s[2][2], r[2][2];   // [piece][u, v]
 };
+
+__device__ __forceinline__ void finish_scales(uint32_t mine, Scales &out) {
+  const int lane = threadIdx.x & 31;
+  const float s = tile_scale(mine);
+  const float r = mine < 0x7F800000u ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int from = (lane & 16) + i + 2 * k;
+      out.s[i][k] = __shfl_sync(0xFFFFFFFFu, s, from);
+      out.r[i][k] = __shfl_sync(0xFFFFFFFFu, r, from);
+    }
+}
+
+template <bool GATED>
+__device__ __forceinline__ void find_scales(const Pack8<__nv_bfloat16> (&u)[2],
+                                            const Pack8<__nv_bfloat16> (&v)[2], Scales &out) {
+  const int lane = threadIdx.x & 31;
+  // magnitudes of u in the low and of v in the high half
+  uint32_t m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    m[i] = __byte_perm(u[i].amax_bits(), GATED ? v[i].amax_bits() : 0u, 0x7632);
+  const bool odd = lane & 1;
+  uint32_t t = __vmaxu2(odd ? m[1] : m[0], __shfl_xor_sync(0xFFFFFFFFu, odd ? m[0] : m[1], 1));
+#pragma unroll
+  for (int o = 2; o < 16; o <<= 1) t = __vmaxu2(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+  finish_scales((lane & 2) ? t & 0xFFFF0000u : t << 16, out);
+}
+
+template <bool GATED>
+__device__ __forceinline__ void find_scales(const Pack8<float> (&u)[2], const Pack8<float> (&v)[2],
+                                            Scales &out) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1, two = lane & 2;
+  uint32_t m[2];   // u, v of this lane's piece
+#pragma unroll
+  for (int k = 0; k < (GATED ? 2 : 1); ++k) {
+    const uint32_t a = k ? v[0].amax_bits() : u[0].amax_bits();
+    const uint32_t b = k ? v[1].amax_bits() : u[1].amax_bits();
+    m[k] = max(odd ? b : a, __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1));
+  }
+  uint32_t t = m[0];
+  if (GATED) t = max(two ? m[1] : m[0], __shfl_xor_sync(0xFFFFFFFFu, two ? m[0] : m[1], 2));
+  else t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
+#pragma unroll
+  for (int o = 4; o < 16; o <<= 1) t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+  finish_scales(t, out);
+}
 
 template <int ACT, typename T, bool GATED, bool VEC>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const ForwardArgs p) {
+__global__ void __launch_bounds__(kThreads, 3) forward_kernel(const ForwardArgs p) {
   const int lane = threadIdx.x & 31;
-  Walk walk(p.T, p.F);
-  while (walk.in()) {
-    // two pieces at a time: their loads are in flight together
-    Place at[2] = {Place(walk, p.T, p.F), (walk.next(), Place(walk, p.T, p.F))};
-    walk.next();
-    Pack8<T> u[2], v[2];
+  const Walk walk(p.T, p.F);
+  for (int64_t tile = walk.tile; tile < walk.tiles; tile += walk.tile_step) {
+    const int64_t col = tile * 128 + (lane & 15) * 8;
+    const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.F - col));
+    int64_t row = 2 * walk.pair0 + (lane >> 4);
+    // nothing is addressed where nothing is valid
+    const int64_t c = cols_in > 0 ? col : 0;
+    const T *pu = static_cast<const T *>(p.u) + row * p.ldu + c;
+    const T *pv = static_cast<const T *>(p.v) + (GATED ? row * p.ldv + c : 0);
+    T *pa = static_cast<T *>(p.a) + row * p.lda + c;
+    int64_t at8 = row * p.F + c, at_s = tile * p.T + row;
+    const int64_t step = 2 * walk.step;
+    for (int64_t pair = walk.pair0; pair < walk.pairs; pair += 2 * walk.step) {
+      Pack8<T> u[2], v[2];
+      int valid[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      // nothing is addressed where nothing is valid
-      const int64_t on = at[i].valid > 0 ? 1 : 0;
-      load<VEC>(u[i], static_cast<const T *>(p.u) + on * (at[i].row * p.ldu + at[i].col), at[i].valid);
-      if (GATED)
-        load<VEC>(v[i], static_cast<const T *>(p.v) + on * (at[i].row * p.ldv + at[i].col), at[i].valid);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const Place &a = at[i];
-      uint32_t mu = u[i].amax_bits(), mv = GATED ? v[i].amax_bits() : 0u;
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) {
-        mu = max(mu, __shfl_xor_sync(0xFFFFFFFFu, mu, o));
-        if (GATED) mv = max(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, o));
+      for (int i = 0; i < 2; ++i) {
+        valid[i] = row + i * step < p.T ? cols_in : 0;
+        load<VEC>(u[i], pu + (valid[i] > 0 ? i * step * p.ldu : 0), valid[i]);
+        if (GATED) load<VEC>(v[i], pv + (valid[i] > 0 ? i * step * p.ldv : 0), valid[i]);
       }
-      float su, sv = 0.0f;
-      const uint2 bu = cast_tile(u[i], mu, su);
-      uint2 bv = make_uint2(0u, 0u);
-      if (GATED) bv = cast_tile(v[i], mv, sv);
-      if (a.valid > 0) {
-        store_bytes<VEC>(p.u8 + a.row * p.F + a.col, a.valid, bu);
-        if (GATED) store_bytes<VEC>(p.v8 + a.row * p.F + a.col, a.valid, bv);
-        if ((lane & 15) == 0) {
-          p.u_scales[a.tile * p.T + a.row] = su;
-          if (GATED) p.v_scales[a.tile * p.T + a.row] = sv;
-        }
-        float out[8], unused;
+      Scales sc;
+      find_scales<GATED>(u, v, sc);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          activation<ACT, false>(u[i].at(j), out[j], unused);
-          if (GATED) out[j] *= v[i].at(j);
+      for (int i = 0; i < 2; ++i) {
+        u[i].negate();
+        if (GATED) v[i].negate();
+        if (valid[i] > 0) {
+          store_bytes<VEC>(p.u8 + at8 + i * step * p.F, valid[i], cast8(u[i], sc.s[i][0], sc.r[i][0]));
+          if (GATED)
+            store_bytes<VEC>(p.v8 + at8 + i * step * p.F, valid[i], cast8(v[i], sc.s[i][1], sc.r[i][1]));
+          if ((lane & 15) == 0) {
+            p.u_scales[at_s + i * step] = sc.s[i][0];
+            if (GATED) p.v_scales[at_s + i * step] = sc.s[i][1];
+          }
+          float out[8], unused;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            activation<ACT, false>(-u[i].at(j), out[j], unused);
+            out[j] = GATED ? -out[j] * v[i].at(j) : out[j];
+          }
+          store<VEC>(pa + i * step * p.lda, valid[i], out);
         }
-        store<VEC>(static_cast<T *>(p.a) + a.row * p.lda + a.col, a.valid, out);
       }
+      row += 2 * step;
+      pu += 2 * step * p.ldu;
+      pv += 2 * step * p.ldv;
+      pa += 2 * step * p.lda;
+      at8 += 2 * step * p.F;
+      at_s += 2 * step;
     }
   }
 }
 
 template <int ACT, typename T, bool GATED, bool VEC>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const BackwardArgs p) {
-  Walk walk(p.T, p.F);
-  while (walk.in()) {
-    Place at[2] = {Place(walk, p.T, p.F), (walk.next(), Place(walk, p.T, p.F))};
-    walk.next();
-    Pack8<T> d[2];
-    uint2 bu[2], bv[2];
-    float su[2], sv[2];
+__global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardArgs p) {
+  const int lane = threadIdx.x & 31;
+  const Walk walk(p.T, p.F);
+  for (int64_t tile = walk.tile; tile < walk.tiles; tile += walk.tile_step) {
+    const int64_t col = tile * 128 + (lane & 15) * 8;
+    const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.F - col));
+    int64_t row = 2 * walk.pair0 + (lane >> 4);
+    const int64_t c = cols_in > 0 ? col : 0;
+    const T *pd = static_cast<const T *>(p.da) + row * p.ldda + c;
+    T *pu = static_cast<T *>(p.du) + row * p.lddu + c;
+    T *pv = static_cast<T *>(p.dv) + (GATED ? row * p.lddv + c : 0);
+    T *pa = static_cast<T *>(p.a) + row * p.lda + c;
+    int64_t at8 = row * p.F + c, at_s = tile * p.T + row;
+    const int64_t step = 2 * walk.step;
+    for (int64_t pair = walk.pair0; pair < walk.pairs; pair += 2 * walk.step) {
+      Pack8<T> d[2];
+      uint2 bu[2], bv[2];
+      float su[2], sv[2];
+      int valid[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const Place &a = at[i];
-      if (a.valid > 0) {
-        bu[i] = load_bytes<VEC>(p.u8 + a.row * p.F + a.col, a.valid);
-        su[i] = p.u_scales[a.tile * p.T + a.row];
-        if (GATED) {
-          bv[i] = load_bytes<VEC>(p.v8 + a.row * p.F + a.col, a.valid);
-          sv[i] = p.v_scales[a.tile * p.T + a.row];
+      for (int i = 0; i < 2; ++i) {
+        valid[i] = row + i * step < p.T ? cols_in : 0;
+        if (valid[i] > 0) {
+          bu[i] = load_bytes<VEC>(p.u8 + at8 + i * step * p.F, valid[i]);
+          su[i] = p.u_scales[at_s + i * step];
+          if (GATED) {
+            bv[i] = load_bytes<VEC>(p.v8 + at8 + i * step * p.F, valid[i]);
+            sv[i] = p.v_scales[at_s + i * step];
+          }
+          load<VEC>(d[i], pd + i * step * p.ldda, valid[i]);
         }
-        load<VEC>(d[i], static_cast<const T *>(p.da) + a.row * p.ldda + a.col, a.valid);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const Place &a = at[i];
-      if (a.valid == 0) continue;
-      float u[8], v[8], du[8], dv[8], out[8];
-      saved(bu[i], su[i], u);
-      if (GATED) saved(bv[i], sv[i], v);
+      for (int i = 0; i < 2; ++i) {
+        if (valid[i] == 0) continue;
+        float u[8], v[8], du[8], dv[8], out[8];
+        saved(bu[i], su[i], u);
+        if (GATED) saved(bv[i], sv[i], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float f, df;
-        const float da = d[i].at(j);
-        activation<ACT, true>(u[j], f, df);
-        du[j] = GATED ? da * v[j] * df : da * df;
-        dv[j] = da * f;
-        out[j] = GATED ? f * v[j] : f;
+        for (int j = 0; j < 8; ++j) {
+          float f, df;
+          const float da = d[i].at(j);
+          activation<ACT, true>(u[j], f, df);
+          du[j] = GATED ? da * v[j] * df : da * df;
+          dv[j] = da * f;
+          out[j] = GATED ? f * v[j] : f;
+        }
+        store<VEC>(pu + i * step * p.lddu, valid[i], du);
+        if (GATED) store<VEC>(pv + i * step * p.lddv, valid[i], dv);
+        if (p.a != nullptr) store<VEC>(pa + i * step * p.lda, valid[i], out);
       }
-      store<VEC>(static_cast<T *>(p.du) + a.row * p.lddu + a.col, a.valid, du);
-      if (GATED) store<VEC>(static_cast<T *>(p.dv) + a.row * p.lddv + a.col, a.valid, dv);
-      if (p.a != nullptr) store<VEC>(static_cast<T *>(p.a) + a.row * p.lda + a.col, a.valid, out);
+      row += 2 * step;
+      pd += 2 * step * p.ldda;
+      pu += 2 * step * p.lddu;
+      pv += 2 * step * p.lddv;
+      pa += 2 * step * p.lda;
+      at8 += 2 * step * p.F;
+      at_s += 2 * step;
     }
   }
 }

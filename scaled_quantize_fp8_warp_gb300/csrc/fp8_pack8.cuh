@@ -105,16 +105,5 @@ __device__ __forceinline__ void store(T *p, int valid, const float (&v)[8]) {
     if (j < valid) p[j] = (T)v[j];
 }
 
-// RN(x / d) for a pair, by Markstein's correction of x r with r = RN(1 / d)
-// (P. Markstein, IBM J. Res. Dev. 34(1), 1990), written with the negated
-// reciprocal so that a zero quotient keeps x's sign: q0 = x r, e = q0 d - x,
-// q = q0 - e r.  Exact unless the remainder underflows, where the narrow
-// formats' codes are zeros either way.
-__device__ __forceinline__ float2 divide2(float2 x, float d, float r) {
-  const float2 q0 = __fmul2_rn(x, make_float2(r, r));
-  const float2 e = __ffma2_rn(q0, make_float2(d, d), make_float2(-x.x, -x.y));
-  return __ffma2_rn(e, make_float2(-r, -r), q0);
-}
-
 }  // namespace pack8
 }  // namespace fp8q
