@@ -60,9 +60,10 @@ template <int LANES>
 __device__ __forceinline__ void block_max_cols(const Pack8<__nv_bfloat16> (&x)[8], uint32_t (&m)[8]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint32_t t = 0;
+    uint32_t t = x[0].w[k];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t = __vmaxu2(t, x[i].w[k] & 0x7FFF7FFFu);
+    for (int i = 1; i < 8; ++i) t = pack8::max_abs2(t, x[i].w[k]);
+    t &= 0x7FFF7FFFu;
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) t = __vmaxu2(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8 * o));
     m[2 * k] = t << 16;
@@ -146,8 +147,14 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs p) {
   const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.cols - col));
   {
     const T *x = static_cast<const T *>(p.x) + (rows_in > 0 && cols_in > 0 ? row * p.ld + col : 0);
+    if (VEC && rows_in == 8 && cols_in == 8) {   // all loads in a row, no test between them
 #pragma unroll
-    for (int i = 0; i < 8; ++i) load<VEC>(y[i], i < rows_in ? x + i * p.ld : x, i < rows_in ? cols_in : 0);
+      for (int i = 0; i < 8; ++i) y[i].load_vec(x + i * p.ld);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        load<VEC>(y[i], i < rows_in ? x + i * p.ld : x, i < rows_in ? cols_in : 0);
+    }
   }
   float g = 1.0f, rg = 1.0f;
   if (KIND == FP4Q_NVFP4) {
@@ -278,38 +285,56 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Values of an operand: one thread per 8 codes (one 32-bit word) of four rows
+// Values of an operand: one thread per 8 codes (one 32-bit word) of kRows rows
 // at a time, whose reads are in flight together.  VEC: every row of y starts on
-// a 16-byte boundary.
+// a 16-byte boundary and K is a multiple of 16.  For fp32 two neighbouring
+// lanes (16 codes, one scale) share their words out so that together they
+// store whole 32-byte sectors.
 template <int KIND, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const fp4q_operand op, int64_t rows, int64_t K, T *y) {
   constexpr int kRows = 4;
+  constexpr bool kShare = VEC && sizeof(T) == 4;
   const int64_t ldq = row_bytes(K), nk = num_atoms_k(KIND, K);
   const int64_t w = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int valid = (int)min((int64_t)8, K - w * 8);
-  if (valid <= 0) return;
+  const int valid = (int)max((int64_t)0, min((int64_t)8, K - w * 8));
+  const bool odd = threadIdx.x & 1;
   const float g = KIND == FP4Q_NVFP4 ? *op.global_scale : 1.0f;
   for (int64_t r0 = (int64_t)blockIdx.y * kRows; r0 < rows; r0 += (int64_t)gridDim.y * kRows) {
     uint32_t code[kRows], byte[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int64_t r = min(r0 + i, rows - 1);
-      code[i] = *reinterpret_cast<const uint32_t *>(op.data + r * ldq + w * 4);
-      byte[i] = op.scales[atom_byte(r, w * 8 / Kind<KIND>::kBlock, nk)];
+      code[i] = byte[i] = 0u;
+      if (valid > 0) {
+        code[i] = *reinterpret_cast<const uint32_t *>(op.data + r * ldq + w * 4);
+        byte[i] = op.scales[atom_byte(r, w * 8 / Kind<KIND>::kBlock, nk)];
+      }
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if (r0 + i >= rows) break;
       const float s = scale_value<KIND>(byte[i], g);
+      uint32_t c = code[i];
+      if (kShare) {   // even lanes: both low halves, odd lanes: both high ones
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, c, 1);
+        c = odd ? __byte_perm(other, c, 0x7632) : __byte_perm(c, other, 0x5410);
+      }
       float v[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 f = e2m1x2_values(code[i] >> (8 * j));
+        const float2 f = e2m1x2_values(c >> (8 * j));
         v[2 * j] = __fmul_rn(f.x, s);
         v[2 * j + 1] = __fmul_rn(f.y, s);
       }
-      pack8::store<VEC>(y + (r0 + i) * K + w * 8, valid, v);
+      if (r0 + i >= rows || valid == 0) continue;
+      T *out = y + (r0 + i) * K + w * 8;
+      if constexpr (kShare) {
+        out += odd ? -4 : 0;
+        *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(out + 8) = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        pack8::store<VEC>(out, valid, v);
+      }
     }
   }
 }
@@ -319,7 +344,8 @@ cudaError_t run_quantize(const QuantArgs &a, cudaStream_t stream) {
   const int64_t tiles = ((a.cols + kTile - 1) / kTile) * ((a.rows + kTile - 1) / kTile);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)tiles;
-  const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ld * (int64_t)sizeof(T) % 16 == 0;
+  const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 &&
+                   a.ld * (int64_t)sizeof(T) % 16 == 0 && a.cols % 8 == 0;
   if (vec)
     quantize_kernel<KIND, T, true><<<grid, kThreads, 0, stream>>>(a);
   else
@@ -365,7 +391,7 @@ static cudaError_t run_dequantize(const fp4q_operand &op, int64_t rows, int64_t 
   const int64_t gx = (K + 8 * kThreads - 1) / (8 * kThreads);
   if (gx > INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>((rows + 3) / 4, 65535));
-  if (K * (int64_t)sizeof(T) % 16 == 0)
+  if (K % 16 == 0)
     dequantize_kernel<KIND, T, true><<<grid, kThreads, 0, stream>>>(op, rows, K, static_cast<T *>(y));
   else
     dequantize_kernel<KIND, T, false><<<grid, kThreads, 0, stream>>>(op, rows, K, static_cast<T *>(y));

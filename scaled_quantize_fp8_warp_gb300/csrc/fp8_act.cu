@@ -21,7 +21,6 @@ namespace act {
 namespace {
 
 using pack8::Pack8;
-using pack8::load;
 using pack8::store;
 
 constexpr int kThreads = 256;
@@ -63,48 +62,51 @@ __device__ __forceinline__ void activation(float u, float &f, float &df) {
   }
 }
 
-// One element where the tile is not finite: a NaN keeps its sign, a NaN that
-// the division makes is 0x7F (s is infinite or NaN, so nothing else than
-// zeros and NaN comes out).
-__device__ __forceinline__ uint32_t cast1_slow(float x, float s) {
-  if (x != x) return 0x7Fu | ((__float_as_uint(x) >> 24) & 0x80u);
-  const float q = __fdiv_rn(x, s);
-  if (q != q) return 0x7Fu;
-  return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
-}
-
 // A tile's scale from its max |x|.
 __device__ __forceinline__ float tile_scale(uint32_t amax_bits) {
   const float s = __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
   return s < 1e-12f ? 1e-12f : s;
 }
 
-// E4M3 bytes of eight elements, given negated, under scale s with r = RN(1/s).
-// r is 0 where s is not finite.
+// E4M3 bytes of eight elements, given negated, under a finite scale s with
+// r = RN(1 / s): RN(x / s) by Markstein's correction, a zero keeping x's sign.
 template <typename T>
 __device__ __forceinline__ uint2 cast8(const Pack8<T> &y, float s, float r) {
-  uint32_t b[8];
-  if (r != 0.0f) {
-    const float2 nr = make_float2(-r, -r), s2 = make_float2(s, s);
+  uint32_t b[4];
+  const float2 nr = make_float2(-r, -r), s2 = make_float2(s, s);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      // RN(x / s) by Markstein's correction, a zero keeping x's sign
-      const float2 v = y.pair(k), q = __fmul2_rn(v, nr);
-      b[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(__ffma2_rn(__ffma2_rn(q, s2, v), nr, q),
-                                                __NV_SATFINITE, __NV_E4M3);
-    }
-    return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
+  for (int k = 0; k < 4; ++k) {
+    const float2 v = y.pair(k), q = __fmul2_rn(v, nr);
+    b[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(__ffma2_rn(__ffma2_rn(q, s2, v), nr, q),
+                                              __NV_SATFINITE, __NV_E4M3);
   }
+  return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
+}
+
+// One element, not negated, of a tile that is not finite: a NaN keeps its
+// sign, a NaN that the division makes is 0x7F, and all else is a zero (s is
+// infinite or NaN).
+__device__ __noinline__ uint32_t cast1_careful(float x, float s) {
+  if (x != x) return 0x7Fu | ((__float_as_uint(x) >> 24) & 0x80u);
+  const float q = __fdiv_rn(x, s);
+  if (q != q) return 0x7Fu;
+  return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+}
+
+template <typename T>
+__device__ __forceinline__ uint2 cast8_any(const Pack8<T> &y, float s, float r) {
+  if (s < __uint_as_float(0x7F800000u)) return cast8(y, s, r);
+  uint32_t b[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = cast1_slow(-y.at(j), s);
+  for (int j = 0; j < 8; ++j) b[j] = cast1_careful(-y.at(j), s);
   return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
                     b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
 }
 
 template <bool VEC>
 __device__ __forceinline__ void store_bytes(uint8_t *p, int valid, uint2 w) {
-  if (VEC && valid >= 8) {
-    *reinterpret_cast<uint2 *>(p) = w;
+  if (VEC) {
+    if (valid > 0) *reinterpret_cast<uint2 *>(p) = w;
     return;
   }
 #pragma unroll
@@ -114,7 +116,7 @@ __device__ __forceinline__ void store_bytes(uint8_t *p, int valid, uint2 w) {
 
 template <bool VEC>
 __device__ __forceinline__ uint2 load_bytes(const uint8_t *p, int valid) {
-  if (VEC && valid >= 8) return *reinterpret_cast<const uint2 *>(p);
+  if (VEC) return *reinterpret_cast<const uint2 *>(p);
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -158,12 +160,14 @@ struct Walk {
 // 1: u or v), and the results are handed round.
 struct Scales {
   float s[2][2], r[2][2];   // [piece][u, v]
+  bool finite;              // all four of every half warp
 };
 
 __device__ __forceinline__ void finish_scales(uint32_t mine, Scales &out) {
   const int lane = threadIdx.x & 31;
   const float s = tile_scale(mine);
-  const float r = mine < 0x7F800000u ? __frcp_rn(s) : 0.0f;
+  out.finite = __all_sync(0xFFFFFFFFu, mine < 0x7F800000u);
+  const float r = __frcp_rn(s);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -210,29 +214,98 @@ __device__ __forceinline__ void find_scales(const Pack8<float> (&u)[2], const Pa
   finish_scales(t, out);
 }
 
+// The rows of a step: two, `apart` rows apart; each thread keeps kStages steps'
+// inputs in shared memory slots of its own, filled by asynchronous copies two
+// steps ahead (VEC) -- no thread reads another's, so no barrier is needed.
+constexpr int kStages = 3;
+
+struct __align__(16) Slots {
+  uint8_t at[kStages][2][kThreads * 16];
+  __device__ __forceinline__ uint8_t *slot(int stage, int i) { return &at[stage][i][threadIdx.x * 16]; }
+};
+
+template <typename T>
+__device__ __forceinline__ void fetch(Slots *s, int stage, int i, const T *p,
+                                      bool on) {
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+    pack8::copy_async16(s[k].slot(stage, i), reinterpret_cast<const uint8_t *>(p) + 16 * k, on);
+}
+
+template <typename T>
+__device__ __forceinline__ void take(Pack8<T> &x, Slots *s, int stage, int i) {
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+    const uint4 t = *reinterpret_cast<const uint4 *>(s[k].slot(stage, i));
+    if constexpr (sizeof(T) == 2) {
+      x.w[0] = t.x, x.w[1] = t.y, x.w[2] = t.z, x.w[3] = t.w;
+    } else {
+      x.v[4 * k] = __uint_as_float(t.x), x.v[4 * k + 1] = __uint_as_float(t.y);
+      x.v[4 * k + 2] = __uint_as_float(t.z), x.v[4 * k + 3] = __uint_as_float(t.w);
+    }
+  }
+}
+
+template <typename T, bool GATED>
+struct ForwardSmem {
+  static constexpr int kV = sizeof(T) / 2;   // 16-byte slots of an element octet
+  Slots x[(GATED ? 2 : 1) * kV];         // u, then v
+};
+
 template <int ACT, typename T, bool GATED, bool VEC>
 __global__ void __launch_bounds__(kThreads, 3) forward_kernel(const ForwardArgs p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  auto &in = *reinterpret_cast<ForwardSmem<T, GATED> *>(smem);
   const int lane = threadIdx.x & 31;
   const Walk walk(p.T, p.F);
+  const int64_t apart = 2 * walk.step;
   for (int64_t tile = walk.tile; tile < walk.tiles; tile += walk.tile_step) {
     const int64_t col = tile * 128 + (lane & 15) * 8;
     const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.F - col));
     int64_t row = 2 * walk.pair0 + (lane >> 4);
-    // nothing is addressed where nothing is valid
-    const int64_t c = cols_in > 0 ? col : 0;
+    const int64_t c = cols_in > 0 ? col : 0;   // nothing is addressed where nothing is valid
     const T *pu = static_cast<const T *>(p.u) + row * p.ldu + c;
     const T *pv = static_cast<const T *>(p.v) + (GATED ? row * p.ldv + c : 0);
     T *pa = static_cast<T *>(p.a) + row * p.lda + c;
     int64_t at8 = row * p.F + c, at_s = tile * p.T + row;
-    const int64_t step = 2 * walk.step;
-    for (int64_t pair = walk.pair0; pair < walk.pairs; pair += 2 * walk.step) {
+    int64_t next = row;   // first row of the next step to fetch
+    auto fetch_step = [&](int stage) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool on = next + i * apart < p.T && cols_in > 0;
+        fetch<T>(in.x, stage, i, on ? pu + i * apart * p.ldu : static_cast<const T *>(p.u), on);
+        if (GATED) fetch<T>(in.x + in.kV, stage, i, on ? pv + i * apart * p.ldv : static_cast<const T *>(p.v), on);
+      }
+      pack8::copy_commit();
+      next += 2 * apart;
+      pu += 2 * apart * p.ldu;
+      pv += 2 * apart * p.ldv;
+    };
+    if (VEC)
+      for (int k = 0; k < kStages - 1; ++k) fetch_step(k);
+    int stage = 0;
+    for (int64_t pair = walk.pair0; pair < walk.pairs; pair += apart) {
       Pack8<T> u[2], v[2];
       int valid[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        valid[i] = row + i * step < p.T ? cols_in : 0;
-        load<VEC>(u[i], pu + (valid[i] > 0 ? i * step * p.ldu : 0), valid[i]);
-        if (GATED) load<VEC>(v[i], pv + (valid[i] > 0 ? i * step * p.ldv : 0), valid[i]);
+      for (int i = 0; i < 2; ++i) valid[i] = row + i * apart < p.T ? cols_in : 0;
+      if (VEC) {
+        fetch_step(stage == 0 ? kStages - 1 : stage - 1);
+        pack8::copy_wait<kStages - 1>();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          take<T>(u[i], in.x, stage, i);
+          if (GATED) take<T>(v[i], in.x + in.kV, stage, i);
+        }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          u[i].load_some(pu + (valid[i] > 0 ? i * apart * p.ldu : 0), valid[i]);
+          if (GATED) v[i].load_some(pv + (valid[i] > 0 ? i * apart * p.ldv : 0), valid[i]);
+        }
+        pu += 2 * apart * p.ldu;
+        pv += 2 * apart * p.ldv;
       }
       Scales sc;
       find_scales<GATED>(u, v, sc);
@@ -240,13 +313,20 @@ __global__ void __launch_bounds__(kThreads, 3) forward_kernel(const ForwardArgs 
       for (int i = 0; i < 2; ++i) {
         u[i].negate();
         if (GATED) v[i].negate();
+        uint2 bu, bv;
+        if (sc.finite) {
+          bu = cast8(u[i], sc.s[i][0], sc.r[i][0]);
+          if (GATED) bv = cast8(v[i], sc.s[i][1], sc.r[i][1]);
+        } else {
+          bu = cast8_any(u[i], sc.s[i][0], sc.r[i][0]);
+          if (GATED) bv = cast8_any(v[i], sc.s[i][1], sc.r[i][1]);
+        }
         if (valid[i] > 0) {
-          store_bytes<VEC>(p.u8 + at8 + i * step * p.F, valid[i], cast8(u[i], sc.s[i][0], sc.r[i][0]));
-          if (GATED)
-            store_bytes<VEC>(p.v8 + at8 + i * step * p.F, valid[i], cast8(v[i], sc.s[i][1], sc.r[i][1]));
+          store_bytes<VEC>(p.u8 + at8 + i * apart * p.F, valid[i], bu);
+          if (GATED) store_bytes<VEC>(p.v8 + at8 + i * apart * p.F, valid[i], bv);
           if ((lane & 15) == 0) {
-            p.u_scales[at_s + i * step] = sc.s[i][0];
-            if (GATED) p.v_scales[at_s + i * step] = sc.s[i][1];
+            p.u_scales[at_s + i * apart] = sc.s[i][0];
+            if (GATED) p.v_scales[at_s + i * apart] = sc.s[i][1];
           }
           float out[8], unused;
 #pragma unroll
@@ -254,16 +334,15 @@ __global__ void __launch_bounds__(kThreads, 3) forward_kernel(const ForwardArgs 
             activation<ACT, false>(-u[i].at(j), out[j], unused);
             out[j] = GATED ? -out[j] * v[i].at(j) : out[j];
           }
-          store<VEC>(pa + i * step * p.lda, valid[i], out);
+          store<VEC>(pa + i * apart * p.lda, valid[i], out);
         }
       }
-      row += 2 * step;
-      pu += 2 * step * p.ldu;
-      pv += 2 * step * p.ldv;
-      pa += 2 * step * p.lda;
-      at8 += 2 * step * p.F;
-      at_s += 2 * step;
+      row += 2 * apart;
+      pa += 2 * apart * p.lda;
+      at8 += 2 * apart * p.F;
+      at_s += 2 * apart;
     }
+    if (VEC) pack8::copy_wait<0>();   // the slots are free for the next tile column
   }
 }
 
@@ -271,6 +350,7 @@ template <int ACT, typename T, bool GATED, bool VEC>
 __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardArgs p) {
   const int lane = threadIdx.x & 31;
   const Walk walk(p.T, p.F);
+  const int64_t apart = 2 * walk.step;
   for (int64_t tile = walk.tile; tile < walk.tiles; tile += walk.tile_step) {
     const int64_t col = tile * 128 + (lane & 15) * 8;
     const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.F - col));
@@ -281,23 +361,22 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardArg
     T *pv = static_cast<T *>(p.dv) + (GATED ? row * p.lddv + c : 0);
     T *pa = static_cast<T *>(p.a) + row * p.lda + c;
     int64_t at8 = row * p.F + c, at_s = tile * p.T + row;
-    const int64_t step = 2 * walk.step;
-    for (int64_t pair = walk.pair0; pair < walk.pairs; pair += 2 * walk.step) {
+    for (int64_t pair = walk.pair0; pair < walk.pairs; pair += apart) {
       Pack8<T> d[2];
       uint2 bu[2], bv[2];
       float su[2], sv[2];
       int valid[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        valid[i] = row + i * step < p.T ? cols_in : 0;
+        valid[i] = row + i * apart < p.T ? cols_in : 0;
         if (valid[i] > 0) {
-          bu[i] = load_bytes<VEC>(p.u8 + at8 + i * step * p.F, valid[i]);
-          su[i] = p.u_scales[at_s + i * step];
+          bu[i] = load_bytes<VEC>(p.u8 + at8 + i * apart * p.F, valid[i]);
+          su[i] = p.u_scales[at_s + i * apart];
           if (GATED) {
-            bv[i] = load_bytes<VEC>(p.v8 + at8 + i * step * p.F, valid[i]);
-            sv[i] = p.v_scales[at_s + i * step];
+            bv[i] = load_bytes<VEC>(p.v8 + at8 + i * apart * p.F, valid[i]);
+            sv[i] = p.v_scales[at_s + i * apart];
           }
-          load<VEC>(d[i], pd + i * step * p.ldda, valid[i]);
+          pack8::load<VEC>(d[i], pd + i * apart * p.ldda, valid[i]);
         }
       }
 #pragma unroll
@@ -315,65 +394,89 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardArg
           dv[j] = da * f;
           out[j] = GATED ? f * v[j] : f;
         }
-        store<VEC>(pu + i * step * p.lddu, valid[i], du);
-        if (GATED) store<VEC>(pv + i * step * p.lddv, valid[i], dv);
-        if (p.a != nullptr) store<VEC>(pa + i * step * p.lda, valid[i], out);
+        store<VEC>(pu + i * apart * p.lddu, valid[i], du);
+        if (GATED) store<VEC>(pv + i * apart * p.lddv, valid[i], dv);
+        if (p.a != nullptr) store<VEC>(pa + i * apart * p.lda, valid[i], out);
       }
-      row += 2 * step;
-      pd += 2 * step * p.ldda;
-      pu += 2 * step * p.lddu;
-      pv += 2 * step * p.lddv;
-      pa += 2 * step * p.lda;
-      at8 += 2 * step * p.F;
-      at_s += 2 * step;
+      row += 2 * apart;
+      pd += 2 * apart * p.ldda;
+      pu += 2 * apart * p.lddu;
+      pv += 2 * apart * p.lddv;
+      pa += 2 * apart * p.lda;
+      at8 += 2 * apart * p.F;
+      at_s += 2 * apart;
     }
   }
 }
 
-int grid_for(int64_t T, int64_t F) {
+// CTAs that fit on the device at once, no more than there is work for.
+template <typename Tag, typename Kernel>
+int grid_for(Kernel kernel, int smem, int64_t T, int64_t F) {
+  static PerDeviceOnce setup;   // per Tag
+  const int fit = setup.get([&] {
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, smem) != cudaSuccess)
+      return 0;
+    return n * sm_count();
+  });
   const int64_t warps = ((T + 1) / 2) * ((F + 127) / 128);
-  return (int)std::min<int64_t>((warps + kThreads / 32 - 1) / (kThreads / 32), 8 * sm_count());
+  return (int)std::min<int64_t>((warps + kThreads / 32 - 1) / (kThreads / 32), fit);
 }
 
 bool vec_ok(const void *p, int64_t ld, int64_t size) {
   return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * size % 16 == 0);
 }
 
-template <int ACT, typename T, bool GATED>
-void forward(const ForwardArgs &a, bool vec, cudaStream_t stream) {
-  const int grid = grid_for(a.T, a.F);
-  if (vec)
-    forward_kernel<ACT, T, GATED, true><<<grid, kThreads, 0, stream>>>(a);
-  else
-    forward_kernel<ACT, T, GATED, false><<<grid, kThreads, 0, stream>>>(a);
+template <int ACT, typename T, bool GATED, bool VEC>
+cudaError_t run_forward(const ForwardArgs &a, cudaStream_t stream) {
+  constexpr auto kernel = forward_kernel<ACT, T, GATED, VEC>;
+  constexpr int smem = VEC ? (int)sizeof(ForwardSmem<T, GATED>) : 0;
+  struct Tag {};   // a set-up of its own for every kernel of this signature
+  const int grid = grid_for<Tag>(kernel, smem, a.T, a.F);
+  if (grid < 1) return cudaErrorInvalidValue;
+  kernel<<<grid, kThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int ACT, typename T, bool GATED, bool VEC>
+cudaError_t run_backward(const BackwardArgs &a, cudaStream_t stream) {
+  constexpr auto kernel = backward_kernel<ACT, T, GATED, VEC>;
+  constexpr int smem = 0;
+  struct Tag {};
+  const int grid = grid_for<Tag>(kernel, smem, a.T, a.F);
+  if (grid < 1) return cudaErrorInvalidValue;
+  kernel<<<grid, kThreads, smem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 template <int ACT, typename T, bool GATED>
-void backward(const BackwardArgs &a, bool vec, cudaStream_t stream) {
-  const int grid = grid_for(a.T, a.F);
-  if (vec)
-    backward_kernel<ACT, T, GATED, true><<<grid, kThreads, 0, stream>>>(a);
-  else
-    backward_kernel<ACT, T, GATED, false><<<grid, kThreads, 0, stream>>>(a);
+cudaError_t forward(const ForwardArgs &a, bool vec, cudaStream_t stream) {
+  return vec ? run_forward<ACT, T, GATED, true>(a, stream) : run_forward<ACT, T, GATED, false>(a, stream);
+}
+
+template <int ACT, typename T, bool GATED>
+cudaError_t backward(const BackwardArgs &a, bool vec, cudaStream_t stream) {
+  return vec ? run_backward<ACT, T, GATED, true>(a, stream)
+             : run_backward<ACT, T, GATED, false>(a, stream);
 }
 
 template <int ACT>
-void forward_type(int dtype, const ForwardArgs &a, bool vec, cudaStream_t s) {
+cudaError_t forward_type(int dtype, const ForwardArgs &a, bool vec, cudaStream_t s) {
   const bool gated = a.v != nullptr;
   if (dtype == FP8Q_DT_BF16)
-    gated ? forward<ACT, __nv_bfloat16, true>(a, vec, s) : forward<ACT, __nv_bfloat16, false>(a, vec, s);
-  else
-    gated ? forward<ACT, float, true>(a, vec, s) : forward<ACT, float, false>(a, vec, s);
+    return gated ? forward<ACT, __nv_bfloat16, true>(a, vec, s) : forward<ACT, __nv_bfloat16, false>(a, vec, s);
+  return gated ? forward<ACT, float, true>(a, vec, s) : forward<ACT, float, false>(a, vec, s);
 }
 
 template <int ACT>
-void backward_type(int dtype, const BackwardArgs &a, bool vec, cudaStream_t s) {
+cudaError_t backward_type(int dtype, const BackwardArgs &a, bool vec, cudaStream_t s) {
   const bool gated = a.v8 != nullptr;
   if (dtype == FP8Q_DT_BF16)
-    gated ? backward<ACT, __nv_bfloat16, true>(a, vec, s)
+    return gated ? backward<ACT, __nv_bfloat16, true>(a, vec, s)
           : backward<ACT, __nv_bfloat16, false>(a, vec, s);
-  else
-    gated ? backward<ACT, float, true>(a, vec, s) : backward<ACT, float, false>(a, vec, s);
+  return gated ? backward<ACT, float, true>(a, vec, s) : backward<ACT, float, false>(a, vec, s);
 }
 
 }  // namespace
@@ -383,12 +486,10 @@ cudaError_t launch_forward(int act, int dtype, const ForwardArgs &a, cudaStream_
   const bool vec = a.F % 16 == 0 && vec_ok(a.u, a.ldu, size) && vec_ok(a.v, a.ldv, size) &&
                    vec_ok(a.a, a.lda, size) && vec_ok(a.u8, a.F, 1) && vec_ok(a.v8, a.F, 1);
   if (act == FP8Q_ACT_SILU)
-    forward_type<FP8Q_ACT_SILU>(dtype, a, vec, stream);
-  else if (act == FP8Q_ACT_GELU)
-    forward_type<FP8Q_ACT_GELU>(dtype, a, vec, stream);
-  else
-    forward_type<FP8Q_ACT_GELU_TANH>(dtype, a, vec, stream);
-  return cudaGetLastError();
+    return forward_type<FP8Q_ACT_SILU>(dtype, a, vec, stream);
+  if (act == FP8Q_ACT_GELU)
+    return forward_type<FP8Q_ACT_GELU>(dtype, a, vec, stream);
+  return forward_type<FP8Q_ACT_GELU_TANH>(dtype, a, vec, stream);
 }
 
 cudaError_t launch_backward(int act, int dtype, const BackwardArgs &a, cudaStream_t stream) {
@@ -397,12 +498,10 @@ cudaError_t launch_backward(int act, int dtype, const BackwardArgs &a, cudaStrea
                    vec_ok(a.da, a.ldda, size) && vec_ok(a.du, a.lddu, size) &&
                    vec_ok(a.dv, a.lddv, size) && vec_ok(a.a, a.lda, size);
   if (act == FP8Q_ACT_SILU)
-    backward_type<FP8Q_ACT_SILU>(dtype, a, vec, stream);
-  else if (act == FP8Q_ACT_GELU)
-    backward_type<FP8Q_ACT_GELU>(dtype, a, vec, stream);
-  else
-    backward_type<FP8Q_ACT_GELU_TANH>(dtype, a, vec, stream);
-  return cudaGetLastError();
+    return backward_type<FP8Q_ACT_SILU>(dtype, a, vec, stream);
+  if (act == FP8Q_ACT_GELU)
+    return backward_type<FP8Q_ACT_GELU>(dtype, a, vec, stream);
+  return backward_type<FP8Q_ACT_GELU_TANH>(dtype, a, vec, stream);
 }
 
 }  // namespace act

@@ -11,6 +11,14 @@
 namespace fp8q {
 namespace pack8 {
 
+// The larger magnitudes of two pairs of bf16, NaN if either is one; the signs
+// of the result mean nothing.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <typename T>
 struct Pack8;
 
@@ -21,6 +29,7 @@ struct Pack8<__nv_bfloat16> {
     const uint4 t = *reinterpret_cast<const uint4 *>(p);
     w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
   }
+  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
   __device__ __forceinline__ void load_some(const __nv_bfloat16 *p, int valid) {
     const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
@@ -40,8 +49,7 @@ struct Pack8<__nv_bfloat16> {
   }
   // max |element| as an fp32 bit pattern (NaN sorts above infinity)
   __device__ __forceinline__ uint32_t amax_bits() const {
-    const uint32_t k = 0x7FFF7FFFu;
-    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & k, w[1] & k), __vmaxu2(w[2] & k, w[3] & k));
+    const uint32_t m = max_abs2(max_abs2(w[0], w[1]), max_abs2(w[2], w[3])) & 0x7FFF7FFFu;
     return max(m << 16, m & 0xFFFF0000u);
   }
 };
@@ -54,6 +62,10 @@ struct Pack8<float> {
     const float4 b = *(reinterpret_cast<const float4 *>(p) + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
   }
   __device__ __forceinline__ void load_some(const float *p, int valid) {
 #pragma unroll
@@ -73,24 +85,30 @@ struct Pack8<float> {
   }
 };
 
-// Elements [0, valid) of a row from p, zeros after; VEC: p is 16-byte aligned.
+// Elements [0, valid) of a row from p, zeros after; VEC: p is 16-byte aligned
+// and valid is 0 or 8.
 template <bool VEC, typename T>
 __device__ __forceinline__ void load(Pack8<T> &x, const T *p, int valid) {
-  if (VEC && valid >= 8)
-    x.load_vec(p);
-  else
+  if (!VEC) {
     x.load_some(p, valid);
+  } else if (valid > 0) {
+    x.load_vec(p);
+  } else {
+    x.clear();
+  }
 }
 
-// Two values to two elements of T.
+// Two values to two bf16 elements, the first in the low half.
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&b);
 }
 
+// VEC: p is 16-byte aligned and valid is 0 or 8.
 template <bool VEC, typename T>
 __device__ __forceinline__ void store(T *p, int valid, const float (&v)[8]) {
-  if (VEC && valid >= 8) {
+  if (VEC) {
+    if (valid <= 0) return;
     if constexpr (sizeof(T) == 2) {
       *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]),
                                                  bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
@@ -103,6 +121,21 @@ __device__ __forceinline__ void store(T *p, int valid, const float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (j < valid) p[j] = (T)v[j];
+}
+
+// Asynchronous copy of 16 bytes (both sides aligned) into shared memory;
+// nothing is read and zeros are written where `on` is false.
+__device__ __forceinline__ void copy_async16(void *dst, const void *src, bool on) {
+  asm volatile("cp.async.cg.shared::cta.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(on ? 16u : 0u)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's newest groups are still under way.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 }  // namespace pack8
