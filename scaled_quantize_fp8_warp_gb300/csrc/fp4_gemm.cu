@@ -13,10 +13,12 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4_common.cuh"
 #include "fp4_internal.h"
 #include "fp4_ptx.cuh"
+#include "fp8_pack8.cuh"
 #include "fp8q_gemm_common.cuh"
 
 namespace fp8q {
@@ -60,31 +62,77 @@ struct Layout {
   static_assert(kSmemBytes <= 227 * 1024, "the ring fits in shared memory");
 };
 
-// 32 consecutive results of row m from column n0.  VEC: every row of C starts
-// on a 16-byte boundary, so whole groups of 16 bytes are stored at once.
-template <typename T, bool VEC>
-__device__ __forceinline__ void store32(T *C, int64_t N, int64_t m, int64_t n0,
-                                        const float (&v)[32]) {
-  constexpr int kVec = 16 / sizeof(T);
-  T *row = C + m * N + n0;
+// One K block in the ring slot at `sa` (A, B, A's atoms, B's atoms of its two
+// row blocks), by one elected thread: scales into tensor memory at sf, then up
+// to four MMAs of 64 K.  The last block may hold fewer steps: K past the
+// matrix would multiply zeros with scales that were not loaded.
+template <int KIND, bool PAIR>
+__device__ __forceinline__ void issue_block(uint32_t sa, uint32_t b_off, uint32_t sfa_off,
+                                            uint32_t d_tmem, uint32_t sf, uint32_t idesc,
+                                            int steps, bool first) {
+  constexpr int kAtoms = kBK / Kind<KIND>::kAtomK;
+  const uint32_t sfa = sf, sfb = sf + 4 * kAtoms;
+  const uint64_t atom = sdesc_plain(sa + sfa_off, 128);   // + 32 per atom (512 bytes >> 4)
 #pragma unroll
-  for (int g = 0; g < 32 / kVec; ++g) {
-    if (VEC) {
-      if (n0 + g * kVec < N) {
-        __align__(16) T w[kVec];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) w[j] = (T)v[g * kVec + j];
-        __stcs(reinterpret_cast<uint4 *>(row + g * kVec), *reinterpret_cast<const uint4 *>(w));
-      }
+  for (int a = 0; a < kAtoms; ++a) {
+    const uint64_t a0 = atom + 32 * a, b0 = atom + 32 * (kAtoms + a), b1 = atom + 32 * (2 * kAtoms + a);
+    if (PAIR) {
+      tmem_cp_32x128b_x4_pair(sfa + 4 * a, a0);
+      tmem_cp_32x128b_x4_pair(sfb + 8 * a, b0);
+      tmem_cp_32x128b_x4_pair(sfb + 8 * a + 4, b1);
     } else {
+      tmem_cp_32x128b_x4(sfa + 4 * a, a0);
+      tmem_cp_32x128b_x4(sfb + 8 * a, b0);
+      tmem_cp_32x128b_x4(sfb + 8 * a + 4, b1);
+    }
+  }
+  const uint64_t ad = sdesc_k(sa, gemm::kSwzSBO, gemm::kSwzMode);
+  const uint64_t bd = sdesc_k(sa + b_off, gemm::kSwzSBO, gemm::kSwzMode);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (n0 + g * kVec + j < N) row[g * kVec + j] = (T)v[g * kVec + j];
+  for (int k = 0; k < 4; ++k) {
+    if (k < steps) {
+      const int a = KIND == FP4Q_MXFP4 ? k >> 1 : k;
+      const uint32_t half = KIND == FP4Q_MXFP4 ? 2u * (k & 1) : 0u;   // of the scale word
+      const uint32_t id = idesc | (half << 29) | (half << 4);
+      const uint32_t acc = (!first || k > 0) ? 1u : 0u;
+      if (PAIR)
+        mma_fp4_pair<KIND>(d_tmem, ad + 2 * k, bd + 2 * k, id, sfa + 4 * a, sfb + 8 * a, acc);
+      else
+        mma_fp4<KIND>(d_tmem, ad + 2 * k, bd + 2 * k, id, sfa + 4 * a, sfb + 8 * a, acc);
     }
   }
 }
 
-template <int KIND, typename T, bool VEC>
+// 32 consecutive results of row m from column n0.  WIDTH: every row of C starts
+// on a boundary of so many bytes (32 or 16), and whole groups of that size are
+// stored at once; 0: element by element.
+template <typename T, int WIDTH>
+__device__ __forceinline__ void store32(T *C, int64_t N, int64_t m, int64_t n0,
+                                        const float (&v)[32]) {
+  T *row = C + m * N + n0;
+  if constexpr (WIDTH == 0) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (n0 + j < N) row[j] = (T)v[j];
+  } else {
+    constexpr int kGroup = WIDTH / (int)sizeof(T);
+#pragma unroll
+    for (int g = 0; g < 32; g += kGroup) {
+      if (n0 + g >= N) break;
+      uint32_t w[WIDTH / 4];
+#pragma unroll
+      for (int h = 0; h < WIDTH / 4; ++h)
+        w[h] = sizeof(T) == 2 ? pack8::bf16x2(v[(g + 2 * h) & 31], v[(g + 2 * h + 1) & 31])
+                              : __float_as_uint(v[g + h]);
+      if constexpr (WIDTH == 32)
+        store_32b(row + g, w);
+      else
+        __stcs(reinterpret_cast<uint4 *>(row + g), make_uint4(w[0], w[1], w[2], w[3]));
+    }
+  }
+}
+
+template <int KIND, typename T, int WIDTH>
 __global__ void __launch_bounds__(320, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const Args p) {
@@ -166,50 +214,29 @@ __global__ void __launch_bounds__(320, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t it = 0, acc_it = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++acc_it) {
-        if (!wait_bounded(acce, (acc_it & 1u) ^ 1u, abort_flag, p.err)) {
+    uint32_t it = 0, acc_it = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++acc_it) {
+      if (!wait_bounded_all(acce, (acc_it & 1u) ^ 1u, abort_flag, p.err)) break;
+      tc_fence_after();
+      for (int kb = 0; kb < p.num_k_blocks; ++kb, ++it) {
+        const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+        if (!wait_bounded_all(full0 + 8 * s, ph, abort_flag, p.err)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        for (int kb = 0; kb < p.num_k_blocks; ++kb, ++it) {
-          const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
-          if (!wait_bounded(full0 + 8 * s, ph, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = ring + s * L::kStageBytes;
-          const uint32_t sfa = tmem_base + L::kSfCol0 + L::kSfCols * s;
-          const uint32_t sfb = sfa + 4 * L::kAtoms;
-#pragma unroll
-          for (int a = 0; a < L::kAtoms; ++a) {
-            tmem_cp_32x128b_x4(sfa + 4 * a, sdesc_plain(sa + L::kSfaOff + 512 * a, 128));
-            tmem_cp_32x128b_x4(sfb + 8 * a, sdesc_plain(sa + L::kSfbOff + 512 * a, 128));
-            tmem_cp_32x128b_x4(sfb + 8 * a + 4,
-                               sdesc_plain(sa + L::kSfbOff + 512 * (L::kAtoms + a), 128));
-          }
-          // the last block may hold fewer than four steps: K past the matrix
-          // would multiply zeros with scales that were not loaded
-          const int steps = min(4, p.num_steps - 4 * kb);
-          for (int k = 0; k < steps; ++k) {
-            const uint64_t ad = sdesc_k(sa + 32 * k, gemm::kSwzSBO, gemm::kSwzMode);
-            const uint64_t bd = sdesc_k(sa + L::kABytes + 32 * k, gemm::kSwzSBO, gemm::kSwzMode);
-            const int a = KIND == FP4Q_MXFP4 ? k >> 1 : k;
-            const uint32_t half = KIND == FP4Q_MXFP4 ? 2u * (k & 1) : 0u;
-            mma_fp4<KIND>(tmem_base, ad, bd, p.idesc | (half << 29) | (half << 4), sfa + 4 * a,
-                          sfb + 8 * a, (kb > 0 || k > 0) ? 1u : 0u);
-          }
+        if (elect_one()) {
+          issue_block<KIND, false>(ring + s * L::kStageBytes, L::kABytes, L::kSfaOff, tmem_base,
+                                   tmem_base + L::kSfCol0 + L::kSfCols * s, p.idesc,
+                                   p.num_steps - 4 * kb, kb == 0);
           mma_commit(empty0 + 8 * s);
+          if (kb == p.num_k_blocks - 1) mma_commit(accf);
         }
-        if (!ok) break;
-        mma_commit(accf);
+        __syncwarp();
       }
-      gemm::drain_mma(drain, abort_flag);
     }
+    if (elect_one()) gemm::drain_mma(drain, abort_flag);
     __syncwarp();
   } else {
     // Warps 2..9: warp w drains TMEM lane quarter w % 4, columns
@@ -242,7 +269,7 @@ __global__ void __launch_bounds__(320, 1)
             for (int j = 0; j < 32; ++j)
               v[j] = KIND == FP4Q_NVFP4 ? __fmul_rn(__uint_as_float(r[c][j]), g)
                                         : __uint_as_float(r[c][j]);
-            store32<T, VEC>(static_cast<T *>(p.C), p.N, m, n0, v);
+            store32<T, WIDTH>(static_cast<T *>(p.C), p.N, m, n0, v);
           }
         }
       }
@@ -255,9 +282,222 @@ __global__ void __launch_bounds__(320, 1)
   if (warp == 1) tmem_dealloc(tmem_base, L::kTmemCols);
 }
 
-template <int KIND, typename T, bool VEC>
+// ------------------------------------------------------------------------
+// The same on CTA pairs (tcgen05.mma.cta_group::2): 256 x 256 tiles, each CTA
+// staging its own 128 rows of A and half of B's rows, so that a stage brings
+// 32 KB for twice the work of the 48 KB above.  On one SM a 128 x 256 tile
+// moves 24 KB through shared memory (fill and operand reads) for each MMA of
+// 128 cycles, above its 128 bytes a cycle; the pair moves 16 KB.  Scales: each
+// CTA loads the atoms of its own 128 rows of A and of all 256 rows of B (by
+// tensor map: an atom is a row of 128 words), and the even CTA's copies put
+// both CTAs' into tensor memory.  A slot of scales per ring stage leaves room
+// for one accumulator: the epilogue's eight warps take it into registers at
+// once and release it before they convert and store.
+// ------------------------------------------------------------------------
+template <int KIND>
+struct PairLayout {
+  static constexpr int kStages = KIND == FP4Q_MXFP4 ? 6 : 5;
+  static constexpr int kAtoms = kBK / Kind<KIND>::kAtomK;
+  static constexpr int kABytes = 128 * kBKBytes, kBBytes = 128 * kBKBytes;
+  static constexpr int kSfaOff = kABytes + kBBytes;
+  static constexpr int kSfbOff = kSfaOff + kAtoms * 512;
+  static constexpr int kLoadBytes = kSfbOff + 2 * kAtoms * 512;
+  static constexpr int kStageBytes = (kLoadBytes + 1023) / 1024 * 1024;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kBarBytes = 8 * (2 * kStages + 3);
+  static constexpr int kSmemBytes = kRingBytes + kBarBytes + 16 + 1024;
+  static constexpr uint32_t kSfCol0 = 256;
+  static constexpr uint32_t kSfCols = 12 * kAtoms;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kSfCol0 + kSfCols * kStages <= kTmemCols, "scale slots fit in TMEM");
+  static_assert(kSmemBytes <= 227 * 1024, "the ring fits in shared memory");
+};
+
+struct PairMaps {
+  CUtensorMap a, b, sfa, sfb;
+};
+
+template <int KIND, typename T, int WIDTH>
+__global__ void __launch_bounds__(320, 1)
+    gemm_pair_kernel(const __grid_constant__ PairMaps maps, const Args p) {
+  using L = PairLayout<KIND>;
+  constexpr int kStages = L::kStages;
+  constexpr uint16_t kBoth = 3;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;
+  const uint32_t bars = ring + L::kRingBytes;
+  const uint32_t full0 = bars, empty0 = bars + 8 * kStages;
+  const uint32_t accf = bars + 8 * (2 * kStages), acce = accf + 8, drain = acce + 8;
+  const uint32_t slot = bars + L::kBarBytes;
+  uint8_t *slot_ptr = smem_raw + (slot - raw);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(slot_ptr + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();   // 0: issues the pair's MMAs
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(accf, 1);
+    mbar_init(acce, 16);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+    prefetch_tmap(&maps.sfa);
+    prefetch_tmap(&maps.sfb);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(slot, L::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(slot_ptr);
+  // One allocation serves the pair: both CTAs must hold the same address.
+  // Otherwise neither does any work (a symmetric decision, no waiting).
+  const bool paired = ld_shared_cluster_u32(mapa_shared(slot, rank ^ 1u)) == tmem_base;
+  if (!paired && threadIdx.x == 0) atomicOr(p.err, 4u);
+
+  const int num_mu = (p.num_m_tiles + 1) / 2;
+  const int total = num_mu * p.num_n_tiles;
+  const int unit0 = blockIdx.x / 2, unit_step = gridDim.x / 2;
+
+  if (!paired) {
+  } else if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = unit0; u < total && ok; u += unit_step) {
+        int mu, nt;
+        gemm::tile_coords(u, num_mu, p.num_n_tiles, mu, nt, p.group, p.along_n);
+        // past the last M tile (odd count): re-read that tile's A, store nothing
+        const int mt = min(2 * mu + (int)rank, p.num_m_tiles - 1);
+        for (int kb = 0; kb < p.num_k_blocks; ++kb, ++it) {
+          const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+          if (!wait_bounded(empty0 + 8 * s, ph ^ 1u, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = ring + s * L::kStageBytes;
+          const uint32_t full_even = mapa_shared(full0 + 8 * s, 0);
+          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * L::kLoadBytes);
+          tma_load_2d_pair(sa, &maps.a, kb * kBKBytes, mt * 128, full_even);
+          tma_load_2d_pair(sa + L::kABytes, &maps.b, kb * kBKBytes, nt * 256 + (int)rank * 128,
+                           full_even);
+          // Atoms past the last of a row block are the next block's or zeros;
+          // no MMA step reads them.
+          const int ka = kb * L::kAtoms;
+          tma_load_2d_pair(sa + L::kSfaOff, &maps.sfa, 0, mt * p.atoms_k + ka, full_even);
+          tma_load_2d_pair(sa + L::kSfbOff, &maps.sfb, 0, 2 * nt * p.atoms_k + ka, full_even);
+          tma_load_2d_pair(sa + L::kSfbOff + L::kAtoms * 512, &maps.sfb, 0,
+                           (2 * nt + 1) * p.atoms_k + ka, full_even);
+        }
+      }
+      // every slot's last release (the even CTA's commits) has arrived here
+      for (uint32_t j = 0, jt = it; ok && j < (uint32_t)kStages; ++j, ++jt)
+        ok = wait_bounded(empty0 + 8 * (jt % kStages), ((jt / kStages) & 1u) ^ 1u, abort_flag,
+                          p.err);
+      if (!ok) {
+        // aborting: give copies already issued (their barrier may be the
+        // other CTA's) a millisecond to land before the CTA can leave
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    uint32_t it = 0, acc_it = 0;
+    bool ok = true;
+    for (int u = unit0; u < total && ok; u += unit_step, ++acc_it) {
+      if (!wait_bounded_all(acce, (acc_it & 1u) ^ 1u, abort_flag, p.err)) break;
+      tc_fence_after();
+      for (int kb = 0; kb < p.num_k_blocks; ++kb, ++it) {
+        const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+        if (!wait_bounded_all(full0 + 8 * s, ph, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          issue_block<KIND, true>(ring + s * L::kStageBytes, L::kABytes, L::kSfaOff, tmem_base,
+                                  tmem_base + L::kSfCol0 + L::kSfCols * s, p.idesc,
+                                  p.num_steps - 4 * kb, kb == 0);
+          mma_commit_pair_multicast(empty0 + 8 * s, kBoth);
+          if (kb == p.num_k_blocks - 1) mma_commit_pair_multicast(accf, kBoth);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) {
+      mma_commit_pair(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < 200000000ull) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+  } else {
+    // Warps 2..9: warp w drains TMEM lane quarter w % 4, columns
+    // [128 h, 128 h + 128) with h = (w - 2) / 4, of this CTA's 128 rows.
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const float g = KIND == FP4Q_NVFP4 ? __fmul_rn(*p.ga, *p.gb) : 1.0f;
+    const uint32_t acce_even = mapa_shared(acce, 0);
+    uint32_t acc_it = 0;
+    for (int u = unit0; u < total; u += unit_step, ++acc_it) {
+      int mu, nt;
+      gemm::tile_coords(u, num_mu, p.num_n_tiles, mu, nt, p.group, p.along_n);
+      if (!wait_bounded_warp(accf, acc_it & 1u, abort_flag, p.err)) break;
+      tc_fence_after();
+      uint32_t r[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 128 + c * 32,
+                           r[c]);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {   // the accumulator is free for the next tile
+        if (rank == 0)
+          mbar_arrive(acce);
+        else
+          mbar_arrive_cluster(acce_even);
+      }
+      const int64_t m = (int64_t)(2 * mu + (int)rank) * 128 + quarter * 32 + lane;
+      if (m < p.M) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int64_t n0 = (int64_t)nt * 256 + half * 128 + c * 32;
+          if (n0 < p.N) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              v[j] = KIND == FP4Q_NVFP4 ? __fmul_rn(__uint_as_float(r[c][j]), g)
+                                        : __uint_as_float(r[c][j]);
+            store32<T, WIDTH>(static_cast<T *>(p.C), p.N, m, n0, v);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while the other may still signal it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, L::kTmemCols);
+}
+
+template <int KIND, typename T, int WIDTH>
 int run(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t stream) {
-  auto kernel = gemm_kernel<KIND, T, VEC>;
+  auto kernel = gemm_kernel<KIND, T, WIDTH>;
   static PerDeviceOnce setup;  // per instantiation
   if (setup.get([&] {
         return gemm::set_smem(kernel, Layout<KIND>::kSmemBytes) == cudaSuccess ? 1 : 0;
@@ -269,10 +509,33 @@ int run(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_
   return cudaGetLastError() == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
 }
 
-template <int KIND, typename T>
-int run_vec(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t stream) {
-  return a.N * (int64_t)sizeof(T) % 16 == 0 ? run<KIND, T, true>(ta, tb, a, stream)
-                                            : run<KIND, T, false>(ta, tb, a, stream);
+template <int KIND, typename T, int WIDTH>
+int run_pair(const PairMaps &maps, const Args &a, cudaStream_t stream) {
+  using L = PairLayout<KIND>;
+  auto kernel = gemm_pair_kernel<KIND, T, WIDTH>;
+  static PerDeviceOnce setup;  // per instantiation: the pairs that fit at once, 0 on failure
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.blockDim = dim3(320, 1, 1);
+  cfg.dynamicSmemBytes = L::kSmemBytes;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int pairs = setup.get([&] {
+    if (gemm::set_smem(kernel, L::kSmemBytes) != cudaSuccess) return 0;
+    cudaLaunchConfig_t q = cfg;
+    q.gridDim = dim3(2 * (sm_count() / 2), 1, 1);
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &q) == cudaSuccess ? n : 0;
+  });
+  if (pairs < 1) return FP8Q_ERR_CUDA;
+  const int units = (a.num_m_tiles + 1) / 2 * a.num_n_tiles;
+  cfg.gridDim = dim3(2 * std::min(units, pairs), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
 }
 
 bool make_tmap(CUtensorMap *m, const void *base, int64_t rows, int64_t K, uint32_t box_rows) {
@@ -281,13 +544,52 @@ bool make_tmap(CUtensorMap *m, const void *base, int64_t rows, int64_t K, uint32
                       kBKBytes, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// A scale array as rows of one atom (128 words); the box is the atoms of one
+// stage.
+bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_t atoms_k,
+                     uint32_t box) {
+  return make_tmap_2d(m, scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 128,
+                      (uint64_t)((rows + 127) / 128 * atoms_k), 512, 128, box,
+                      CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Calls f(width) with the widest store that every row of C allows, as a
+// compile-time constant.
+template <typename T, typename F>
+int with_width(const Args &a, F &&f) {
+  const int64_t row = a.N * (int64_t)sizeof(T);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.C);
+  if (row % 32 == 0 && at % 32 == 0) return f(std::integral_constant<int, 32>{});
+  if (row % 16 == 0) return f(std::integral_constant<int, 16>{});
+  return f(std::integral_constant<int, 0>{});
+}
+
+template <int KIND, typename T>
+int launch_typed(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K,
+                 cudaStream_t stream) {
+  if (a.M > 128) {
+    PairMaps maps;
+    constexpr int kAtoms = PairLayout<KIND>::kAtoms;
+    if (!make_tmap(&maps.a, A.data, a.M, K, 128) || !make_tmap(&maps.b, B.data, a.N, K, 128) ||
+        !make_scale_tmap(&maps.sfa, A.scales, a.M, a.atoms_k, kAtoms) ||
+        !make_scale_tmap(&maps.sfb, B.scales, a.N, a.atoms_k, kAtoms))
+      return FP8Q_ERR_CUDA;
+    a.idesc = idesc_fp4(KIND, 256, 256);
+    a.group = 8;
+    return with_width<T>(a, [&](auto w) { return run_pair<KIND, T, decltype(w)::value>(maps, a, stream); });
+  }
+  CUtensorMap ta, tb;
+  if (!make_tmap(&ta, A.data, a.M, K, kBM) || !make_tmap(&tb, B.data, a.N, K, kBN))
+    return FP8Q_ERR_CUDA;
+  a.idesc = idesc_fp4(KIND, kBM, kBN);
+  a.group = 16;
+  return with_width<T>(a, [&](auto w) { return run<KIND, T, decltype(w)::value>(ta, tb, a, stream); });
+}
+
 }  // namespace
 
 int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_dtype, void *C,
                 int64_t M, int64_t N, int64_t K, cudaStream_t stream) {
-  CUtensorMap ta, tb;
-  if (!make_tmap(&ta, A.data, M, K, kBM) || !make_tmap(&tb, B.data, N, K, kBN))
-    return FP8Q_ERR_CUDA;
   Args a{};
   a.M = M;
   a.N = N;
@@ -296,9 +598,7 @@ int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_
   a.num_k_blocks = (int)((K + kBK - 1) / kBK);
   a.num_steps = (int)((K + 63) / 64);
   a.atoms_k = (int)num_atoms_k(kind, K);
-  a.group = 16;
   a.along_n = 0;
-  a.idesc = idesc_fp4(kind, kBM, kBN);
   a.C = C;
   a.sfa = A.scales;
   a.sfb = B.scales;
@@ -306,15 +606,19 @@ int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_
   a.gb = B.global_scale;
   a.err = device_error_word();
   if (a.err == nullptr) return FP8Q_ERR_CUDA;
-  if ((int64_t)a.num_m_tiles * a.num_n_tiles > INT32_MAX / 2) return FP8Q_ERR_INVALID_ARG;
+  // coordinates of tiles and scale atoms are 32-bit
+  if ((M + 255) / 128 * ((N + 511) / 128) > INT32_MAX || K > INT32_MAX ||
+      (std::max(M, N) + 255) / 128 * a.atoms_k > INT32_MAX)
+    return FP8Q_ERR_INVALID_ARG;
   if (log_enabled())
-    fprintf(stderr, "[fp8q] launch fp4 gemm_kernel %lldx%lldx%lld kind %d out %d\n", (long long)M,
+    fprintf(stderr, "[fp8q] launch fp4 gemm %lldx%lldx%lld kind %d out %d\n", (long long)M,
             (long long)N, (long long)K, kind, out_dtype);
   if (kind == FP4Q_MXFP4)
-    return out_dtype == FP8Q_DT_BF16 ? run_vec<FP4Q_MXFP4, __nv_bfloat16>(ta, tb, a, stream)
-                                     : run_vec<FP4Q_MXFP4, float>(ta, tb, a, stream);
-  return out_dtype == FP8Q_DT_BF16 ? run_vec<FP4Q_NVFP4, __nv_bfloat16>(ta, tb, a, stream)
-                                   : run_vec<FP4Q_NVFP4, float>(ta, tb, a, stream);
+    return out_dtype == FP8Q_DT_BF16
+               ? launch_typed<FP4Q_MXFP4, __nv_bfloat16>(A, B, a, K, stream)
+               : launch_typed<FP4Q_MXFP4, float>(A, B, a, K, stream);
+  return out_dtype == FP8Q_DT_BF16 ? launch_typed<FP4Q_NVFP4, __nv_bfloat16>(A, B, a, K, stream)
+                                   : launch_typed<FP4Q_NVFP4, float>(A, B, a, K, stream);
 }
 
 }  // namespace fp4
