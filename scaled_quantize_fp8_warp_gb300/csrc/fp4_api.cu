@@ -222,6 +222,15 @@ int fp4_linear(const void *x, int in_dtype, int64_t ldx, const fp4q_operand *w, 
   q.data = ws.take(data_bytes(M, K));
   q.scales = ws.take(fp4q_scale_bytes(w->kind, M, K));
   q.global_scale = w->kind == FP4Q_NVFP4 ? words + 1 : nullptr;
+  if (M <= fp4::kSplitQuantizeMax && K > 0) {   // the product quantises x itself
+    if (w->kind == FP4Q_NVFP4 && x_amax == nullptr) {
+      if (fp4::launch_amax_ld(x, in_dtype, M, K, ldx, words, stream) != cudaSuccess)
+        return FP8Q_ERR_CUDA;
+      x_amax = words;
+    }
+    return fp4::launch_split(w->kind, x, in_dtype, ldx, x_amax, nullptr, *w, out_dtype, y, M, N, K,
+                             stream);
+  }
   rc = quantize_into(x, in_dtype, M, K, ldx, w->kind, x_amax, words, &q, nullptr, words + 1,
                      stream);
   if (rc != FP8Q_OK) return rc;

@@ -4,10 +4,16 @@
 // whole K range accumulates in fp32 in tensor memory, and the epilogue
 // multiplies by the tensor scales (NVFP4), converts and stores.
 //
-// A ring stage holds 256 elements of K (128 bytes a row, 128-byte swizzle):
-// 128 rows of A, 256 of B, and the scale atoms of both (one 512-byte atom per
-// 128 rows and 128 (MXFP4) or 64 (NVFP4) of K).  Tensor memory: the
-// accumulator in columns [0, 256), then one slot of scales per ring stage.
+// CTA pairs (tcgen05.mma.cta_group::2) compute 256 x 256 tiles, each CTA
+// staging its own 128 rows of A and half of B's rows per 256 elements of K
+// (128 bytes a row, 128-byte swizzle): 32 KB a stage and CTA.  (On one SM a
+// 128 x 256 tile would bring 48 KB for the same MMAs.)  Each CTA loads the
+// scale atoms of its own rows of A and of all 256 rows of B, by tensor maps in
+// which an atom is a row of 128 words; the even CTA's copies put both CTAs'
+// into tensor memory.  Tensor memory: the accumulator in columns [0, 256),
+// then a slot of scales per ring stage, which leaves no room for a second
+// accumulator: the epilogue's eight warps take it into registers at once and
+// release it before they convert and store.
 #include <cuda.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -27,46 +33,26 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kBM = 128, kBN = 256;
 constexpr int kBKBytes = 128;          // bytes of K per stage
 constexpr int kBK = 256;               // elements of K per stage
-constexpr int kStages = 4;
 
 struct Args {
   int64_t M, N;
   int num_m_tiles, num_n_tiles, num_k_blocks;
   int num_steps;            // MMAs of 64 K over all of K
   int atoms_k;              // scale atoms along K
-  int group, along_n;       // raster
+  int group;                // raster: tile rows visited together
   uint32_t idesc;
   void *C;
-  const uint8_t *sfa, *sfb;
   const float *ga, *gb;     // NVFP4 tensor scales
   unsigned int *err;
-};
-
-template <int KIND>
-struct Layout {
-  static constexpr int kAtoms = kBK / Kind<KIND>::kAtomK;     // per stage and 128 rows: 2 or 4
-  static constexpr int kABytes = kBM * kBKBytes, kBBytes = kBN * kBKBytes;
-  static constexpr int kSfaOff = kABytes + kBBytes;
-  static constexpr int kSfbOff = kSfaOff + kAtoms * 512;       // B's two row blocks, one after the other
-  static constexpr int kStageBytes = (kSfbOff + 2 * kAtoms * 512 + 1023) / 1024 * 1024;
-  static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kBarBytes = 8 * (2 * kStages + 3);
-  static constexpr int kSmemBytes = kRingBytes + kBarBytes + 16 + 1024;
-  static constexpr uint32_t kSfCol0 = kBN;
-  static constexpr uint32_t kSfCols = 12 * kAtoms;             // A: 4 columns an atom, B: 8
-  static constexpr uint32_t kTmemCols = 512;
-  static_assert(kSfCol0 + kSfCols * kStages <= kTmemCols, "scale slots fit in TMEM");
-  static_assert(kSmemBytes <= 227 * 1024, "the ring fits in shared memory");
 };
 
 // One K block in the ring slot at `sa` (A, B, A's atoms, B's atoms of its two
 // row blocks), by one elected thread: scales into tensor memory at sf, then up
 // to four MMAs of 64 K.  The last block may hold fewer steps: K past the
 // matrix would multiply zeros with scales that were not loaded.
-template <int KIND, bool PAIR>
+template <int KIND>
 __device__ __forceinline__ void issue_block(uint32_t sa, uint32_t b_off, uint32_t sfa_off,
                                             uint32_t d_tmem, uint32_t sf, uint32_t idesc,
                                             int steps, bool first) {
@@ -76,15 +62,9 @@ __device__ __forceinline__ void issue_block(uint32_t sa, uint32_t b_off, uint32_
 #pragma unroll
   for (int a = 0; a < kAtoms; ++a) {
     const uint64_t a0 = atom + 32 * a, b0 = atom + 32 * (kAtoms + a), b1 = atom + 32 * (2 * kAtoms + a);
-    if (PAIR) {
-      tmem_cp_32x128b_x4_pair(sfa + 4 * a, a0);
-      tmem_cp_32x128b_x4_pair(sfb + 8 * a, b0);
-      tmem_cp_32x128b_x4_pair(sfb + 8 * a + 4, b1);
-    } else {
-      tmem_cp_32x128b_x4(sfa + 4 * a, a0);
-      tmem_cp_32x128b_x4(sfb + 8 * a, b0);
-      tmem_cp_32x128b_x4(sfb + 8 * a + 4, b1);
-    }
+    tmem_cp_32x128b_x4_pair(sfa + 4 * a, a0);
+    tmem_cp_32x128b_x4_pair(sfb + 8 * a, b0);
+    tmem_cp_32x128b_x4_pair(sfb + 8 * a + 4, b1);
   }
   const uint64_t ad = sdesc_k(sa, gemm::kSwzSBO, gemm::kSwzMode);
   const uint64_t bd = sdesc_k(sa + b_off, gemm::kSwzSBO, gemm::kSwzMode);
@@ -95,10 +75,7 @@ __device__ __forceinline__ void issue_block(uint32_t sa, uint32_t b_off, uint32_
       const uint32_t half = KIND == FP4Q_MXFP4 ? 2u * (k & 1) : 0u;   // of the scale word
       const uint32_t id = idesc | (half << 29) | (half << 4);
       const uint32_t acc = (!first || k > 0) ? 1u : 0u;
-      if (PAIR)
-        mma_fp4_pair<KIND>(d_tmem, ad + 2 * k, bd + 2 * k, id, sfa + 4 * a, sfb + 8 * a, acc);
-      else
-        mma_fp4<KIND>(d_tmem, ad + 2 * k, bd + 2 * k, id, sfa + 4 * a, sfb + 8 * a, acc);
+      mma_fp4_pair<KIND>(d_tmem, ad + 2 * k, bd + 2 * k, id, sfa + 4 * a, sfb + 8 * a, acc);
     }
   }
 }
@@ -132,168 +109,6 @@ __device__ __forceinline__ void store32(T *C, int64_t N, int64_t m, int64_t n0,
   }
 }
 
-template <int KIND, typename T, int WIDTH>
-__global__ void __launch_bounds__(320, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                const Args p) {
-  using L = Layout<KIND>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t ring = (raw + 1023u) & ~1023u;
-  const uint32_t bars = ring + L::kRingBytes;
-  const uint32_t full0 = bars, empty0 = bars + 8 * kStages;
-  const uint32_t accf = bars + 8 * (2 * kStages), acce = accf + 8, drain = acce + 8;
-  const uint32_t slot = bars + L::kBarBytes;
-  uint8_t *slot_ptr = smem_raw + (slot - raw);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(slot_ptr + 4);
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0 && lane == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, 1);
-    }
-    mbar_init(accf, 1);
-    mbar_init(acce, 8);
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-    fence_proxy_async_smem();
-    prefetch_tmap(&ta);
-    prefetch_tmap(&tb);
-  }
-  if (warp == 1) {
-    tmem_alloc(slot, L::kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(slot_ptr);
-  const int total = p.num_m_tiles * p.num_n_tiles;
-  const int num_nb = (int)((p.N + 127) / 128);   // 128-row blocks of B
-
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        int mt, nt;
-        gemm::tile_coords(u, p.num_m_tiles, p.num_n_tiles, mt, nt, p.group, p.along_n);
-        const int nbv = min(2, num_nb - 2 * nt);   // B's row blocks inside the matrix
-        for (int kb = 0; kb < p.num_k_blocks; ++kb, ++it) {
-          const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
-          const uint32_t full = full0 + 8 * s;
-          if (!wait_bounded(empty0 + 8 * s, ph ^ 1u, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = ring + s * L::kStageBytes;
-          const int ka = kb * L::kAtoms;
-          const uint32_t bytes = 512u * (uint32_t)min(L::kAtoms, p.atoms_k - ka);
-          mbar_arrive_expect_tx(full, L::kABytes + L::kBBytes + bytes * (1u + (uint32_t)nbv));
-          tma_load_2d(sa, &ta, kb * kBKBytes, mt * kBM, full);
-          tma_load_2d(sa + L::kABytes, &tb, kb * kBKBytes, nt * kBN, full);
-          bulk_load(sa + L::kSfaOff, p.sfa + ((int64_t)mt * p.atoms_k + ka) * 512, bytes, full);
-          for (int h = 0; h < nbv; ++h)
-            bulk_load(sa + L::kSfbOff + h * L::kAtoms * 512,
-                      p.sfb + ((int64_t)(2 * nt + h) * p.atoms_k + ka) * 512, bytes, full);
-        }
-      }
-      if (!ok) {
-        // Let the copies already issued land before the CTA goes away.
-        const uint32_t n = it < (uint32_t)kStages ? it : (uint32_t)kStages;
-        for (uint32_t j = 0; j < n; ++j) {
-          const uint32_t jj = it - 1 - j;
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(full0 + 8 * (jj % kStages), (jj / kStages) & 1u) &&
-                 globaltimer_ns() - t0 < 200000000ull) {
-          }
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    uint32_t it = 0, acc_it = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++acc_it) {
-      if (!wait_bounded_all(acce, (acc_it & 1u) ^ 1u, abort_flag, p.err)) break;
-      tc_fence_after();
-      for (int kb = 0; kb < p.num_k_blocks; ++kb, ++it) {
-        const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
-        if (!wait_bounded_all(full0 + 8 * s, ph, abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          issue_block<KIND, false>(ring + s * L::kStageBytes, L::kABytes, L::kSfaOff, tmem_base,
-                                   tmem_base + L::kSfCol0 + L::kSfCols * s, p.idesc,
-                                   p.num_steps - 4 * kb, kb == 0);
-          mma_commit(empty0 + 8 * s);
-          if (kb == p.num_k_blocks - 1) mma_commit(accf);
-        }
-        __syncwarp();
-      }
-    }
-    if (elect_one()) gemm::drain_mma(drain, abort_flag);
-    __syncwarp();
-  } else {
-    // Warps 2..9: warp w drains TMEM lane quarter w % 4, columns
-    // [128 h, 128 h + 128) with h = (w - 2) / 4.
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const float g = KIND == FP4Q_NVFP4 ? __fmul_rn(*p.ga, *p.gb) : 1.0f;
-    uint32_t acc_it = 0;
-    for (int u = blockIdx.x; u < total; u += gridDim.x, ++acc_it) {
-      int mt, nt;
-      gemm::tile_coords(u, p.num_m_tiles, p.num_n_tiles, mt, nt, p.group, p.along_n);
-      if (!wait_bounded_warp(accf, acc_it & 1u, abort_flag, p.err)) break;
-      tc_fence_after();
-      uint32_t r[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 128 + c * 32,
-                           r[c]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acce);   // the accumulator is free for the next tile
-      const int64_t m = (int64_t)mt * kBM + quarter * 32 + lane;
-      if (m < p.M) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int64_t n0 = (int64_t)nt * kBN + half * 128 + c * 32;
-          if (n0 < p.N) {
-            float v[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = KIND == FP4Q_NVFP4 ? __fmul_rn(__uint_as_float(r[c][j]), g)
-                                        : __uint_as_float(r[c][j]);
-            store32<T, WIDTH>(static_cast<T *>(p.C), p.N, m, n0, v);
-          }
-        }
-      }
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, L::kTmemCols);
-}
-
-// ------------------------------------------------------------------------
-// The same on CTA pairs (tcgen05.mma.cta_group::2): 256 x 256 tiles, each CTA
-// staging its own 128 rows of A and half of B's rows, so that a stage brings
-// 32 KB for twice the work of the 48 KB above.  On one SM a 128 x 256 tile
-// moves 24 KB through shared memory (fill and operand reads) for each MMA of
-// 128 cycles, above its 128 bytes a cycle; the pair moves 16 KB.  Scales: each
-// CTA loads the atoms of its own 128 rows of A and of all 256 rows of B (by
-// tensor map: an atom is a row of 128 words), and the even CTA's copies put
-// both CTAs' into tensor memory.  A slot of scales per ring stage leaves room
-// for one accumulator: the epilogue's eight warps take it into registers at
-// once and release it before they convert and store.
-// ------------------------------------------------------------------------
 template <int KIND>
 struct PairLayout {
   static constexpr int kStages = KIND == FP4Q_MXFP4 ? 6 : 5;
@@ -376,7 +191,7 @@ __global__ void __launch_bounds__(320, 1)
       bool ok = true;
       for (int u = unit0; u < total && ok; u += unit_step) {
         int mu, nt;
-        gemm::tile_coords(u, num_mu, p.num_n_tiles, mu, nt, p.group, p.along_n);
+        gemm::tile_coords(u, num_mu, p.num_n_tiles, mu, nt, p.group, 0);
         // past the last M tile (odd count): re-read that tile's A, store nothing
         const int mt = min(2 * mu + (int)rank, p.num_m_tiles - 1);
         for (int kb = 0; kb < p.num_k_blocks; ++kb, ++it) {
@@ -427,7 +242,7 @@ __global__ void __launch_bounds__(320, 1)
         }
         tc_fence_after();
         if (elect_one()) {
-          issue_block<KIND, true>(ring + s * L::kStageBytes, L::kABytes, L::kSfaOff, tmem_base,
+          issue_block<KIND>(ring + s * L::kStageBytes, L::kABytes, L::kSfaOff, tmem_base,
                                   tmem_base + L::kSfCol0 + L::kSfCols * s, p.idesc,
                                   p.num_steps - 4 * kb, kb == 0);
           mma_commit_pair_multicast(empty0 + 8 * s, kBoth);
@@ -453,7 +268,7 @@ __global__ void __launch_bounds__(320, 1)
     uint32_t acc_it = 0;
     for (int u = unit0; u < total; u += unit_step, ++acc_it) {
       int mu, nt;
-      gemm::tile_coords(u, num_mu, p.num_n_tiles, mu, nt, p.group, p.along_n);
+      gemm::tile_coords(u, num_mu, p.num_n_tiles, mu, nt, p.group, 0);
       if (!wait_bounded_warp(accf, acc_it & 1u, abort_flag, p.err)) break;
       tc_fence_after();
       uint32_t r[4][32];
@@ -496,20 +311,6 @@ __global__ void __launch_bounds__(320, 1)
 }
 
 template <int KIND, typename T, int WIDTH>
-int run(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t stream) {
-  auto kernel = gemm_kernel<KIND, T, WIDTH>;
-  static PerDeviceOnce setup;  // per instantiation
-  if (setup.get([&] {
-        return gemm::set_smem(kernel, Layout<KIND>::kSmemBytes) == cudaSuccess ? 1 : 0;
-      }) != 1)
-    return FP8Q_ERR_CUDA;
-  const int64_t tiles = (int64_t)a.num_m_tiles * a.num_n_tiles;
-  kernel<<<(int)std::min<int64_t>(tiles, sm_count()), 320, Layout<KIND>::kSmemBytes, stream>>>(
-      ta, tb, a);
-  return cudaGetLastError() == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
-}
-
-template <int KIND, typename T, int WIDTH>
 int run_pair(const PairMaps &maps, const Args &a, cudaStream_t stream) {
   using L = PairLayout<KIND>;
   auto kernel = gemm_pair_kernel<KIND, T, WIDTH>;
@@ -538,21 +339,6 @@ int run_pair(const PairMaps &maps, const Args &a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, maps, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
 }
 
-bool make_tmap(CUtensorMap *m, const void *base, int64_t rows, int64_t K, uint32_t box_rows) {
-  const uint64_t bytes = (uint64_t)row_bytes(K);
-  return make_tmap_2d(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, bytes, (uint64_t)rows, bytes,
-                      kBKBytes, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-// A scale array as rows of one atom (128 words); the box is the atoms of one
-// stage.
-bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_t atoms_k,
-                     uint32_t box) {
-  return make_tmap_2d(m, scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 128,
-                      (uint64_t)((rows + 127) / 128 * atoms_k), 512, 128, box,
-                      CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
 // Calls f(width) with the widest store that every row of C allows, as a
 // compile-time constant.
 template <typename T, typename F>
@@ -565,43 +351,47 @@ int with_width(const Args &a, F &&f) {
 }
 
 template <int KIND, typename T>
-int launch_typed(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K,
-                 cudaStream_t stream) {
-  if (a.M > 128) {
-    PairMaps maps;
-    constexpr int kAtoms = PairLayout<KIND>::kAtoms;
-    if (!make_tmap(&maps.a, A.data, a.M, K, 128) || !make_tmap(&maps.b, B.data, a.N, K, 128) ||
-        !make_scale_tmap(&maps.sfa, A.scales, a.M, a.atoms_k, kAtoms) ||
-        !make_scale_tmap(&maps.sfb, B.scales, a.N, a.atoms_k, kAtoms))
-      return FP8Q_ERR_CUDA;
-    a.idesc = idesc_fp4(KIND, 256, 256);
-    a.group = 8;
-    return with_width<T>(a, [&](auto w) { return run_pair<KIND, T, decltype(w)::value>(maps, a, stream); });
-  }
-  CUtensorMap ta, tb;
-  if (!make_tmap(&ta, A.data, a.M, K, kBM) || !make_tmap(&tb, B.data, a.N, K, kBN))
+int launch_pair(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K,
+                cudaStream_t stream) {
+  PairMaps maps;
+  constexpr int kAtoms = PairLayout<KIND>::kAtoms;
+  if (!make_tmap(&maps.a, A.data, a.M, K, 128) || !make_tmap(&maps.b, B.data, a.N, K, 128) ||
+      !make_scale_tmap(&maps.sfa, A.scales, a.M, a.atoms_k, kAtoms) ||
+      !make_scale_tmap(&maps.sfb, B.scales, a.N, a.atoms_k, kAtoms))
     return FP8Q_ERR_CUDA;
-  a.idesc = idesc_fp4(KIND, kBM, kBN);
-  a.group = 16;
-  return with_width<T>(a, [&](auto w) { return run<KIND, T, decltype(w)::value>(ta, tb, a, stream); });
+  return with_width<T>(a, [&](auto w) { return run_pair<KIND, T, decltype(w)::value>(maps, a, stream); });
 }
 
 }  // namespace
 
+bool make_tmap(CUtensorMap *m, const void *base, int64_t rows, int64_t K, uint32_t box_rows) {
+  const uint64_t bytes = (uint64_t)row_bytes(K);
+  return make_tmap_2d(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, bytes, (uint64_t)rows, bytes,
+                      kBKBytes, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_t atoms_k,
+                     uint32_t box) {
+  return make_tmap_2d(m, scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 128,
+                      (uint64_t)((rows + 127) / 128 * atoms_k), 512, 128, box,
+                      CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_dtype, void *C,
                 int64_t M, int64_t N, int64_t K, cudaStream_t stream) {
+  if (M <= 128)
+    return launch_split(kind, nullptr, FP8Q_DT_BF16, 0, nullptr, &A, B, out_dtype, C, M, N, K, stream);
   Args a{};
   a.M = M;
   a.N = N;
-  a.num_m_tiles = (int)((M + kBM - 1) / kBM);
-  a.num_n_tiles = (int)((N + kBN - 1) / kBN);
+  a.num_m_tiles = (int)((M + 127) / 128);
+  a.num_n_tiles = (int)((N + 255) / 256);
   a.num_k_blocks = (int)((K + kBK - 1) / kBK);
   a.num_steps = (int)((K + 63) / 64);
   a.atoms_k = (int)num_atoms_k(kind, K);
-  a.along_n = 0;
+  a.group = 8;
+  a.idesc = idesc_fp4(kind, 256, 256);
   a.C = C;
-  a.sfa = A.scales;
-  a.sfb = B.scales;
   a.ga = A.global_scale;
   a.gb = B.global_scale;
   a.err = device_error_word();
@@ -611,14 +401,14 @@ int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_
       (std::max(M, N) + 255) / 128 * a.atoms_k > INT32_MAX)
     return FP8Q_ERR_INVALID_ARG;
   if (log_enabled())
-    fprintf(stderr, "[fp8q] launch fp4 gemm %lldx%lldx%lld kind %d out %d\n", (long long)M,
+    fprintf(stderr, "[fp8q] launch fp4 gemm_pair_kernel %lldx%lldx%lld kind %d out %d\n", (long long)M,
             (long long)N, (long long)K, kind, out_dtype);
   if (kind == FP4Q_MXFP4)
     return out_dtype == FP8Q_DT_BF16
-               ? launch_typed<FP4Q_MXFP4, __nv_bfloat16>(A, B, a, K, stream)
-               : launch_typed<FP4Q_MXFP4, float>(A, B, a, K, stream);
-  return out_dtype == FP8Q_DT_BF16 ? launch_typed<FP4Q_NVFP4, __nv_bfloat16>(A, B, a, K, stream)
-                                   : launch_typed<FP4Q_NVFP4, float>(A, B, a, K, stream);
+               ? launch_pair<FP4Q_MXFP4, __nv_bfloat16>(A, B, a, K, stream)
+               : launch_pair<FP4Q_MXFP4, float>(A, B, a, K, stream);
+  return out_dtype == FP8Q_DT_BF16 ? launch_pair<FP4Q_NVFP4, __nv_bfloat16>(A, B, a, K, stream)
+                                   : launch_pair<FP4Q_NVFP4, float>(A, B, a, K, stream);
 }
 
 }  // namespace fp4

@@ -24,6 +24,21 @@ cudaError_t launch_amax_ld(const void *x, int in_dtype, int64_t rows, int64_t co
 cudaError_t launch_dequantize(int kind, const fp4q_operand &op, int64_t rows, int64_t K,
                               int out_dtype, void *y, cudaStream_t stream);
 
+// Tensor maps of an operand's codes (box: 128 bytes of K x box_rows, 128-byte
+// swizzle) and of its scale atoms as rows of 128 words (box: that many atoms).
+bool make_tmap(CUtensorMap *m, const void *base, int64_t rows, int64_t K, uint32_t box_rows);
+bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_t atoms_k,
+                     uint32_t box);
+
+// y[M,N] = x . w^T on tiles of 128 rows of w by up to 128 rows of x, K split
+// over the CTAs of a cluster.  x is either the 4-bit operand `q` or, with q
+// null, a bf16 / fp32 matrix that the kernel quantises as it goes (M at most
+// kSplitQuantizeMax; x_amax: NVFP4's amax).
+constexpr int64_t kSplitQuantizeMax = 16;
+int launch_split(int kind, const void *x, int in_dtype, int64_t ldx, const float *x_amax,
+                 const fp4q_operand *q, const fp4q_operand &w, int out_dtype, void *y, int64_t M,
+                 int64_t N, int64_t K, cudaStream_t stream);
+
 // C[M,N] = A . B^T for non-empty sizes; a FP8Q status.
 int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_dtype, void *C,
                 int64_t M, int64_t N, int64_t K, cudaStream_t stream);

@@ -1,0 +1,416 @@
+// The 4-bit product for few rows: y[M, N] = x . w^T where reading w once is
+// the work (M = 1: two operations per code read) or where 256 x 256 tiles
+// would leave most SMs idle.
+//
+// The operands change places: 128 rows of w are the MMA's M, up to 128 rows of
+// x its N, so that one row of x costs an MMA of N = 16 and not of 128.  The K
+// range of a tile is split over the CTAs of a cluster, which stream their
+// parts of w at once; their partial sums meet in distributed shared memory and
+// are added in the order of the ranks, so results do not depend on timing.
+// For a few rows of x in bf16 or fp32 the kernel quantises them itself, each
+// CTA its own K range, while its part of w is on the way: one launch in all.
+//
+// Roles: warp 0 loads (TMA), warp 1 issues the MMAs, warps 2-9 quantise x and
+// then add, scale and store.  Two CTAs share an SM: 256 of the 512 columns of
+// tensor memory each.  (No third one fits their 112 KB of shared memory, nor any
+// other kernel of this library that allocates tensor memory: an allocation
+// never waits for a CTA that waits for this one's cluster.)
+#include <cuda.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "fp4_common.cuh"
+#include "fp4_internal.h"
+#include "fp4_ptx.cuh"
+#include "fp8_pack8.cuh"
+#include "fp8q_gemm_common.cuh"
+
+namespace fp8q {
+namespace fp4 {
+namespace {
+
+using namespace ptx;
+using pack8::Pack8;
+
+constexpr int kThreads = 320;
+constexpr int kQuantWarps = 8;
+constexpr int kBKBytes = 128, kBK = 256;    // K per stage
+constexpr int kMaxStages = 8;
+constexpr int kMaxRows = 128;               // rows of x per tile
+constexpr uint32_t kTmemCols = 256;
+constexpr int kSmemBytes = 112 * 1024;      // two CTAs on an SM, never three
+constexpr int kFixedBytes = 1024 /* alignment */ + 8 * (2 * kMaxStages + 2) + 16 + 1024 /* table */;
+
+struct Args {
+  int64_t M, N, K, ldx;
+  const void *x;
+  const float *x_amax;       // quantising NVFP4
+  const float *gx, *gw;      // NVFP4 tensor scales (gx: of a quantised x)
+  void *y;
+  int nb;                    // rows of x per tile: 16, 32, 64 or 128
+  int m_tiles, split, stages, stage_bytes;
+  int num_k_blocks, num_steps, atoms_k;
+  int vec, out_bf16;
+  uint32_t idesc;
+  unsigned int *err;
+};
+
+struct Maps {
+  CUtensorMap w, sfw, x, sfx;
+};
+
+// XT: the type of x to quantise, or void for a quantised x.
+template <int KIND, typename XT>
+__global__ void __launch_bounds__(kThreads, 2)
+    split_kernel(const __grid_constant__ Maps maps, const Args p) {
+  constexpr int kAtoms = kBK / Kind<KIND>::kAtomK;
+  constexpr bool kQuantize = !std::is_same<XT, void>::value;
+  constexpr int kSfaOff = 128 * kBKBytes, kSfbOff = kSfaOff + kAtoms * 512;
+  constexpr int kXOff = (kSfbOff + kAtoms * 512 + 1023) / 1024 * 1024;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;
+  uint8_t *ring_ptr = smem_raw + (ring - raw);
+  const uint32_t bars = ring + p.stages * p.stage_bytes;
+  const uint32_t full0 = bars, empty0 = bars + 8 * kMaxStages;
+  const uint32_t accf = bars + 8 * (2 * kMaxStages), drain = accf + 8;
+  uint8_t *slot_ptr = smem_raw + (drain + 8 - raw);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(slot_ptr + 4);
+  ScaleTable &table = *reinterpret_cast<ScaleTable *>(slot_ptr + 16);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = p.split > 1 ? cluster_ctarank() : 0u;
+  const int tile = blockIdx.x / p.split;
+  const int nt = tile / p.m_tiles, mt = tile - nt * p.m_tiles;
+  const int rows = (int)min((int64_t)p.nb, p.M - (int64_t)mt * p.nb);   // of x in this tile
+  // K blocks of this CTA
+  const int kb0 = (int)((int64_t)p.num_k_blocks * rank / p.split);
+  const int kb1 = (int)((int64_t)p.num_k_blocks * (rank + 1) / p.split);
+  const uint32_t sf_col0 = max(32, p.nb);
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full0 + 8 * s, kQuantize ? 1 + rows : 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(accf, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    prefetch_tmap(&maps.w);
+    prefetch_tmap(&maps.sfw);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(slot_ptr), kTmemCols);
+    tmem_relinquish();
+  }
+  float g = 1.0f, rg = 1.0f;
+  if (kQuantize && KIND == FP4Q_NVFP4) {
+    g = nv_global(*p.x_amax);
+    rg = __frcp_rn(g);
+    table.fill(g);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(slot_ptr);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      int it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int s = it % p.stages, ph = (it / p.stages) & 1;
+        const uint32_t full = full0 + 8 * s;
+        if (!wait_bounded(empty0 + 8 * s, ph ^ 1u, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = ring + s * p.stage_bytes;
+        const int ka = kb * kAtoms;
+        mbar_arrive_expect_tx(full, 128 * kBKBytes + kAtoms * 512 +
+                                        (kQuantize ? 0 : p.nb * kBKBytes + kAtoms * 512));
+        tma_load_2d(sa, &maps.w, kb * kBKBytes, nt * 128, full);
+        // Atoms past the last of a row block are the next block's or zeros;
+        // no MMA step reads them.
+        tma_load_2d(sa + kSfaOff, &maps.sfw, 0, nt * p.atoms_k + ka, full);
+        if (!kQuantize) {
+          // more than one tile of rows only where a tile has 128
+          tma_load_2d(sa + kXOff, &maps.x, kb * kBKBytes, mt * p.nb, full);
+          tma_load_2d(sa + kSfbOff, &maps.sfx, 0, mt * p.atoms_k + ka, full);
+        }
+      }
+      if (!ok) {
+        // Let the copies already issued land before the CTA goes away.
+        for (int j = 0; j < min(it, p.stages); ++j) {
+          const int jj = it - 1 - j;
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(full0 + 8 * (jj % p.stages), (jj / p.stages) & 1) &&
+                 globaltimer_ns() - t0 < 200000000ull) {
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    bool ok = true;
+    int it = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      const int s = it % p.stages, ph = (it / p.stages) & 1;
+      if (!wait_bounded_all(full0 + 8 * s, ph, abort_flag, p.err)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t sa = ring + s * p.stage_bytes;
+        const uint32_t sfa = tmem_base + sf_col0 + 8u * kAtoms * s, sfb = sfa + 4 * kAtoms;
+        const uint64_t atom = sdesc_plain(sa + kSfaOff, 128);
+#pragma unroll
+        for (int a = 0; a < kAtoms; ++a) {
+          tmem_cp_32x128b_x4(sfa + 4 * a, atom + 32 * a);
+          tmem_cp_32x128b_x4(sfb + 4 * a, atom + 32 * (kAtoms + a));
+        }
+        const uint64_t ad = sdesc_k(sa, gemm::kSwzSBO, gemm::kSwzMode);
+        const uint64_t bd = sdesc_k(sa + kXOff, gemm::kSwzSBO, gemm::kSwzMode);
+        const int steps = p.num_steps - 4 * kb;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k < steps) {
+            const int a = KIND == FP4Q_MXFP4 ? k >> 1 : k;
+            const uint32_t half = KIND == FP4Q_MXFP4 ? 2u * (k & 1) : 0u;
+            mma_fp4<KIND>(tmem_base, ad + 2 * k, bd + 2 * k, p.idesc | (half << 29) | (half << 4),
+                          sfa + 4 * a, sfb + 4 * a, (it > 0 || k > 0) ? 1u : 0u);
+          }
+        }
+        mma_commit(empty0 + 8 * s);
+        if (kb == kb1 - 1) mma_commit(accf);
+      }
+      __syncwarp();
+    }
+    if (!ok && elect_one()) gemm::drain_mma(drain, abort_flag);
+    __syncwarp();
+  } else if constexpr (kQuantize) {
+    // One task is 256 elements of one row: 8 to a lane, blocks in 4 (MXFP4) or
+    // 2 neighbouring lanes.  Tasks run K block after K block.
+    constexpr int kLanes = Kind<KIND>::kBlock / 8;
+    constexpr int kBatch = 4;     // tasks whose loads are in flight together
+    const int tasks = rows * (kb1 - kb0);
+    const XT *x = static_cast<const XT *>(p.x) + (int64_t)mt * p.nb * p.ldx;
+    const bool g_bad = !(g < __uint_as_float(0x7F800000u));
+    bool ok = true;
+    for (int t0 = warp - 2; t0 < tasks && ok; t0 += kBatch * kQuantWarps) {
+      Pack8<XT> y[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int t = t0 + i * kQuantWarps;
+        const int kbl = t / rows, row = t - kbl * rows;
+        const int64_t k = (int64_t)(kb0 + kbl) * kBK + lane * 8;
+        const int valid = t < tasks ? (int)max((int64_t)0, min((int64_t)8, p.K - k)) : 0;
+        const XT *at = x + (valid > 0 ? row * p.ldx + k : 0);
+        if (p.vec)
+          pack8::load<true>(y[i], at, valid);
+        else
+          y[i].load_some(at, valid);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int t = t0 + i * kQuantWarps;
+        if (t >= tasks || !ok) break;
+        const int kbl = t / rows, row = t - kbl * rows;
+        const int s = kbl % p.stages, ph = (kbl / p.stages) & 1;
+        uint32_t m = y[i].amax_bits();
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        y[i].negate();
+        uint32_t byte, w;
+        if (!__any_sync(0xFFFFFFFFu, m >= kCarefulBits || g_bad)) {
+          float d = 0.0f, r;
+          if (KIND == FP4Q_MXFP4) {
+            byte = mx_byte(m);
+            r = mx_reciprocal(byte);
+          } else {
+            byte = (uint32_t)__nv_cvt_float_to_fp8(
+                fmaxf(nv_ratio(__uint_as_float(m), g, rg), 0x1p-9f), __NV_SATFINITE, __NV_E4M3);
+            const float2 dr = table.d_r[byte];
+            d = dr.x;
+            r = dr.y;
+          }
+          const float2 v[4] = {y[i].pair(0), y[i].pair(1), y[i].pair(2), y[i].pair(3)};
+          w = encode8<KIND>(v, d, r);
+        } else {
+          w = encode8_careful<KIND>(y[i].pair(0), y[i].pair(1), y[i].pair(2), y[i].pair(3), m, g,
+                                    &byte);
+        }
+        if (!wait_bounded_all(empty0 + 8 * s, ph ^ 1u, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        uint8_t *stage = ring_ptr + s * p.stage_bytes;
+        // the 128-byte swizzle: 16-byte chunk index xor row of the 8-row group
+        *reinterpret_cast<uint32_t *>(stage + kXOff + row * 128 +
+                                      ((((lane >> 2) ^ row) & 7) << 4 | (lane & 3) << 2)) = w;
+        if ((lane & (kLanes - 1)) == 0) {
+          const int block = lane / kLanes;   // of this stage
+          stage[kSfbOff + (block >> 2) * 512 + row * 16 + (block & 3)] = (uint8_t)byte;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full0 + 8 * s);
+      }
+    }
+  }
+
+  // Partial sums [row of x][row of w] in shared memory (the ring is free: its
+  // last MMAs are done), then every rank adds its share of the tile.
+  float *part = reinterpret_cast<float *>(ring_ptr);
+  if (warp >= 2) {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const bool ok = wait_bounded_all(accf, 0, abort_flag, p.err);
+    tc_fence_after();
+    for (int c = 32 * half; c < rows; c += 64) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + c, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (c + j < rows) part[(c + j) * 128 + quarter * 32 + lane] = ok ? __uint_as_float(r[j]) : 0.0f;
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (p.split > 1) cluster_sync_all();
+  {
+    float scale = 1.0f;
+    if (KIND == FP4Q_NVFP4) scale = __fmul_rn(kQuantize ? g : *p.gx, *p.gw);
+    const int total = rows * 128;
+    const int first = total / p.split * (int)rank, last = (int)rank == p.split - 1 ? total : first + total / p.split;
+    const uint32_t part_u32 = smem_u32(part);
+    for (int i = first + (int)threadIdx.x; i < last; i += kThreads) {
+      const int row = i >> 7, n = i & 127;
+      float v;
+      if (p.split == 1) {
+        v = part[i];
+      } else {
+        float t[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < p.split)
+            t[r] = __uint_as_float(ld_shared_cluster_u32(mapa_shared(part_u32 + 4 * i, r)));
+        v = t[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < p.split) v += t[r];
+      }
+      if (KIND == FP4Q_NVFP4) v = __fmul_rn(v, scale);
+      const int64_t col = (int64_t)nt * 128 + n;
+      if (col < p.N) {
+        const int64_t at = ((int64_t)mt * p.nb + row) * p.N + col;
+        if (p.out_bf16)
+          static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v);
+        else
+          static_cast<float *>(p.y)[at] = v;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (p.split > 1) cluster_sync_all();   // no CTA leaves while another may read its sums
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
+}
+
+template <int KIND, typename XT>
+int run_split(const Maps &maps, const Args &a, int64_t tiles, cudaStream_t stream) {
+  auto kernel = split_kernel<KIND, XT>;
+  static PerDeviceOnce setup;  // per instantiation
+  if (setup.get([&] { return gemm::set_smem(kernel, kSmemBytes) == cudaSuccess ? 1 : 0; }) != 1)
+    return FP8Q_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)(tiles * a.split), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_split(int kind, const void *x, int in_dtype, int64_t ldx, const float *x_amax,
+                 const fp4q_operand *q, const fp4q_operand &w, int out_dtype, void *y, int64_t M,
+                 int64_t N, int64_t K, cudaStream_t stream) {
+  Args a{};
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.ldx = ldx;
+  a.x = x;
+  a.x_amax = x_amax;
+  a.gx = q == nullptr ? nullptr : q->global_scale;
+  a.gw = w.global_scale;
+  a.y = y;
+  a.nb = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+  a.num_k_blocks = (int)((K + kBK - 1) / kBK);
+  a.num_steps = (int)((K + 63) / 64);
+  a.atoms_k = (int)num_atoms_k(kind, K);
+  a.out_bf16 = out_dtype == FP8Q_DT_BF16;
+  const int64_t size = in_dtype == FP8Q_DT_BF16 ? 2 : 4;
+  a.vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ldx * size % 16 == 0 && K % 8 == 0;
+  a.err = device_error_word();
+  if (a.err == nullptr) return FP8Q_ERR_CUDA;
+  const int64_t n_tiles = (N + 127) / 128, m_tiles = (M + a.nb - 1) / a.nb;
+  const int64_t tiles = n_tiles * m_tiles;
+  // coordinates of rows, tiles and scale atoms are 32-bit
+  if (tiles > INT32_MAX / 8 || K > INT32_MAX || (std::max(M, N) + 255) / 128 * a.atoms_k > INT32_MAX)
+    return FP8Q_ERR_INVALID_ARG;
+  a.m_tiles = (int)m_tiles;
+  // As many CTAs as run at once, at most one per K block and eight (the
+  // portable cluster size) per tile.
+  a.split = (int)std::max<int64_t>(
+      1, std::min<int64_t>({8, (int64_t)a.num_k_blocks, 2 * sm_count() / tiles}));
+  a.idesc = idesc_fp4(kind, 128, (uint32_t)a.nb);
+  const int atoms = kind == FP4Q_MXFP4 ? 2 : 4;
+  a.stage_bytes = (128 * kBKBytes + 2 * atoms * 512 + 1023) / 1024 * 1024 + a.nb * kBKBytes;
+  a.stages = std::min(kMaxStages, (kSmemBytes - kFixedBytes) / a.stage_bytes);
+  const int sf_cols = 8 * atoms;   // tensor memory of a stage's scales
+  a.stages = std::min<int>(a.stages, ((int)kTmemCols - std::max(32, a.nb)) / sf_cols);
+  Maps maps;
+  if (!make_tmap(&maps.w, w.data, N, K, 128) ||
+      !make_scale_tmap(&maps.sfw, w.scales, N, a.atoms_k, (uint32_t)atoms))
+    return FP8Q_ERR_CUDA;
+  if (q != nullptr) {
+    if (!make_tmap(&maps.x, q->data, M, K, (uint32_t)a.nb) ||
+        !make_scale_tmap(&maps.sfx, q->scales, M, a.atoms_k, (uint32_t)atoms))
+      return FP8Q_ERR_CUDA;
+  } else {
+    maps.x = maps.w;
+    maps.sfx = maps.sfw;
+  }
+  if (log_enabled())
+    fprintf(stderr,
+            "[fp8q] launch fp4 split_kernel %lldx%lldx%lld kind %d rows %d tiles %lld split %d "
+            "stages %d%s\n",
+            (long long)M, (long long)N, (long long)K, kind, a.nb, (long long)tiles, a.split,
+            a.stages, q == nullptr ? " quantising x" : "");
+  if (kind == FP4Q_MXFP4) {
+    if (q != nullptr) return run_split<FP4Q_MXFP4, void>(maps, a, tiles, stream);
+    return in_dtype == FP8Q_DT_BF16 ? run_split<FP4Q_MXFP4, __nv_bfloat16>(maps, a, tiles, stream)
+                                    : run_split<FP4Q_MXFP4, float>(maps, a, tiles, stream);
+  }
+  if (q != nullptr) return run_split<FP4Q_NVFP4, void>(maps, a, tiles, stream);
+  return in_dtype == FP8Q_DT_BF16 ? run_split<FP4Q_NVFP4, __nv_bfloat16>(maps, a, tiles, stream)
+                                  : run_split<FP4Q_NVFP4, float>(maps, a, tiles, stream);
+}
+
+}  // namespace fp4
+}  // namespace fp8q
