@@ -641,8 +641,11 @@ size_t fp4q_linear_workspace_size(int kind, int64_t M, int64_t N, int64_t K);
  * kind as fp4_quantize does and multiplied as fp4_gemm does, in this call.
  *   x_amax     NVFP4: device float, a calibrated amax of x, or NULL: the call
  *              finds max|x| itself.  MXFP4: ignored.
- *   workspace  device, >= fp4q_linear_workspace_size, 256-byte aligned
+ *   workspace  device, >= fp4q_linear_workspace_size, 256-byte aligned.  Up
+ *              to FP4Q_LINEAR_FUSED_ROWS rows are quantised inside the product
+ *              and need none (NULL) unless the call has to find NVFP4's amax.
  * Errors: INVALID_ARG, MISALIGNED, WORKSPACE, ARCH, CUDA. */
+#define FP4Q_LINEAR_FUSED_ROWS 16
 int fp4_linear(const void *x, int in_dtype, int64_t ldx,
                const fp4q_operand *w, int64_t M, int64_t N, int64_t K,
                const float *x_amax, void *y, int out_dtype, void *workspace,

@@ -614,16 +614,37 @@ class _Fp4Struct(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
-def _ptr_rows(t: torch.Tensor):
+def _rows(t: torch.Tensor):
     """(pointer, row stride in elements) of a 2-D matrix whose rows are dense;
     the rows may lie apart (a slice of a wider matrix)."""
     if not t.is_cuda:
         raise ValueError("fp8q needs CUDA tensors")
     rows, cols = _rows_cols(t)
+    if t.is_contiguous():
+        return t.data_ptr(), cols
     ld = t.stride(0) if rows > 1 else max(cols, 1)
     if (cols > 1 and t.stride(1) != 1) or ld < cols:
         raise ValueError("fp8q needs matrices whose rows are dense and do not overlap")
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return t.data_ptr(), ld
+
+
+def _addr(t: torch.Tensor | None):
+    """Pointer of a dense tensor."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("fp8q needs CUDA tensors")
+    if not t.is_contiguous():
+        raise ValueError("fp8q needs contiguous tensors")
+    return t.data_ptr()
+
+
+def _raw_stream(stream=None) -> int:
+    """The CUDA stream's handle.  The raw query of the current one costs a
+    thirtieth of building a Stream object (0.1 against 3 us on a Grace core)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _new(shape, dtype, device, stream):
@@ -637,52 +658,73 @@ def _new(shape, dtype, device, stream):
 
 def _like(t: torch.Tensor, shape, dtype, what: str):
     """Checks a caller's tensor against what a call is about to write or read."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of shape "
                          f"{tuple(t.shape)}")
     return t
 
 
+def _one(t: torch.Tensor, what: str):
+    """Pointer of a one-element fp32 device tensor."""
+    if t.numel() != 1 or t.dtype != torch.float32:
+        raise ValueError(f"{what} is one fp32 value")
+    return _addr(t)
+
+
+def _out(out, shape, dtype, device, stream, what="out"):
+    """(tensor, dtype code) of a result: the caller's, checked, or a new one."""
+    if out is None:
+        return _new(shape, dtype, device, stream), _out_dtype(dtype)
+    return _like(out, shape, out.dtype, what), _out_dtype(out.dtype)
+
+
 def fp4_scale_bytes(kind: int, rows: int, K: int) -> int:
     """Bytes of the scale atoms of an [rows, K] 4-bit operand."""
-    return int(lib().fp4q_scale_bytes(kind, rows, K))
+    return (rows + 127) // 128 * ((K + 127) // 128 if kind == MXFP4 else (K + 63) // 64) * 512
 
 
 class Fp4Operand:
     """A 4-bit operand [rows, K] (MXFP4 or NVFP4): packed codes [rows, 16
     ceil(K/32)] and scale atoms, both uint8 device tensors, and for NVFP4 the
     one-element fp32 tensor scale; see fp4q_operand in include/fp8q.h."""
+    __slots__ = ("data", "scales", "kind", "rows", "K", "global_scale", "struct")
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, kind: int, K: int,
                  global_scale: torch.Tensor | None = None):
         if data.dim() != 2 or data.dtype != torch.uint8 or data.shape[1] != (K + 31) // 32 * 16:
             raise ValueError("4-bit data must be uint8 [rows, 16 ceil(K/32)]")
-        self.rows, self.K, self.kind = data.shape[0], K, kind
-        need = fp4_scale_bytes(kind, self.rows, K)
+        if kind not in (MXFP4, NVFP4):
+            raise ValueError("a 4-bit operand is MXFP4 or NVFP4")
+        rows = data.shape[0]
+        need = fp4_scale_bytes(kind, rows, K)
         if scales.dtype != torch.uint8 or scales.numel() != need:
             raise ValueError(f"4-bit scales must be {need} uint8 values")
         if (kind == NVFP4) != (global_scale is not None):
             raise ValueError("NVFP4 operands, and only they, have a global scale")
-        if global_scale is not None and (global_scale.dtype != torch.float32
-                                         or global_scale.numel() != 1):
-            raise ValueError("a global scale is one fp32 value")
-        self.data, self.scales, self.global_scale = data, scales, global_scale
-        self.struct = _Fp4Struct(_ptr(data), _ptr(scales), _ptr(global_scale), kind, 0)
+        g = None if global_scale is None else _one(global_scale, "a global scale")
+        self._set(data, scales, kind, rows, K, global_scale, g)
+
+    def _set(self, data, scales, kind, rows, K, global_scale, g):
+        self.data, self.scales, self.kind, self.rows, self.K = data, scales, kind, rows, K
+        self.global_scale = global_scale
+        self.struct = _Fp4Struct(_addr(data), _addr(scales), g, kind, 0)
 
     @classmethod
     def empty(cls, kind: int, rows: int, K: int, device, global_scale=None, stream=None):
         """Uninitialised storage for an operand."""
-        data = _new((rows, (K + 31) // 32 * 16), torch.uint8, device, stream)
-        scales = _new((fp4_scale_bytes(kind, rows, K),), torch.uint8, device, stream)
-        return cls(data, scales, kind, K, global_scale)
+        op = cls.__new__(cls)
+        op._set(_new((rows, (K + 31) // 32 * 16), torch.uint8, device, stream),
+                _new((fp4_scale_bytes(kind, rows, K),), torch.uint8, device, stream), kind, rows, K,
+                global_scale, None if global_scale is None else _one(global_scale, "a global scale"))
+        return op
 
 
 def fp4_amax(x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """max |x| of a matrix whose rows may lie apart, as a one-element fp32 tensor."""
-    p, ld = _ptr_rows(x)
+    p, ld = _rows(x)
     out = out if out is not None else _new((1,), torch.float32, x.device, stream)
-    _check(lib().fp4_amax(p, _in_dtype(x), x.shape[0], x.shape[1], ld, _ptr(out),
-                          _stream(stream)), "fp4_amax")
+    _check(lib().fp4_amax(p, _in_dtype(x), x.shape[0], x.shape[1], ld, _one(out, "out"),
+                          _raw_stream(stream)), "fp4_amax")
     return out
 
 
@@ -692,38 +734,38 @@ def fp4_quantize(x: torch.Tensor, kind: int, rows=True, cols=False,
     """x [R, C] (rows may lie apart) -> (operand [R, C] | None, operand [C, R]
     of x^T | None).  NVFP4 takes the tensor's amax from ``amax`` (one fp32
     device value) or finds it first."""
-    p, ld = _ptr_rows(x)
+    p, ld = _rows(x)
     R, C = x.shape
+    if kind not in (MXFP4, NVFP4):
+        raise ValueError("a 4-bit operand is MXFP4 or NVFP4")
     g = None
     if kind == NVFP4:
         amax = amax if amax is not None else fp4_amax(x, stream=stream)
-        _like(amax.reshape(-1), (1,), torch.float32, "amax")
         given = q if q is not None else q_t
-        g = given.global_scale if given is not None else _new((1,), torch.float32, x.device,
-                                                                             stream)
+        g = given.global_scale if given is not None else _new((1,), torch.float32, x.device, stream)
     if rows:
         q = q if q is not None else Fp4Operand.empty(kind, R, C, x.device, g, stream)
+        if (q.kind, q.rows, q.K) != (kind, R, C):
+            raise ValueError(f"an operand of kind, rows, K {(kind, R, C)} is needed")
     if cols:
         q_t = q_t if q_t is not None else Fp4Operand.empty(kind, C, R, x.device, g, stream)
-    for op, shape in ((q if rows else None, (kind, R, C)), (q_t if cols else None, (kind, C, R))):
-        if op is not None and (op.kind, op.rows, op.K) != shape:
-            raise ValueError(f"an operand of kind, rows, K {shape} is needed")
+        if (q_t.kind, q_t.rows, q_t.K) != (kind, C, R):
+            raise ValueError(f"an operand of kind, rows, K {(kind, C, R)} is needed")
     if rows and cols and kind == NVFP4 and q.global_scale.data_ptr() != q_t.global_scale.data_ptr():
         raise ValueError("both orientations share one global scale")
+    a, b = (q.struct if rows else None), (q_t.struct if cols else None)
     _check(lib().fp4_quantize(
-        p, _in_dtype(x), R, C, ld, kind, _ptr(amax) if kind == NVFP4 else None,
-        _ptr(q.data) if rows else None, _ptr(q.scales) if rows else None,
-        _ptr(q_t.data) if cols else None, _ptr(q_t.scales) if cols else None, _ptr(g),
-        _stream(stream)), "fp4_quantize")
+        p, _in_dtype(x), R, C, ld, kind, _one(amax, "amax") if kind == NVFP4 else None,
+        a.data if rows else None, a.scales if rows else None, b.data if cols else None,
+        b.scales if cols else None, _addr(g), _raw_stream(stream)), "fp4_quantize")
     return (q if rows else None), (q_t if cols else None)
 
 
 def fp4_dequantize(op: Fp4Operand, out_dtype=torch.bfloat16, out=None, stream=None):
     """The values [rows, K] an operand stands for."""
-    out = out if out is not None else _new((op.rows, op.K), out_dtype, op.data.device, stream)
-    _like(out, (op.rows, op.K), out.dtype, "out")
-    _check(lib().fp4_dequantize(ctypes.byref(op.struct), op.rows, op.K, _ptr(out),
-                                _out_dtype(out.dtype), _stream(stream)), "fp4_dequantize")
+    out, dt = _out(out, (op.rows, op.K), out_dtype, op.data.device, stream)
+    _check(lib().fp4_dequantize(ctypes.byref(op.struct), op.rows, op.K, _addr(out), dt,
+                                _raw_stream(stream)), "fp4_dequantize")
     return out
 
 
@@ -731,16 +773,18 @@ def fp4_gemm(A: Fp4Operand, B: Fp4Operand, out_dtype=torch.bfloat16, out=None, s
     """C [M, N] = A [M, K] . B [N, K]^T of two operands of one kind."""
     if A.K != B.K:
         raise ValueError(f"operands contract over {A.K} and {B.K}")
-    out = out if out is not None else _new((A.rows, B.rows), out_dtype, A.data.device, stream)
-    _like(out, (A.rows, B.rows), out.dtype, "out")
-    _check(lib().fp4_gemm(ctypes.byref(A.struct), ctypes.byref(B.struct), _ptr(out),
-                          _out_dtype(out.dtype), A.rows, B.rows, A.K, _stream(stream)),
-           "fp4_gemm")
+    out, dt = _out(out, (A.rows, B.rows), out_dtype, A.data.device, stream)
+    _check(lib().fp4_gemm(ctypes.byref(A.struct), ctypes.byref(B.struct), _addr(out), dt, A.rows,
+                          B.rows, A.K, _raw_stream(stream)), "fp4_gemm")
     return out
 
 
 def fp4_linear_workspace_size(kind: int, M: int, N: int, K: int) -> int:
     return int(lib().fp4q_linear_workspace_size(kind, M, N, K))
+
+
+#: most rows of x that fp4_linear quantises inside the product (FP4Q_LINEAR_FUSED_ROWS)
+FP4_LINEAR_FUSED_ROWS = 16
 
 
 def fp4_linear(x: torch.Tensor, w: Fp4Operand, x_amax: torch.Tensor | None = None,
@@ -749,20 +793,19 @@ def fp4_linear(x: torch.Tensor, w: Fp4Operand, x_amax: torch.Tensor | None = Non
     apart) is quantised to w's kind in the call.  ``x_amax``: a calibrated
     amax of x for NVFP4 (one fp32 device value); without it the call finds
     max |x|."""
-    p, ld = _ptr_rows(x)
+    p, ld = _rows(x)
     M, K = x.shape
+    N, kind = w.rows, w.kind
     if K != w.K:
         raise ValueError(f"x has {K} columns, w contracts over {w.K}")
-    if x_amax is not None:
-        _like(x_amax.reshape(-1), (1,), torch.float32, "x_amax")
-    if workspace is None:
-        workspace = _new((max(1, fp4_linear_workspace_size(w.kind, M, w.rows, K)),), torch.uint8,
-                         x.device, stream)
-    out = out if out is not None else _new((M, w.rows), out_dtype, x.device, stream)
-    _like(out, (M, w.rows), out.dtype, "out")
+    if workspace is None and not (M <= FP4_LINEAR_FUSED_ROWS
+                                  and (kind == MXFP4 or x_amax is not None)):
+        workspace = _new((fp4_linear_workspace_size(kind, M, N, K),), torch.uint8, x.device, stream)
+    out, dt = _out(out, (M, N), out_dtype, x.device, stream)
     _check(lib().fp4_linear(
-        p, _in_dtype(x), ld, ctypes.byref(w.struct), M, w.rows, K, _ptr(x_amax), _ptr(out),
-        _out_dtype(out.dtype), _ptr(workspace), workspace.numel(), _stream(stream)), "fp4_linear")
+        p, _in_dtype(x), ld, ctypes.byref(w.struct), M, N, K,
+        None if x_amax is None else _one(x_amax, "x_amax"), _addr(out), dt, _addr(workspace),
+        0 if workspace is None else workspace.numel(), _raw_stream(stream)), "fp4_linear")
     return out
 
 
@@ -779,17 +822,16 @@ def fp4_linear_train(x, w, g, kind: int, out_dtype=torch.bfloat16, workspace=Non
     _like(w, (N, K), x.dtype, "w")
     _like(g, (M, N), x.dtype, "g")
     if workspace is None:
-        workspace = _new((max(1, fp4_linear_train_workspace_size(kind, M, N, K)),), torch.uint8,
-                         x.device, stream)
-    y = y if y is not None else _new((M, N), out_dtype, x.device, stream)
-    dx = dx if dx is not None else _new((M, K), out_dtype, x.device, stream)
-    dw = dw if dw is not None else _new((N, K), out_dtype, x.device, stream)
-    for t, shape, what in ((y, (M, N), "y"), (dx, (M, K), "dx"), (dw, (N, K), "dw")):
-        _like(t, shape, y.dtype, what)
+        workspace = _new((fp4_linear_train_workspace_size(kind, M, N, K),), torch.uint8, x.device,
+                         stream)
+    y, dt = _out(y, (M, N), out_dtype, x.device, stream, "y")
+    dx, _ = _out(dx, (M, K), y.dtype, x.device, stream, "dx")
+    dw, _ = _out(dw, (N, K), y.dtype, x.device, stream, "dw")
+    if dx.dtype != y.dtype or dw.dtype != y.dtype:
+        raise ValueError("y, dx and dw have one type")
     _check(lib().fp4_linear_train(
-        _ptr(x), _ptr(w), _ptr(g), _in_dtype(x), M, N, K, kind, _ptr(y), _ptr(dx), _ptr(dw),
-        _out_dtype(y.dtype), _ptr(workspace), workspace.numel(), _stream(stream)),
-        "fp4_linear_train")
+        _addr(x), _addr(w), _addr(g), _in_dtype(x), M, N, K, kind, _addr(y), _addr(dx), _addr(dw),
+        dt, _addr(workspace), workspace.numel(), _raw_stream(stream)), "fp4_linear_train")
     return y, dx, dw
 
 
@@ -799,44 +841,54 @@ class ActCheckpoint:
     """What fp8_act_forward keeps for the backward pass: E4M3 bytes [T, F]
     (uint8) of u, and of v for a gated activation, under 1x128 tile scales
     (fp32 [ceil(F/128), T])."""
+    __slots__ = ("T", "F", "u", "u_scales", "v", "v_scales")
 
     def __init__(self, u: torch.Tensor, u_scales: torch.Tensor, v: torch.Tensor | None = None,
                  v_scales: torch.Tensor | None = None):
         self.T, self.F = _rows_cols(u)
         if (v is None) != (v_scales is None):
             raise ValueError("v and v_scales come together")
-        for q, s in ((u, u_scales), (v, v_scales)):
-            if q is not None:
-                _like(q, (self.T, self.F), torch.uint8, "checkpoint bytes")
-                _like(s, ((self.F + 127) // 128, self.T), torch.float32, "checkpoint scales")
+        shape = ((self.F + 127) // 128, self.T)
+        _like(u, (self.T, self.F), torch.uint8, "checkpoint bytes")
+        _like(u_scales, shape, torch.float32, "checkpoint scales")
+        if v is not None:
+            _like(v, (self.T, self.F), torch.uint8, "checkpoint bytes")
+            _like(v_scales, shape, torch.float32, "checkpoint scales")
         self.u, self.u_scales, self.v, self.v_scales = u, u_scales, v, v_scales
 
     @classmethod
     def empty(cls, T: int, F: int, gated: bool, device, stream=None):
         """Uninitialised storage for a checkpoint."""
-        def pair():
-            return (_new((T, F), torch.uint8, device, stream),
-                    _new(((F + 127) // 128, T), torch.float32, device, stream))
-        return cls(*pair(), *(pair() if gated else ()))
+        c = cls.__new__(cls)
+        c.T, c.F, shape = T, F, ((F + 127) // 128, T)
+        c.u = _new((T, F), torch.uint8, device, stream)
+        c.u_scales = _new(shape, torch.float32, device, stream)
+        c.v = _new((T, F), torch.uint8, device, stream) if gated else None
+        c.v_scales = _new(shape, torch.float32, device, stream) if gated else None
+        return c
 
 
 def fp8_act_forward(act: int, u: torch.Tensor, v: torch.Tensor | None = None, out=None,
                     ckpt: ActCheckpoint | None = None, stream=None):
     """(a, checkpoint) with a = f(u), or f(u) * v.  u and v are [T, F] of one
     type; their rows may lie apart (the two halves of one matrix)."""
-    T, F = _rows_cols(u)
+    pu, ldu = _rows(u)
+    T, F = u.shape
+    pv, ldv = None, 0
     if v is not None:
-        _like(v, (T, F), u.dtype, "v")
-    out = out if out is not None else _new((T, F), u.dtype, u.device, stream)
-    _like(out, (T, F), u.dtype, "out")
-    ckpt = ckpt if ckpt is not None else ActCheckpoint.empty(T, F, v is not None, u.device, stream)
-    if (ckpt.T, ckpt.F, ckpt.v is None) != (T, F, v is None):
+        pv, ldv = _rows(_like(v, (T, F), u.dtype, "v"))
+    if out is None:
+        out = _new((T, F), u.dtype, u.device, stream)
+    else:
+        _like(out, (T, F), u.dtype, "out")
+    if ckpt is None:
+        ckpt = ActCheckpoint.empty(T, F, v is not None, u.device, stream)
+    elif (ckpt.T, ckpt.F, ckpt.v is None) != (T, F, v is None):
         raise ValueError("the checkpoint's shape is another")
-    (pu, ldu), (pa, lda) = _ptr_rows(u), _ptr_rows(out)
-    pv, ldv = _ptr_rows(v) if v is not None else (None, 0)
+    pa, lda = _rows(out)
     _check(lib().fp8_act_forward(
-        act, _in_dtype(u), T, F, pu, ldu, pv, ldv, pa, lda, _ptr(ckpt.u), _ptr(ckpt.u_scales),
-        _ptr(ckpt.v), _ptr(ckpt.v_scales), _stream(stream)), "fp8_act_forward")
+        act, _in_dtype(u), T, F, pu, ldu, pv, ldv, pa, lda, _addr(ckpt.u), _addr(ckpt.u_scales),
+        _addr(ckpt.v), _addr(ckpt.v_scales), _raw_stream(stream)), "fp8_act_forward")
     return out, ckpt
 
 
@@ -844,24 +896,22 @@ def fp8_act_backward(act: int, ckpt: ActCheckpoint, da: torch.Tensor, want_a=Fal
                      dv=None, a=None, stream=None):
     """(du, dv | None, a | None) from the checkpoint and the gradient of a;
     ``want_a`` (or a given ``a``) asks for the activation again."""
-    T, F = ckpt.T, ckpt.F
-    _like(da, (T, F), da.dtype, "da")
-    gated = ckpt.v is not None
-    new = lambda: _new((T, F), da.dtype, da.device, stream)
-    du = du if du is not None else new()
-    if gated:
-        dv = dv if dv is not None else new()
-    elif dv is not None:
+    shape, dtype, device = (ckpt.T, ckpt.F), da.dtype, da.device
+    pd, ldd = _rows(_like(da, shape, dtype, "da"))
+    if ckpt.v is None and dv is not None:
         raise ValueError("an ungated activation has no dv")
-    if want_a and a is None:
-        a = new()
-    for t, what in ((du, "du"), (dv, "dv"), (a, "a")):
-        if t is not None:
-            _like(t, (T, F), da.dtype, what)
-    rows = lambda t: _ptr_rows(t) if t is not None else (None, 0)
+    du = _new(shape, dtype, device, stream) if du is None else _like(du, shape, dtype, "du")
+    pu, ldu = _rows(du)
+    pv, ldv, pa, lda = None, 0, None, 0
+    if ckpt.v is not None:
+        dv = _new(shape, dtype, device, stream) if dv is None else _like(dv, shape, dtype, "dv")
+        pv, ldv = _rows(dv)
+    if want_a or a is not None:
+        a = _new(shape, dtype, device, stream) if a is None else _like(a, shape, dtype, "a")
+        pa, lda = _rows(a)
     _check(lib().fp8_act_backward(
-        act, _in_dtype(da), T, F, _ptr(ckpt.u), _ptr(ckpt.u_scales), _ptr(ckpt.v),
-        _ptr(ckpt.v_scales), *rows(da), *rows(du), *rows(dv), *rows(a), _stream(stream)),
+        act, _in_dtype(da), ckpt.T, ckpt.F, _addr(ckpt.u), _addr(ckpt.u_scales), _addr(ckpt.v),
+        _addr(ckpt.v_scales), pd, ldd, pu, ldu, pv, ldv, pa, lda, _raw_stream(stream)),
         "fp8_act_backward")
     return du, dv, a
 

@@ -210,7 +210,10 @@ int fp4_linear(const void *x, int in_dtype, int64_t ldx, const fp4q_operand *w, 
   if ((rc = check_matrix(x, M, K, ldx, dtype_size(in_dtype))) != FP8Q_OK) return rc;
   if ((rc = check_matrix(y, M, N, N, 16)) != FP8Q_OK) return rc;
   if (!aligned(x_amax, 4)) return FP8Q_ERR_MISALIGNED;
-  if (workspace == nullptr || ws_bytes < fp4q_linear_workspace_size(w->kind, M, N, K))
+  const bool fused = M <= FP4Q_LINEAR_FUSED_ROWS;   // the product quantises x itself
+  const bool find_amax = w->kind == FP4Q_NVFP4 && x_amax == nullptr;
+  if ((!fused || find_amax) &&
+      (workspace == nullptr || ws_bytes < fp4q_linear_workspace_size(w->kind, M, N, K)))
     return FP8Q_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
@@ -222,8 +225,8 @@ int fp4_linear(const void *x, int in_dtype, int64_t ldx, const fp4q_operand *w, 
   q.data = ws.take(data_bytes(M, K));
   q.scales = ws.take(fp4q_scale_bytes(w->kind, M, K));
   q.global_scale = w->kind == FP4Q_NVFP4 ? words + 1 : nullptr;
-  if (M <= fp4::kSplitQuantizeMax && K > 0) {   // the product quantises x itself
-    if (w->kind == FP4Q_NVFP4 && x_amax == nullptr) {
+  if (fused && K > 0) {
+    if (find_amax) {
       if (fp4::launch_amax_ld(x, in_dtype, M, K, ldx, words, stream) != cudaSuccess)
         return FP8Q_ERR_CUDA;
       x_amax = words;

@@ -33,8 +33,7 @@ bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_
 // y[M,N] = x . w^T on tiles of 128 rows of w by up to 128 rows of x, K split
 // over the CTAs of a cluster.  x is either the 4-bit operand `q` or, with q
 // null, a bf16 / fp32 matrix that the kernel quantises as it goes (M at most
-// kSplitQuantizeMax; x_amax: NVFP4's amax).
-constexpr int64_t kSplitQuantizeMax = 16;
+// FP4Q_LINEAR_FUSED_ROWS; x_amax: NVFP4's amax).
 int launch_split(int kind, const void *x, int in_dtype, int64_t ldx, const float *x_amax,
                  const fp4q_operand *q, const fp4q_operand &w, int out_dtype, void *y, int64_t M,
                  int64_t N, int64_t K, cudaStream_t stream);
