@@ -82,36 +82,49 @@ __device__ __forceinline__ void issue_block(uint32_t sa, uint32_t b_off, uint32_
 
 // 32 consecutive results of row m from column n0.  WIDTH: every row of C starts
 // on a boundary of so many bytes (32 or 16), and whole groups of that size are
-// stored at once; 0: element by element.
+// stored at once.
 template <typename T, int WIDTH>
 __device__ __forceinline__ void store32(T *C, int64_t N, int64_t m, int64_t n0,
                                         const float (&v)[32]) {
   T *row = C + m * N + n0;
-  if constexpr (WIDTH == 0) {
+  constexpr int kGroup = WIDTH / (int)sizeof(T);
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (n0 + j < N) row[j] = (T)v[j];
-  } else {
-    constexpr int kGroup = WIDTH / (int)sizeof(T);
+  for (int g = 0; g < 32; g += kGroup) {
+    if (n0 + g >= N) break;
+    uint32_t w[WIDTH / 4];
 #pragma unroll
-    for (int g = 0; g < 32; g += kGroup) {
-      if (n0 + g >= N) break;
-      uint32_t w[WIDTH / 4];
-#pragma unroll
-      for (int h = 0; h < WIDTH / 4; ++h)
-        w[h] = sizeof(T) == 2 ? pack8::bf16x2(v[(g + 2 * h) & 31], v[(g + 2 * h + 1) & 31])
-                              : __float_as_uint(v[g + h]);
-      if constexpr (WIDTH == 32)
-        store_32b(row + g, w);
-      else
-        __stcs(reinterpret_cast<uint4 *>(row + g), make_uint4(w[0], w[1], w[2], w[3]));
-    }
+    for (int h = 0; h < WIDTH / 4; ++h)
+      w[h] = sizeof(T) == 2 ? pack8::bf16x2(v[(g + 2 * h) & 31], v[(g + 2 * h + 1) & 31])
+                            : __float_as_uint(v[g + h]);
+    if constexpr (WIDTH == 32)
+      store_32b(row + g, w);
+    else
+      __stcs(reinterpret_cast<uint4 *>(row + g), make_uint4(w[0], w[1], w[2], w[3]));
   }
 }
 
-template <int KIND>
+// The same for a warp's 32 rows from m0 where rows start anywhere: turned in
+// shared memory so that lanes store neighbouring elements (stores of single
+// elements by the lanes that own the rows measured 33 us more on 2048 x 650).
+template <typename T>
+__device__ __forceinline__ void store32_turned(T *C, int64_t M, int64_t N, int64_t m0, int64_t n0,
+                                               const float (&v)[32], float *turn) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = v[j];
+  __syncwarp();
+  T *at = C + m0 * N + n0 + lane;
+  const int rows = (int)min((int64_t)32, M - m0);
+  if (n0 + lane < N)
+    for (int r = 0; r < rows; ++r) at[r * N] = (T)turn[r * 33 + lane];
+  __syncwarp();
+}
+
+template <int KIND, int WIDTH>
 struct PairLayout {
-  static constexpr int kStages = KIND == FP4Q_MXFP4 ? 6 : 5;
+  // rows that allow no vector store pass through shared memory: a stage less
+  static constexpr int kStages = (KIND == FP4Q_MXFP4 ? 6 : 5) - (WIDTH == 0 ? 1 : 0);
+  static constexpr int kTurnBytes = WIDTH == 0 ? 8 * 32 * 33 * 4 : 0;   // a 32 x 32 block a warp
   static constexpr int kAtoms = kBK / Kind<KIND>::kAtomK;
   static constexpr int kABytes = 128 * kBKBytes, kBBytes = 128 * kBKBytes;
   static constexpr int kSfaOff = kABytes + kBBytes;
@@ -120,7 +133,7 @@ struct PairLayout {
   static constexpr int kStageBytes = (kLoadBytes + 1023) / 1024 * 1024;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kBarBytes = 8 * (2 * kStages + 3);
-  static constexpr int kSmemBytes = kRingBytes + kBarBytes + 16 + 1024;
+  static constexpr int kSmemBytes = kRingBytes + kTurnBytes + kBarBytes + 16 + 1024;
   static constexpr uint32_t kSfCol0 = 256;
   static constexpr uint32_t kSfCols = 12 * kAtoms;
   static constexpr uint32_t kTmemCols = 512;
@@ -135,13 +148,13 @@ struct PairMaps {
 template <int KIND, typename T, int WIDTH>
 __global__ void __launch_bounds__(320, 1)
     gemm_pair_kernel(const __grid_constant__ PairMaps maps, const Args p) {
-  using L = PairLayout<KIND>;
+  using L = PairLayout<KIND, WIDTH>;
   constexpr int kStages = L::kStages;
   constexpr uint16_t kBoth = 3;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
-  const uint32_t bars = ring + L::kRingBytes;
+  const uint32_t bars = ring + L::kRingBytes + L::kTurnBytes;
   const uint32_t full0 = bars, empty0 = bars + 8 * kStages;
   const uint32_t accf = bars + 8 * (2 * kStages), acce = accf + 8, drain = acce + 8;
   const uint32_t slot = bars + L::kBarBytes;
@@ -172,7 +185,7 @@ __global__ void __launch_bounds__(320, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  cluster_sync_any();
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(slot_ptr);
   // One allocation serves the pair: both CTAs must hold the same address.
@@ -285,34 +298,39 @@ __global__ void __launch_bounds__(320, 1)
         else
           mbar_arrive_cluster(acce_even);
       }
-      const int64_t m = (int64_t)(2 * mu + (int)rank) * 128 + quarter * 32 + lane;
-      if (m < p.M) {
+      const int64_t m0 = (int64_t)(2 * mu + (int)rank) * 128 + quarter * 32;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int64_t n0 = (int64_t)nt * 256 + half * 128 + c * 32;
-          if (n0 < p.N) {
-            float v[32];
+      for (int c = 0; c < 4; ++c) {
+        const int64_t n0 = (int64_t)nt * 256 + half * 128 + c * 32;
+        if (n0 >= p.N || m0 >= p.M) break;
+        float v[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = KIND == FP4Q_NVFP4 ? __fmul_rn(__uint_as_float(r[c][j]), g)
-                                        : __uint_as_float(r[c][j]);
-            store32<T, WIDTH>(static_cast<T *>(p.C), p.N, m, n0, v);
-          }
-        }
+        for (int j = 0; j < 32; ++j)
+          v[j] = KIND == FP4Q_NVFP4 ? __fmul_rn(__uint_as_float(r[c][j]), g)
+                                    : __uint_as_float(r[c][j]);
+        T *C = static_cast<T *>(p.C);
+        if constexpr (WIDTH == 0)
+          store32_turned(C, p.M, p.N, m0, n0, v,
+                         reinterpret_cast<float *>(smem_raw + (ring - raw) + L::kRingBytes) +
+                             (warp - 2) * 32 * 33);
+        else if (m0 + lane < p.M)
+          store32<T, WIDTH>(C, p.N, m0 + lane, n0, v);
       }
     }
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // neither CTA leaves while the other may still signal it
+  cluster_sync_any();  // neither CTA leaves while the other may still signal it
   tc_fence_after();
+  __syncwarp();
   if (warp == 1) tmem_dealloc_pair(tmem_base, L::kTmemCols);
 }
 
 template <int KIND, typename T, int WIDTH>
 int run_pair(const PairMaps &maps, const Args &a, cudaStream_t stream) {
-  using L = PairLayout<KIND>;
+  using L = PairLayout<KIND, WIDTH>;
   auto kernel = gemm_pair_kernel<KIND, T, WIDTH>;
   static PerDeviceOnce setup;  // per instantiation: the pairs that fit at once, 0 on failure
   cudaLaunchConfig_t cfg = {};
@@ -354,7 +372,7 @@ template <int KIND, typename T>
 int launch_pair(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K,
                 cudaStream_t stream) {
   PairMaps maps;
-  constexpr int kAtoms = PairLayout<KIND>::kAtoms;
+  constexpr int kAtoms = PairLayout<KIND, 32>::kAtoms;
   if (!make_tmap(&maps.a, A.data, a.M, K, 128) || !make_tmap(&maps.b, B.data, a.N, K, 128) ||
       !make_scale_tmap(&maps.sfa, A.scales, a.M, a.atoms_k, kAtoms) ||
       !make_scale_tmap(&maps.sfb, B.scales, a.N, a.atoms_k, kAtoms))
@@ -379,7 +397,16 @@ bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_
 
 int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_dtype, void *C,
                 int64_t M, int64_t N, int64_t K, cudaStream_t stream) {
-  if (M <= 128)
+  // Which kernel.  Up to 64 rows reading B once is the work, and the split
+  // kernel does little else.  Past that, by a model fitted to both kernels
+  // timed on 130 shapes (M 160-2048, N 256-12288, K 512-16384): beyond a common
+  // 6.5 us a wave of 256 x 256 tiles takes 0.33 us per 256 of K; a wave of
+  // split tiles 0.45 us per 256 of each CTA's K, and 2 us (0.3 us with an SM
+  // to itself) to join the sums.  Both sides of the line: 256 x 4096 x 16384
+  // pairs 27.7 us, split 16.6; 512 x 12288 x 4096 pairs 18.5 us, split 25.9.
+  const double pair_waves = (double)(((M + 255) / 256 * ((N + 255) / 256) + sm_count() / 2 - 1) /
+                                     (sm_count() / 2));
+  if (M <= 64 || split_cost(M, N, K) < pair_waves * 0.33 * (double)((K + kBK - 1) / kBK))
     return launch_split(kind, nullptr, FP8Q_DT_BF16, 0, nullptr, &A, B, out_dtype, C, M, N, K, stream);
   Args a{};
   a.M = M;

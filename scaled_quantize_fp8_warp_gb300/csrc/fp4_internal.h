@@ -34,6 +34,9 @@ bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_
 // over the CTAs of a cluster.  x is either the 4-bit operand `q` or, with q
 // null, a bf16 / fp32 matrix that the kernel quantises as it goes (M at most
 // FP4Q_LINEAR_FUSED_ROWS; x_amax: NVFP4's amax).
+// Microseconds beyond a launch's fixed cost that launch_split would take for a
+// quantised x, by the model that chooses between it and CTA pairs.
+double split_cost(int64_t M, int64_t N, int64_t K);
 int launch_split(int kind, const void *x, int in_dtype, int64_t ldx, const float *x_amax,
                  const fp4q_operand *q, const fp4q_operand &w, int out_dtype, void *y, int64_t M,
                  int64_t N, int64_t K, cudaStream_t stream);

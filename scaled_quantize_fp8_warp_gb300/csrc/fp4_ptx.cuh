@@ -91,6 +91,62 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// A counter in shared memory that one thread raises and others wait for.
+__device__ __forceinline__ void counter_set(uint32_t addr, int value) {
+  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(addr), "r"(value) : "memory");
+}
+__device__ __forceinline__ int counter_get(uint32_t addr) {
+  int v;
+  asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Bounded wait of a converged warp for a counter above `value` (as
+// wait_bounded_all for a barrier).
+__device__ __forceinline__ bool wait_counter_all(uint32_t addr, int value,
+                                                 volatile int *abort_flag, unsigned int *err) {
+  uint64_t t0 = 0;
+  uint32_t spins = 0;
+  while (true) {
+    if (__all_sync(0xFFFFFFFFu, counter_get(addr) > value)) return true;
+    if ((spins++ & 255u) == 0) {
+      int verdict = 0;   // 1: another thread aborted, 2: this wait ran out of time
+      if ((threadIdx.x & 31) == 0) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        verdict = *abort_flag ? 1 : (now - t0 > kWaitLimitNs ? 2 : 0);
+      }
+      verdict = __shfl_sync(0xFFFFFFFFu, verdict, 0);
+      if (verdict != 0) {
+        if (verdict == 2 && (threadIdx.x & 31) == 0) {
+          *abort_flag = 1;
+          atomicOr(err, 1u);
+        }
+        return false;
+      }
+    }
+  }
+}
+
+// Every thread of every CTA in the cluster: release this CTA's prior writes,
+// wait for all the others.  Not the .aligned form, whose warps must be
+// converged: threads come here from loops of different lengths, and an arrival
+// counted twice would let a CTA leave while another still reads its memory.
+__device__ __forceinline__ void cluster_sync_any() {
+  asm volatile(
+      "barrier.cluster.arrive.release;\n\t"
+      "barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // 32 bytes to global memory, streaming (written once, not read here).
 __device__ __forceinline__ void store_32b(void *p, const uint32_t (&w)[8]) {
   asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),

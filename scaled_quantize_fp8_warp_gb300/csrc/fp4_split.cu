@@ -38,6 +38,7 @@ constexpr int kThreads = 320;
 constexpr int kQuantWarps = 8;
 constexpr int kBKBytes = 128, kBK = 256;    // K per stage
 constexpr int kMaxStages = 8;
+constexpr int kMaxSplit = 8;                // CTAs of a cluster (the portable limit)
 constexpr int kMaxRows = 128;               // rows of x per tile
 constexpr uint32_t kTmemCols = 256;
 constexpr int kSmemBytes = 112 * 1024;      // two CTAs on an SM, never three
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t accf = bars + 8 * (2 * kMaxStages), drain = accf + 8;
   uint8_t *slot_ptr = smem_raw + (drain + 8 - raw);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(slot_ptr + 4);
+  const uint32_t free_kb = smem_u32(slot_ptr + 8);   // K blocks below this have a free slot
   ScaleTable &table = *reinterpret_cast<ScaleTable *>(slot_ptr + 16);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -98,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(accf, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
+    counter_set(free_kb, 0);
     fence_barrier_init();
     fence_proxy_async_smem();
     prefetch_tmap(&maps.w);
@@ -129,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           ok = false;
           break;
         }
+        if (kQuantize) counter_set(free_kb, it + 1);
         const uint32_t sa = ring + s * p.stage_bytes;
         const int ka = kb * kAtoms;
         mbar_arrive_expect_tx(full, 128 * kBKBytes + kAtoms * 512 +
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // One task is 256 elements of one row: 8 to a lane, blocks in 4 (MXFP4) or
     // 2 neighbouring lanes.  Tasks run K block after K block.
     constexpr int kLanes = Kind<KIND>::kBlock / 8;
-    constexpr int kBatch = 4;     // tasks whose loads are in flight together
+    constexpr int kBatch = sizeof(XT) == 2 ? 8 : 4;   // tasks whose loads are in flight together
     const int tasks = rows * (kb1 - kb0);
     const XT *x = static_cast<const XT *>(p.x) + (int64_t)mt * p.nb * p.ldx;
     const bool g_bad = !(g < __uint_as_float(0x7F800000u));
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int t = t0 + i * kQuantWarps;
         if (t >= tasks || !ok) break;
         const int kbl = t / rows, row = t - kbl * rows;
-        const int s = kbl % p.stages, ph = (kbl / p.stages) & 1;
+        const int s = kbl % p.stages;
         uint32_t m = y[i].amax_bits();
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -245,7 +249,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           w = encode8_careful<KIND>(y[i].pair(0), y[i].pair(1), y[i].pair(2), y[i].pair(3), m, g,
                                     &byte);
         }
-        if (!wait_bounded_all(empty0 + 8 * s, ph ^ 1u, abort_flag, p.err)) {
+        // Not the slot's own barrier: a warp's next task may be several turns of
+        // the ring ahead, where a phase's parity does not tell which turn it is.
+        if (!wait_counter_all(free_kb, kbl, abort_flag, p.err)) {
           ok = false;
           break;
         }
@@ -281,70 +287,142 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     tc_fence_before();
   }
+  __syncwarp();
   __syncthreads();
-  if (p.split > 1) cluster_sync_all();
+  if (p.split > 1) cluster_sync_any();
   {
     float scale = 1.0f;
     if (KIND == FP4Q_NVFP4) scale = __fmul_rn(kQuantize ? g : *p.gx, *p.gw);
-    const int total = rows * 128;
-    const int first = total / p.split * (int)rank, last = (int)rank == p.split - 1 ? total : first + total / p.split;
+    const int total = rows * 32;   // groups of four columns
+    const int first = (int)((int64_t)total * rank / p.split);
+    const int last = (int)((int64_t)total * (rank + 1) / p.split);
     const uint32_t part_u32 = smem_u32(part);
+    const bool whole = p.N % 4 == 0;   // whole groups, 8- or 16-byte aligned (y is)
+#pragma unroll 2
     for (int i = first + (int)threadIdx.x; i < last; i += kThreads) {
-      const int row = i >> 7, n = i & 127;
-      float v;
-      if (p.split == 1) {
-        v = part[i];
-      } else {
-        float t[8];
+      const int row = i >> 5, n = (i & 31) * 4;
+      float4 t[kMaxSplit];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < p.split)
-            t[r] = __uint_as_float(ld_shared_cluster_u32(mapa_shared(part_u32 + 4 * i, r)));
-        v = t[0];
+      for (int r = 0; r < kMaxSplit; ++r)
+        if (r < p.split) t[r] = ld_shared_cluster_f4(mapa_shared(part_u32 + 16 * i, r));
+      float4 v = t[0];
 #pragma unroll
-        for (int r = 1; r < 8; ++r)
-          if (r < p.split) v += t[r];
+      for (int r = 1; r < kMaxSplit; ++r)
+        if (r < p.split) v.x += t[r].x, v.y += t[r].y, v.z += t[r].z, v.w += t[r].w;
+      if (KIND == FP4Q_NVFP4) {
+        v.x = __fmul_rn(v.x, scale), v.y = __fmul_rn(v.y, scale);
+        v.z = __fmul_rn(v.z, scale), v.w = __fmul_rn(v.w, scale);
       }
-      if (KIND == FP4Q_NVFP4) v = __fmul_rn(v, scale);
       const int64_t col = (int64_t)nt * 128 + n;
-      if (col < p.N) {
-        const int64_t at = ((int64_t)mt * p.nb + row) * p.N + col;
+      const int64_t at = ((int64_t)mt * p.nb + row) * p.N + col;
+      if (whole) {
+        if (col >= p.N) continue;
         if (p.out_bf16)
-          static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v);
+          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.y) + at) =
+              make_uint2(pack8::bf16x2(v.x, v.y), pack8::bf16x2(v.z, v.w));
         else
-          static_cast<float *>(p.y)[at] = v;
+          *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at) = v;
+      } else {
+        const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (col + j >= p.N) break;
+          if (p.out_bf16)
+            static_cast<__nv_bfloat16 *>(p.y)[at + j] = __float2bfloat16_rn(e[j]);
+          else
+            static_cast<float *>(p.y)[at + j] = e[j];
+        }
       }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (p.split > 1) cluster_sync_all();   // no CTA leaves while another may read its sums
+  if (p.split > 1) cluster_sync_any();   // no CTA leaves while another may read its sums
   tc_fence_after();
+  __syncwarp();
   if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
+}
+
+// Shared memory of one CTA, and all of the SM's on-chip memory for two.
+template <typename Kernel>
+bool set_up(Kernel kernel) {
+  return gemm::set_smem(kernel, kSmemBytes) == cudaSuccess &&
+         cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                              cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+}
+
+cudaLaunchConfig_t launch_config(unsigned grid, int split, cudaLaunchAttribute *attr,
+                                 cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)split;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of 1 .. kMaxSplit CTAs that run at once on the current device: a
+// cluster keeps to one of the GPU's partitions, so fewer CTAs fit as sixes or
+// sevens than alone.  Every instantiation has the same block, shared memory
+// and residence, so one kernel answers for all.  Null on failure.
+const int *clusters_at_once() {
+  static int fit[64][kMaxSplit];
+  static PerDeviceOnce setup;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  const int ok = setup.get([&] {
+    auto kernel = split_kernel<FP4Q_MXFP4, void>;
+    if (!set_up(kernel)) return 0;
+    for (int s = 1; s <= kMaxSplit; ++s) {
+      cudaLaunchAttribute attr;
+      cudaLaunchConfig_t cfg = launch_config(s, s, &attr, nullptr);
+      if (cudaOccupancyMaxActiveClusters(&fit[dev][s - 1], kernel, &cfg) != cudaSuccess ||
+          fit[dev][s - 1] < 1)
+        return 0;
+    }
+    return 1;
+  });
+  return ok == 1 ? fit[dev] : nullptr;
+}
+
+int rows_per_tile(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
+
+// CTAs a tile: the most of which all tiles run at once, at most one per K
+// block.
+int split_of(const int *fit, int64_t tiles, int64_t k_blocks) {
+  int s = (int)std::min<int64_t>(kMaxSplit, k_blocks);
+  while (s > 1 && fit[s - 1] < tiles) --s;
+  return s;
 }
 
 template <int KIND, typename XT>
 int run_split(const Maps &maps, const Args &a, int64_t tiles, cudaStream_t stream) {
   auto kernel = split_kernel<KIND, XT>;
   static PerDeviceOnce setup;  // per instantiation
-  if (setup.get([&] { return gemm::set_smem(kernel, kSmemBytes) == cudaSuccess ? 1 : 0; }) != 1)
-    return FP8Q_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)(tiles * a.split), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  if (setup.get([&] { return set_up(kernel) ? 1 : 0; }) != 1) return FP8Q_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = launch_config((unsigned)(tiles * a.split), a.split, &attr, stream);
   return cudaLaunchKernelEx(&cfg, kernel, maps, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
 }
 
 }  // namespace
+
+double split_cost(int64_t M, int64_t N, int64_t K) {
+  const int *fit = clusters_at_once();
+  if (fit == nullptr) return 0.0;
+  const int64_t nb = rows_per_tile(M), kb = (K + kBK - 1) / kBK;
+  const int64_t tiles = (N + 127) / 128 * ((M + nb - 1) / nb);
+  const int s = split_of(fit, tiles, kb);
+  const int64_t waves = (tiles + fit[s - 1] - 1) / fit[s - 1];
+  return (double)waves * (0.45 * (double)((kb + s - 1) / s) + (tiles * s > sm_count() ? 2.0 : 0.3));
+}
 
 int launch_split(int kind, const void *x, int in_dtype, int64_t ldx, const float *x_amax,
                  const fp4q_operand *q, const fp4q_operand &w, int out_dtype, void *y, int64_t M,
@@ -359,7 +437,7 @@ int launch_split(int kind, const void *x, int in_dtype, int64_t ldx, const float
   a.gx = q == nullptr ? nullptr : q->global_scale;
   a.gw = w.global_scale;
   a.y = y;
-  a.nb = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+  a.nb = rows_per_tile(M);
   a.num_k_blocks = (int)((K + kBK - 1) / kBK);
   a.num_steps = (int)((K + 63) / 64);
   a.atoms_k = (int)num_atoms_k(kind, K);
@@ -374,10 +452,9 @@ int launch_split(int kind, const void *x, int in_dtype, int64_t ldx, const float
   if (tiles > INT32_MAX / 8 || K > INT32_MAX || (std::max(M, N) + 255) / 128 * a.atoms_k > INT32_MAX)
     return FP8Q_ERR_INVALID_ARG;
   a.m_tiles = (int)m_tiles;
-  // As many CTAs as run at once, at most one per K block and eight (the
-  // portable cluster size) per tile.
-  a.split = (int)std::max<int64_t>(
-      1, std::min<int64_t>({8, (int64_t)a.num_k_blocks, 2 * sm_count() / tiles}));
+  const int *fit = clusters_at_once();
+  if (fit == nullptr) return FP8Q_ERR_CUDA;
+  a.split = split_of(fit, tiles, a.num_k_blocks);
   a.idesc = idesc_fp4(kind, 128, (uint32_t)a.nb);
   const int atoms = kind == FP4Q_MXFP4 ? 2 : 4;
   a.stage_bytes = (128 * kBKBytes + 2 * atoms * 512 + 1023) / 1024 * 1024 + a.nb * kBKBytes;

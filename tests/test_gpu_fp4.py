@@ -309,3 +309,22 @@ def test_offsets_past_32_bits(fq):
     y = fq.fp4_gemm(qa, qb)
     tail = fq.fp4_gemm(fq.fp4_quantize(a[-130:].contiguous(), fq.MXFP4)[0], qb)
     assert torch.equal(y[-130:], tail)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [(1, 12288, 4096), (2, 4096, 16384), (13, 4096, 16384),
+                                  (16, 16384, 4096), (48, 12288, 4096), (128, 4096, 16384),
+                                  (500, 1000, 16384), (300, 4096, 8192)])
+def test_few_rows_of_a_layer(fq, kind, size):
+    """Rings that wrap and clusters of every size, against a 64-bit product of
+    the values the operands stand for."""
+    M, N, K = size
+    x, w = normal((M, K), 81).cuda(), normal((N, K), 82, 0.02).cuda()
+    qx, qw = fq.fp4_quantize(x, kind)[0], fq.fp4_quantize(w, kind)[0]
+    a = fq.fp4_dequantize(qx, out_dtype=torch.float32).double()
+    b = fq.fp4_dequantize(qw, out_dtype=torch.float32).double()
+    want, mag = a @ b.T, a.abs() @ b.abs().T
+    bound = (K / 64 + 12) * 2.0 ** -23 * mag + 2.0 ** -23 * want.abs()
+    for y in (fq.fp4_linear(x, qw, out_dtype=torch.float32),
+              fq.fp4_gemm(qx, qw, out_dtype=torch.float32)):
+        assert ((y.double() - want).abs() <= bound).all()
