@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(full0 + 8 * s, kQuantize ? 1 + rows : 1);
+      mbar_init(full0 + 8 * s, kQuantize ? 1 + (rows + 3) / 4 : 1);   // loads; tasks
       mbar_init(empty0 + 8 * s, 1);
     }
     mbar_init(accf, 1);
@@ -198,75 +198,97 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!ok && elect_one()) gemm::drain_mma(drain, abort_flag);
     __syncwarp();
   } else if constexpr (kQuantize) {
-    // One task is 256 elements of one row: 8 to a lane, blocks in 4 (MXFP4) or
-    // 2 neighbouring lanes.  Tasks run K block after K block.
+    // One task is 256 elements of K of up to four rows: 8 elements of each to a
+    // lane, blocks in 4 (MXFP4) or 2 neighbouring lanes.  Tasks run K block
+    // after K block; the next one's loads are under way while one is cast.
     constexpr int kLanes = Kind<KIND>::kBlock / 8;
-    constexpr int kBatch = sizeof(XT) == 2 ? 8 : 4;   // tasks whose loads are in flight together
-    const int tasks = rows * (kb1 - kb0);
+    const int groups = (rows + 3) / 4, tasks = groups * (kb1 - kb0);
     const XT *x = static_cast<const XT *>(p.x) + (int64_t)mt * p.nb * p.ldx;
     const bool g_bad = !(g < __uint_as_float(0x7F800000u));
-    bool ok = true;
-    for (int t0 = warp - 2; t0 < tasks && ok; t0 += kBatch * kQuantWarps) {
-      Pack8<XT> y[kBatch];
+    const bool odd = lane & 1;
+    auto fetch = [&](int t, Pack8<XT> (&v)[4]) {
+      const int kbl = t / groups, row0 = (t - kbl * groups) * 4;
+      const int64_t k = (int64_t)(kb0 + kbl) * kBK + lane * 8;
+      const int in = t < tasks ? (int)max((int64_t)0, min((int64_t)8, p.K - k)) : 0;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int t = t0 + i * kQuantWarps;
-        const int kbl = t / rows, row = t - kbl * rows;
-        const int64_t k = (int64_t)(kb0 + kbl) * kBK + lane * 8;
-        const int valid = t < tasks ? (int)max((int64_t)0, min((int64_t)8, p.K - k)) : 0;
-        const XT *at = x + (valid > 0 ? row * p.ldx + k : 0);
+      for (int i = 0; i < 4; ++i) {
+        const int valid = row0 + i < rows ? in : 0;
+        const XT *at = x + (valid > 0 ? (row0 + i) * p.ldx + k : 0);
         if (p.vec)
-          pack8::load<true>(y[i], at, valid);
+          pack8::load<true>(v[i], at, valid);
         else
-          y[i].load_some(at, valid);
+          v[i].load_some(at, valid);
       }
+    };
+    Pack8<XT> next[4];
+    fetch(warp - 2, next);
+    for (int t = warp - 2; t < tasks; t += kQuantWarps) {
+      Pack8<XT> y[4];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int t = t0 + i * kQuantWarps;
-        if (t >= tasks || !ok) break;
-        const int kbl = t / rows, row = t - kbl * rows;
-        const int s = kbl % p.stages;
-        uint32_t m = y[i].amax_bits();
+      for (int i = 0; i < 4; ++i) y[i] = next[i];
+      fetch(t + kQuantWarps, next);
+      const int kbl = t / groups, row0 = (t - kbl * groups) * 4;
+      const int s = kbl % p.stages;
+      uint32_t m[4], top = 0, byte[4], w[4];
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      for (int i = 0; i < 4; ++i) {
+        m[i] = y[i].amax_bits();
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) m[i] = max(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+        top = max(top, m[i]);
         y[i].negate();
-        uint32_t byte, w;
-        if (!__any_sync(0xFFFFFFFFu, m >= kCarefulBits || g_bad)) {
+      }
+      if (!__any_sync(0xFFFFFFFFu, top >= kCarefulBits || g_bad)) {
+        if (KIND == FP4Q_NVFP4) {   // the two lanes of a block find two rows' scales each
+          const float t0 = fmaxf(nv_ratio(__uint_as_float(odd ? m[2] : m[0]), g, rg), 0x1p-9f);
+          const float t1 = fmaxf(nv_ratio(__uint_as_float(odd ? m[3] : m[1]), g, rg), 0x1p-9f);
+          const uint32_t mine =
+              (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(t0, t1), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+          const uint32_t all = odd ? other | mine << 16 : mine | other << 16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) byte[i] = (all >> (8 * i)) & 0xFFu;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (row0 + i >= rows) break;
           float d = 0.0f, r;
           if (KIND == FP4Q_MXFP4) {
-            byte = mx_byte(m);
-            r = mx_reciprocal(byte);
+            byte[i] = mx_byte(m[i]);
+            r = mx_reciprocal(byte[i]);
           } else {
-            byte = (uint32_t)__nv_cvt_float_to_fp8(
-                fmaxf(nv_ratio(__uint_as_float(m), g, rg), 0x1p-9f), __NV_SATFINITE, __NV_E4M3);
-            const float2 dr = table.d_r[byte];
+            const float2 dr = table.d_r[byte[i]];
             d = dr.x;
             r = dr.y;
           }
           const float2 v[4] = {y[i].pair(0), y[i].pair(1), y[i].pair(2), y[i].pair(3)};
-          w = encode8<KIND>(v, d, r);
-        } else {
-          w = encode8_careful<KIND>(y[i].pair(0), y[i].pair(1), y[i].pair(2), y[i].pair(3), m, g,
-                                    &byte);
+          w[i] = encode8<KIND>(v, d, r);
         }
-        // Not the slot's own barrier: a warp's next task may be several turns of
-        // the ring ahead, where a phase's parity does not tell which turn it is.
-        if (!wait_counter_all(free_kb, kbl, abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
-        uint8_t *stage = ring_ptr + s * p.stage_bytes;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = encode8_careful<KIND>(y[i].pair(0), y[i].pair(1), y[i].pair(2), y[i].pair(3),
+                                       m[i], g, &byte[i]);
+      }
+      // Not the slot's own barrier: a warp's next task may be several turns of
+      // the ring ahead, where a phase's parity does not tell which turn it is.
+      if (!wait_counter_all(free_kb, kbl, abort_flag, p.err)) break;
+      uint8_t *stage = ring_ptr + s * p.stage_bytes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = row0 + i;
+        if (row >= rows) break;
         // the 128-byte swizzle: 16-byte chunk index xor row of the 8-row group
         *reinterpret_cast<uint32_t *>(stage + kXOff + row * 128 +
-                                      ((((lane >> 2) ^ row) & 7) << 4 | (lane & 3) << 2)) = w;
+                                      ((((lane >> 2) ^ row) & 7) << 4 | (lane & 3) << 2)) = w[i];
         if ((lane & (kLanes - 1)) == 0) {
           const int block = lane / kLanes;   // of this stage
-          stage[kSfbOff + (block >> 2) * 512 + row * 16 + (block & 3)] = (uint8_t)byte;
+          stage[kSfbOff + (block >> 2) * 512 + row * 16 + (block & 3)] = (uint8_t)byte[i];
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full0 + 8 * s);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full0 + 8 * s);
     }
   }
 
@@ -371,7 +393,9 @@ cudaLaunchConfig_t launch_config(unsigned grid, int split, cudaLaunchAttribute *
 // Clusters of 1 .. kMaxSplit CTAs that run at once on the current device: a
 // cluster keeps to one of the GPU's partitions, so fewer CTAs fit as sixes or
 // sevens than alone.  Every instantiation has the same block, shared memory
-// and residence, so one kernel answers for all.  Null on failure.
+// and residence, so one kernel answers for all.  The query counts one CTA an
+// SM here whatever the shared memory; two run (start and end times of 304 CTAs
+// overlap in pairs on an SM), hence twice its answer.  Null on failure.
 const int *clusters_at_once() {
   static int fit[64][kMaxSplit];
   static PerDeviceOnce setup;
@@ -386,6 +410,7 @@ const int *clusters_at_once() {
       if (cudaOccupancyMaxActiveClusters(&fit[dev][s - 1], kernel, &cfg) != cudaSuccess ||
           fit[dev][s - 1] < 1)
         return 0;
+      fit[dev][s - 1] *= 2;
     }
     return 1;
   });
