@@ -1,6 +1,6 @@
 // 4-bit quantisation (MXFP4, NVFP4) and its inverse.
 //
-// quantize_kernel: a CTA of 256 threads owns a 128 x 128 tile of x.  Warp w
+// quantize_kernel: CTAs of 256 threads own 128 x 128 tiles of x.  In one, warp w
 // holds rows [32 (w / 2), +32) and columns [64 (w % 2), +64); lane l the rows
 // [8 (l / 8), +8) and columns [8 (l % 8), +8) of that, so a block of 32 (or
 // 16) along a row lies in 4 (2) neighbouring lanes and a block of 32 (16) down
@@ -14,6 +14,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4_common.cuh"
 #include "fp4_internal.h"
@@ -84,11 +85,11 @@ __device__ __forceinline__ void block_max_cols(const Pack8<float> (&x)[8], uint3
 }
 
 // The transposed codes of a tile in shared memory: word w (8 rows) of column
-// c.  Sixteen-byte chunks are permuted by the column and every 32 columns
-// shift by 16 words, so that a warp's stores (8 columns eight apart x 4 words)
-// fall into 32 banks.
+// c.  Sixteen-byte chunks are permuted by the column and neighbouring columns
+// change places in every second 32, so that a warp's stores (8 columns eight
+// apart x 4 words) fall into 32 banks.
 __device__ __forceinline__ int t_word(int c, int w) {
-  return (c + (c >> 5)) * 16 + ((((w >> 2) ^ (c >> 3)) & 3) << 2 | (w & 3));
+  return (c ^ ((c >> 5) & 1)) * 16 + ((((w >> 2) ^ (c >> 3)) & 3) << 2 | (w & 3));
 }
 
 // Scale bytes of eight blocks of one thread, rows (or columns) 0-3 in the low
@@ -125,14 +126,75 @@ __device__ __forceinline__ uint32_t encode_block(const float2 (&y)[4], uint32_t 
   return encode8<KIND>(y, dr.x, dr.y);
 }
 
+// A tile of x in shared memory, each thread's 8 x 8 patch in 16-byte slots:
+// slot (row i of the patch, 16-byte part h) of thread t at
+// ((i * kParts + h) * kThreads + t) * 16.
+template <typename T>
+struct InTile {
+  static constexpr int kParts = (int)sizeof(T) / 2;
+  uint8_t at[8 * kParts * kThreads * 16];
+};
+struct NoTile {};
+
 template <int KIND, typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs p) {
+struct QuantSmem {
+  static constexpr int kAtoms = kTile / Kind<KIND>::kAtomK;
+  typename std::conditional<VEC, NoTile, InTile<T>>::type in;
+  __align__(16) uint32_t t_code[kTile * 16];
+  __align__(16) uint8_t s_scale[kAtoms * 512];
+  __align__(16) uint8_t t_scale[kAtoms * 512];
+  ScaleTable table;
+};
+
+// Rows that are not 16-byte aligned: a warp loads its 32 x 64 elements of the
+// tile one by one, neighbouring lanes neighbouring elements, and deals them
+// out to the lanes whose patches they belong to.
+template <typename T>
+__device__ __forceinline__ void load_dealt(const QuantArgs &p, int64_t row, int64_t col,
+                                           InTile<T> &in, Pack8<T> (&y)[8]) {
+  constexpr int kParts = InTile<T>::kParts;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T *x = static_cast<const T *>(p.x);
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    T v[8][2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t r = row + r0 + i, c = col + lane + 32 * k;
+        v[i][k] = r < p.rows && c < p.cols ? x[r * p.ld + c] : (T)0.0f;
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // element (r, c) of the 32 x 64 belongs to lane (r / 8) * 8 + c / 8
+        const int c = lane + 32 * k, owner = warp * 32 + r0 + (c >> 3);
+        const int byte = (c & 7) * (int)sizeof(T);
+        *reinterpret_cast<T *>(in.at + ((i * kParts + (byte >> 4)) * kThreads + owner) * 16 +
+                               (byte & 15)) = v[i][k];
+      }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int h = 0; h < kParts; ++h)
+      y[i].take(h, *reinterpret_cast<const uint4 *>(
+                       in.at + ((i * kParts + h) * kThreads + threadIdx.x) * 16));
+}
+
+template <int KIND, typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_kernel(const QuantArgs p) {
   constexpr int kBlock = Kind<KIND>::kBlock;
   constexpr int kAtoms = kTile / Kind<KIND>::kAtomK;   // atoms along K per tile: 1 or 2
   constexpr int kLanes = kBlock / 8;                   // lanes that share a block: 4 or 2
-  __shared__ __align__(16) uint8_t s_scale[kAtoms * 512], t_scale[kAtoms * 512];
-  __shared__ __align__(16) uint32_t t_code[(kTile + kTile / 32) * 16];
-  __shared__ ScaleTable table;
+  extern __shared__ __align__(16) uint8_t smem[];
+  auto &sm = *reinterpret_cast<QuantSmem<KIND, T, VEC> *>(smem);
+  uint8_t *const s_scale = sm.s_scale, *const t_scale = sm.t_scale;
+  uint32_t *const t_code = sm.t_code;
+  ScaleTable &table = sm.table;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tr = (warp >> 1) * 32 + (lane >> 3) * 8;   // this thread's first row in the tile
@@ -141,20 +203,22 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs p) {
   const unsigned by = blockIdx.x / tiles_c, bx = blockIdx.x - by * tiles_c;
   const int64_t r0 = (int64_t)by * kTile, c0 = (int64_t)bx * kTile;
   const int64_t row = r0 + tr, col = c0 + tc;
-
-  Pack8<T> y[8];
   const int rows_in = (int)max((int64_t)0, min((int64_t)8, p.rows - row));
   const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.cols - col));
-  {
+
+  Pack8<T> y[8];
+  if constexpr (VEC) {
     const T *x = static_cast<const T *>(p.x) + (rows_in > 0 && cols_in > 0 ? row * p.ld + col : 0);
-    if (VEC && rows_in == 8 && cols_in == 8) {   // all loads in a row, no test between them
+    if (rows_in == 8 && cols_in == 8) {   // all loads in a row, no test between them
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i].load_vec(x + i * p.ld);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        load<VEC>(y[i], i < rows_in ? x + i * p.ld : x, i < rows_in ? cols_in : 0);
+        load<true>(y[i], i < rows_in ? x + i * p.ld : x, i < rows_in ? cols_in : 0);
     }
+  } else {
+    load_dealt(p, r0 + (warp >> 1) * 32, c0 + (warp & 1) * 64, sm.in, y);
   }
   float g = 1.0f, rg = 1.0f;
   if (KIND == FP4Q_NVFP4) {
@@ -263,24 +327,43 @@ __global__ void global_kernel(const float *amax, float *global_scale) {
   *global_scale = nv_global(*amax);
 }
 
-// max |x| for matrices whose rows lie apart or are not 16-byte aligned.  The
-// maximum of bit patterns does not depend on the order of the atomics; NaN
-// patterns sort above infinity.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-    amax_ld_kernel(const T *x, int64_t rows, int64_t cols, int64_t ld, unsigned int *amax) {
+// max |x| of a matrix whose rows lie ld apart.  The maximum of bit patterns
+// does not depend on the order of the atomics; NaN patterns sort above
+// infinity.  VEC: 16-byte aligned rows.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    amax_kernel(const T *x, int64_t rows, int64_t cols, int64_t ld, unsigned int *amax) {
+  constexpr int kBatch = 4;   // groups of 8 elements in flight
   uint32_t m = 0;
-  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < cols; c += (int64_t)gridDim.x * 256)
-      m = max(m, abs_bits((float)x[r * ld + c]));
+  const int64_t step = (int64_t)gridDim.x * kThreads * (VEC ? 8 : 1);
+  const int64_t first = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * (VEC ? 8 : 1);
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    const T *p = x + r * ld;
+    if (VEC) {
+      for (int64_t c = first; c < cols; c += kBatch * step) {
+        Pack8<T> v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int64_t left = cols - (c + b * step);
+          if (left >= 8)
+            v[b].load_vec(p + c + b * step);
+          else
+            v[b].load_some(p + (left > 0 ? c + b * step : 0), (int)max(left, (int64_t)0));
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) m = max(m, v[b].amax_bits());
+      }
+    } else {
+      for (int64_t c = first; c < cols; c += step)
+        m = max(m, __float_as_uint((float)p[c]) & 0x7FFFFFFFu);
+    }
+  }
   m = __reduce_max_sync(0xFFFFFFFFu, m);
-  __shared__ uint32_t part[8];
+  __shared__ uint32_t part[kThreads / 32];
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 8; ++i) m = max(m, part[i]);
+    for (int i = 1; i < kThreads / 32; ++i) m = max(m, part[i]);
     if (m != 0) atomicMax(amax, m);
   }
 }
@@ -289,12 +372,16 @@ __global__ void __launch_bounds__(256)
 // at a time, whose reads are in flight together.  VEC: every row of y starts on
 // a 16-byte boundary and K is a multiple of 16.  For fp32 two neighbouring
 // lanes (16 codes, one scale) share their words out so that together they
-// store whole 32-byte sectors.
+// store whole 32-byte sectors.  Otherwise a warp's 256 values of a row pass
+// through shared memory and leave one by one, neighbouring lanes neighbouring
+// elements.
 template <int KIND, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const fp4q_operand op, int64_t rows, int64_t K, T *y) {
   constexpr int kRows = 4;
   constexpr bool kShare = VEC && sizeof(T) == 4;
+  __shared__ __align__(16) T turn[VEC ? 1 : kThreads / 32][VEC ? 1 : 256];
+  const int lane = threadIdx.x & 31;
   const int64_t ldq = row_bytes(K), nk = num_atoms_k(KIND, K);
   const int64_t w = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int valid = (int)max((int64_t)0, min((int64_t)8, K - w * 8));
@@ -326,8 +413,20 @@ __global__ void __launch_bounds__(kThreads)
         v[2 * j] = __fmul_rn(f.x, s);
         v[2 * j + 1] = __fmul_rn(f.y, s);
       }
-      if (r0 + i >= rows || valid == 0) continue;
       T *out = y + (r0 + i) * K + w * 8;
+      if constexpr (!VEC) {
+        T *line = turn[threadIdx.x >> 5];
+        pack8::store<true>(line + lane * 8, 8, v);
+        __syncwarp();
+        const int64_t c0 = (w - lane) * 8;   // the warp's first column
+        if (r0 + i < rows)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (c0 + lane + 32 * k < K) y[(r0 + i) * K + c0 + lane + 32 * k] = line[lane + 32 * k];
+        __syncwarp();
+        continue;
+      }
+      if (r0 + i >= rows || valid == 0) continue;
       if constexpr (kShare) {
         out += odd ? -4 : 0;
         *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
@@ -339,18 +438,32 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+template <int KIND, typename T, bool VEC>
+cudaError_t start_quantize(const QuantArgs &a, int64_t tiles, cudaStream_t stream) {
+  auto kernel = quantize_kernel<KIND, T, VEC>;
+  constexpr int smem = (int)sizeof(QuantSmem<KIND, T, VEC>);
+  if (smem > 48 * 1024) {
+    static PerDeviceOnce setup;   // per instantiation
+    if (setup.get([&] {
+          return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+                         cudaSuccess
+                     ? 1
+                     : 0;
+        }) != 1)
+      return cudaErrorInvalidValue;
+  }
+  kernel<<<(unsigned)tiles, kThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
 template <int KIND, typename T>
 cudaError_t run_quantize(const QuantArgs &a, cudaStream_t stream) {
   const int64_t tiles = ((a.cols + kTile - 1) / kTile) * ((a.rows + kTile - 1) / kTile);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  const unsigned grid = (unsigned)tiles;
   const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 &&
                    a.ld * (int64_t)sizeof(T) % 16 == 0 && a.cols % 8 == 0;
-  if (vec)
-    quantize_kernel<KIND, T, true><<<grid, kThreads, 0, stream>>>(a);
-  else
-    quantize_kernel<KIND, T, false><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return vec ? start_quantize<KIND, T, true>(a, tiles, stream)
+             : start_quantize<KIND, T, false>(a, tiles, stream);
 }
 
 }  // namespace
@@ -368,20 +481,33 @@ cudaError_t launch_global(const float *amax, float *global_scale, cudaStream_t s
   return cudaGetLastError();
 }
 
+template <typename T>
+static void start_amax(const void *x, int64_t rows, int64_t cols, int64_t ld, unsigned int *amax,
+                       cudaStream_t stream) {
+  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
+  // about 8 CTAs an SM, each with a batch of loads for its threads
+  const int64_t per_cta = kThreads * (vec ? 8 * 4 : 8);
+  const int64_t gx = std::min<int64_t>((cols + per_cta - 1) / per_cta, 8 * sm_count());
+  const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>(rows, 8 * sm_count() / gx + 1));
+  const T *p = static_cast<const T *>(x);
+  if (vec)
+    amax_kernel<T, true><<<grid, kThreads, 0, stream>>>(p, rows, cols, ld, amax);
+  else
+    amax_kernel<T, false><<<grid, kThreads, 0, stream>>>(p, rows, cols, ld, amax);
+}
+
 cudaError_t launch_amax_ld(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_t ld,
                            float *amax, cudaStream_t stream) {
+  // a dense matrix is one long row for the per-tensor amax
   if ((ld == cols || rows <= 1) && (reinterpret_cast<uintptr_t>(x) & 15u) == 0)
     return launch_amax(x, in_dtype, rows * cols, amax, stream);
   cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(float), stream);
-  if (e != cudaSuccess || rows * cols == 0) return e;
-  const int64_t gx = std::min<int64_t>((cols + 255) / 256, 8);
-  const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>(rows, 8 * sm_count() / gx + 1));
+  if (e != cudaSuccess || rows == 0 || cols == 0) return e;
+  unsigned int *m = reinterpret_cast<unsigned int *>(amax);
   if (in_dtype == FP8Q_DT_BF16)
-    amax_ld_kernel<<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16 *>(x), rows, cols, ld,
-                                             reinterpret_cast<unsigned int *>(amax));
+    start_amax<__nv_bfloat16>(x, rows, cols, ld, m, stream);
   else
-    amax_ld_kernel<<<grid, 256, 0, stream>>>(static_cast<const float *>(x), rows, cols, ld,
-                                             reinterpret_cast<unsigned int *>(amax));
+    start_amax<float>(x, rows, cols, ld, m, stream);
   return cudaGetLastError();
 }
 

@@ -235,15 +235,8 @@ __device__ __forceinline__ void fetch(Slots *s, int stage, int i, const T *p,
 template <typename T>
 __device__ __forceinline__ void take(Pack8<T> &x, Slots *s, int stage, int i) {
 #pragma unroll
-  for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
-    const uint4 t = *reinterpret_cast<const uint4 *>(s[k].slot(stage, i));
-    if constexpr (sizeof(T) == 2) {
-      x.w[0] = t.x, x.w[1] = t.y, x.w[2] = t.z, x.w[3] = t.w;
-    } else {
-      x.v[4 * k] = __uint_as_float(t.x), x.v[4 * k + 1] = __uint_as_float(t.y);
-      x.v[4 * k + 2] = __uint_as_float(t.z), x.v[4 * k + 3] = __uint_as_float(t.w);
-    }
-  }
+  for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+    x.take(k, *reinterpret_cast<const uint4 *>(s[k].slot(stage, i)));
 }
 
 template <typename T, bool GATED>

@@ -29,6 +29,7 @@ struct Pack8<__nv_bfloat16> {
     const uint4 t = *reinterpret_cast<const uint4 *>(p);
     w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
   }
+  __device__ __forceinline__ void take(int, const uint4 &t) { w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w; }
   __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
   __device__ __forceinline__ void load_some(const __nv_bfloat16 *p, int valid) {
     const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
@@ -62,6 +63,11 @@ struct Pack8<float> {
     const float4 b = *(reinterpret_cast<const float4 *>(p) + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  // 16-byte part h of the eight elements
+  __device__ __forceinline__ void take(int h, const uint4 &t) {
+    v[4 * h] = __uint_as_float(t.x), v[4 * h + 1] = __uint_as_float(t.y);
+    v[4 * h + 2] = __uint_as_float(t.z), v[4 * h + 3] = __uint_as_float(t.w);
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
