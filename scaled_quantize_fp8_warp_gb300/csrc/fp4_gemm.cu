@@ -23,6 +23,7 @@
 
 #include "fp4_common.cuh"
 #include "fp4_internal.h"
+#include "fp4_launch.cuh"
 #include "fp4_ptx.cuh"
 #include "fp8_pack8.cuh"
 #include "fp8q_gemm_common.cuh"
@@ -183,6 +184,8 @@ __global__ void __launch_bounds__(320, 1)
     tmem_alloc_pair(slot, L::kTmemCols);
     tmem_relinquish_pair();
   }
+  follow_previous();
+  allow_next();
   tc_fence_before();
   __syncthreads();
   cluster_sync_any();
@@ -333,28 +336,18 @@ int run_pair(const PairMaps &maps, const Args &a, cudaStream_t stream) {
   using L = PairLayout<KIND, WIDTH>;
   auto kernel = gemm_pair_kernel<KIND, T, WIDTH>;
   static PerDeviceOnce setup;  // per instantiation: the pairs that fit at once, 0 on failure
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.blockDim = dim3(320, 1, 1);
-  cfg.dynamicSmemBytes = L::kSmemBytes;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const int pairs = setup.get([&] {
     if (gemm::set_smem(kernel, L::kSmemBytes) != cudaSuccess) return 0;
-    cudaLaunchConfig_t q = cfg;
-    q.gridDim = dim3(2 * (sm_count() / 2), 1, 1);
+    Launch q(2 * (sm_count() / 2), 1, 320, L::kSmemBytes, stream, 2);
     int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, kernel, &q) == cudaSuccess ? n : 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &q.cfg) == cudaSuccess ? n : 0;
   });
   if (pairs < 1) return FP8Q_ERR_CUDA;
   const int units = (a.num_m_tiles + 1) / 2 * a.num_n_tiles;
-  cfg.gridDim = dim3(2 * std::min(units, pairs), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kernel, maps, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+  return Launch(2 * std::min(units, pairs), 1, 320, L::kSmemBytes, stream, 2).run(kernel, maps, a) ==
+                 cudaSuccess
+             ? FP8Q_OK
+             : FP8Q_ERR_CUDA;
 }
 
 // Calls f(width) with the widest store that every row of C allows, as a

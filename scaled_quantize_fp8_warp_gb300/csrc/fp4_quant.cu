@@ -18,6 +18,7 @@
 
 #include "fp4_common.cuh"
 #include "fp4_internal.h"
+#include "fp4_launch.cuh"
 #include "fp8_pack8.cuh"
 
 namespace fp8q {
@@ -206,6 +207,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_ker
   const int rows_in = (int)max((int64_t)0, min((int64_t)8, p.rows - row));
   const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.cols - col));
 
+  follow_previous();
+  allow_next();
   Pack8<T> y[8];
   if constexpr (VEC) {
     const T *x = static_cast<const T *>(p.x) + (rows_in > 0 && cols_in > 0 ? row * p.ld + col : 0);
@@ -324,6 +327,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_ker
 }
 
 __global__ void global_kernel(const float *amax, float *global_scale) {
+  follow_previous();
+  allow_next();
   *global_scale = nv_global(*amax);
 }
 
@@ -334,6 +339,8 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     amax_kernel(const T *x, int64_t rows, int64_t cols, int64_t ld, unsigned int *amax) {
   constexpr int kBatch = 4;   // groups of 8 elements in flight
+  follow_previous();
+  allow_next();
   uint32_t m = 0;
   const int64_t step = (int64_t)gridDim.x * kThreads * (VEC ? 8 : 1);
   const int64_t first = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * (VEC ? 8 : 1);
@@ -386,6 +393,8 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t w = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int valid = (int)max((int64_t)0, min((int64_t)8, K - w * 8));
   const bool odd = threadIdx.x & 1;
+  follow_previous();
+  allow_next();
   const float g = KIND == FP4Q_NVFP4 ? *op.global_scale : 1.0f;
   for (int64_t r0 = (int64_t)blockIdx.y * kRows; r0 < rows; r0 += (int64_t)gridDim.y * kRows) {
     uint32_t code[kRows], byte[kRows];
@@ -452,8 +461,7 @@ cudaError_t start_quantize(const QuantArgs &a, int64_t tiles, cudaStream_t strea
         }) != 1)
       return cudaErrorInvalidValue;
   }
-  kernel<<<(unsigned)tiles, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return Launch((unsigned)tiles, 1, kThreads, smem, stream).run(kernel, a);
 }
 
 template <int KIND, typename T>
@@ -477,23 +485,20 @@ cudaError_t launch_quantize(int kind, int in_dtype, const QuantArgs &a, cudaStre
 }
 
 cudaError_t launch_global(const float *amax, float *global_scale, cudaStream_t stream) {
-  global_kernel<<<1, 1, 0, stream>>>(amax, global_scale);
-  return cudaGetLastError();
+  return Launch(1, 1, 1, 0, stream).run(global_kernel, amax, global_scale);
 }
 
 template <typename T>
-static void start_amax(const void *x, int64_t rows, int64_t cols, int64_t ld, unsigned int *amax,
+static cudaError_t start_amax(const void *x, int64_t rows, int64_t cols, int64_t ld, unsigned int *amax,
                        cudaStream_t stream) {
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
   // about 8 CTAs an SM, each with a batch of loads for its threads
   const int64_t per_cta = kThreads * (vec ? 8 * 4 : 8);
   const int64_t gx = std::min<int64_t>((cols + per_cta - 1) / per_cta, 8 * sm_count());
-  const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>(rows, 8 * sm_count() / gx + 1));
-  const T *p = static_cast<const T *>(x);
-  if (vec)
-    amax_kernel<T, true><<<grid, kThreads, 0, stream>>>(p, rows, cols, ld, amax);
-  else
-    amax_kernel<T, false><<<grid, kThreads, 0, stream>>>(p, rows, cols, ld, amax);
+  const unsigned gy = (unsigned)std::min<int64_t>(rows, 8 * sm_count() / gx + 1);
+  return Launch((unsigned)gx, gy, kThreads, 0, stream)
+      .run(vec ? amax_kernel<T, true> : amax_kernel<T, false>, static_cast<const T *>(x), rows, cols,
+           ld, amax);
 }
 
 cudaError_t launch_amax_ld(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_t ld,
@@ -504,11 +509,8 @@ cudaError_t launch_amax_ld(const void *x, int in_dtype, int64_t rows, int64_t co
   cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(float), stream);
   if (e != cudaSuccess || rows == 0 || cols == 0) return e;
   unsigned int *m = reinterpret_cast<unsigned int *>(amax);
-  if (in_dtype == FP8Q_DT_BF16)
-    start_amax<__nv_bfloat16>(x, rows, cols, ld, m, stream);
-  else
-    start_amax<float>(x, rows, cols, ld, m, stream);
-  return cudaGetLastError();
+  return in_dtype == FP8Q_DT_BF16 ? start_amax<__nv_bfloat16>(x, rows, cols, ld, m, stream)
+                                  : start_amax<float>(x, rows, cols, ld, m, stream);
 }
 
 template <int KIND, typename T>
@@ -516,12 +518,9 @@ static cudaError_t run_dequantize(const fp4q_operand &op, int64_t rows, int64_t 
                                   cudaStream_t stream) {
   const int64_t gx = (K + 8 * kThreads - 1) / (8 * kThreads);
   if (gx > INT32_MAX) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>((rows + 3) / 4, 65535));
-  if (K % 16 == 0)
-    dequantize_kernel<KIND, T, true><<<grid, kThreads, 0, stream>>>(op, rows, K, static_cast<T *>(y));
-  else
-    dequantize_kernel<KIND, T, false><<<grid, kThreads, 0, stream>>>(op, rows, K, static_cast<T *>(y));
-  return cudaGetLastError();
+  return Launch((unsigned)gx, (unsigned)std::min<int64_t>((rows + 3) / 4, 65535), kThreads, 0, stream)
+      .run(K % 16 == 0 ? dequantize_kernel<KIND, T, true> : dequantize_kernel<KIND, T, false>, op,
+           rows, K, static_cast<T *>(y));
 }
 
 cudaError_t launch_dequantize(int kind, const fp4q_operand &op, int64_t rows, int64_t K,

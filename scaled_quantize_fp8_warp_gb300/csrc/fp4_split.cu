@@ -23,6 +23,7 @@
 
 #include "fp4_common.cuh"
 #include "fp4_internal.h"
+#include "fp4_launch.cuh"
 #include "fp4_ptx.cuh"
 #include "fp8_pack8.cuh"
 #include "fp8q_gemm_common.cuh"
@@ -110,6 +111,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_alloc(smem_u32(slot_ptr), kTmemCols);
     tmem_relinquish();
   }
+  follow_previous();
+  allow_next();
   float g = 1.0f, rg = 1.0f;
   if (kQuantize && KIND == FP4Q_NVFP4) {
     g = nv_global(*p.x_amax);
@@ -374,22 +377,6 @@ bool set_up(Kernel kernel) {
                               cudaSharedmemCarveoutMaxShared) == cudaSuccess;
 }
 
-cudaLaunchConfig_t launch_config(unsigned grid, int split, cudaLaunchAttribute *attr,
-                                 cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = (unsigned)split;
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
-}
-
 // Clusters of 1 .. kMaxSplit CTAs that run at once on the current device: a
 // cluster keeps to one of the GPU's partitions, so fewer CTAs fit as sixes or
 // sevens than alone.  Every instantiation has the same block, shared memory
@@ -405,9 +392,9 @@ const int *clusters_at_once() {
     auto kernel = split_kernel<FP4Q_MXFP4, void>;
     if (!set_up(kernel)) return 0;
     for (int s = 1; s <= kMaxSplit; ++s) {
-      cudaLaunchAttribute attr;
-      cudaLaunchConfig_t cfg = launch_config(s, s, &attr, nullptr);
-      if (cudaOccupancyMaxActiveClusters(&fit[dev][s - 1], kernel, &cfg) != cudaSuccess ||
+      Launch q(s, 1, kThreads, kSmemBytes, nullptr, s);
+      q.cfg.numAttrs = 2;   // the query wants the cluster size, one included
+      if (cudaOccupancyMaxActiveClusters(&fit[dev][s - 1], kernel, &q.cfg) != cudaSuccess ||
           fit[dev][s - 1] < 1)
         return 0;
       fit[dev][s - 1] *= 2;
@@ -432,9 +419,10 @@ int run_split(const Maps &maps, const Args &a, int64_t tiles, cudaStream_t strea
   auto kernel = split_kernel<KIND, XT>;
   static PerDeviceOnce setup;  // per instantiation
   if (setup.get([&] { return set_up(kernel) ? 1 : 0; }) != 1) return FP8Q_ERR_CUDA;
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = launch_config((unsigned)(tiles * a.split), a.split, &attr, stream);
-  return cudaLaunchKernelEx(&cfg, kernel, maps, a) == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA;
+  return Launch((unsigned)(tiles * a.split), 1, kThreads, kSmemBytes, stream, a.split)
+                     .run(kernel, maps, a) == cudaSuccess
+             ? FP8Q_OK
+             : FP8Q_ERR_CUDA;
 }
 
 }  // namespace

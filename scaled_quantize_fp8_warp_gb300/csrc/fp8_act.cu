@@ -13,6 +13,7 @@
 
 #include <algorithm>
 
+#include "fp4_launch.cuh"
 #include "fp8_act.h"
 #include "fp8_pack8.cuh"
 
@@ -251,6 +252,8 @@ __global__ void __launch_bounds__(kThreads, 3) forward_kernel(const ForwardArgs 
   auto &in = *reinterpret_cast<ForwardSmem<T, GATED> *>(smem);
   const int lane = threadIdx.x & 31;
   const Walk walk(p.T, p.F);
+  follow_previous();
+  allow_next();
   const int64_t apart = 2 * walk.step;
   for (int64_t tile = walk.tile; tile < walk.tiles; tile += walk.tile_step) {
     const int64_t col = tile * 128 + (lane & 15) * 8;
@@ -343,6 +346,8 @@ template <int ACT, typename T, bool GATED, bool VEC>
 __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardArgs p) {
   const int lane = threadIdx.x & 31;
   const Walk walk(p.T, p.F);
+  follow_previous();
+  allow_next();
   const int64_t apart = 2 * walk.step;
   for (int64_t tile = walk.tile; tile < walk.tiles; tile += walk.tile_step) {
     const int64_t col = tile * 128 + (lane & 15) * 8;
@@ -424,24 +429,22 @@ bool vec_ok(const void *p, int64_t ld, int64_t size) {
 
 template <int ACT, typename T, bool GATED, bool VEC>
 cudaError_t run_forward(const ForwardArgs &a, cudaStream_t stream) {
-  constexpr auto kernel = forward_kernel<ACT, T, GATED, VEC>;
+  auto kernel = forward_kernel<ACT, T, GATED, VEC>;
   constexpr int smem = VEC ? (int)sizeof(ForwardSmem<T, GATED>) : 0;
   struct Tag {};   // a set-up of its own for every kernel of this signature
   const int grid = grid_for<Tag>(kernel, smem, a.T, a.F);
   if (grid < 1) return cudaErrorInvalidValue;
-  kernel<<<grid, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return Launch((unsigned)grid, 1, kThreads, smem, stream).run(kernel, a);
 }
 
 template <int ACT, typename T, bool GATED, bool VEC>
 cudaError_t run_backward(const BackwardArgs &a, cudaStream_t stream) {
-  constexpr auto kernel = backward_kernel<ACT, T, GATED, VEC>;
+  auto kernel = backward_kernel<ACT, T, GATED, VEC>;
   constexpr int smem = 0;
   struct Tag {};
   const int grid = grid_for<Tag>(kernel, smem, a.T, a.F);
   if (grid < 1) return cudaErrorInvalidValue;
-  kernel<<<grid, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return Launch((unsigned)grid, 1, kThreads, smem, stream).run(kernel, a);
 }
 
 template <int ACT, typename T, bool GATED>
