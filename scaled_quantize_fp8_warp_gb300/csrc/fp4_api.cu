@@ -32,6 +32,11 @@ bool dims_ok(int64_t rows, int64_t cols) {
   return cols == 0 || rows + 128 <= kLim / (cols + 128);
 }
 
+// Row and column indexes of the activation kernels are 32-bit (offsets are not).
+bool act_dims_ok(int64_t T, int64_t F) {
+  return dims_ok(T, F) && T <= INT32_MAX / 4 && F <= INT32_MAX / 4;
+}
+
 // Matrix argument [rows, cols] with rows ld elements apart; `align` in bytes.
 int check_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t align) {
   if (rows == 0 || cols == 0) return FP8Q_OK;
@@ -293,7 +298,7 @@ int fp4_linear_train(const void *x, const void *w, const void *g, int in_dtype, 
 int fp8_act_forward(int act, int dtype, int64_t T, int64_t F, const void *u, int64_t ldu,
                     const void *v, int64_t ldv, void *a, int64_t lda, uint8_t *u8,
                     float *u_scales, uint8_t *v8, float *v_scales, cudaStream_t stream) {
-  if (act < FP8Q_ACT_SILU || act > FP8Q_ACT_GELU_TANH || !valid_dtype(dtype) || !dims_ok(T, F))
+  if (act < FP8Q_ACT_SILU || act > FP8Q_ACT_GELU_TANH || !valid_dtype(dtype) || !act_dims_ok(T, F))
     return FP8Q_ERR_INVALID_ARG;
   const int64_t size = dtype_size(dtype);
   const bool gated = v != nullptr;
@@ -331,7 +336,7 @@ int fp8_act_backward(int act, int dtype, int64_t T, int64_t F, const uint8_t *u8
                      const float *u_scales, const uint8_t *v8, const float *v_scales,
                      const void *da, int64_t ldda, void *du, int64_t lddu, void *dv,
                      int64_t lddv, void *a, int64_t lda, cudaStream_t stream) {
-  if (act < FP8Q_ACT_SILU || act > FP8Q_ACT_GELU_TANH || !valid_dtype(dtype) || !dims_ok(T, F))
+  if (act < FP8Q_ACT_SILU || act > FP8Q_ACT_GELU_TANH || !valid_dtype(dtype) || !act_dims_ok(T, F))
     return FP8Q_ERR_INVALID_ARG;
   const int64_t size = dtype_size(dtype);
   const bool gated = v8 != nullptr;

@@ -84,25 +84,24 @@ __device__ __forceinline__ float nv_ratio(float amax, float g, float rg) {
 // too small (d >= 448e-12 > 2^-32 wherever the quotient is past 6).
 constexpr uint32_t kCarefulBits = 0x6F800000u;   // 2^96
 
-// Codes of two elements of a block, given negated (the first in the low four
-// bits); r = RN(1 / d).  MXFP4: d is a power of two and the product exact.
-// NVFP4: RN(x / d) by Markstein's correction, signs arranged so that a zero
-// quotient keeps x's sign: q0 = x r, e = q0 d - x, q = q0 - e r.
+// -q for two elements of a block, q the quotient by its d; r = RN(1 / d).
+// MXFP4: d is a power of two and the product exact.  NVFP4: RN(x / d) by
+// Markstein's correction; as -q (q0 = x (-r), e = q0 d + x, e (-r) + q0), because
+// a zero quotient then has the sign opposite to x's whatever that is.
 template <int KIND>
-__device__ __forceinline__ uint32_t encode2(float2 y, float d, float r) {
+__device__ __forceinline__ uint32_t encode2(float2 x, float d, float r) {
   const float2 nr = make_float2(-r, -r);
-  float2 q = __fmul2_rn(y, nr);
-  if (KIND == FP4Q_NVFP4) q = __ffma2_rn(__ffma2_rn(q, make_float2(d, d), y), nr, q);
+  float2 q = __fmul2_rn(x, nr);
+  if (KIND == FP4Q_NVFP4) q = __ffma2_rn(__ffma2_rn(q, make_float2(d, d), x), nr, q);
   return e2m1x2(q.x, q.y);
 }
 
-// Codes of eight elements given as negated pairs, element j in bits
-// [4j, 4j + 4).
+// Codes of eight elements, element j in bits [4j, 4j + 4); the signs turn here.
 template <int KIND>
-__device__ __forceinline__ uint32_t encode8(const float2 (&y)[4], float d, float r) {
-  const uint32_t lo = __byte_perm(encode2<KIND>(y[0], d, r), encode2<KIND>(y[1], d, r), 0x0040);
-  const uint32_t hi = __byte_perm(encode2<KIND>(y[2], d, r), encode2<KIND>(y[3], d, r), 0x0040);
-  return __byte_perm(lo, hi, 0x5410);
+__device__ __forceinline__ uint32_t encode8(const float2 (&x)[4], float d, float r) {
+  const uint32_t lo = __byte_perm(encode2<KIND>(x[0], d, r), encode2<KIND>(x[1], d, r), 0x0040);
+  const uint32_t hi = __byte_perm(encode2<KIND>(x[2], d, r), encode2<KIND>(x[3], d, r), 0x0040);
+  return __byte_perm(lo, hi, 0x5410) ^ 0x88888888u;
 }
 
 // 1 / d of an MXFP4 block by scale byte: d = 2^(byte - 127) and the byte is
@@ -121,10 +120,10 @@ __device__ __forceinline__ uint32_t mx_byte(uint32_t amax_bits) {
 // The careful path: scale byte and codes of eight elements for any maximum
 // and any tensor scale.
 template <int KIND>
-__device__ __noinline__ uint32_t encode8_careful(float2 y0, float2 y1, float2 y2, float2 y3,
+__device__ __noinline__ uint32_t encode8_careful(float2 x0, float2 x1, float2 x2, float2 x3,
                                                  uint32_t amax_bits, float g, uint32_t *byte) {
   bool nan = amax_bits >= 0x7F800000u;
-  float2 y[4] = {y0, y1, y2, y3};
+  float2 x[4] = {x0, x1, x2, x3};
   float d = 0.0f, r;
   if (KIND == FP4Q_MXFP4) {
     *byte = nan ? 0xFFu : mx_byte(amax_bits);
@@ -141,9 +140,9 @@ __device__ __noinline__ uint32_t encode8_careful(float2 y0, float2 y1, float2 y2
     const float lim = 6.5f * d;   // past 6 d the code is 6's
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      y[k] = make_float2(fminf(fmaxf(y[k].x, -lim), lim), fminf(fmaxf(y[k].y, -lim), lim));
+      x[k] = make_float2(fminf(fmaxf(x[k].x, -lim), lim), fminf(fmaxf(x[k].y, -lim), lim));
   }
-  return nan ? 0u : encode8<KIND>(y, d, r);
+  return nan ? 0u : encode8<KIND>(x, d, r);
 }
 
 // Values of the two codes in a byte, the low one first: exact in fp32.

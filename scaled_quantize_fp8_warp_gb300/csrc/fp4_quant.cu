@@ -231,9 +231,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_ker
     if (p.global_scale != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.global_scale = g;
     __syncthreads();
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i].negate();   // encode8 takes the negated elements
-
   if (p.q != nullptr) {
     const int64_t ldq = row_bytes(p.cols);
     uint8_t *q = p.q + row * ldq + col / 2;

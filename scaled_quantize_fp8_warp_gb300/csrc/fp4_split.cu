@@ -239,7 +239,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) m[i] = max(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
         top = max(top, m[i]);
-        y[i].negate();
       }
       if (!__any_sync(0xFFFFFFFFu, top >= kCarefulBits || g_bad)) {
         if (KIND == FP4Q_NVFP4) {   // the two lanes of a block find two rows' scales each

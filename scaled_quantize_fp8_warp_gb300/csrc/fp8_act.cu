@@ -4,8 +4,8 @@
 // 1e-12), RNE of the correctly rounded quotient x / s, reached by one
 // reciprocal per tile and Markstein's correction).
 //
-// A warp works on pieces of 2 rows x 128 columns, 16 lanes of 8 columns to a
-// tile, two pieces at a time.
+// A warp works on 2 rows x 256 columns at a time: two tiles of each row, 16
+// lanes of 8 columns to a tile.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
@@ -69,22 +69,25 @@ __device__ __forceinline__ float tile_scale(uint32_t amax_bits) {
   return s < 1e-12f ? 1e-12f : s;
 }
 
-// E4M3 bytes of eight elements, given negated, under a finite scale s with
-// r = RN(1 / s): RN(x / s) by Markstein's correction, a zero keeping x's sign.
+// E4M3 bytes of eight elements under a finite scale s with r = RN(1 / s):
+// RN(x / s) by Markstein's correction.  Found as -q (q0 = x (-r), e = q0 s + x,
+// q = e (-r) + q0), whose sign bits are turned at the end, so that a zero
+// keeps x's sign.
 template <typename T>
-__device__ __forceinline__ uint2 cast8(const Pack8<T> &y, float s, float r) {
+__device__ __forceinline__ uint2 cast8(const Pack8<T> &x, float s, float r) {
   uint32_t b[4];
   const float2 nr = make_float2(-r, -r), s2 = make_float2(s, s);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float2 v = y.pair(k), q = __fmul2_rn(v, nr);
+    const float2 v = x.pair(k), q = __fmul2_rn(v, nr);
     b[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(__ffma2_rn(__ffma2_rn(q, s2, v), nr, q),
                                               __NV_SATFINITE, __NV_E4M3);
   }
-  return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
+  return make_uint2(__byte_perm(b[0], b[1], 0x5410) ^ 0x80808080u,
+                    __byte_perm(b[2], b[3], 0x5410) ^ 0x80808080u);
 }
 
-// One element, not negated, of a tile that is not finite: a NaN keeps its
+// One element of a tile that is not finite: a NaN keeps its
 // sign, a NaN that the division makes is 0x7F, and all else is a zero (s is
 // infinite or NaN).
 __device__ __noinline__ uint32_t cast1_careful(float x, float s) {
@@ -95,11 +98,11 @@ __device__ __noinline__ uint32_t cast1_careful(float x, float s) {
 }
 
 template <typename T>
-__device__ __forceinline__ uint2 cast8_any(const Pack8<T> &y, float s, float r) {
-  if (s < __uint_as_float(0x7F800000u)) return cast8(y, s, r);
+__device__ __forceinline__ uint2 cast8_any(const Pack8<T> &x, float s, float r) {
+  if (s < __uint_as_float(0x7F800000u)) return cast8(x, s, r);
   uint32_t b[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = cast1_careful(-y.at(j), s);
+  for (int j = 0; j < 8; ++j) b[j] = cast1_careful(x.at(j), s);
   return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24),
                     b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
 }
@@ -107,7 +110,7 @@ __device__ __forceinline__ uint2 cast8_any(const Pack8<T> &y, float s, float r) 
 template <bool VEC>
 __device__ __forceinline__ void store_bytes(uint8_t *p, int valid, uint2 w) {
   if (VEC) {
-    if (valid > 0) *reinterpret_cast<uint2 *>(p) = w;
+    if (valid > 0) __stcs(reinterpret_cast<uint2 *>(p), w);
     return;
   }
 #pragma unroll
@@ -137,37 +140,57 @@ __device__ __forceinline__ void saved(uint2 w, float s, float (&v)[8]) {
   }
 }
 
-// One warp keeps to one tile column and walks down the rows, two row pairs at
-// a time (`step` pairs apart, so that four rows' loads are in flight), with
-// pointers that advance by constants.  Lanes 0-15 have a pair's first row.
+// One warp keeps to one strip of two tile columns (256 columns) and walks down
+// consecutive row pairs of it, with pointers that advance by constants; the
+// second tile lies at constant offsets from the first.  Lanes 0-15 have a
+// pair's first row.
 struct Walk {
-  int64_t tile, tile_step, tiles;   // tile columns this warp serves
-  int64_t pair0, pairs, step;
+  int strip, strip_step, strips;   // strips this warp serves
+  int pair0, pairs;                // and row pairs [pair0, pairs) of each
   __device__ __forceinline__ Walk(int64_t T, int64_t F) {
-    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t all = (int64_t)gridDim.x * (kThreads / 32);
-    tiles = (F + 127) / 128;
-    pairs = (T + 1) / 2;
-    step = max(all / tiles, (int64_t)1);              // warps per tile column
-    tile_step = all < tiles ? all : tiles;
-    pair0 = w / tiles;
-    tile = pair0 < step ? w - pair0 * tiles : tiles;  // the warps left over have none
+    const int w = (int)blockIdx.x * (kThreads / 32) + (int)(threadIdx.x >> 5);
+    const int all = (int)gridDim.x * (kThreads / 32);
+    strips = (int)((F + 255) / 256);
+    const int total = (int)((T + 1) / 2), share = max(all / strips, 1);   // warps per strip
+    const int per = (total + share - 1) / share, mine = w / strips;
+    strip_step = all < strips ? all : strips;
+    strip = mine < share ? w - mine * strips : strips;   // the warps left over have none
+    pair0 = mine * per;
+    pairs = min(total, pair0 + per);
   }
 };
 
-// Scales and reciprocals of the four tiles (two pieces of u, v) of a half warp
-// from the lanes' maxima: the halving steps leave piece 0's maxima in even
-// lanes and piece 1's in odd ones, each lane finds one tile's scale (lane bit
+// This lane's columns in a strip: the first of its eight in the first tile
+// (those in the second are 128 further on), and how many of each exist.
+struct Columns {
+  int64_t col;
+  int in[2];
+  __device__ __forceinline__ Columns(int strip, int64_t F) {
+    col = (int64_t)strip * 256 + (threadIdx.x & 15) * 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      in[i] = (int)max((int64_t)0, min((int64_t)8, F - (col + 128 * i)));
+    if (in[0] == 0) col = 0;   // nothing is addressed where nothing is valid
+  }
+};
+
+// Scales and reciprocals of the four tiles (two of u, two of v) of a half warp
+// from the lanes' maxima: the halving steps leave tile 0's maxima in even
+// lanes and tile 1's in odd ones, each lane finds one tile's scale (lane bit
 // 1: u or v), and the results are handed round.
 struct Scales {
-  float s[2][2], r[2][2];   // [piece][u, v]
+  float s[2][2], r[2][2];   // [tile][u, v]
   bool finite;              // all four of every half warp
 };
 
 __device__ __forceinline__ void finish_scales(uint32_t mine, Scales &out) {
   const int lane = threadIdx.x & 31;
-  const float s = tile_scale(mine);
   out.finite = __all_sync(0xFFFFFFFFu, mine < 0x7F800000u);
+  // RN(m / 448) by Markstein's correction, exact where it is not below 1e-12
+  const float m = __uint_as_float(mine), c = 1.0f / 448.0f, q = __fmul_rn(m, c);
+  float s = __fmaf_rn(__fmaf_rn(q, -448.0f, m), c, q);
+  s = s < 1e-12f ? 1e-12f : s;
+  if (!out.finite) s = tile_scale(mine);
   const float r = __frcp_rn(s);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -200,7 +223,7 @@ __device__ __forceinline__ void find_scales(const Pack8<float> (&u)[2], const Pa
                                             Scales &out) {
   const int lane = threadIdx.x & 31;
   const bool odd = lane & 1, two = lane & 2;
-  uint32_t m[2];   // u, v of this lane's piece
+  uint32_t m[2];   // u, v of this lane's tile
 #pragma unroll
   for (int k = 0; k < (GATED ? 2 : 1); ++k) {
     const uint32_t a = k ? v[0].amax_bits() : u[0].amax_bits();
@@ -215,10 +238,10 @@ __device__ __forceinline__ void find_scales(const Pack8<float> (&u)[2], const Pa
   finish_scales(t, out);
 }
 
-// The rows of a step: two, `apart` rows apart; each thread keeps kStages steps'
-// inputs in shared memory slots of its own, filled by asynchronous copies two
-// steps ahead (VEC) -- no thread reads another's, so no barrier is needed.
-constexpr int kStages = 3;
+// Each thread keeps kStages steps' inputs (two tiles of one row) in shared
+// memory slots of its own, filled by asynchronous copies a step ahead (VEC)
+// -- no thread reads another's, so no barrier is needed.
+constexpr int kStages = 2;
 
 struct __align__(16) Slots {
   uint8_t at[kStages][2][kThreads * 16];
@@ -247,44 +270,47 @@ struct ForwardSmem {
 };
 
 template <int ACT, typename T, bool GATED, bool VEC>
-__global__ void __launch_bounds__(kThreads, 3) forward_kernel(const ForwardArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   auto &in = *reinterpret_cast<ForwardSmem<T, GATED> *>(smem);
   const int lane = threadIdx.x & 31;
   const Walk walk(p.T, p.F);
   follow_previous();
   allow_next();
-  const int64_t apart = 2 * walk.step;
-  for (int64_t tile = walk.tile; tile < walk.tiles; tile += walk.tile_step) {
-    const int64_t col = tile * 128 + (lane & 15) * 8;
-    const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.F - col));
-    int64_t row = 2 * walk.pair0 + (lane >> 4);
-    const int64_t c = cols_in > 0 ? col : 0;   // nothing is addressed where nothing is valid
-    const T *pu = static_cast<const T *>(p.u) + row * p.ldu + c;
-    const T *pv = static_cast<const T *>(p.v) + (GATED ? row * p.ldv + c : 0);
-    T *pa = static_cast<T *>(p.a) + row * p.lda + c;
-    int64_t at8 = row * p.F + c, at_s = tile * p.T + row;
-    int64_t next = row;   // first row of the next step to fetch
+  constexpr int rows = 2;   // from one step to the next
+  const int T_rows = (int)p.T, tiles = (int)((p.F + 127) / 128);
+  for (int strip = walk.strip; strip < walk.strips; strip += walk.strip_step) {
+    const Columns c(strip, p.F);
+    int row = 2 * walk.pair0 + (lane >> 4);
+    const T *pu = static_cast<const T *>(p.u) + row * p.ldu + c.col;
+    const T *pv = static_cast<const T *>(p.v) + (GATED ? row * p.ldv + c.col : 0);
+    T *pa = static_cast<T *>(p.a) + row * p.lda + c.col;
+    uint8_t *u8 = p.u8 + row * p.F + c.col, *v8 = p.v8 + (GATED ? row * p.F + c.col : 0);
+    // scales of the last 16 steps: step k's in lanes k (first row) and 16 + k, so
+    // that they leave as 32 neighbouring rows
+    float *us = p.u_scales + 2 * (int64_t)strip * p.T, *vs = p.v_scales + (GATED ? 2 * (int64_t)strip * p.T : 0);
+    float keep[2][2];
+    int next = row;   // row of the next step to fetch
     auto fetch_step = [&](int stage) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const bool on = next + i * apart < p.T && cols_in > 0;
-        fetch<T>(in.x, stage, i, on ? pu + i * apart * p.ldu : static_cast<const T *>(p.u), on);
-        if (GATED) fetch<T>(in.x + in.kV, stage, i, on ? pv + i * apart * p.ldv : static_cast<const T *>(p.v), on);
+        const bool on = next < T_rows && c.in[i] > 0;
+        fetch<T>(in.x, stage, i, on ? pu + 128 * i : static_cast<const T *>(p.u), on);
+        if (GATED) fetch<T>(in.x + in.kV, stage, i, on ? pv + 128 * i : static_cast<const T *>(p.v), on);
       }
       pack8::copy_commit();
-      next += 2 * apart;
-      pu += 2 * apart * p.ldu;
-      pv += 2 * apart * p.ldv;
+      next += rows;
+      pu += rows * p.ldu;
+      if (GATED) pv += rows * p.ldv;
     };
     if (VEC)
       for (int k = 0; k < kStages - 1; ++k) fetch_step(k);
     int stage = 0;
-    for (int64_t pair = walk.pair0; pair < walk.pairs; pair += apart) {
+    for (int pair = walk.pair0; pair < walk.pairs; ++pair) {
       Pack8<T> u[2], v[2];
       int valid[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) valid[i] = row + i * apart < p.T ? cols_in : 0;
+      for (int i = 0; i < 2; ++i) valid[i] = row < T_rows ? c.in[i] : 0;
       if (VEC) {
         fetch_step(stage == 0 ? kStages - 1 : stage - 1);
         pack8::copy_wait<kStages - 1>();
@@ -297,18 +323,32 @@ __global__ void __launch_bounds__(kThreads, 3) forward_kernel(const ForwardArgs 
       } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          u[i].load_some(pu + (valid[i] > 0 ? i * apart * p.ldu : 0), valid[i]);
-          if (GATED) v[i].load_some(pv + (valid[i] > 0 ? i * apart * p.ldv : 0), valid[i]);
+          u[i].load_some(valid[i] > 0 ? pu + 128 * i : static_cast<const T *>(p.u), valid[i]);
+          if (GATED) v[i].load_some(valid[i] > 0 ? pv + 128 * i : static_cast<const T *>(p.v), valid[i]);
         }
-        pu += 2 * apart * p.ldu;
-        pv += 2 * apart * p.ldv;
+        pu += rows * p.ldu;
+        if (GATED) pv += rows * p.ldv;
       }
       Scales sc;
       find_scales<GATED>(u, v, sc);
+      const int k = (pair - walk.pair0) & 15;
+      if ((lane & 15) == k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) keep[i][0] = sc.s[i][0], keep[i][1] = sc.s[i][1];
+      }
+      if (k == 15 || pair == walk.pairs - 1) {
+        const int at = 2 * (pair - k + (lane & 15)) + (lane >> 4);
+        if ((lane & 15) <= k && at < T_rows) {
+          us[at] = keep[0][0];
+          if (GATED) vs[at] = keep[0][1];
+          if (2 * strip + 1 < tiles) {
+            us[p.T + at] = keep[1][0];
+            if (GATED) vs[p.T + at] = keep[1][1];
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        u[i].negate();
-        if (GATED) v[i].negate();
         uint2 bu, bv;
         if (sc.finite) {
           bu = cast8(u[i], sc.s[i][0], sc.r[i][0]);
@@ -318,27 +358,23 @@ __global__ void __launch_bounds__(kThreads, 3) forward_kernel(const ForwardArgs 
           if (GATED) bv = cast8_any(v[i], sc.s[i][1], sc.r[i][1]);
         }
         if (valid[i] > 0) {
-          store_bytes<VEC>(p.u8 + at8 + i * apart * p.F, valid[i], bu);
-          if (GATED) store_bytes<VEC>(p.v8 + at8 + i * apart * p.F, valid[i], bv);
-          if ((lane & 15) == 0) {
-            p.u_scales[at_s + i * apart] = sc.s[i][0];
-            if (GATED) p.v_scales[at_s + i * apart] = sc.s[i][1];
-          }
+          store_bytes<VEC>(u8 + 128 * i, valid[i], bu);
+          if (GATED) store_bytes<VEC>(v8 + 128 * i, valid[i], bv);
           float out[8], unused;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            activation<ACT, false>(-u[i].at(j), out[j], unused);
-            out[j] = GATED ? -out[j] * v[i].at(j) : out[j];
+            activation<ACT, false>(u[i].at(j), out[j], unused);
+            if (GATED) out[j] *= v[i].at(j);
           }
-          store<VEC>(pa + i * apart * p.lda, valid[i], out);
+          store<VEC, true>(pa + 128 * i, valid[i], out);
         }
       }
-      row += 2 * apart;
-      pa += 2 * apart * p.lda;
-      at8 += 2 * apart * p.F;
-      at_s += 2 * apart;
+      row += rows;
+      pa += rows * p.lda;
+      u8 += rows * p.F;
+      if (GATED) v8 += rows * p.F;
     }
-    if (VEC) pack8::copy_wait<0>();   // the slots are free for the next tile column
+    if (VEC) pack8::copy_wait<0>();   // the slots are free for the next strip
   }
 }
 
@@ -348,33 +384,34 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardArg
   const Walk walk(p.T, p.F);
   follow_previous();
   allow_next();
-  const int64_t apart = 2 * walk.step;
-  for (int64_t tile = walk.tile; tile < walk.tiles; tile += walk.tile_step) {
-    const int64_t col = tile * 128 + (lane & 15) * 8;
-    const int cols_in = (int)max((int64_t)0, min((int64_t)8, p.F - col));
-    int64_t row = 2 * walk.pair0 + (lane >> 4);
-    const int64_t c = cols_in > 0 ? col : 0;
-    const T *pd = static_cast<const T *>(p.da) + row * p.ldda + c;
-    T *pu = static_cast<T *>(p.du) + row * p.lddu + c;
-    T *pv = static_cast<T *>(p.dv) + (GATED ? row * p.lddv + c : 0);
-    T *pa = static_cast<T *>(p.a) + row * p.lda + c;
-    int64_t at8 = row * p.F + c, at_s = tile * p.T + row;
-    for (int64_t pair = walk.pair0; pair < walk.pairs; pair += apart) {
+  constexpr int rows = 2;
+  const int T_rows = (int)p.T;
+  for (int strip = walk.strip; strip < walk.strips; strip += walk.strip_step) {
+    const Columns c(strip, p.F);
+    int row = 2 * walk.pair0 + (lane >> 4);
+    const T *pd = static_cast<const T *>(p.da) + row * p.ldda + c.col;
+    T *pu = static_cast<T *>(p.du) + row * p.lddu + c.col;
+    T *pv = static_cast<T *>(p.dv) + (GATED ? row * p.lddv + c.col : 0);
+    T *pa = static_cast<T *>(p.a) + row * p.lda + c.col;
+    const uint8_t *u8 = p.u8 + row * p.F + c.col, *v8 = p.v8 + (GATED ? row * p.F + c.col : 0);
+    const float *us = p.u_scales + 2 * (int64_t)strip * p.T + row;
+    const float *vs = p.v_scales + (GATED ? 2 * (int64_t)strip * p.T + row : 0);
+    for (int pair = walk.pair0; pair < walk.pairs; ++pair) {
       Pack8<T> d[2];
       uint2 bu[2], bv[2];
       float su[2], sv[2];
       int valid[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        valid[i] = row + i * apart < p.T ? cols_in : 0;
+        valid[i] = row < T_rows ? c.in[i] : 0;
         if (valid[i] > 0) {
-          bu[i] = load_bytes<VEC>(p.u8 + at8 + i * apart * p.F, valid[i]);
-          su[i] = p.u_scales[at_s + i * apart];
+          bu[i] = load_bytes<VEC>(u8 + 128 * i, valid[i]);
+          su[i] = us[i * p.T];
           if (GATED) {
-            bv[i] = load_bytes<VEC>(p.v8 + at8 + i * apart * p.F, valid[i]);
-            sv[i] = p.v_scales[at_s + i * apart];
+            bv[i] = load_bytes<VEC>(v8 + 128 * i, valid[i]);
+            sv[i] = vs[i * p.T];
           }
-          pack8::load<VEC>(d[i], pd + i * apart * p.ldda, valid[i]);
+          pack8::load<VEC>(d[i], pd + 128 * i, valid[i]);
         }
       }
 #pragma unroll
@@ -392,17 +429,21 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardArg
           dv[j] = da * f;
           out[j] = GATED ? f * v[j] : f;
         }
-        store<VEC>(pu + i * apart * p.lddu, valid[i], du);
-        if (GATED) store<VEC>(pv + i * apart * p.lddv, valid[i], dv);
-        if (p.a != nullptr) store<VEC>(pa + i * apart * p.lda, valid[i], out);
+        store<VEC, true>(pu + 128 * i, valid[i], du);
+        if (GATED) store<VEC, true>(pv + 128 * i, valid[i], dv);
+        if (p.a != nullptr) store<VEC, true>(pa + 128 * i, valid[i], out);
       }
-      row += 2 * apart;
-      pd += 2 * apart * p.ldda;
-      pu += 2 * apart * p.lddu;
-      pv += 2 * apart * p.lddv;
-      pa += 2 * apart * p.lda;
-      at8 += 2 * apart * p.F;
-      at_s += 2 * apart;
+      row += rows;
+      pd += rows * p.ldda;
+      pu += rows * p.lddu;
+      pa += rows * p.lda;
+      u8 += rows * p.F;
+      us += rows;
+      if (GATED) {
+        pv += rows * p.lddv;
+        v8 += rows * p.F;
+        vs += rows;
+      }
     }
   }
 }
@@ -419,7 +460,7 @@ int grid_for(Kernel kernel, int smem, int64_t T, int64_t F) {
       return 0;
     return n * sm_count();
   });
-  const int64_t warps = ((T + 1) / 2) * ((F + 127) / 128);
+  const int64_t warps = ((T + 1) / 2) * ((F + 255) / 256);
   return (int)std::min<int64_t>((warps + kThreads / 32 - 1) / (kThreads / 32), fit);
 }
 

@@ -44,10 +44,6 @@ struct Pack8<__nv_bfloat16> {
   __device__ __forceinline__ float at(int j) const {
     return __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
   }
-  __device__ __forceinline__ void negate() {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] ^= 0x80008000u;
-  }
   // max |element| as an fp32 bit pattern (NaN sorts above infinity)
   __device__ __forceinline__ uint32_t amax_bits() const {
     const uint32_t m = max_abs2(max_abs2(w[0], w[1]), max_abs2(w[2], w[3])) & 0x7FFF7FFFu;
@@ -79,10 +75,6 @@ struct Pack8<float> {
   }
   __device__ __forceinline__ float2 pair(int k) const { return make_float2(v[2 * k], v[2 * k + 1]); }
   __device__ __forceinline__ float at(int j) const { return v[j]; }
-  __device__ __forceinline__ void negate() {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = -v[j];
-  }
   __device__ __forceinline__ uint32_t amax_bits() const {
     uint32_t m = 0;
 #pragma unroll
@@ -110,17 +102,27 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// VEC: p is 16-byte aligned and valid is 0 or 8.
-template <bool VEC, typename T>
+template <bool STREAM, typename V>
+__device__ __forceinline__ void put(V *p, V v) {
+  if (STREAM)
+    __stcs(p, v);
+  else
+    *p = v;
+}
+
+// VEC: p is 16-byte aligned and valid is 0 or 8.  STREAM: first out of L2 (a
+// large result that is not read here; 2-4% of the activation kernels' time).
+template <bool VEC, bool STREAM = false, typename T>
 __device__ __forceinline__ void store(T *p, int valid, const float (&v)[8]) {
   if (VEC) {
     if (valid <= 0) return;
     if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]),
-                                                 bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+      put<STREAM>(reinterpret_cast<uint4 *>(p),
+                  make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                             bf16x2(v[6], v[7])));
     } else {
-      *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      *(reinterpret_cast<float4 *>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+      put<STREAM>(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+      put<STREAM>(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
     }
     return;
   }
