@@ -43,64 +43,101 @@ struct Args {
   int num_steps;            // MMAs of 64 K over all of K
   int atoms_k;              // scale atoms along K
   int group;                // raster: tile rows visited together
-  uint32_t idesc;
   void *C;
   const float *ga, *gb;     // NVFP4 tensor scales
   unsigned int *err;
 };
 
-// One K block in the ring slot at `sa` (A, B, A's atoms, B's atoms of its two
-// row blocks), by one elected thread: scales into tensor memory at sf, then up
-// to four MMAs of 64 K.  The last block may hold fewer steps: K past the
+// BN: columns of a tile, 256 or 384.
+template <int KIND, int WIDTH, int BN>
+struct PairLayout {
+  static constexpr int kAtoms = kBK / Kind<KIND>::kAtomK;     // per stage and 128 rows: 2 or 4
+  static constexpr int kRowBlocks = BN / 128;                 // of B
+  static constexpr int kABytes = 128 * kBKBytes, kBBytes = BN / 2 * kBKBytes;
+  static constexpr int kSfaOff = kABytes + kBBytes;
+  static constexpr int kSfbOff = kSfaOff + kAtoms * 512;
+  static constexpr int kLoadBytes = kSfbOff + kRowBlocks * kAtoms * 512;
+  static constexpr int kStageBytes = (kLoadBytes + 1023) / 1024 * 1024;
+  // Epilogue warps: 128 (of 256) or 96 (of 384) columns and 32 rows each.
+  static constexpr int kEpilogueColumns = BN == 384 ? 96 : 128;
+  static constexpr int kEpilogueWarps = 4 * BN / kEpilogueColumns;
+  static constexpr int kThreads = 32 * (2 + kEpilogueWarps);
+  // rows that allow no vector store pass through shared memory, a 32 x 32
+  // block a warp: a stage less
+  static constexpr int kTurnBytes = WIDTH == 0 ? kEpilogueWarps * 32 * 33 * 4 : 0;
+  static constexpr int kStages =
+      (BN == 384 ? 4 : (KIND == FP4Q_MXFP4 ? 6 : 5)) - (WIDTH == 0 ? 1 : 0);
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kBarBytes = 8 * (2 * kStages + 3);
+  static constexpr int kSmemBytes = kRingBytes + kTurnBytes + kBarBytes + 16 + 1024;
+  // Tensor memory: the accumulator, then slots of scales, one per stage where
+  // that fits (NVFP4 at 384 columns: two).
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kSfCols = 4 * kAtoms * (1 + kRowBlocks);
+  static constexpr int kSlots =
+      (int)((kTmemCols - BN) / kSfCols) < kStages ? (int)((kTmemCols - BN) / kSfCols) : kStages;
+  static_assert(kSlots >= 2, "a block's scales arrive while another's are read");
+  static_assert(kSmemBytes <= 227 * 1024, "the ring fits in shared memory");
+};
+
+// One K block in the ring slot at `sa` (A, B, A's atoms, B's atoms row block
+// after row block), by one elected thread: scales into tensor memory at sf,
+// then up to four steps of 64 K.  A step is one MMA of N = 256 and, for tiles
+// 384 wide, one of N = 128.  The last block may hold fewer steps: K past the
 // matrix would multiply zeros with scales that were not loaded.
-template <int KIND>
-__device__ __forceinline__ void issue_block(uint32_t sa, uint32_t b_off, uint32_t sfa_off,
-                                            uint32_t d_tmem, uint32_t sf, uint32_t idesc,
-                                            int steps, bool first) {
-  constexpr int kAtoms = kBK / Kind<KIND>::kAtomK;
+template <int KIND, int BN>
+__device__ __forceinline__ void issue_block(uint32_t sa, uint32_t d_tmem, uint32_t sf, int steps,
+                                            bool first) {
+  using L = PairLayout<KIND, 32, BN>;   // offsets do not depend on the width of stores
+  constexpr int kAtoms = L::kAtoms, kRowBlocks = BN / 128;
   const uint32_t sfa = sf, sfb = sf + 4 * kAtoms;
-  const uint64_t atom = sdesc_plain(sa + sfa_off, 128);   // + 32 per atom (512 bytes >> 4)
+  const uint64_t atom = sdesc_plain(sa + L::kSfaOff, 128);   // + 32 per atom (512 bytes >> 4)
 #pragma unroll
   for (int a = 0; a < kAtoms; ++a) {
-    const uint64_t a0 = atom + 32 * a, b0 = atom + 32 * (kAtoms + a), b1 = atom + 32 * (2 * kAtoms + a);
-    tmem_cp_32x128b_x4_pair(sfa + 4 * a, a0);
-    tmem_cp_32x128b_x4_pair(sfb + 8 * a, b0);
-    tmem_cp_32x128b_x4_pair(sfb + 8 * a + 4, b1);
-  }
-  const uint64_t ad = sdesc_k(sa, gemm::kSwzSBO, gemm::kSwzMode);
-  const uint64_t bd = sdesc_k(sa + b_off, gemm::kSwzSBO, gemm::kSwzMode);
+    tmem_cp_32x128b_x4_pair(sfa + 4 * a, atom + 32 * a);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (k < steps) {
-      const int a = KIND == FP4Q_MXFP4 ? k >> 1 : k;
-      const uint32_t half = KIND == FP4Q_MXFP4 ? 2u * (k & 1) : 0u;   // of the scale word
-      const uint32_t id = idesc | (half << 29) | (half << 4);
-      const uint32_t acc = (!first || k > 0) ? 1u : 0u;
-      mma_fp4_pair<KIND>(d_tmem, ad + 2 * k, bd + 2 * k, id, sfa + 4 * a, sfb + 8 * a, acc);
-    }
+    for (int h = 0; h < kRowBlocks; ++h)
+      tmem_cp_32x128b_x4_pair(sfb + 4 * (kRowBlocks * a + h), atom + 32 * (kAtoms * (1 + h) + a));
+  }
+  constexpr uint32_t idesc = idesc_fp4(KIND, 256, 256), idesc128 = idesc_fp4(KIND, 256, 128);
+  const uint64_t ad = sdesc_k(sa, gemm::kSwzSBO, gemm::kSwzMode);
+  const uint64_t bd = sdesc_k(sa + L::kABytes, gemm::kSwzSBO, gemm::kSwzMode);
+  const auto step = [&](int k) {
+    const int a = KIND == FP4Q_MXFP4 ? k >> 1 : k;
+    const uint32_t half = KIND == FP4Q_MXFP4 ? 2u * (k & 1) : 0u;   // of the scale word
+    const uint32_t pick = (half << 29) | (half << 4), acc = (!first || k > 0) ? 1u : 0u;
+    mma_fp4_pair<KIND>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | pick, sfa + 4 * a,
+                       sfb + 4 * kRowBlocks * a, acc);
+    if (BN == 384)   // B's rows 128-191 of each CTA
+      mma_fp4_pair<KIND>(d_tmem + 256, ad + 2 * k, bd + 2 * k + (128 * kBKBytes >> 4),
+                         idesc128 | pick, sfa + 4 * a, sfb + 4 * (kRowBlocks * a + 2), acc);
+  };
+  if (steps >= 4) {   // without a test per step: those alone cost NVFP4 7%
+#pragma unroll
+    for (int k = 0; k < 4; ++k) step(k);
+  } else {
+    for (int k = 0; k < steps; ++k) step(k);
   }
 }
 
-// 32 consecutive results of row m from column n0.  WIDTH: every row of C starts
-// on a boundary of so many bytes (32 or 16), and whole groups of that size are
-// stored at once.
+// 32 consecutive results of row m from column n0, as the words they are stored
+// as.  WIDTH: every row of C starts on a boundary of so many bytes (32 or 16),
+// and whole groups of that size are stored at once.
 template <typename T, int WIDTH>
 __device__ __forceinline__ void store32(T *C, int64_t N, int64_t m, int64_t n0,
-                                        const float (&v)[32]) {
+                                        const uint32_t (&r)[8 * sizeof(T)]) {
   T *row = C + m * N + n0;
-  constexpr int kGroup = WIDTH / (int)sizeof(T);
+  constexpr int kWords = WIDTH / 4, kGroup = WIDTH / (int)sizeof(T);
 #pragma unroll
-  for (int g = 0; g < 32; g += kGroup) {
-    if (n0 + g >= N) break;
-    uint32_t w[WIDTH / 4];
+  for (int g = 0; g < 32 / kGroup; ++g) {
+    if (n0 + g * kGroup >= N) break;
+    uint32_t w[kWords];
 #pragma unroll
-    for (int h = 0; h < WIDTH / 4; ++h)
-      w[h] = sizeof(T) == 2 ? pack8::bf16x2(v[(g + 2 * h) & 31], v[(g + 2 * h + 1) & 31])
-                            : __float_as_uint(v[g + h]);
+    for (int h = 0; h < kWords; ++h) w[h] = r[g * kWords + h];
     if constexpr (WIDTH == 32)
-      store_32b(row + g, w);
+      store_32b(row + g * kGroup, w);
     else
-      __stcs(reinterpret_cast<uint4 *>(row + g), make_uint4(w[0], w[1], w[2], w[3]));
+      __stcs(reinterpret_cast<uint4 *>(row + g * kGroup), make_uint4(w[0], w[1], w[2], w[3]));
   }
 }
 
@@ -109,47 +146,28 @@ __device__ __forceinline__ void store32(T *C, int64_t N, int64_t m, int64_t n0,
 // elements by the lanes that own the rows measured 33 us more on 2048 x 650).
 template <typename T>
 __device__ __forceinline__ void store32_turned(T *C, int64_t M, int64_t N, int64_t m0, int64_t n0,
-                                               const float (&v)[32], float *turn) {
+                                               const uint32_t (&r)[8 * sizeof(T)], uint32_t *turn) {
+  constexpr int kWords = 8 * (int)sizeof(T);
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = v[j];
+  for (int j = 0; j < kWords; ++j) turn[lane * (kWords + 1) + j] = r[j];
   __syncwarp();
   T *at = C + m0 * N + n0 + lane;
+  const T *from = reinterpret_cast<const T *>(turn) + lane;
   const int rows = (int)min((int64_t)32, M - m0);
   if (n0 + lane < N)
-    for (int r = 0; r < rows; ++r) at[r * N] = (T)turn[r * 33 + lane];
+    for (int i = 0; i < rows; ++i) at[i * N] = from[i * (kWords + 1) * (4 / (int)sizeof(T))];
   __syncwarp();
 }
 
-template <int KIND, int WIDTH>
-struct PairLayout {
-  // rows that allow no vector store pass through shared memory: a stage less
-  static constexpr int kStages = (KIND == FP4Q_MXFP4 ? 6 : 5) - (WIDTH == 0 ? 1 : 0);
-  static constexpr int kTurnBytes = WIDTH == 0 ? 8 * 32 * 33 * 4 : 0;   // a 32 x 32 block a warp
-  static constexpr int kAtoms = kBK / Kind<KIND>::kAtomK;
-  static constexpr int kABytes = 128 * kBKBytes, kBBytes = 128 * kBKBytes;
-  static constexpr int kSfaOff = kABytes + kBBytes;
-  static constexpr int kSfbOff = kSfaOff + kAtoms * 512;
-  static constexpr int kLoadBytes = kSfbOff + 2 * kAtoms * 512;
-  static constexpr int kStageBytes = (kLoadBytes + 1023) / 1024 * 1024;
-  static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kBarBytes = 8 * (2 * kStages + 3);
-  static constexpr int kSmemBytes = kRingBytes + kTurnBytes + kBarBytes + 16 + 1024;
-  static constexpr uint32_t kSfCol0 = 256;
-  static constexpr uint32_t kSfCols = 12 * kAtoms;
-  static constexpr uint32_t kTmemCols = 512;
-  static_assert(kSfCol0 + kSfCols * kStages <= kTmemCols, "scale slots fit in TMEM");
-  static_assert(kSmemBytes <= 227 * 1024, "the ring fits in shared memory");
-};
-
 struct PairMaps {
-  CUtensorMap a, b, sfa, sfb;
+  CUtensorMap a, b, b64, sfa, sfb;   // b64: boxes of 64 rows of B, for tiles 384 wide
 };
 
-template <int KIND, typename T, int WIDTH>
-__global__ void __launch_bounds__(320, 1)
+template <int KIND, typename T, int WIDTH, int BN>
+__global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
     gemm_pair_kernel(const __grid_constant__ PairMaps maps, const Args p) {
-  using L = PairLayout<KIND, WIDTH>;
+  using L = PairLayout<KIND, WIDTH, BN>;
   constexpr int kStages = L::kStages;
   constexpr uint16_t kBoth = 3;
   extern __shared__ uint8_t smem_raw[];
@@ -170,13 +188,14 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(empty0 + 8 * s, 1);
     }
     mbar_init(accf, 1);
-    mbar_init(acce, 16);
+    mbar_init(acce, 2 * L::kEpilogueWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
     prefetch_tmap(&maps.a);
     prefetch_tmap(&maps.b);
+    if (BN == 384) prefetch_tmap(&maps.b64);
     prefetch_tmap(&maps.sfa);
     prefetch_tmap(&maps.sfb);
   }
@@ -220,15 +239,19 @@ __global__ void __launch_bounds__(320, 1)
           const uint32_t full_even = mapa_shared(full0 + 8 * s, 0);
           if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * L::kLoadBytes);
           tma_load_2d_pair(sa, &maps.a, kb * kBKBytes, mt * 128, full_even);
-          tma_load_2d_pair(sa + L::kABytes, &maps.b, kb * kBKBytes, nt * 256 + (int)rank * 128,
+          tma_load_2d_pair(sa + L::kABytes, &maps.b, kb * kBKBytes, nt * BN + (int)rank * 128,
                            full_even);
+          if (BN == 384)
+            tma_load_2d_pair(sa + L::kABytes + 128 * kBKBytes, &maps.b64, kb * kBKBytes,
+                             nt * BN + 256 + (int)rank * 64, full_even);
           // Atoms past the last of a row block are the next block's or zeros;
           // no MMA step reads them.
           const int ka = kb * L::kAtoms;
           tma_load_2d_pair(sa + L::kSfaOff, &maps.sfa, 0, mt * p.atoms_k + ka, full_even);
-          tma_load_2d_pair(sa + L::kSfbOff, &maps.sfb, 0, 2 * nt * p.atoms_k + ka, full_even);
-          tma_load_2d_pair(sa + L::kSfbOff + L::kAtoms * 512, &maps.sfb, 0,
-                           (2 * nt + 1) * p.atoms_k + ka, full_even);
+#pragma unroll
+          for (int h = 0; h < L::kRowBlocks; ++h)
+            tma_load_2d_pair(sa + L::kSfbOff + h * L::kAtoms * 512, &maps.sfb, 0,
+                             (L::kRowBlocks * nt + h) * p.atoms_k + ka, full_even);
         }
       }
       // every slot's last release (the even CTA's commits) has arrived here
@@ -256,11 +279,20 @@ __global__ void __launch_bounds__(320, 1)
           ok = false;
           break;
         }
+        // the MMAs that read this slot of scales last are done
+        if (L::kSlots < kStages && it >= (uint32_t)L::kSlots) {
+          const uint32_t old = it - L::kSlots;
+          if (!wait_bounded_all(empty0 + 8 * (old % kStages), (old / kStages) & 1u, abort_flag,
+                                p.err)) {
+            ok = false;
+            break;
+          }
+        }
         tc_fence_after();
         if (elect_one()) {
-          issue_block<KIND>(ring + s * L::kStageBytes, L::kABytes, L::kSfaOff, tmem_base,
-                                  tmem_base + L::kSfCol0 + L::kSfCols * s, p.idesc,
-                                  p.num_steps - 4 * kb, kb == 0);
+          issue_block<KIND, BN>(ring + s * L::kStageBytes, tmem_base,
+                                tmem_base + BN + L::kSfCols * (it % L::kSlots),
+                                p.num_steps - 4 * kb, kb == 0);
           mma_commit_pair_multicast(empty0 + 8 * s, kBoth);
           if (kb == p.num_k_blocks - 1) mma_commit_pair_multicast(accf, kBoth);
         }
@@ -276,9 +308,10 @@ __global__ void __launch_bounds__(320, 1)
     __syncwarp();
   } else if (warp == 1) {
   } else {
-    // Warps 2..9: warp w drains TMEM lane quarter w % 4, columns
-    // [128 h, 128 h + 128) with h = (w - 2) / 4, of this CTA's 128 rows.
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    // Warp w drains TMEM lane quarter w % 4, columns [W h, W h + W) with W =
+    // kEpilogueColumns and h = (w - 2) / 4, of this CTA's 128 rows.
+    constexpr int kChunks = L::kEpilogueColumns / 32;
+    const int quarter = warp & 3, first = (warp - 2) / 4 * L::kEpilogueColumns;
     const float g = KIND == FP4Q_NVFP4 ? __fmul_rn(*p.ga, *p.gb) : 1.0f;
     const uint32_t acce_even = mapa_shared(acce, 0);
     uint32_t acc_it = 0;
@@ -287,12 +320,33 @@ __global__ void __launch_bounds__(320, 1)
       gemm::tile_coords(u, num_mu, p.num_n_tiles, mu, nt, p.group, 0);
       if (!wait_bounded_warp(accf, acc_it & 1u, abort_flag, p.err)) break;
       tc_fence_after();
-      uint32_t r[4][32];
+      // bf16 results are rounded as they come, two to a register: fewer live
+      constexpr int kRegs = sizeof(T) == 2 ? 16 : 32;
+      uint32_t r[kChunks][kRegs];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 128 + c * 32,
-                           r[c]);
-      tmem_ld_wait();
+      for (int c = 0; c < kChunks; c += 2) {
+        uint32_t t[2][32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (c + k < kChunks)
+            tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + first + (c + k) * 32, t[k]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (c + k < kChunks)
+#pragma unroll
+            for (int j = 0; j < kRegs; ++j) {
+              if constexpr (sizeof(T) == 2) {
+                float a = __uint_as_float(t[k][2 * j]), b = __uint_as_float(t[k][2 * j + 1]);
+                if (KIND == FP4Q_NVFP4) a = __fmul_rn(a, g), b = __fmul_rn(b, g);
+                r[c + k][j] = pack8::bf16x2(a, b);
+              } else {
+                float a = __uint_as_float(t[k][j]);
+                if (KIND == FP4Q_NVFP4) a = __fmul_rn(a, g);
+                r[c + k][j] = __float_as_uint(a);
+              }
+            }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {   // the accumulator is free for the next tile
@@ -303,21 +357,16 @@ __global__ void __launch_bounds__(320, 1)
       }
       const int64_t m0 = (int64_t)(2 * mu + (int)rank) * 128 + quarter * 32;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int64_t n0 = (int64_t)nt * 256 + half * 128 + c * 32;
+      for (int c = 0; c < kChunks; ++c) {
+        const int64_t n0 = (int64_t)nt * BN + first + c * 32;
         if (n0 >= p.N || m0 >= p.M) break;
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          v[j] = KIND == FP4Q_NVFP4 ? __fmul_rn(__uint_as_float(r[c][j]), g)
-                                    : __uint_as_float(r[c][j]);
         T *C = static_cast<T *>(p.C);
         if constexpr (WIDTH == 0)
-          store32_turned(C, p.M, p.N, m0, n0, v,
-                         reinterpret_cast<float *>(smem_raw + (ring - raw) + L::kRingBytes) +
+          store32_turned(C, p.M, p.N, m0, n0, r[c],
+                         reinterpret_cast<uint32_t *>(smem_raw + (ring - raw) + L::kRingBytes) +
                              (warp - 2) * 32 * 33);
         else if (m0 + lane < p.M)
-          store32<T, WIDTH>(C, p.N, m0 + lane, n0, v);
+          store32<T, WIDTH>(C, p.N, m0 + lane, n0, r[c]);
       }
     }
   }
@@ -331,21 +380,21 @@ __global__ void __launch_bounds__(320, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, L::kTmemCols);
 }
 
-template <int KIND, typename T, int WIDTH>
+template <int KIND, typename T, int WIDTH, int BN>
 int run_pair(const PairMaps &maps, const Args &a, cudaStream_t stream) {
-  using L = PairLayout<KIND, WIDTH>;
-  auto kernel = gemm_pair_kernel<KIND, T, WIDTH>;
+  using L = PairLayout<KIND, WIDTH, BN>;
+  auto kernel = gemm_pair_kernel<KIND, T, WIDTH, BN>;
   static PerDeviceOnce setup;  // per instantiation: the pairs that fit at once, 0 on failure
   const int pairs = setup.get([&] {
     if (gemm::set_smem(kernel, L::kSmemBytes) != cudaSuccess) return 0;
-    Launch q(2 * (sm_count() / 2), 1, 320, L::kSmemBytes, stream, 2);
+    Launch q(2 * (sm_count() / 2), 1, L::kThreads, L::kSmemBytes, stream, 2);
     int n = 0;
     return cudaOccupancyMaxActiveClusters(&n, kernel, &q.cfg) == cudaSuccess ? n : 0;
   });
   if (pairs < 1) return FP8Q_ERR_CUDA;
   const int units = (a.num_m_tiles + 1) / 2 * a.num_n_tiles;
-  return Launch(2 * std::min(units, pairs), 1, 320, L::kSmemBytes, stream, 2).run(kernel, maps, a) ==
-                 cudaSuccess
+  return Launch(2 * std::min(units, pairs), 1, L::kThreads, L::kSmemBytes, stream, 2)
+                     .run(kernel, maps, a) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
 }
@@ -361,16 +410,30 @@ int with_width(const Args &a, F &&f) {
   return f(std::integral_constant<int, 0>{});
 }
 
-template <int KIND, typename T>
+template <int KIND, typename T, int BN>
 int launch_pair(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K,
                 cudaStream_t stream) {
   PairMaps maps;
-  constexpr int kAtoms = PairLayout<KIND, 32>::kAtoms;
+  constexpr int kAtoms = PairLayout<KIND, 32, BN>::kAtoms;
   if (!make_tmap(&maps.a, A.data, a.M, K, 128) || !make_tmap(&maps.b, B.data, a.N, K, 128) ||
       !make_scale_tmap(&maps.sfa, A.scales, a.M, a.atoms_k, kAtoms) ||
       !make_scale_tmap(&maps.sfb, B.scales, a.N, a.atoms_k, kAtoms))
     return FP8Q_ERR_CUDA;
-  return with_width<T>(a, [&](auto w) { return run_pair<KIND, T, decltype(w)::value>(maps, a, stream); });
+  if (BN == 384) {
+    if (!make_tmap(&maps.b64, B.data, a.N, K, 64)) return FP8Q_ERR_CUDA;
+  } else {
+    maps.b64 = maps.b;
+  }
+  a.num_n_tiles = (int)((a.N + BN - 1) / BN);
+  return with_width<T>(
+      a, [&](auto w) { return run_pair<KIND, T, decltype(w)::value, BN>(maps, a, stream); });
+}
+
+template <int KIND, typename T>
+int launch_typed(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K, bool wide,
+                 cudaStream_t stream) {
+  return wide ? launch_pair<KIND, T, 384>(A, B, a, K, stream)
+              : launch_pair<KIND, T, 256>(A, B, a, K, stream);
 }
 
 }  // namespace
@@ -391,26 +454,28 @@ bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_
 int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_dtype, void *C,
                 int64_t M, int64_t N, int64_t K, cudaStream_t stream) {
   // Which kernel.  Up to 64 rows reading B once is the work, and the split
-  // kernel does little else.  Past that, by a model fitted to both kernels
-  // timed on 130 shapes (M 160-2048, N 256-12288, K 512-16384): beyond a common
+  // kernel does little else.  Past that, by a model fitted to the kernels timed
+  // on some 180 shapes (M 128-2048, N 256-12288, K 512-16384): beyond a common
   // 6.5 us a wave of 256 x 256 tiles takes 0.33 us per 256 of K; a wave of
   // split tiles 0.45 us per 256 of each CTA's K, and 2 us (0.3 us with an SM
   // to itself) to join the sums.  Both sides of the line: 256 x 4096 x 16384
   // pairs 27.7 us, split 16.6; 512 x 12288 x 4096 pairs 18.5 us, split 25.9.
-  const double pair_waves = (double)(((M + 255) / 256 * ((N + 255) / 256) + sm_count() / 2 - 1) /
-                                     (sm_count() / 2));
-  if (M <= 64 || split_cost(M, N, K) < pair_waves * 0.33 * (double)((K + kBK - 1) / kBK))
+  const int64_t kb = (K + kBK - 1) / kBK, pairs = sm_count() / 2;
+  const auto waves = [&](int64_t bn) {
+    return (double)(((M + 255) / 256 * ((N + bn - 1) / bn) + pairs - 1) / pairs);
+  };
+  const double cost256 = waves(256) * 0.33 * (double)kb;
+  if (M <= 64 || split_cost(M, N, K) < cost256)
     return launch_split(kind, nullptr, FP8Q_DT_BF16, 0, nullptr, &A, B, out_dtype, C, M, N, K, stream);
+  const bool wide = waves(384) * (0.487 * (double)kb + 1.65) < waves(256) * (0.354 * (double)kb + 1.38);
   Args a{};
   a.M = M;
   a.N = N;
   a.num_m_tiles = (int)((M + 127) / 128);
-  a.num_n_tiles = (int)((N + 255) / 256);
   a.num_k_blocks = (int)((K + kBK - 1) / kBK);
   a.num_steps = (int)((K + 63) / 64);
   a.atoms_k = (int)num_atoms_k(kind, K);
   a.group = 8;
-  a.idesc = idesc_fp4(kind, 256, 256);
   a.C = C;
   a.ga = A.global_scale;
   a.gb = B.global_scale;
@@ -425,10 +490,11 @@ int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_
             (long long)N, (long long)K, kind, out_dtype);
   if (kind == FP4Q_MXFP4)
     return out_dtype == FP8Q_DT_BF16
-               ? launch_pair<FP4Q_MXFP4, __nv_bfloat16>(A, B, a, K, stream)
-               : launch_pair<FP4Q_MXFP4, float>(A, B, a, K, stream);
-  return out_dtype == FP8Q_DT_BF16 ? launch_pair<FP4Q_NVFP4, __nv_bfloat16>(A, B, a, K, stream)
-                                   : launch_pair<FP4Q_NVFP4, float>(A, B, a, K, stream);
+               ? launch_typed<FP4Q_MXFP4, __nv_bfloat16>(A, B, a, K, wide, stream)
+               : launch_typed<FP4Q_MXFP4, float>(A, B, a, K, wide, stream);
+  return out_dtype == FP8Q_DT_BF16
+             ? launch_typed<FP4Q_NVFP4, __nv_bfloat16>(A, B, a, K, wide, stream)
+             : launch_typed<FP4Q_NVFP4, float>(A, B, a, K, wide, stream);
 }
 
 }  // namespace fp4
