@@ -399,41 +399,41 @@ int run_pair(const PairMaps &maps, const Args &a, cudaStream_t stream) {
              : FP8Q_ERR_CUDA;
 }
 
-// Calls f(width) with the widest store that every row of C allows, as a
-// compile-time constant.
-template <typename T, typename F>
-int with_width(const Args &a, F &&f) {
-  const int64_t row = a.N * (int64_t)sizeof(T);
-  const uintptr_t at = reinterpret_cast<uintptr_t>(a.C);
-  if (row % 32 == 0 && at % 32 == 0) return f(std::integral_constant<int, 32>{});
-  if (row % 16 == 0) return f(std::integral_constant<int, 16>{});
-  return f(std::integral_constant<int, 0>{});
+// Bytes that every row of C starts on: 32, 16 or 0 (neither).
+int row_width(const void *C, int64_t N, int64_t size) {
+  if (N * size % 32 == 0 && reinterpret_cast<uintptr_t>(C) % 32 == 0) return 32;
+  return N * size % 16 == 0 ? 16 : 0;
 }
 
-template <int KIND, typename T, int BN>
-int launch_pair(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K,
-                cudaStream_t stream) {
-  PairMaps maps;
+template <int KIND, int BN>
+bool make_maps(PairMaps &maps, const fp4q_operand &A, const fp4q_operand &B, const Args &a,
+               int64_t K) {
   constexpr int kAtoms = PairLayout<KIND, 32, BN>::kAtoms;
   if (!make_tmap(&maps.a, A.data, a.M, K, 128) || !make_tmap(&maps.b, B.data, a.N, K, 128) ||
       !make_scale_tmap(&maps.sfa, A.scales, a.M, a.atoms_k, kAtoms) ||
       !make_scale_tmap(&maps.sfb, B.scales, a.N, a.atoms_k, kAtoms))
-    return FP8Q_ERR_CUDA;
-  if (BN == 384) {
-    if (!make_tmap(&maps.b64, B.data, a.N, K, 64)) return FP8Q_ERR_CUDA;
-  } else {
-    maps.b64 = maps.b;
-  }
-  a.num_n_tiles = (int)((a.N + BN - 1) / BN);
-  return with_width<T>(
-      a, [&](auto w) { return run_pair<KIND, T, decltype(w)::value, BN>(maps, a, stream); });
+    return false;
+  if (BN == 384) return make_tmap(&maps.b64, B.data, a.N, K, 64);
+  maps.b64 = maps.b;
+  return true;
 }
 
 template <int KIND, typename T>
-int launch_typed(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K, bool wide,
-                 cudaStream_t stream) {
-  return wide ? launch_pair<KIND, T, 384>(A, B, a, K, stream)
-              : launch_pair<KIND, T, 256>(A, B, a, K, stream);
+int launch_pair(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K, int width,
+                bool wide, cudaStream_t stream) {
+  PairMaps maps;
+  if constexpr (sizeof(T) == 2) {
+    if (wide) {   // only where rows of bf16 start on 32 bytes (see launch_gemm)
+      a.num_n_tiles = (int)((a.N + 383) / 384);
+      if (!make_maps<KIND, 384>(maps, A, B, a, K)) return FP8Q_ERR_CUDA;
+      return run_pair<KIND, T, 32, 384>(maps, a, stream);
+    }
+  }
+  a.num_n_tiles = (int)((a.N + 255) / 256);
+  if (!make_maps<KIND, 256>(maps, A, B, a, K)) return FP8Q_ERR_CUDA;
+  if (width == 32) return run_pair<KIND, T, 32, 256>(maps, a, stream);
+  if (width == 16) return run_pair<KIND, T, 16, 256>(maps, a, stream);
+  return run_pair<KIND, T, 0, 256>(maps, a, stream);
 }
 
 }  // namespace
@@ -467,7 +467,15 @@ int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_
   const double cost256 = waves(256) * 0.33 * (double)kb;
   if (M <= 64 || split_cost(M, N, K) < cost256)
     return launch_split(kind, nullptr, FP8Q_DT_BF16, 0, nullptr, &A, B, out_dtype, C, M, N, K, stream);
-  const bool wide = waves(384) * (0.487 * (double)kb + 1.65) < waves(256) * (0.354 * (double)kb + 1.38);
+  // Tiles 384 wide, by the same kind of model for a busy device (us a wave, K
+  // in 256s): 0.487 K + 1.65 against 0.354 K + 1.38.  Only for bf16 rows on 32
+  // bytes: the others' stores need more registers than the 576 threads have
+  // (8192 x 8200 x 4096 bf16: 110 us at 256, 121 at 384; fp32 402 against 460
+  // us at 15872 x 16384 x 4096).
+  const int width = row_width(C, N, out_dtype == FP8Q_DT_BF16 ? 2 : 4);
+  const bool wide = out_dtype == FP8Q_DT_BF16 && width == 32 &&
+                    waves(384) * (0.487 * (double)kb + 1.65) <
+                        waves(256) * (0.354 * (double)kb + 1.38);
   Args a{};
   a.M = M;
   a.N = N;
@@ -486,15 +494,15 @@ int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_
       (std::max(M, N) + 255) / 128 * a.atoms_k > INT32_MAX)
     return FP8Q_ERR_INVALID_ARG;
   if (log_enabled())
-    fprintf(stderr, "[fp8q] launch fp4 gemm_pair_kernel %lldx%lldx%lld kind %d out %d\n", (long long)M,
-            (long long)N, (long long)K, kind, out_dtype);
+    fprintf(stderr, "[fp8q] launch fp4 gemm_pair_kernel %lldx%lldx%lld kind %d tile 256x%d out %d\n",
+            (long long)M, (long long)N, (long long)K, kind, wide ? 384 : 256, out_dtype);
   if (kind == FP4Q_MXFP4)
     return out_dtype == FP8Q_DT_BF16
-               ? launch_typed<FP4Q_MXFP4, __nv_bfloat16>(A, B, a, K, wide, stream)
-               : launch_typed<FP4Q_MXFP4, float>(A, B, a, K, wide, stream);
+               ? launch_pair<FP4Q_MXFP4, __nv_bfloat16>(A, B, a, K, width, wide, stream)
+               : launch_pair<FP4Q_MXFP4, float>(A, B, a, K, width, wide, stream);
   return out_dtype == FP8Q_DT_BF16
-             ? launch_typed<FP4Q_NVFP4, __nv_bfloat16>(A, B, a, K, wide, stream)
-             : launch_typed<FP4Q_NVFP4, float>(A, B, a, K, wide, stream);
+             ? launch_pair<FP4Q_NVFP4, __nv_bfloat16>(A, B, a, K, width, wide, stream)
+             : launch_pair<FP4Q_NVFP4, float>(A, B, a, K, width, wide, stream);
 }
 
 }  // namespace fp4
