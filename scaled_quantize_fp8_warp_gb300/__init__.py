@@ -619,9 +619,12 @@ def _rows(t: torch.Tensor):
     the rows may lie apart (a slice of a wider matrix)."""
     if not t.is_cuda:
         raise ValueError("fp8q needs CUDA tensors")
-    rows, cols = _rows_cols(t)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("expected a 2-D matrix")
     if t.is_contiguous():
-        return t.data_ptr(), cols
+        return t.data_ptr(), shape[1]
+    rows, cols = shape
     ld = t.stride(0) if rows > 1 else max(cols, 1)
     if (cols > 1 and t.stride(1) != 1) or ld < cols:
         raise ValueError("fp8q needs matrices whose rows are dense and do not overlap")
@@ -672,10 +675,21 @@ def _one(t: torch.Tensor, what: str):
 
 
 def _out(out, shape, dtype, device, stream, what="out"):
-    """(tensor, dtype code) of a result: the caller's, checked, or a new one."""
+    """(tensor, its address, dtype code) of a dense result: the caller's,
+    checked, or a new one."""
     if out is None:
-        return _new(shape, dtype, device, stream), _out_dtype(dtype)
-    return _like(out, shape, out.dtype, what), _out_dtype(out.dtype)
+        out = _new(shape, dtype, device, stream)
+        return out, out.data_ptr(), _out_dtype(dtype)
+    return _like(out, shape, out.dtype, what), _addr(out), _out_dtype(out.dtype)
+
+
+def _out_rows(out, shape, dtype, device, stream, what):
+    """(tensor, address, row stride) of a result whose rows may lie apart: the
+    caller's, checked, or a new one."""
+    if out is None:
+        out = _new(shape, dtype, device, stream)
+        return out, out.data_ptr(), shape[1]
+    return _like(out, shape, dtype, what), *_rows(out)
 
 
 def fp4_scale_bytes(kind: int, rows: int, K: int) -> int:
@@ -702,9 +716,6 @@ class Fp4Operand:
         if (kind == NVFP4) != (global_scale is not None):
             raise ValueError("NVFP4 operands, and only they, have a global scale")
         g = None if global_scale is None else _one(global_scale, "a global scale")
-        self._set(data, scales, kind, rows, K, global_scale, g)
-
-    def _set(self, data, scales, kind, rows, K, global_scale, g):
         self.data, self.scales, self.kind, self.rows, self.K = data, scales, kind, rows, K
         self.global_scale = global_scale
         self.struct = _Fp4Struct(_addr(data), _addr(scales), g, kind, 0)
@@ -713,9 +724,11 @@ class Fp4Operand:
     def empty(cls, kind: int, rows: int, K: int, device, global_scale=None, stream=None):
         """Uninitialised storage for an operand."""
         op = cls.__new__(cls)
-        op._set(_new((rows, (K + 31) // 32 * 16), torch.uint8, device, stream),
-                _new((fp4_scale_bytes(kind, rows, K),), torch.uint8, device, stream), kind, rows, K,
-                global_scale, None if global_scale is None else _one(global_scale, "a global scale"))
+        op.data = data = _new((rows, (K + 31) // 32 * 16), torch.uint8, device, stream)
+        op.scales = scales = _new((fp4_scale_bytes(kind, rows, K),), torch.uint8, device, stream)
+        op.kind, op.rows, op.K, op.global_scale = kind, rows, K, global_scale
+        g = None if global_scale is None else _one(global_scale, "a global scale")
+        op.struct = _Fp4Struct(data.data_ptr(), scales.data_ptr(), g, kind, 0)
         return op
 
 
@@ -763,8 +776,8 @@ def fp4_quantize(x: torch.Tensor, kind: int, rows=True, cols=False,
 
 def fp4_dequantize(op: Fp4Operand, out_dtype=torch.bfloat16, out=None, stream=None):
     """The values [rows, K] an operand stands for."""
-    out, dt = _out(out, (op.rows, op.K), out_dtype, op.data.device, stream)
-    _check(lib().fp4_dequantize(ctypes.byref(op.struct), op.rows, op.K, _addr(out), dt,
+    out, po, dt = _out(out, (op.rows, op.K), out_dtype, op.data.device, stream)
+    _check(lib().fp4_dequantize(ctypes.byref(op.struct), op.rows, op.K, po, dt,
                                 _raw_stream(stream)), "fp4_dequantize")
     return out
 
@@ -773,8 +786,8 @@ def fp4_gemm(A: Fp4Operand, B: Fp4Operand, out_dtype=torch.bfloat16, out=None, s
     """C [M, N] = A [M, K] . B [N, K]^T of two operands of one kind."""
     if A.K != B.K:
         raise ValueError(f"operands contract over {A.K} and {B.K}")
-    out, dt = _out(out, (A.rows, B.rows), out_dtype, A.data.device, stream)
-    _check(lib().fp4_gemm(ctypes.byref(A.struct), ctypes.byref(B.struct), _addr(out), dt, A.rows,
+    out, po, dt = _out(out, (A.rows, B.rows), out_dtype, A.data.device, stream)
+    _check(lib().fp4_gemm(ctypes.byref(A.struct), ctypes.byref(B.struct), po, dt, A.rows,
                           B.rows, A.K, _raw_stream(stream)), "fp4_gemm")
     return out
 
@@ -801,10 +814,10 @@ def fp4_linear(x: torch.Tensor, w: Fp4Operand, x_amax: torch.Tensor | None = Non
     if workspace is None and not (M <= FP4_LINEAR_FUSED_ROWS
                                   and (kind == MXFP4 or x_amax is not None)):
         workspace = _new((fp4_linear_workspace_size(kind, M, N, K),), torch.uint8, x.device, stream)
-    out, dt = _out(out, (M, N), out_dtype, x.device, stream)
+    out, po, dt = _out(out, (M, N), out_dtype, x.device, stream)
     _check(lib().fp4_linear(
         p, _in_dtype(x), ld, ctypes.byref(w.struct), M, N, K,
-        None if x_amax is None else _one(x_amax, "x_amax"), _addr(out), dt, _addr(workspace),
+        None if x_amax is None else _one(x_amax, "x_amax"), po, dt, _addr(workspace),
         0 if workspace is None else workspace.numel(), _raw_stream(stream)), "fp4_linear")
     return out
 
@@ -824,14 +837,14 @@ def fp4_linear_train(x, w, g, kind: int, out_dtype=torch.bfloat16, workspace=Non
     if workspace is None:
         workspace = _new((fp4_linear_train_workspace_size(kind, M, N, K),), torch.uint8, x.device,
                          stream)
-    y, dt = _out(y, (M, N), out_dtype, x.device, stream, "y")
-    dx, _ = _out(dx, (M, K), y.dtype, x.device, stream, "dx")
-    dw, _ = _out(dw, (N, K), y.dtype, x.device, stream, "dw")
+    y, py, dt = _out(y, (M, N), out_dtype, x.device, stream, "y")
+    dx, pdx, _ = _out(dx, (M, K), y.dtype, x.device, stream, "dx")
+    dw, pdw, _ = _out(dw, (N, K), y.dtype, x.device, stream, "dw")
     if dx.dtype != y.dtype or dw.dtype != y.dtype:
         raise ValueError("y, dx and dw have one type")
     _check(lib().fp4_linear_train(
-        _addr(x), _addr(w), _addr(g), _in_dtype(x), M, N, K, kind, _addr(y), _addr(dx), _addr(dw),
-        dt, _addr(workspace), workspace.numel(), _raw_stream(stream)), "fp4_linear_train")
+        _addr(x), _addr(w), _addr(g), _in_dtype(x), M, N, K, kind, py, pdx, pdw, dt,
+        _addr(workspace), workspace.numel(), _raw_stream(stream)), "fp4_linear_train")
     return y, dx, dw
 
 
@@ -877,15 +890,11 @@ def fp8_act_forward(act: int, u: torch.Tensor, v: torch.Tensor | None = None, ou
     pv, ldv = None, 0
     if v is not None:
         pv, ldv = _rows(_like(v, (T, F), u.dtype, "v"))
-    if out is None:
-        out = _new((T, F), u.dtype, u.device, stream)
-    else:
-        _like(out, (T, F), u.dtype, "out")
+    out, pa, lda = _out_rows(out, (T, F), u.dtype, u.device, stream, "out")
     if ckpt is None:
         ckpt = ActCheckpoint.empty(T, F, v is not None, u.device, stream)
     elif (ckpt.T, ckpt.F, ckpt.v is None) != (T, F, v is None):
         raise ValueError("the checkpoint's shape is another")
-    pa, lda = _rows(out)
     _check(lib().fp8_act_forward(
         act, _in_dtype(u), T, F, pu, ldu, pv, ldv, pa, lda, _addr(ckpt.u), _addr(ckpt.u_scales),
         _addr(ckpt.v), _addr(ckpt.v_scales), _raw_stream(stream)), "fp8_act_forward")
@@ -900,15 +909,12 @@ def fp8_act_backward(act: int, ckpt: ActCheckpoint, da: torch.Tensor, want_a=Fal
     pd, ldd = _rows(_like(da, shape, dtype, "da"))
     if ckpt.v is None and dv is not None:
         raise ValueError("an ungated activation has no dv")
-    du = _new(shape, dtype, device, stream) if du is None else _like(du, shape, dtype, "du")
-    pu, ldu = _rows(du)
+    du, pu, ldu = _out_rows(du, shape, dtype, device, stream, "du")
     pv, ldv, pa, lda = None, 0, None, 0
     if ckpt.v is not None:
-        dv = _new(shape, dtype, device, stream) if dv is None else _like(dv, shape, dtype, "dv")
-        pv, ldv = _rows(dv)
+        dv, pv, ldv = _out_rows(dv, shape, dtype, device, stream, "dv")
     if want_a or a is not None:
-        a = _new(shape, dtype, device, stream) if a is None else _like(a, shape, dtype, "a")
-        pa, lda = _rows(a)
+        a, pa, lda = _out_rows(a, shape, dtype, device, stream, "a")
     _check(lib().fp8_act_backward(
         act, _in_dtype(da), ckpt.T, ckpt.F, _addr(ckpt.u), _addr(ckpt.u_scales), _addr(ckpt.v),
         _addr(ckpt.v_scales), pd, ldd, pu, ldu, pv, ldv, pa, lda, _raw_stream(stream)),
