@@ -78,11 +78,9 @@ struct Pieces {
 // One matrix quantised in both orientations, in a workspace.
 struct Both {
   fp4q_operand rows, cols;
-  float *amax, *global;
+  float *global;
   void lay_out(Pieces &ws, int kind, int64_t R, int64_t C) {
-    uint8_t *words = ws.take(8);   // amax and g
-    amax = reinterpret_cast<float *>(words);
-    global = amax == nullptr ? nullptr : amax + 1;
+    global = reinterpret_cast<float *>(ws.take(sizeof(float)));
     const float *g = kind == FP4Q_NVFP4 ? global : nullptr;
     uint8_t *q = ws.take(data_bytes(R, C)), *qs = ws.take(fp4q_scale_bytes(kind, R, C));
     uint8_t *t = ws.take(data_bytes(C, R)), *ts = ws.take(fp4q_scale_bytes(kind, C, R));
@@ -91,15 +89,9 @@ struct Both {
   }
 };
 
-int quantize_into(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_t ld, int kind,
-                  const float *amax, float *amax_ws, const fp4q_operand *q,
-                  const fp4q_operand *qt, float *global, cudaStream_t stream) {
-  if (rows == 0 || cols == 0) return FP8Q_OK;
-  if (kind == FP4Q_NVFP4 && amax == nullptr) {
-    const cudaError_t e = fp4::launch_amax_ld(x, in_dtype, rows, cols, ld, amax_ws, stream);
-    if (e != cudaSuccess) return FP8Q_ERR_CUDA;
-    amax = amax_ws;
-  }
+fp4::QuantArgs quant_args(const void *x, int64_t rows, int64_t cols, int64_t ld,
+                          const float *amax, const fp4q_operand *q, const fp4q_operand *qt,
+                          float *global) {
   fp4::QuantArgs a{};
   a.x = x;
   a.rows = rows;
@@ -110,17 +102,8 @@ int quantize_into(const void *x, int in_dtype, int64_t rows, int64_t cols, int64
   a.q_scales = q == nullptr ? nullptr : const_cast<uint8_t *>(q->scales);
   a.qt = qt == nullptr ? nullptr : const_cast<uint8_t *>(qt->data);
   a.qt_scales = qt == nullptr ? nullptr : const_cast<uint8_t *>(qt->scales);
-  a.global_scale = kind == FP4Q_NVFP4 ? global : nullptr;
-  return from_cuda(fp4::launch_quantize(kind, in_dtype, a, stream));
-}
-
-// C = A . B^T for checked operands of one kind, any sizes.
-int product(const fp4q_operand &A, const fp4q_operand &B, void *C, int out_dtype, int64_t M,
-            int64_t N, int64_t K, cudaStream_t stream) {
-  if (M == 0 || N == 0) return FP8Q_OK;
-  if (K == 0)
-    return from_cuda(cudaMemsetAsync(C, 0, (size_t)(M * N * dtype_size(out_dtype)), stream));
-  return fp4::launch_gemm(A.kind, A, B, out_dtype, C, M, N, K, stream);
+  a.global_scale = global;
+  return a;
 }
 
 }  // namespace
@@ -158,8 +141,9 @@ int fp4_quantize(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_
   if (empty)
     return kind == FP4Q_NVFP4 ? from_cuda(fp4::launch_global(amax, global_scale, stream)) : FP8Q_OK;
   const fp4q_operand a{q, q_scales, nullptr, kind, 0}, b{qt, qt_scales, nullptr, kind, 0};
-  return quantize_into(x, in_dtype, rows, cols, ld, kind, amax, nullptr, q ? &a : nullptr,
-                       qt ? &b : nullptr, global_scale, stream);
+  const fp4::QuantArgs args =
+      quant_args(x, rows, cols, ld, amax, q ? &a : nullptr, qt ? &b : nullptr, global_scale);
+  return from_cuda(fp4::launch_quantize(kind, in_dtype, &args, 1, stream));
 }
 
 int fp4_amax(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_t ld, float *amax,
@@ -193,7 +177,8 @@ int fp4_gemm(const fp4q_operand *A, const fp4q_operand *B, void *C, int out_dtyp
   if (A->kind != B->kind) return FP8Q_ERR_INVALID_ARG;
   if ((rc = check_matrix(C, M, N, N, 16)) != FP8Q_OK) return rc;
   if ((rc = check_device()) != FP8Q_OK) return rc;
-  return product(*A, *B, C, out_dtype, M, N, K, stream);
+  const fp4::Product d{*A, *B, C, M, N, K};
+  return fp4::launch_products(A->kind, &d, 1, out_dtype, stream);
 }
 
 size_t fp4q_linear_workspace_size(int kind, int64_t M, int64_t N, int64_t K) {
@@ -230,24 +215,27 @@ int fp4_linear(const void *x, int in_dtype, int64_t ldx, const fp4q_operand *w, 
   q.data = ws.take(data_bytes(M, K));
   q.scales = ws.take(fp4q_scale_bytes(w->kind, M, K));
   q.global_scale = w->kind == FP4Q_NVFP4 ? words + 1 : nullptr;
-  if (fused && K > 0) {
+  fp4::Product d{q, *w, y, M, N, K};
+  if (K > 0) {
     if (find_amax) {
       if (fp4::launch_amax_ld(x, in_dtype, M, K, ldx, words, stream) != cudaSuccess)
         return FP8Q_ERR_CUDA;
       x_amax = words;
     }
-    return fp4::launch_split(w->kind, x, in_dtype, ldx, x_amax, nullptr, *w, out_dtype, y, M, N, K,
-                             stream);
+    if (fused)
+      return fp4::launch_split_quantizing(w->kind, x, in_dtype, ldx, x_amax, d, out_dtype, stream);
+    float *global = w->kind == FP4Q_NVFP4 ? words + 1 : nullptr;
+    const fp4::QuantArgs args = quant_args(x, M, K, ldx, x_amax, &q, nullptr, global);
+    if (fp4::launch_quantize(w->kind, in_dtype, &args, 1, stream) != cudaSuccess)
+      return FP8Q_ERR_CUDA;
   }
-  rc = quantize_into(x, in_dtype, M, K, ldx, w->kind, x_amax, words, &q, nullptr, words + 1,
-                     stream);
-  if (rc != FP8Q_OK) return rc;
-  return product(q, *w, y, out_dtype, M, N, K, stream);
+  return fp4::launch_products(w->kind, &d, 1, out_dtype, stream);
 }
 
 size_t fp4q_linear_train_workspace_size(int kind, int64_t M, int64_t N, int64_t K) {
   if (!valid_kind(kind) || !linear_ok(M, N, K)) return 0;
   Pieces ws{nullptr};
+  ws.take(3 * sizeof(float));   // the amaxes
   Both b;
   b.lay_out(ws, kind, M, K);
   b.lay_out(ws, kind, N, K);
@@ -275,6 +263,7 @@ int fp4_linear_train(const void *x, const void *w, const void *g, int in_dtype, 
   if (!aligned(workspace, 256)) return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
   Pieces ws{static_cast<uint8_t *>(workspace)};
+  float *amax = reinterpret_cast<float *>(ws.take(3 * sizeof(float)));
   Both bx, bw, bg;
   bx.lay_out(ws, kind, M, K);
   bw.lay_out(ws, kind, N, K);
@@ -284,15 +273,28 @@ int fp4_linear_train(const void *x, const void *w, const void *g, int in_dtype, 
     int64_t rows, cols;
     const Both *to;
   } in_m[3] = {{x, M, K, &bx}, {w, N, K, &bw}, {g, M, N, &bg}};
-  for (const auto &m : in_m) {
-    rc = quantize_into(m.p, in_dtype, m.rows, m.cols, m.cols, kind, nullptr, m.to->amax,
-                       &m.to->rows, &m.to->cols, m.to->global, stream);
-    if (rc != FP8Q_OK) return rc;
+  fp4::QuantArgs args[3];
+  const void *src[3];
+  int64_t size[3];
+  int n = 0;
+  for (const auto &m : in_m) {   // the empty ones have nothing to cast
+    if (m.rows == 0 || m.cols == 0) continue;
+    src[n] = m.p;
+    size[n] = m.rows * m.cols;
+    args[n] = quant_args(m.p, m.rows, m.cols, m.cols, amax + n, &m.to->rows, &m.to->cols,
+                         kind == FP4Q_NVFP4 ? m.to->global : nullptr);
+    ++n;
   }
-  if ((rc = product(bx.rows, bw.rows, y, out_dtype, M, N, K, stream)) != FP8Q_OK ||
-      (rc = product(bg.rows, bw.cols, dx, out_dtype, M, K, N, stream)) != FP8Q_OK)
-    return rc;
-  return product(bg.cols, bx.cols, dw, out_dtype, N, K, M, stream);
+  if (n > 0) {
+    if (kind == FP4Q_NVFP4 &&
+        fp4::launch_amax_group(src, size, n, in_dtype, amax, stream) != cudaSuccess)
+      return FP8Q_ERR_CUDA;
+    if (fp4::launch_quantize(kind, in_dtype, args, n, stream) != cudaSuccess) return FP8Q_ERR_CUDA;
+  }
+  const fp4::Product prod[3] = {{bx.rows, bw.rows, y, M, N, K},
+                                {bg.rows, bw.cols, dx, M, K, N},
+                                {bg.cols, bx.cols, dw, N, K, M}};
+  return fp4::launch_products(kind, prod, 3, out_dtype, stream);
 }
 
 int fp8_act_forward(int act, int dtype, int64_t T, int64_t F, const void *u, int64_t ldu,

@@ -19,7 +19,9 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
+#include <utility>
 
 #include "fp4_common.cuh"
 #include "fp4_internal.h"
@@ -164,9 +166,33 @@ struct PairMaps {
   CUtensorMap a, b, b64, sfa, sfb;   // b64: boxes of 64 rows of B, for tiles 384 wide
 };
 
-template <int KIND, typename T, int WIDTH, int BN>
+// The products of one launch, their tiles numbered one product after the other,
+// so that only the last wave of all is partial.  A launch of one (GROUPED
+// false) reads it at constant offsets.
+template <bool GROUPED>
+struct PairGroup {
+  static constexpr int kMax = GROUPED ? kGroupMax : 1;
+  int n;
+  int unit_end[kMax];
+  Args prob[kMax];
+  PairMaps maps[kMax];
+};
+
+template <bool GROUPED>
+__device__ __forceinline__ int group_coords(const PairGroup<GROUPED> &g, int u, int &mu, int &nt) {
+  int q = 0;
+  if (GROUPED) {
+    while (q + 1 < g.n && u >= g.unit_end[q]) ++q;
+    if (q > 0) u -= g.unit_end[q - 1];
+  }
+  const Args &p = g.prob[q];
+  gemm::tile_coords(u, (p.num_m_tiles + 1) / 2, p.num_n_tiles, mu, nt, p.group, 0);
+  return q;
+}
+
+template <int KIND, typename T, int WIDTH, int BN, bool GROUPED>
 __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
-    gemm_pair_kernel(const __grid_constant__ PairMaps maps, const Args p) {
+    gemm_pair_kernel(const __grid_constant__ PairGroup<GROUPED> grp) {
   using L = PairLayout<KIND, WIDTH, BN>;
   constexpr int kStages = L::kStages;
   constexpr uint16_t kBoth = 3;
@@ -193,11 +219,13 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
-    prefetch_tmap(&maps.a);
-    prefetch_tmap(&maps.b);
-    if (BN == 384) prefetch_tmap(&maps.b64);
-    prefetch_tmap(&maps.sfa);
-    prefetch_tmap(&maps.sfb);
+    for (int q = 0; q < (GROUPED ? grp.n : 1); ++q) {
+      prefetch_tmap(&grp.maps[q].a);
+      prefetch_tmap(&grp.maps[q].b);
+      if (BN == 384) prefetch_tmap(&grp.maps[q].b64);
+      prefetch_tmap(&grp.maps[q].sfa);
+      prefetch_tmap(&grp.maps[q].sfb);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(slot, L::kTmemCols);
@@ -213,10 +241,10 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
   // One allocation serves the pair: both CTAs must hold the same address.
   // Otherwise neither does any work (a symmetric decision, no waiting).
   const bool paired = ld_shared_cluster_u32(mapa_shared(slot, rank ^ 1u)) == tmem_base;
-  if (!paired && threadIdx.x == 0) atomicOr(p.err, 4u);
+  unsigned int *const err = grp.prob[0].err;
+  if (!paired && threadIdx.x == 0) atomicOr(err, 4u);
 
-  const int num_mu = (p.num_m_tiles + 1) / 2;
-  const int total = num_mu * p.num_n_tiles;
+  const int total = grp.unit_end[GROUPED ? grp.n - 1 : 0];
   const int unit0 = blockIdx.x / 2, unit_step = gridDim.x / 2;
 
   if (!paired) {
@@ -226,12 +254,14 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
       bool ok = true;
       for (int u = unit0; u < total && ok; u += unit_step) {
         int mu, nt;
-        gemm::tile_coords(u, num_mu, p.num_n_tiles, mu, nt, p.group, 0);
+        const int q = group_coords(grp, u, mu, nt);
+        const PairMaps &maps = grp.maps[q];
+        const int num_k_blocks = grp.prob[q].num_k_blocks, atoms_k = grp.prob[q].atoms_k;
         // past the last M tile (odd count): re-read that tile's A, store nothing
-        const int mt = min(2 * mu + (int)rank, p.num_m_tiles - 1);
-        for (int kb = 0; kb < p.num_k_blocks; ++kb, ++it) {
+        const int mt = min(2 * mu + (int)rank, grp.prob[q].num_m_tiles - 1);
+        for (int kb = 0; kb < num_k_blocks; ++kb, ++it) {
           const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
-          if (!wait_bounded(empty0 + 8 * s, ph ^ 1u, abort_flag, p.err)) {
+          if (!wait_bounded(empty0 + 8 * s, ph ^ 1u, abort_flag, err)) {
             ok = false;
             break;
           }
@@ -247,17 +277,17 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
           // Atoms past the last of a row block are the next block's or zeros;
           // no MMA step reads them.
           const int ka = kb * L::kAtoms;
-          tma_load_2d_pair(sa + L::kSfaOff, &maps.sfa, 0, mt * p.atoms_k + ka, full_even);
+          tma_load_2d_pair(sa + L::kSfaOff, &maps.sfa, 0, mt * atoms_k + ka, full_even);
 #pragma unroll
           for (int h = 0; h < L::kRowBlocks; ++h)
             tma_load_2d_pair(sa + L::kSfbOff + h * L::kAtoms * 512, &maps.sfb, 0,
-                             (L::kRowBlocks * nt + h) * p.atoms_k + ka, full_even);
+                             (L::kRowBlocks * nt + h) * atoms_k + ka, full_even);
         }
       }
       // every slot's last release (the even CTA's commits) has arrived here
       for (uint32_t j = 0, jt = it; ok && j < (uint32_t)kStages; ++j, ++jt)
         ok = wait_bounded(empty0 + 8 * (jt % kStages), ((jt / kStages) & 1u) ^ 1u, abort_flag,
-                          p.err);
+                          err);
       if (!ok) {
         // aborting: give copies already issued (their barrier may be the
         // other CTA's) a millisecond to land before the CTA can leave
@@ -271,11 +301,14 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
     uint32_t it = 0, acc_it = 0;
     bool ok = true;
     for (int u = unit0; u < total && ok; u += unit_step, ++acc_it) {
-      if (!wait_bounded_all(acce, (acc_it & 1u) ^ 1u, abort_flag, p.err)) break;
+      int mu, nt;
+      const int q = group_coords(grp, u, mu, nt);
+      const int num_k_blocks = grp.prob[q].num_k_blocks, num_steps = grp.prob[q].num_steps;
+      if (!wait_bounded_all(acce, (acc_it & 1u) ^ 1u, abort_flag, err)) break;
       tc_fence_after();
-      for (int kb = 0; kb < p.num_k_blocks; ++kb, ++it) {
+      for (int kb = 0; kb < num_k_blocks; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
-        if (!wait_bounded_all(full0 + 8 * s, ph, abort_flag, p.err)) {
+        if (!wait_bounded_all(full0 + 8 * s, ph, abort_flag, err)) {
           ok = false;
           break;
         }
@@ -283,7 +316,7 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
         if (L::kSlots < kStages && it >= (uint32_t)L::kSlots) {
           const uint32_t old = it - L::kSlots;
           if (!wait_bounded_all(empty0 + 8 * (old % kStages), (old / kStages) & 1u, abort_flag,
-                                p.err)) {
+                                err)) {
             ok = false;
             break;
           }
@@ -292,9 +325,9 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
         if (elect_one()) {
           issue_block<KIND, BN>(ring + s * L::kStageBytes, tmem_base,
                                 tmem_base + BN + L::kSfCols * (it % L::kSlots),
-                                p.num_steps - 4 * kb, kb == 0);
+                                num_steps - 4 * kb, kb == 0);
           mma_commit_pair_multicast(empty0 + 8 * s, kBoth);
-          if (kb == p.num_k_blocks - 1) mma_commit_pair_multicast(accf, kBoth);
+          if (kb == num_k_blocks - 1) mma_commit_pair_multicast(accf, kBoth);
         }
         __syncwarp();
       }
@@ -312,13 +345,15 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
     // kEpilogueColumns and h = (w - 2) / 4, of this CTA's 128 rows.
     constexpr int kChunks = L::kEpilogueColumns / 32;
     const int quarter = warp & 3, first = (warp - 2) / 4 * L::kEpilogueColumns;
-    const float g = KIND == FP4Q_NVFP4 ? __fmul_rn(*p.ga, *p.gb) : 1.0f;
     const uint32_t acce_even = mapa_shared(acce, 0);
     uint32_t acc_it = 0;
     for (int u = unit0; u < total; u += unit_step, ++acc_it) {
       int mu, nt;
-      gemm::tile_coords(u, num_mu, p.num_n_tiles, mu, nt, p.group, 0);
-      if (!wait_bounded_warp(accf, acc_it & 1u, abort_flag, p.err)) break;
+      const int q = group_coords(grp, u, mu, nt);
+      const int64_t M = grp.prob[q].M, N = grp.prob[q].N;
+      T *const C = static_cast<T *>(grp.prob[q].C);
+      const float g = KIND == FP4Q_NVFP4 ? __fmul_rn(*grp.prob[q].ga, *grp.prob[q].gb) : 1.0f;
+      if (!wait_bounded_warp(accf, acc_it & 1u, abort_flag, err)) break;
       tc_fence_after();
       // bf16 results are rounded as they come, two to a register: fewer live
       constexpr int kRegs = sizeof(T) == 2 ? 16 : 32;
@@ -359,14 +394,13 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const int64_t n0 = (int64_t)nt * BN + first + c * 32;
-        if (n0 >= p.N || m0 >= p.M) break;
-        T *C = static_cast<T *>(p.C);
+        if (n0 >= N || m0 >= M) break;
         if constexpr (WIDTH == 0)
-          store32_turned(C, p.M, p.N, m0, n0, r[c],
+          store32_turned(C, M, N, m0, n0, r[c],
                          reinterpret_cast<uint32_t *>(smem_raw + (ring - raw) + L::kRingBytes) +
                              (warp - 2) * 32 * 33);
-        else if (m0 + lane < p.M)
-          store32<T, WIDTH>(C, p.N, m0 + lane, n0, r[c]);
+        else if (m0 + lane < M)
+          store32<T, WIDTH>(C, N, m0 + lane, n0, r[c]);
       }
     }
   }
@@ -380,10 +414,10 @@ __global__ void __launch_bounds__(PairLayout<KIND, WIDTH, BN>::kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, L::kTmemCols);
 }
 
-template <int KIND, typename T, int WIDTH, int BN>
-int run_pair(const PairMaps &maps, const Args &a, cudaStream_t stream) {
+template <int KIND, typename T, int WIDTH, int BN, bool GROUPED>
+int run_pair(const PairGroup<GROUPED> &grp, cudaStream_t stream) {
   using L = PairLayout<KIND, WIDTH, BN>;
-  auto kernel = gemm_pair_kernel<KIND, T, WIDTH, BN>;
+  auto kernel = gemm_pair_kernel<KIND, T, WIDTH, BN, GROUPED>;
   static PerDeviceOnce setup;  // per instantiation: the pairs that fit at once, 0 on failure
   const int pairs = setup.get([&] {
     if (gemm::set_smem(kernel, L::kSmemBytes) != cudaSuccess) return 0;
@@ -392,9 +426,9 @@ int run_pair(const PairMaps &maps, const Args &a, cudaStream_t stream) {
     return cudaOccupancyMaxActiveClusters(&n, kernel, &q.cfg) == cudaSuccess ? n : 0;
   });
   if (pairs < 1) return FP8Q_ERR_CUDA;
-  const int units = (a.num_m_tiles + 1) / 2 * a.num_n_tiles;
+  const int units = grp.unit_end[grp.n - 1];
   return Launch(2 * std::min(units, pairs), 1, L::kThreads, L::kSmemBytes, stream, 2)
-                     .run(kernel, maps, a) == cudaSuccess
+                     .run(kernel, grp) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
 }
@@ -405,36 +439,122 @@ int row_width(const void *C, int64_t N, int64_t size) {
   return N * size % 16 == 0 ? 16 : 0;
 }
 
-template <int KIND, int BN>
-bool make_maps(PairMaps &maps, const fp4q_operand &A, const fp4q_operand &B, const Args &a,
-               int64_t K) {
+template <int KIND, int BN, bool GROUPED>
+int fill_group(PairGroup<GROUPED> &grp, const Product *prod, int n) {
   constexpr int kAtoms = PairLayout<KIND, 32, BN>::kAtoms;
-  if (!make_tmap(&maps.a, A.data, a.M, K, 128) || !make_tmap(&maps.b, B.data, a.N, K, 128) ||
-      !make_scale_tmap(&maps.sfa, A.scales, a.M, a.atoms_k, kAtoms) ||
-      !make_scale_tmap(&maps.sfb, B.scales, a.N, a.atoms_k, kAtoms))
-    return false;
-  if (BN == 384) return make_tmap(&maps.b64, B.data, a.N, K, 64);
-  maps.b64 = maps.b;
-  return true;
+  unsigned int *err = device_error_word();
+  if (err == nullptr) return FP8Q_ERR_CUDA;
+  grp.n = n;
+  int64_t units = 0;
+  for (int i = 0; i < n; ++i) {
+    const Product &d = prod[i];
+    Args &a = grp.prob[i];
+    a.M = d.M;
+    a.N = d.N;
+    a.num_m_tiles = (int)((d.M + 127) / 128);
+    a.num_n_tiles = (int)((d.N + BN - 1) / BN);
+    a.num_k_blocks = (int)((d.K + kBK - 1) / kBK);
+    a.num_steps = (int)((d.K + 63) / 64);
+    a.atoms_k = (int)num_atoms_k(KIND, d.K);
+    a.group = 8;
+    a.C = d.C;
+    a.ga = d.A.global_scale;
+    a.gb = d.B.global_scale;
+    a.err = err;
+    units += (int64_t)((a.num_m_tiles + 1) / 2) * a.num_n_tiles;
+    if (units > INT32_MAX / 2) return FP8Q_ERR_INVALID_ARG;
+    grp.unit_end[i] = (int)units;
+    PairMaps &m = grp.maps[i];
+    if (!make_tmap(&m.a, d.A.data, d.M, d.K, 128) || !make_tmap(&m.b, d.B.data, d.N, d.K, 128) ||
+        !make_scale_tmap(&m.sfa, d.A.scales, d.M, a.atoms_k, kAtoms) ||
+        !make_scale_tmap(&m.sfb, d.B.scales, d.N, a.atoms_k, kAtoms) ||
+        (BN == 384 && !make_tmap(&m.b64, d.B.data, d.N, d.K, 64)))
+      return FP8Q_ERR_CUDA;
+  }
+  return FP8Q_OK;
 }
 
-template <int KIND, typename T>
-int launch_pair(const fp4q_operand &A, const fp4q_operand &B, Args &a, int64_t K, int width,
-                bool wide, cudaStream_t stream) {
-  PairMaps maps;
+template <int KIND, typename T, int WIDTH, int BN, bool GROUPED>
+int start_pair(const Product *prod, int n, cudaStream_t stream) {
+  PairGroup<GROUPED> grp{};
+  const int rc = fill_group<KIND, BN>(grp, prod, n);
+  return rc == FP8Q_OK ? run_pair<KIND, T, WIDTH, BN>(grp, stream) : rc;
+}
+
+template <int KIND, typename T, bool GROUPED>
+int launch_pair(const Product *prod, int n, int width, bool wide, cudaStream_t stream) {
   if constexpr (sizeof(T) == 2) {
-    if (wide) {   // only where rows of bf16 start on 32 bytes (see launch_gemm)
-      a.num_n_tiles = (int)((a.N + 383) / 384);
-      if (!make_maps<KIND, 384>(maps, A, B, a, K)) return FP8Q_ERR_CUDA;
-      return run_pair<KIND, T, 32, 384>(maps, a, stream);
+    if (wide) return start_pair<KIND, T, 32, 384, GROUPED>(prod, n, stream);
+  }
+  if (width == 32) return start_pair<KIND, T, 32, 256, GROUPED>(prod, n, stream);
+  if (width == 16) return start_pair<KIND, T, 16, 256, GROUPED>(prod, n, stream);
+  return start_pair<KIND, T, 0, 256, GROUPED>(prod, n, stream);
+}
+
+// The products of a launch on CTA pairs.
+int launch_pairs(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream) {
+  const bool bf16 = out_dtype == FP8Q_DT_BF16;
+  // Tiles 384 wide where they take less, by a model fitted to both widths on a
+  // busy device: a wave (of as many tiles as there are pairs) takes 0.487 us
+  // per 256 of K and 1.65 us at 384, 0.354 and 1.38 at 256.  Only for bf16 rows
+  // on 32 bytes: the others' stores need more registers than 576 threads have
+  // (8192 x 8200 x 4096 bf16: 110 us at 256, 121 at 384; fp32 402 against 460
+  // us at 15872 x 16384 x 4096).
+  int width = 32;
+  const int64_t pairs = sm_count() / 2;
+  double cost[2] = {0.0, 0.0}, waves[2] = {0.0, 0.0};
+  for (int i = 0; i < n; ++i) {
+    width = std::min(width, row_width(prod[i].C, prod[i].N, bf16 ? 2 : 4));
+    const double kb = (double)((prod[i].K + kBK - 1) / kBK);
+    for (int w = 0; w < 2; ++w) {
+      const int64_t bn = w ? 384 : 256;
+      const double tiles = (double)((prod[i].M + 255) / 256 * ((prod[i].N + bn - 1) / bn));
+      waves[w] += tiles / (double)pairs;
+      cost[w] += tiles / (double)pairs * (w ? 0.487 * kb + 1.65 : 0.354 * kb + 1.38);
     }
   }
-  a.num_n_tiles = (int)((a.N + 255) / 256);
-  if (!make_maps<KIND, 256>(maps, A, B, a, K)) return FP8Q_ERR_CUDA;
-  if (width == 32) return run_pair<KIND, T, 32, 256>(maps, a, stream);
-  if (width == 16) return run_pair<KIND, T, 16, 256>(maps, a, stream);
-  return run_pair<KIND, T, 0, 256>(maps, a, stream);
+  // the last wave is a whole one
+  for (int w = 0; w < 2; ++w) cost[w] *= std::ceil(waves[w]) / waves[w];
+  const bool wide = bf16 && width == 32 && cost[1] < cost[0];
+  if (log_enabled())
+    for (int i = 0; i < n; ++i)
+      fprintf(stderr, "[fp8q] launch fp4 gemm_pair_kernel %lldx%lldx%lld kind %d tile 256x%d out %d%s\n",
+              (long long)prod[i].M, (long long)prod[i].N, (long long)prod[i].K, kind,
+              wide ? 384 : 256, out_dtype, n > 1 ? " grouped" : "");
+  if (kind == FP4Q_MXFP4) {
+    if (n > 1)
+      return bf16 ? launch_pair<FP4Q_MXFP4, __nv_bfloat16, true>(prod, n, width, wide, stream)
+                  : launch_pair<FP4Q_MXFP4, float, true>(prod, n, width, wide, stream);
+    return bf16 ? launch_pair<FP4Q_MXFP4, __nv_bfloat16, false>(prod, n, width, wide, stream)
+                : launch_pair<FP4Q_MXFP4, float, false>(prod, n, width, wide, stream);
+  }
+  if (n > 1)
+    return bf16 ? launch_pair<FP4Q_NVFP4, __nv_bfloat16, true>(prod, n, width, wide, stream)
+                : launch_pair<FP4Q_NVFP4, float, true>(prod, n, width, wide, stream);
+  return bf16 ? launch_pair<FP4Q_NVFP4, __nv_bfloat16, false>(prod, n, width, wide, stream)
+              : launch_pair<FP4Q_NVFP4, float, false>(prod, n, width, wide, stream);
 }
+
+// Which kernel a product runs on: how many microseconds the split kernel is
+// expected to save over CTA pairs.  Up to 64 rows reading B once is the work,
+// and the split kernel does little else.  Past that, by a model fitted to both
+// kernels timed alone on some 180 shapes (M 128-2048, N 256-12288, K
+// 512-16384): beyond a common 6.5 us a wave of 256 x 256 tiles takes 0.33 us
+// per 256 of K; a wave of split tiles 0.45 us per 256 of each CTA's K, and 2 us
+// (0.3 us with an SM to itself) to join the sums.  Both sides of the line: 256
+// x 4096 x 16384 pairs 27.7 us, split 16.6; 512 x 12288 x 4096 pairs 18.5 us,
+// split 25.9.
+double split_saves(const Product &d) {
+  if (d.M <= 64) return 1e9;
+  const int64_t pairs = sm_count() / 2;
+  const int64_t waves = ((d.M + 255) / 256 * ((d.N + 255) / 256) + pairs - 1) / pairs;
+  return 0.33 * (double)waves * (double)((d.K + kBK - 1) / kBK) - split_cost(d.M, d.N, d.K);
+}
+
+// What one launch more costs: products of a call that differ by less than this
+// go together (333 x 650 x 1031, all three of a training step: 13.1 us the
+// third alone after 10.3 us the other two, 12 us in one).
+constexpr double kLaunchCost = 3.0;
 
 }  // namespace
 
@@ -451,58 +571,42 @@ bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_
                       CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_dtype, void *C,
-                int64_t M, int64_t N, int64_t K, cudaStream_t stream) {
-  // Which kernel.  Up to 64 rows reading B once is the work, and the split
-  // kernel does little else.  Past that, by a model fitted to the kernels timed
-  // on some 180 shapes (M 128-2048, N 256-12288, K 512-16384): beyond a common
-  // 6.5 us a wave of 256 x 256 tiles takes 0.33 us per 256 of K; a wave of
-  // split tiles 0.45 us per 256 of each CTA's K, and 2 us (0.3 us with an SM
-  // to itself) to join the sums.  Both sides of the line: 256 x 4096 x 16384
-  // pairs 27.7 us, split 16.6; 512 x 12288 x 4096 pairs 18.5 us, split 25.9.
-  const int64_t kb = (K + kBK - 1) / kBK, pairs = sm_count() / 2;
-  const auto waves = [&](int64_t bn) {
-    return (double)(((M + 255) / 256 * ((N + bn - 1) / bn) + pairs - 1) / pairs);
-  };
-  const double cost256 = waves(256) * 0.33 * (double)kb;
-  if (M <= 64 || split_cost(M, N, K) < cost256)
-    return launch_split(kind, nullptr, FP8Q_DT_BF16, 0, nullptr, &A, B, out_dtype, C, M, N, K, stream);
-  // Tiles 384 wide, by the same kind of model for a busy device (us a wave, K
-  // in 256s): 0.487 K + 1.65 against 0.354 K + 1.38.  Only for bf16 rows on 32
-  // bytes: the others' stores need more registers than the 576 threads have
-  // (8192 x 8200 x 4096 bf16: 110 us at 256, 121 at 384; fp32 402 against 460
-  // us at 15872 x 16384 x 4096).
-  const int width = row_width(C, N, out_dtype == FP8Q_DT_BF16 ? 2 : 4);
-  const bool wide = out_dtype == FP8Q_DT_BF16 && width == 32 &&
-                    waves(384) * (0.487 * (double)kb + 1.65) <
-                        waves(256) * (0.354 * (double)kb + 1.38);
-  Args a{};
-  a.M = M;
-  a.N = N;
-  a.num_m_tiles = (int)((M + 127) / 128);
-  a.num_k_blocks = (int)((K + kBK - 1) / kBK);
-  a.num_steps = (int)((K + 63) / 64);
-  a.atoms_k = (int)num_atoms_k(kind, K);
-  a.group = 8;
-  a.C = C;
-  a.ga = A.global_scale;
-  a.gb = B.global_scale;
-  a.err = device_error_word();
-  if (a.err == nullptr) return FP8Q_ERR_CUDA;
-  // coordinates of tiles and scale atoms are 32-bit
-  if ((M + 255) / 128 * ((N + 511) / 128) > INT32_MAX || K > INT32_MAX ||
-      (std::max(M, N) + 255) / 128 * a.atoms_k > INT32_MAX)
-    return FP8Q_ERR_INVALID_ARG;
-  if (log_enabled())
-    fprintf(stderr, "[fp8q] launch fp4 gemm_pair_kernel %lldx%lldx%lld kind %d tile 256x%d out %d\n",
-            (long long)M, (long long)N, (long long)K, kind, wide ? 384 : 256, out_dtype);
-  if (kind == FP4Q_MXFP4)
-    return out_dtype == FP8Q_DT_BF16
-               ? launch_pair<FP4Q_MXFP4, __nv_bfloat16>(A, B, a, K, width, wide, stream)
-               : launch_pair<FP4Q_MXFP4, float>(A, B, a, K, width, wide, stream);
-  return out_dtype == FP8Q_DT_BF16
-             ? launch_pair<FP4Q_NVFP4, __nv_bfloat16>(A, B, a, K, width, wide, stream)
-             : launch_pair<FP4Q_NVFP4, float>(A, B, a, K, width, wide, stream);
+int launch_products(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream) {
+  Product todo[kGroupMax];
+  double saves[kGroupMax];
+  int count = 0;
+  bool some = false;   // of them split
+  for (int i = 0; i < n; ++i) {
+    const Product &d = prod[i];
+    if (d.M == 0 || d.N == 0) continue;
+    if (d.K == 0) {
+      if (cudaMemsetAsync(d.C, 0, (size_t)(d.M * d.N) * (out_dtype == FP8Q_DT_BF16 ? 2 : 4), stream) !=
+          cudaSuccess)
+        return FP8Q_ERR_CUDA;
+      continue;
+    }
+    // coordinates of tiles and scale atoms are 32-bit
+    if ((d.M + 255) / 128 * ((d.N + 511) / 128) > INT32_MAX / 8 || d.K > INT32_MAX ||
+        (std::max(d.M, d.N) + 511) / 128 * (num_atoms_k(kind, d.K) + 4) > INT32_MAX)
+      return FP8Q_ERR_INVALID_ARG;
+    todo[count] = d;
+    saves[count] = split_saves(d);
+    some = some || saves[count] > 0.0;
+    ++count;
+  }
+  // those of the split kernel first
+  int split = 0;
+  for (int i = 0; i < count; ++i)
+    if (saves[i] > (some ? -kLaunchCost : 0.0)) {
+      std::swap(todo[split], todo[i]);
+      std::swap(saves[split], saves[i]);
+      ++split;
+    }
+  if (split > 0) {
+    const int rc = launch_split(kind, todo, split, out_dtype, stream);
+    if (rc != FP8Q_OK) return rc;
+  }
+  return count > split ? launch_pairs(kind, todo + split, count - split, out_dtype, stream) : FP8Q_OK;
 }
 
 }  // namespace fp4

@@ -15,7 +15,14 @@ struct QuantArgs {
   float *global_scale;         // NVFP4: receives g, or null
 };
 
-cudaError_t launch_quantize(int kind, int in_dtype, const QuantArgs &a, cudaStream_t stream);
+// Up to kGroupMax matrices of one type, or products of one kind, in one launch.
+constexpr int kGroupMax = 3;
+
+// n non-empty matrices in one launch.
+cudaError_t launch_quantize(int kind, int in_dtype, const QuantArgs *a, int n, cudaStream_t stream);
+// amax[i] = max |x| of n dense matrices of size[i] elements, one launch.
+cudaError_t launch_amax_group(const void *const *x, const int64_t *size, int n, int in_dtype,
+                              float *amax, cudaStream_t stream);
 // *global_scale = the tensor scale of *amax.
 cudaError_t launch_global(const float *amax, float *global_scale, cudaStream_t stream);
 // max |x| of a matrix with rows ld elements apart; *amax is zeroed first.
@@ -30,20 +37,27 @@ bool make_tmap(CUtensorMap *m, const void *base, int64_t rows, int64_t K, uint32
 bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_t atoms_k,
                      uint32_t box);
 
-// y[M,N] = x . w^T on tiles of 128 rows of w by up to 128 rows of x, K split
-// over the CTAs of a cluster.  x is either the 4-bit operand `q` or, with q
-// null, a bf16 / fp32 matrix that the kernel quantises as it goes (M at most
-// FP4Q_LINEAR_FUSED_ROWS; x_amax: NVFP4's amax).
-// Microseconds beyond a launch's fixed cost that launch_split would take for a
-// quantised x, by the model that chooses between it and CTA pairs.
-double split_cost(int64_t M, int64_t N, int64_t K);
-int launch_split(int kind, const void *x, int in_dtype, int64_t ldx, const float *x_amax,
-                 const fp4q_operand *q, const fp4q_operand &w, int out_dtype, void *y, int64_t M,
-                 int64_t N, int64_t K, cudaStream_t stream);
+// One product C[M,N] = A . B^T; A and B of one kind.
+struct Product {
+  fp4q_operand A, B;
+  void *C;
+  int64_t M, N, K;
+};
 
-// C[M,N] = A . B^T for non-empty sizes; a FP8Q status.
-int launch_gemm(int kind, const fp4q_operand &A, const fp4q_operand &B, int out_dtype, void *C,
-                int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+// y[M,N] = x . w^T on tiles of 128 rows of w by up to 128 rows of x, K split
+// over the CTAs of a cluster: n products in one launch, x their A.
+int launch_split(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream);
+// The same for one x in bf16 or fp32 that the kernel quantises as it goes (at
+// most FP4Q_LINEAR_FUSED_ROWS rows; x_amax: NVFP4's amax); prod.A is unused.
+int launch_split_quantizing(int kind, const void *x, int in_dtype, int64_t ldx,
+                            const float *x_amax, const Product &prod, int out_dtype,
+                            cudaStream_t stream);
+// Microseconds beyond a launch's fixed cost that launch_split would take, by
+// the model that chooses between it and CTA pairs.
+double split_cost(int64_t M, int64_t N, int64_t K);
+
+// n <= kGroupMax independent products, any sizes; a FP8Q status.
+int launch_products(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream);
 
 }  // namespace fp4
 }  // namespace fp8q

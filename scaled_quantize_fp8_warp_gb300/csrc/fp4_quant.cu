@@ -186,8 +186,25 @@ __device__ __forceinline__ void load_dealt(const QuantArgs &p, int64_t row, int6
                        in.at + ((i * kParts + h) * kThreads + threadIdx.x) * 16));
 }
 
-template <int KIND, typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_kernel(const QuantArgs p) {
+// The matrices of one launch, their tiles numbered one matrix after the other.
+// A launch of one (GROUPED false) reads it at constant offsets.
+template <bool GROUPED>
+struct QuantGroup {
+  int n;
+  unsigned tile_end[GROUPED ? kGroupMax : 1];
+  QuantArgs prob[GROUPED ? kGroupMax : 1];
+};
+
+template <int KIND, typename T, bool VEC, bool GROUPED>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+    quantize_kernel(const __grid_constant__ QuantGroup<GROUPED> group) {
+  int which = 0;
+  unsigned tile = blockIdx.x;
+  if (GROUPED) {
+    while (which + 1 < group.n && blockIdx.x >= group.tile_end[which]) ++which;
+    if (which > 0) tile -= group.tile_end[which - 1];
+  }
+  const QuantArgs &p = group.prob[which];
   constexpr int kBlock = Kind<KIND>::kBlock;
   constexpr int kAtoms = kTile / Kind<KIND>::kAtomK;   // atoms along K per tile: 1 or 2
   constexpr int kLanes = kBlock / 8;                   // lanes that share a block: 4 or 2
@@ -201,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_ker
   const int tr = (warp >> 1) * 32 + (lane >> 3) * 8;   // this thread's first row in the tile
   const int tc = (warp & 1) * 64 + (lane & 7) * 8;     // and first column
   const unsigned tiles_c = (unsigned)((p.cols + kTile - 1) / kTile);
-  const unsigned by = blockIdx.x / tiles_c, bx = blockIdx.x - by * tiles_c;
+  const unsigned by = tile / tiles_c, bx = tile - by * tiles_c;
   const int64_t r0 = (int64_t)by * kTile, c0 = (int64_t)bx * kTile;
   const int64_t row = r0 + tr, col = c0 + tc;
   const int rows_in = (int)max((int64_t)0, min((int64_t)8, p.rows - row));
@@ -228,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quantize_ker
     g = nv_global(*p.amax);
     rg = __frcp_rn(g);
     table.fill(g);
-    if (p.global_scale != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.global_scale = g;
+    if (p.global_scale != nullptr && tile == 0 && threadIdx.x == 0) *p.global_scale = g;
     __syncthreads();
   }
   if (p.q != nullptr) {
@@ -329,47 +346,71 @@ __global__ void global_kernel(const float *amax, float *global_scale) {
   *global_scale = nv_global(*amax);
 }
 
-// max |x| of a matrix whose rows lie ld apart.  The maximum of bit patterns
-// does not depend on the order of the atomics; NaN patterns sort above
-// infinity.  VEC: 16-byte aligned rows.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-    amax_kernel(const T *x, int64_t rows, int64_t cols, int64_t ld, unsigned int *amax) {
-  constexpr int kBatch = 4;   // groups of 8 elements in flight
-  follow_previous();
-  allow_next();
-  uint32_t m = 0;
-  const int64_t step = (int64_t)gridDim.x * kThreads * (VEC ? 8 : 1);
-  const int64_t first = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * (VEC ? 8 : 1);
-  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-    const T *p = x + r * ld;
-    if (VEC) {
-      for (int64_t c = first; c < cols; c += kBatch * step) {
-        Pack8<T> v[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int64_t left = cols - (c + b * step);
-          if (left >= 8)
-            v[b].load_vec(p + c + b * step);
-          else
-            v[b].load_some(p + (left > 0 ? c + b * step : 0), (int)max(left, (int64_t)0));
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) m = max(m, v[b].amax_bits());
-      }
-    } else {
-      for (int64_t c = first; c < cols; c += step)
-        m = max(m, __float_as_uint((float)p[c]) & 0x7FFFFFFFu);
-    }
-  }
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
+// max |x| of a span of a matrix, into *amax.  The maximum of bit patterns does
+// not depend on the order of the atomics; NaN patterns sort above infinity.
+__device__ __forceinline__ void publish_amax(uint32_t m, unsigned int *amax) {
   __shared__ uint32_t part[kThreads / 32];
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < kThreads / 32; ++i) m = max(m, part[i]);
     if (m != 0) atomicMax(amax, m);
   }
+}
+
+// This CTA's share of one row; VEC: the row is 16-byte aligned.
+template <typename T, bool VEC>
+__device__ __forceinline__ uint32_t row_amax(const T *p, int64_t cols) {
+  constexpr int kBatch = 4;   // groups of 8 elements in flight
+  uint32_t m = 0;
+  const int64_t step = (int64_t)gridDim.x * kThreads * (VEC ? 8 : 1);
+  const int64_t first = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * (VEC ? 8 : 1);
+  if (VEC) {
+    for (int64_t c = first; c < cols; c += kBatch * step) {
+      Pack8<T> v[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int64_t left = cols - (c + b * step);
+        if (left >= 8)
+          v[b].load_vec(p + c + b * step);
+        else
+          v[b].load_some(p + (left > 0 ? c + b * step : 0), (int)max(left, (int64_t)0));
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) m = max(m, v[b].amax_bits());
+    }
+  } else {
+    for (int64_t c = first; c < cols; c += step)
+      m = max(m, __float_as_uint((float)p[c]) & 0x7FFFFFFFu);
+  }
+  return m;
+}
+
+// A matrix whose rows lie ld apart.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    amax_rows_kernel(const T *x, int64_t rows, int64_t cols, int64_t ld, unsigned int *amax) {
+  follow_previous();
+  allow_next();
+  uint32_t m = 0;
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+    m = max(m, row_amax<T, VEC>(x + r * ld, cols));
+  publish_amax(m, amax);
+}
+
+// Dense matrices, blockIdx.y of them.
+struct AmaxGroup {
+  const void *x[kGroupMax];
+  int64_t size[kGroupMax];
+};
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    amax_group_kernel(const __grid_constant__ AmaxGroup group, unsigned int *amax) {
+  follow_previous();
+  allow_next();
+  publish_amax(row_amax<T, VEC>(static_cast<const T *>(group.x[blockIdx.y]), group.size[blockIdx.y]),
+               amax + blockIdx.y);
 }
 
 // Values of an operand: one thread per 8 codes (one 32-bit word) of kRows rows
@@ -444,9 +485,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <int KIND, typename T, bool VEC>
-cudaError_t start_quantize(const QuantArgs &a, int64_t tiles, cudaStream_t stream) {
-  auto kernel = quantize_kernel<KIND, T, VEC>;
+template <int KIND, typename T, bool VEC, bool GROUPED>
+cudaError_t start_quantize(const QuantArgs *a, int n, cudaStream_t stream) {
+  auto kernel = quantize_kernel<KIND, T, VEC, GROUPED>;
   constexpr int smem = (int)sizeof(QuantSmem<KIND, T, VEC>);
   if (smem > 48 * 1024) {
     static PerDeviceOnce setup;   // per instantiation
@@ -458,27 +499,39 @@ cudaError_t start_quantize(const QuantArgs &a, int64_t tiles, cudaStream_t strea
         }) != 1)
       return cudaErrorInvalidValue;
   }
-  return Launch((unsigned)tiles, 1, kThreads, smem, stream).run(kernel, a);
+  QuantGroup<GROUPED> group{};
+  group.n = n;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    tiles += ((a[i].cols + kTile - 1) / kTile) * ((a[i].rows + kTile - 1) / kTile);
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    group.tile_end[i] = (unsigned)tiles;
+    group.prob[i] = a[i];
+  }
+  return Launch((unsigned)tiles, 1, kThreads, smem, stream).run(kernel, group);
 }
 
 template <int KIND, typename T>
-cudaError_t run_quantize(const QuantArgs &a, cudaStream_t stream) {
-  const int64_t tiles = ((a.cols + kTile - 1) / kTile) * ((a.rows + kTile - 1) / kTile);
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 &&
-                   a.ld * (int64_t)sizeof(T) % 16 == 0 && a.cols % 8 == 0;
-  return vec ? start_quantize<KIND, T, true>(a, tiles, stream)
-             : start_quantize<KIND, T, false>(a, tiles, stream);
+cudaError_t run_quantize(const QuantArgs *a, int n, cudaStream_t stream) {
+  bool vec = true;
+  for (int i = 0; i < n; ++i)
+    vec = vec && (reinterpret_cast<uintptr_t>(a[i].x) & 15u) == 0 &&
+          a[i].ld * (int64_t)sizeof(T) % 16 == 0 && a[i].cols % 8 == 0;
+  if (n == 1)
+    return vec ? start_quantize<KIND, T, true, false>(a, n, stream)
+               : start_quantize<KIND, T, false, false>(a, n, stream);
+  return vec ? start_quantize<KIND, T, true, true>(a, n, stream)
+             : start_quantize<KIND, T, false, true>(a, n, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_quantize(int kind, int in_dtype, const QuantArgs &a, cudaStream_t stream) {
+cudaError_t launch_quantize(int kind, int in_dtype, const QuantArgs *a, int n, cudaStream_t stream) {
   if (kind == FP4Q_MXFP4)
-    return in_dtype == FP8Q_DT_BF16 ? run_quantize<FP4Q_MXFP4, __nv_bfloat16>(a, stream)
-                                    : run_quantize<FP4Q_MXFP4, float>(a, stream);
-  return in_dtype == FP8Q_DT_BF16 ? run_quantize<FP4Q_NVFP4, __nv_bfloat16>(a, stream)
-                                  : run_quantize<FP4Q_NVFP4, float>(a, stream);
+    return in_dtype == FP8Q_DT_BF16 ? run_quantize<FP4Q_MXFP4, __nv_bfloat16>(a, n, stream)
+                                    : run_quantize<FP4Q_MXFP4, float>(a, n, stream);
+  return in_dtype == FP8Q_DT_BF16 ? run_quantize<FP4Q_NVFP4, __nv_bfloat16>(a, n, stream)
+                                  : run_quantize<FP4Q_NVFP4, float>(a, n, stream);
 }
 
 cudaError_t launch_global(const float *amax, float *global_scale, cudaStream_t stream) {
@@ -494,7 +547,7 @@ static cudaError_t start_amax(const void *x, int64_t rows, int64_t cols, int64_t
   const int64_t gx = std::min<int64_t>((cols + per_cta - 1) / per_cta, 8 * sm_count());
   const unsigned gy = (unsigned)std::min<int64_t>(rows, 8 * sm_count() / gx + 1);
   return Launch((unsigned)gx, gy, kThreads, 0, stream)
-      .run(vec ? amax_kernel<T, true> : amax_kernel<T, false>, static_cast<const T *>(x), rows, cols,
+      .run(vec ? amax_rows_kernel<T, true> : amax_rows_kernel<T, false>, static_cast<const T *>(x), rows, cols,
            ld, amax);
 }
 
@@ -508,6 +561,32 @@ cudaError_t launch_amax_ld(const void *x, int in_dtype, int64_t rows, int64_t co
   unsigned int *m = reinterpret_cast<unsigned int *>(amax);
   return in_dtype == FP8Q_DT_BF16 ? start_amax<__nv_bfloat16>(x, rows, cols, ld, m, stream)
                                   : start_amax<float>(x, rows, cols, ld, m, stream);
+}
+
+template <typename T>
+static cudaError_t start_amax_group(const AmaxGroup &group, int n, unsigned int *amax,
+                                    cudaStream_t stream) {
+  bool vec = true;
+  int64_t most = 1;
+  for (int i = 0; i < n; ++i) {
+    vec = vec && (reinterpret_cast<uintptr_t>(group.x[i]) & 15u) == 0;
+    most = std::max(most, group.size[i]);
+  }
+  const int64_t per_cta = kThreads * (vec ? 8 * 4 : 8);
+  const unsigned gx = (unsigned)std::min<int64_t>((most + per_cta - 1) / per_cta, 8 * sm_count() / n);
+  return Launch(gx, (unsigned)n, kThreads, 0, stream)
+      .run(vec ? amax_group_kernel<T, true> : amax_group_kernel<T, false>, group, amax);
+}
+
+cudaError_t launch_amax_group(const void *const *x, const int64_t *size, int n, int in_dtype,
+                              float *amax, cudaStream_t stream) {
+  const cudaError_t e = cudaMemsetAsync(amax, 0, n * sizeof(float), stream);
+  if (e != cudaSuccess) return e;
+  AmaxGroup group{};
+  for (int i = 0; i < n; ++i) group.x[i] = x[i], group.size[i] = size[i];
+  unsigned int *m = reinterpret_cast<unsigned int *>(amax);
+  return in_dtype == FP8Q_DT_BF16 ? start_amax_group<__nv_bfloat16>(group, n, m, stream)
+                                  : start_amax_group<float>(group, n, m, stream);
 }
 
 template <int KIND, typename T>

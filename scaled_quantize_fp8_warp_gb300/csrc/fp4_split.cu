@@ -63,10 +63,28 @@ struct Maps {
   CUtensorMap w, sfw, x, sfx;
 };
 
+// The products of one launch, their tiles numbered one product after the
+// other.  A launch of one (GROUPED false) reads it at constant offsets.
+template <bool GROUPED>
+struct Group {
+  static constexpr int kMax = GROUPED ? kGroupMax : 1;
+  int n;
+  int tile_end[kMax];
+  Args prob[kMax];
+  Maps maps[kMax];
+};
+
 // XT: the type of x to quantise, or void for a quantised x.
-template <int KIND, typename XT>
+template <int KIND, typename XT, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 2)
-    split_kernel(const __grid_constant__ Maps maps, const Args p) {
+    split_kernel(const __grid_constant__ Group<GROUPED> group) {
+  int which = 0, tile = blockIdx.x / group.prob[0].split;   // one split for all
+  if (GROUPED) {
+    while (which + 1 < group.n && tile >= group.tile_end[which]) ++which;
+    if (which > 0) tile -= group.tile_end[which - 1];
+  }
+  const Args &p = group.prob[which];
+  const Maps &maps = group.maps[which];
   constexpr int kAtoms = kBK / Kind<KIND>::kAtomK;
   constexpr bool kQuantize = !std::is_same<XT, void>::value;
   constexpr int kSfaOff = 128 * kBKBytes, kSfbOff = kSfaOff + kAtoms * 512;
@@ -85,7 +103,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = p.split > 1 ? cluster_ctarank() : 0u;
-  const int tile = blockIdx.x / p.split;
   const int nt = tile / p.m_tiles, mt = tile - nt * p.m_tiles;
   const int rows = (int)min((int64_t)p.nb, p.M - (int64_t)mt * p.nb);   // of x in this tile
   // K blocks of this CTA
@@ -299,7 +316,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   float *part = reinterpret_cast<float *>(ring_ptr);
   if (warp >= 2) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const bool ok = wait_bounded_all(accf, 0, abort_flag, p.err);
+    // in a group some CTAs of a cluster may have no K block: they add zeros
+    const bool ok = kb1 > kb0 && wait_bounded_all(accf, 0, abort_flag, p.err);
     tc_fence_after();
     for (int c = 32 * half; c < rows; c += 64) {
       uint32_t r[32];
@@ -388,7 +406,7 @@ const int *clusters_at_once() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   const int ok = setup.get([&] {
-    auto kernel = split_kernel<FP4Q_MXFP4, void>;
+    auto kernel = split_kernel<FP4Q_MXFP4, void, false>;
     if (!set_up(kernel)) return 0;
     for (int s = 1; s <= kMaxSplit; ++s) {
       Launch q(s, 1, kThreads, kSmemBytes, nullptr, s);
@@ -413,15 +431,86 @@ int split_of(const int *fit, int64_t tiles, int64_t k_blocks) {
   return s;
 }
 
-template <int KIND, typename XT>
-int run_split(const Maps &maps, const Args &a, int64_t tiles, cudaStream_t stream) {
-  auto kernel = split_kernel<KIND, XT>;
+template <int KIND, typename XT, bool GROUPED>
+int run_split(const Group<GROUPED> &group, cudaStream_t stream) {
+  auto kernel = split_kernel<KIND, XT, GROUPED>;
   static PerDeviceOnce setup;  // per instantiation
   if (setup.get([&] { return set_up(kernel) ? 1 : 0; }) != 1) return FP8Q_ERR_CUDA;
-  return Launch((unsigned)(tiles * a.split), 1, kThreads, kSmemBytes, stream, a.split)
-                     .run(kernel, maps, a) == cudaSuccess
+  const int split = group.prob[0].split;
+  return Launch((unsigned)(group.tile_end[group.n - 1] * split), 1, kThreads, kSmemBytes, stream,
+                split)
+                     .run(kernel, group) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
+}
+
+// Everything of a group but what is only of the quantising launch.
+template <bool GROUPED>
+int fill_group(Group<GROUPED> &group, int kind, const Product *prod, int n, bool quantized,
+               int out_dtype) {
+  unsigned int *err = device_error_word();
+  const int *fit = clusters_at_once();
+  if (err == nullptr || fit == nullptr) return FP8Q_ERR_CUDA;
+  const int atoms = kind == FP4Q_MXFP4 ? 2 : 4, sf_cols = 8 * atoms;
+  group.n = n;
+  int64_t tiles = 0, k_blocks = 1;
+  for (int i = 0; i < n; ++i) {
+    const Product &d = prod[i];
+    Args &a = group.prob[i];
+    a.M = d.M;
+    a.N = d.N;
+    a.K = d.K;
+    a.gx = d.A.global_scale;
+    a.gw = d.B.global_scale;
+    a.y = d.C;
+    a.nb = rows_per_tile(d.M);
+    a.num_k_blocks = (int)((d.K + kBK - 1) / kBK);
+    a.num_steps = (int)((d.K + 63) / 64);
+    a.atoms_k = (int)num_atoms_k(kind, d.K);
+    a.out_bf16 = out_dtype == FP8Q_DT_BF16;
+    a.err = err;
+    a.m_tiles = (int)((d.M + a.nb - 1) / a.nb);
+    a.idesc = idesc_fp4(kind, 128, (uint32_t)a.nb);
+    a.stage_bytes = (128 * kBKBytes + 2 * atoms * 512 + 1023) / 1024 * 1024 + a.nb * kBKBytes;
+    a.stages = std::min(kMaxStages, (kSmemBytes - kFixedBytes) / a.stage_bytes);
+    a.stages = std::min(a.stages, ((int)kTmemCols - std::max(32, a.nb)) / sf_cols);
+    tiles += (d.N + 127) / 128 * a.m_tiles;
+    if (tiles > INT32_MAX / kMaxSplit) return FP8Q_ERR_INVALID_ARG;
+    group.tile_end[i] = (int)tiles;
+    k_blocks = std::max<int64_t>(k_blocks, a.num_k_blocks);
+    Maps &m = group.maps[i];
+    if (!make_tmap(&m.w, d.B.data, d.N, d.K, 128) ||
+        !make_scale_tmap(&m.sfw, d.B.scales, d.N, a.atoms_k, (uint32_t)atoms))
+      return FP8Q_ERR_CUDA;
+    if (!quantized) {
+      m.x = m.w;   // not used
+      m.sfx = m.sfw;
+    } else if (!make_tmap(&m.x, d.A.data, d.M, d.K, (uint32_t)a.nb) ||
+               !make_scale_tmap(&m.sfx, d.A.scales, d.M, a.atoms_k, (uint32_t)atoms)) {
+      return FP8Q_ERR_CUDA;
+    }
+  }
+  const int split = split_of(fit, tiles, k_blocks);
+  for (int i = 0; i < n; ++i) {
+    group.prob[i].split = split;
+    if (log_enabled())
+      fprintf(stderr,
+              "[fp8q] launch fp4 split_kernel %lldx%lldx%lld kind %d rows %d tiles %lld split %d "
+              "stages %d%s%s\n",
+              (long long)prod[i].M, (long long)prod[i].N, (long long)prod[i].K, kind,
+              group.prob[i].nb, (long long)tiles, split, group.prob[i].stages,
+              quantized ? "" : " quantising x", n > 1 ? " grouped" : "");
+  }
+  return FP8Q_OK;
+}
+
+template <bool GROUPED>
+int start_split(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream) {
+  Group<GROUPED> group{};
+  const int rc = fill_group(group, kind, prod, n, true, out_dtype);
+  if (rc != FP8Q_OK) return rc;
+  return kind == FP4Q_MXFP4 ? run_split<FP4Q_MXFP4, void>(group, stream)
+                            : run_split<FP4Q_NVFP4, void>(group, stream);
 }
 
 }  // namespace
@@ -436,69 +525,31 @@ double split_cost(int64_t M, int64_t N, int64_t K) {
   return (double)waves * (0.45 * (double)((kb + s - 1) / s) + (tiles * s > sm_count() ? 2.0 : 0.3));
 }
 
-int launch_split(int kind, const void *x, int in_dtype, int64_t ldx, const float *x_amax,
-                 const fp4q_operand *q, const fp4q_operand &w, int out_dtype, void *y, int64_t M,
-                 int64_t N, int64_t K, cudaStream_t stream) {
-  Args a{};
-  a.M = M;
-  a.N = N;
-  a.K = K;
-  a.ldx = ldx;
-  a.x = x;
-  a.x_amax = x_amax;
-  a.gx = q == nullptr ? nullptr : q->global_scale;
-  a.gw = w.global_scale;
-  a.y = y;
-  a.nb = rows_per_tile(M);
-  a.num_k_blocks = (int)((K + kBK - 1) / kBK);
-  a.num_steps = (int)((K + 63) / 64);
-  a.atoms_k = (int)num_atoms_k(kind, K);
-  a.out_bf16 = out_dtype == FP8Q_DT_BF16;
-  const int64_t size = in_dtype == FP8Q_DT_BF16 ? 2 : 4;
-  a.vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ldx * size % 16 == 0 && K % 8 == 0;
-  a.err = device_error_word();
-  if (a.err == nullptr) return FP8Q_ERR_CUDA;
-  const int64_t n_tiles = (N + 127) / 128, m_tiles = (M + a.nb - 1) / a.nb;
-  const int64_t tiles = n_tiles * m_tiles;
-  // coordinates of rows, tiles and scale atoms are 32-bit
-  if (tiles > INT32_MAX / 8 || K > INT32_MAX || (std::max(M, N) + 255) / 128 * a.atoms_k > INT32_MAX)
+int launch_split(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream) {
+  return n > 1 ? start_split<true>(kind, prod, n, out_dtype, stream)
+               : start_split<false>(kind, prod, n, out_dtype, stream);
+}
+
+int launch_split_quantizing(int kind, const void *x, int in_dtype, int64_t ldx,
+                            const float *x_amax, const Product &prod, int out_dtype,
+                            cudaStream_t stream) {
+  if ((prod.N + 127) / 128 > INT32_MAX / kMaxSplit || prod.K > INT32_MAX ||
+      (prod.N + 511) / 128 * (num_atoms_k(kind, prod.K) + 4) > INT32_MAX)
     return FP8Q_ERR_INVALID_ARG;
-  a.m_tiles = (int)m_tiles;
-  const int *fit = clusters_at_once();
-  if (fit == nullptr) return FP8Q_ERR_CUDA;
-  a.split = split_of(fit, tiles, a.num_k_blocks);
-  a.idesc = idesc_fp4(kind, 128, (uint32_t)a.nb);
-  const int atoms = kind == FP4Q_MXFP4 ? 2 : 4;
-  a.stage_bytes = (128 * kBKBytes + 2 * atoms * 512 + 1023) / 1024 * 1024 + a.nb * kBKBytes;
-  a.stages = std::min(kMaxStages, (kSmemBytes - kFixedBytes) / a.stage_bytes);
-  const int sf_cols = 8 * atoms;   // tensor memory of a stage's scales
-  a.stages = std::min<int>(a.stages, ((int)kTmemCols - std::max(32, a.nb)) / sf_cols);
-  Maps maps;
-  if (!make_tmap(&maps.w, w.data, N, K, 128) ||
-      !make_scale_tmap(&maps.sfw, w.scales, N, a.atoms_k, (uint32_t)atoms))
-    return FP8Q_ERR_CUDA;
-  if (q != nullptr) {
-    if (!make_tmap(&maps.x, q->data, M, K, (uint32_t)a.nb) ||
-        !make_scale_tmap(&maps.sfx, q->scales, M, a.atoms_k, (uint32_t)atoms))
-      return FP8Q_ERR_CUDA;
-  } else {
-    maps.x = maps.w;
-    maps.sfx = maps.sfw;
-  }
-  if (log_enabled())
-    fprintf(stderr,
-            "[fp8q] launch fp4 split_kernel %lldx%lldx%lld kind %d rows %d tiles %lld split %d "
-            "stages %d%s\n",
-            (long long)M, (long long)N, (long long)K, kind, a.nb, (long long)tiles, a.split,
-            a.stages, q == nullptr ? " quantising x" : "");
-  if (kind == FP4Q_MXFP4) {
-    if (q != nullptr) return run_split<FP4Q_MXFP4, void>(maps, a, tiles, stream);
-    return in_dtype == FP8Q_DT_BF16 ? run_split<FP4Q_MXFP4, __nv_bfloat16>(maps, a, tiles, stream)
-                                    : run_split<FP4Q_MXFP4, float>(maps, a, tiles, stream);
-  }
-  if (q != nullptr) return run_split<FP4Q_NVFP4, void>(maps, a, tiles, stream);
-  return in_dtype == FP8Q_DT_BF16 ? run_split<FP4Q_NVFP4, __nv_bfloat16>(maps, a, tiles, stream)
-                                  : run_split<FP4Q_NVFP4, float>(maps, a, tiles, stream);
+  Group<false> group{};
+  const int rc = fill_group(group, kind, &prod, 1, false, out_dtype);
+  if (rc != FP8Q_OK) return rc;
+  Args &a = group.prob[0];
+  const int64_t size = in_dtype == FP8Q_DT_BF16 ? 2 : 4;
+  a.x = x;
+  a.ldx = ldx;
+  a.x_amax = x_amax;
+  a.vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ldx * size % 16 == 0 && prod.K % 8 == 0;
+  if (kind == FP4Q_MXFP4)
+    return in_dtype == FP8Q_DT_BF16 ? run_split<FP4Q_MXFP4, __nv_bfloat16>(group, stream)
+                                    : run_split<FP4Q_MXFP4, float>(group, stream);
+  return in_dtype == FP8Q_DT_BF16 ? run_split<FP4Q_NVFP4, __nv_bfloat16>(group, stream)
+                                  : run_split<FP4Q_NVFP4, float>(group, stream);
 }
 
 }  // namespace fp4
