@@ -676,7 +676,8 @@ int fp4_linear_train(const void *x, const void *w, const void *g, int in_dtype,
  * scales [ceil(F/128), T].
  *   f: SILU u / (1 + e^-u); GELU u (1 + erf(u / sqrt 2)) / 2; GELU_TANH
  *   u (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))) / 2.
- * All arithmetic is fp32, with one rounding to the output's type. */
+ * All arithmetic is fp32, with one rounding to the output's type.  T and F are
+ * at most INT32_MAX / 4 (else INVALID_ARG). */
 typedef enum fp8q_act {
   FP8Q_ACT_SILU = 0,
   FP8Q_ACT_GELU = 1,

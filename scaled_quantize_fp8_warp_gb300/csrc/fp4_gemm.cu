@@ -4,16 +4,27 @@
 // whole K range accumulates in fp32 in tensor memory, and the epilogue
 // multiplies by the tensor scales (NVFP4), converts and stores.
 //
-// CTA pairs (tcgen05.mma.cta_group::2) compute 256 x 256 tiles, each CTA
-// staging its own 128 rows of A and half of B's rows per 256 elements of K
-// (128 bytes a row, 128-byte swizzle): 32 KB a stage and CTA.  (On one SM a
-// 128 x 256 tile would bring 48 KB for the same MMAs.)  Each CTA loads the
-// scale atoms of its own rows of A and of all 256 rows of B, by tensor maps in
-// which an atom is a row of 128 words; the even CTA's copies put both CTAs'
-// into tensor memory.  Tensor memory: the accumulator in columns [0, 256),
-// then a slot of scales per ring stage, which leaves no room for a second
-// accumulator: the epilogue's eight warps take it into registers at once and
-// release it before they convert and store.
+// CTA pairs (tcgen05.mma.cta_group::2) compute tiles of 256 x 256 or 256 x 384,
+// each CTA staging its own 128 rows of A and half of B's rows per 256 elements
+// of K (128 bytes a row, 128-byte swizzle).  Each CTA loads the scale atoms of
+// its own rows of A and of all rows of B, by tensor maps in which an atom is a
+// row of 128 words; the even CTA's copies put both CTAs' into tensor memory.
+// Tensor memory: the accumulator, then slots of scales, which leaves no room
+// for a second accumulator: the epilogue's warps take it into registers at once
+// and release it before they store.
+//
+// What bounds it: the copies into shared memory, then the MMAs.  8192 cube with
+// 256-wide tiles: 183 us NVFP4 and 176 MXFP4, 157 and 144 with the loads taken
+// out.  A fit over sizes gives a 384-wide tile 0.49 us per 256 of K (48 KB a CTA
+// for NVFP4, so 15 TB/s over all SMs) and 1.65 us at its end.  Long loops meet
+// the board's power limit: 256-wide 398 us at 1.83-1.90 GHz, with operands of
+// zeros 369 at 2.07.  In several runs, NVFP4 15872 x 16384 x 4096: 340-344
+// us (6.2-6.3 PFLOP/s); 15872 x 4096 x 16384: 295-297 us (7.2); 8192 cube: NVFP4
+// 170-193 us, MXFP4 160-173.  15872 x 16384 x 4096 NVFP4 took 654 us with one SM
+// a tile, 747 in pairs with instructions issued under a lane comparison, 377
+// under elect.sync.  Slower: scales and MMAs in elected blocks of their own (388
+// for 376), a wide tile's two column groups handed over in turn (410 for 340),
+// one thread for the whole loop (351 for 347).
 #include <cuda.h>
 #include <stdint.h>
 #include <stdio.h>

