@@ -888,7 +888,7 @@ def tiny_linear_latency(fq, torch, stream, reps: int = 200):
     def quantize():
         # amax, then the cast (two launches per tensor: at these sizes the
         # one-call form, a memset and a cooperative launch, is no faster
-        # eagerly and slower inside a graph)
+        # eagerly and two kernels inside a graph)
         for k in "xwg":
             qq, qt, am, sc = q[k]
             fq.fp8_amax(src[k], out=am, stream=stream)

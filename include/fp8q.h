@@ -50,7 +50,8 @@
  *     current CUDA device and may be called from several host threads at
  *     once, in a process that drives one device or several; each kernel's
  *     one-time launch set-up (its shared-memory size attribute, an occupancy
- *     query) runs once per device.  Work that shares a buffer, an amax
+ *     query) runs once per device.  Calls on different streams and replayed
+ *     graphs may overlap in time.  Work that shares a buffer, an amax
  *     history or a workspace must be ordered by the caller (one stream, or
  *     events).
  */

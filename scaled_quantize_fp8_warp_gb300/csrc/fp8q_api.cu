@@ -7,6 +7,7 @@
 #include <stdio.h>
 #include <stdlib.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "fp8q_internal.h"
@@ -26,6 +27,7 @@ struct DeviceInfo {
   int supported = 0;
   int sms = 0;
   unsigned int *err = nullptr;
+  std::atomic<unsigned long long> streams[kStreamSlots] = {};   // stream id + 1, 0: free
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -180,6 +182,21 @@ int sm_count() {
   return (d && d->sms > 0) ? d->sms : kNumSMsHint;
 }
 
+int stream_slot(cudaStream_t stream) {
+  DeviceInfo *d = current_device();
+  cudaStreamCaptureStatus capture;
+  unsigned long long id = 0;   // never given to another stream of the process
+  if (d == nullptr || cudaStreamIsCapturing(stream, &capture) != cudaSuccess ||
+      capture != cudaStreamCaptureStatusNone || cudaStreamGetId(stream, &id) != cudaSuccess)
+    return -1;
+  for (int i = 0; i < kStreamSlots; ++i) {
+    unsigned long long owner = d->streams[i].load();
+    if (owner == 0 && d->streams[i].compare_exchange_strong(owner, id + 1)) return i;
+    if (owner == id + 1) return i;
+  }
+  return -1;
+}
+
 bool log_enabled() {
   static const bool on = [] {   // initialised once, thread-safe
     const char *e = getenv("FP8Q_LOG");
@@ -286,7 +303,8 @@ int fp8_quantize_tensor_current(const void *x, int in_dtype, int64_t rows, int64
   if ((rc = check_ptr(q, false)) != FP8Q_OK || (rc = check_ptr(q_t, false)) != FP8Q_OK) return rc;
   if ((rc = check_device()) != FP8Q_OK) return rc;
   const int64_t bytes = rows * cols * (in_dtype == FP8Q_DT_BF16 ? 2 : 4);
-  if (rows == 0 || cols == 0 || bytes > kFusedTensorMaxBytes) {
+  const int slot = stream_slot(stream);   // of the grid barrier's counters
+  if (rows == 0 || cols == 0 || bytes > kFusedTensorMaxBytes || slot < 0) {
     if ((rc = fp8_amax(x, in_dtype, rows * cols, amax_out, stream)) != FP8Q_OK) return rc;
     return fp8_quantize_tensor(x, in_dtype, rows, cols, format, amax_out, scale_out, q, q_t,
                                saturate, stream);
@@ -300,6 +318,7 @@ int fp8_quantize_tensor_current(const void *x, int in_dtype, int64_t rows, int64
   p.format = format;
   p.saturate = saturate;
   p.mode = kModeTensorFused;
+  p.work_slot = slot;
   p.err = device_error_word();
   p.amax_out = amax_out;
   p.scale_out = scale_out;

@@ -41,6 +41,15 @@ unsigned int *device_error_word();
 // SM count of the current device (cached).
 int sm_count();
 
+// Counters that a kernel leaves at zero can serve launches that follow one
+// another, not launches that overlap.  Launches on one stream follow one
+// another, so each stream has counters of its own: their index, below
+// kStreamSlots.  -1 where there are none -- a launch being captured into a
+// graph, which may be replayed beside anything, or a stream past the first
+// kStreamSlots of the device -- and the launch has to do without.
+constexpr int kStreamSlots = 128;
+int stream_slot(cudaStream_t stream);
+
 // True when the environment sets FP8Q_LOG (to anything but "0"): every entry
 // point and every kernel launch then prints one line to stderr naming what
 // it runs, so a caller can see which kernel served each call.
@@ -86,7 +95,7 @@ struct QuantParams {
   uint8_t *mx_scales;          // MX: E8M0 atoms of q (see fp8_quantize_mxfp8)
   uint8_t *mxt_scales;         // MX: E8M0 atoms of q_t
   unsigned int *err;           // device error word (bounded waits)
-  int work_slot;               // tile-scheduling slot (set at launch)
+  int work_slot;               // stream_slot of the launch (kModeTensorFused: set by the caller)
   int dynamic;                 // 1: tiles past the first few are claimed (set at launch)
 };
 

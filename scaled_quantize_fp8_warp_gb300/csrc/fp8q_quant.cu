@@ -33,7 +33,6 @@
 #include <cuda.h>
 #include <cuda_fp8.h>
 
-#include <atomic>
 #include <mutex>
 #include <stdint.h>
 #include <stdio.h>
@@ -396,12 +395,10 @@ enum KernelMode : int {
                      // -> q_t, each with its tile's 512-byte E8M0 atom
 };
 
-// Dynamic tile scheduling: each launch of the quantize kernel takes one slot
-// (round-robin over kQuantWorkSlots, so launches that overlap in time use
-// different slots); work[0] hands out tile indices, work[1] counts CTAs that
-// are done, and the last CTA returns both to zero for the slot's next launch.
-constexpr int kQuantWorkSlots = 256;
-__device__ unsigned int g_quant_work[2 * kQuantWorkSlots];
+// Dynamic tile scheduling, by counters of the launch's stream: work[0] hands
+// out tile indices, work[1] counts CTAs that are done, and the last CTA
+// returns both to zero for the stream's next launch.
+__device__ unsigned int g_quant_work[2 * kStreamSlots];
 
 // Input tiles (128 x 128 elements) reach shared memory by TMA through a ring
 // of kStages buffers; thread 0 claims the next tile and refills a buffer as
@@ -1006,15 +1003,15 @@ __global__ void __launch_bounds__(kQuantThreads, (QuantShape<InT, KM>::kMinBlock
 // amax over a flat array: 16-byte loads, packed 16-bit max for bf16,
 // warp/CTA reduction; each CTA stores its maximum (as an fp32 bit pattern:
 // |x| bit patterns order like the values, NaN patterns above Inf) in its own
-// entry of a slot of g_amax_partials and takes a ticket, and the last CTA
-// reduces the partials with all its threads and writes the output.  The call
-// therefore needs no zeroing launch ahead of it, and no two CTAs contend on
-// one address except for the ticket.  Each launch takes its own slot
-// (round-robin), so launches that overlap in time do not share one.
-constexpr int kAmaxSlots = 32;
-constexpr int kAmaxMaxCtas = 8 * 256;   // partial entries per slot (grids of <= 8 CTAs per SM)
-__device__ unsigned int g_amax_partials[kAmaxSlots][kAmaxMaxCtas];
-__device__ unsigned int g_amax_tickets[kAmaxSlots];
+// entry of its stream's slot of g_amax_partials and takes a ticket, and the
+// last CTA reduces the partials with all its threads and writes the output.
+// The call therefore needs no zeroing launch ahead of it, and no two CTAs
+// contend on one address except for the ticket.  A launch without a slot has
+// its output zeroed first and its CTAs take the maximum there; one of a single
+// CTA needs neither.
+constexpr int kAmaxMaxCtas = 256;   // partial entries per slot (grids of <= 1 CTA per SM)
+__device__ unsigned int g_amax_partials[kStreamSlots][kAmaxMaxCtas];
+__device__ unsigned int g_amax_tickets[kStreamSlots];
 
 // Each CTA streams 32 KB chunks of x (chunk c = blockIdx.x + k gridDim.x)
 // through a ring of kAmaxStages shared-memory stages filled by bulk copies
@@ -1118,6 +1115,16 @@ __global__ void __launch_bounds__(256, 1)
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   if (lane == 0) red[warp] = m;
   __syncthreads();
+  if (slot < 0 || gridDim.x == 1) {
+    if (tid == 0) {
+      for (int w = 0; w < 8; ++w) m = max(m, red[w]);
+      if (gridDim.x == 1)
+        *out = m;
+      else if (m != 0)
+        atomicMax(out, m);
+    }
+    return;
+  }
   unsigned int *partials = g_amax_partials[slot];
   if (tid == 0) {
     uint32_t r = red[0];
@@ -1177,12 +1184,12 @@ cudaError_t launch_variant(const QuantParams &p, cudaStream_t stream) {
   int64_t grid = (int64_t)sm_count() * blocks_per_sm;
   if (ntiles < grid) grid = ntiles;
   if (grid < 1) grid = 1;
-  static std::atomic<unsigned int> next_slot{0};
   QuantParams q = p;
-  q.dynamic = (KM != kKTensorFused && ntiles >= 8 * grid) ? 1 : 0;
-  q.work_slot = (q.dynamic || KM == kKTensorFused)
-                    ? (int)(next_slot.fetch_add(1u) % kQuantWorkSlots)
-                    : 0;
+  if (KM != kKTensorFused) {
+    q.work_slot = ntiles >= 8 * grid ? stream_slot(stream) : -1;
+    q.dynamic = q.work_slot >= 0 ? 1 : 0;
+    if (!q.dynamic) q.work_slot = 0;   // not used
+  }
   if (log_enabled()) {
     static const char *const kModeNames[] = {"tensor",   "delayed",  "tile_rows", "tile_cols",
                                              "tile_both", "block",   "row_amax",  "row_cast",
@@ -1274,8 +1281,11 @@ cudaError_t launch_amax(const void *x, int in_dtype, int64_t n, float *amax,
   if (cap > kAmaxMaxCtas) cap = kAmaxMaxCtas;
   if (blocks > cap) blocks = cap;
   if (blocks < 1) blocks = 1;
-  static std::atomic<unsigned int> next_slot{0};
-  const int slot = (int)(next_slot.fetch_add(1u) % kAmaxSlots);
+  const int slot = blocks > 1 ? stream_slot(stream) : -1;
+  if (slot < 0 && blocks > 1) {
+    const cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(float), stream);
+    if (e != cudaSuccess) return e;
+  }
   unsigned int *out = reinterpret_cast<unsigned int *>(amax);
   unsigned int *err = device_error_word();
   if (err == nullptr) return cudaErrorInvalidValue;
