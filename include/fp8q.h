@@ -626,8 +626,11 @@ int fp4_dequantize(const fp4q_operand *op, int64_t rows, int64_t K, void *y,
 
 /* C [M, N] (dense, out_dtype) = A [M, K] . B [N, K]^T of two operands of one
  * kind, accumulated in fp32 on the tensor cores, which apply the block
- * scales; NVFP4 results are multiplied by fl32(g_A g_B).  Any M, N, K; M or
- * N == 0: nothing to do, K == 0: C is zero.  C is 16-byte aligned.
+ * scales; NVFP4 results are multiplied by fl32(g_A g_B).  Any M, N, K up to
+ * INT32_MAX - 1024 whose 128 x 128 tiles of C number at most INT32_MAX / 32 and
+ * whose operands have at most INT32_MAX scale atoms (else INVALID_ARG; so for
+ * fp4_linear and each product of fp4_linear_train); M or N == 0: nothing to do,
+ * K == 0: C is zero.  C is 16-byte aligned.
  * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
 int fp4_gemm(const fp4q_operand *A, const fp4q_operand *B, void *C,
              int out_dtype, int64_t M, int64_t N, int64_t K,

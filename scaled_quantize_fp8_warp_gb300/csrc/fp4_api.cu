@@ -174,7 +174,7 @@ int fp4_gemm(const fp4q_operand *A, const fp4q_operand *B, void *C, int out_dtyp
   int rc = check_operand(A, M, K);
   if (rc != FP8Q_OK) return rc;
   if ((rc = check_operand(B, N, K)) != FP8Q_OK) return rc;
-  if (A->kind != B->kind) return FP8Q_ERR_INVALID_ARG;
+  if (A->kind != B->kind || !fp4::product_fits(A->kind, M, N, K)) return FP8Q_ERR_INVALID_ARG;
   if ((rc = check_matrix(C, M, N, N, 16)) != FP8Q_OK) return rc;
   if ((rc = check_device()) != FP8Q_OK) return rc;
   const fp4::Product d{*A, *B, C, M, N, K};
@@ -197,6 +197,7 @@ int fp4_linear(const void *x, int in_dtype, int64_t ldx, const fp4q_operand *w, 
     return FP8Q_ERR_INVALID_ARG;
   int rc = check_operand(w, N, K);
   if (rc != FP8Q_OK) return rc;
+  if (!fp4::product_fits(w->kind, M, N, K)) return FP8Q_ERR_INVALID_ARG;
   if ((rc = check_matrix(x, M, K, ldx, dtype_size(in_dtype))) != FP8Q_OK) return rc;
   if ((rc = check_matrix(y, M, N, N, 16)) != FP8Q_OK) return rc;
   if (!aligned(x_amax, 4)) return FP8Q_ERR_MISALIGNED;
@@ -247,7 +248,8 @@ int fp4_linear_train(const void *x, const void *w, const void *g, int in_dtype, 
                      int64_t N, int64_t K, int kind, void *y, void *dx, void *dw, int out_dtype,
                      void *workspace, size_t ws_bytes, cudaStream_t stream) {
   if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype) || !valid_kind(kind) ||
-      !linear_ok(M, N, K))
+      !linear_ok(M, N, K) || !fp4::product_fits(kind, M, N, K) ||
+      !fp4::product_fits(kind, M, K, N) || !fp4::product_fits(kind, N, K, M))
     return FP8Q_ERR_INVALID_ARG;
   const int64_t in = dtype_size(in_dtype);
   int rc;

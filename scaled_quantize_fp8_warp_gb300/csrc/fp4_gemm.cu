@@ -582,6 +582,15 @@ bool make_scale_tmap(CUtensorMap *m, const uint8_t *scales, int64_t rows, int64_
                       CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+bool product_fits(int kind, int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0 || K == 0) return true;   // no kernel runs
+  const int64_t longest = std::max(M, N);
+  // a launch of three products numbers the tiles of all, and CTAs of up to eight a tile
+  return longest <= INT32_MAX - 1024 && K <= INT32_MAX - 1024 &&
+         (M + 255) / 128 * ((N + 511) / 128) <= INT32_MAX / 32 &&
+         (longest + 511) / 128 * (num_atoms_k(kind, K) + 4) <= INT32_MAX;
+}
+
 int launch_products(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream) {
   Product todo[kGroupMax];
   double saves[kGroupMax];
@@ -596,10 +605,6 @@ int launch_products(int kind, const Product *prod, int n, int out_dtype, cudaStr
         return FP8Q_ERR_CUDA;
       continue;
     }
-    // coordinates of tiles and scale atoms are 32-bit
-    if ((d.M + 255) / 128 * ((d.N + 511) / 128) > INT32_MAX / 8 || d.K > INT32_MAX ||
-        (std::max(d.M, d.N) + 511) / 128 * (num_atoms_k(kind, d.K) + 4) > INT32_MAX)
-      return FP8Q_ERR_INVALID_ARG;
     todo[count] = d;
     saves[count] = split_saves(d);
     some = some || saves[count] > 0.0;

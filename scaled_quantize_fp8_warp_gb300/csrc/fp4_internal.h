@@ -44,6 +44,11 @@ struct Product {
   int64_t M, N, K;
 };
 
+// Whether a product's sizes fit the kernels' indexes: element offsets are
+// 64-bit, but rows, tiles and scale atoms are counted in 32 bits, and the
+// coordinates of a tile past the last row have to fit too.
+bool product_fits(int kind, int64_t M, int64_t N, int64_t K);
+
 // y[M,N] = x . w^T on tiles of 128 rows of w by up to 128 rows of x, K split
 // over the CTAs of a cluster: n products in one launch, x their A.
 int launch_split(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream);
@@ -56,7 +61,7 @@ int launch_split_quantizing(int kind, const void *x, int in_dtype, int64_t ldx,
 // the model that chooses between it and CTA pairs.
 double split_cost(int64_t M, int64_t N, int64_t K);
 
-// n <= kGroupMax independent products, any sizes; a FP8Q status.
+// n <= kGroupMax independent products that fit; a FP8Q status.
 int launch_products(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream);
 
 }  // namespace fp4

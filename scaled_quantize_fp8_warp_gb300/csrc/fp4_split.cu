@@ -545,9 +545,6 @@ int launch_split(int kind, const Product *prod, int n, int out_dtype, cudaStream
 int launch_split_quantizing(int kind, const void *x, int in_dtype, int64_t ldx,
                             const float *x_amax, const Product &prod, int out_dtype,
                             cudaStream_t stream) {
-  if ((prod.N + 127) / 128 > INT32_MAX / kMaxSplit || prod.K > INT32_MAX ||
-      (prod.N + 511) / 128 * (num_atoms_k(kind, prod.K) + 4) > INT32_MAX)
-    return FP8Q_ERR_INVALID_ARG;
   Group<false> group{};
   const int rc = fill_group(group, kind, &prod, 1, false, out_dtype);
   if (rc != FP8Q_OK) return rc;
