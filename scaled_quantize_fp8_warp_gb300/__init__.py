@@ -746,12 +746,14 @@ def fp4_quantize(x: torch.Tensor, kind: int, rows=True, cols=False,
                  q_t: Fp4Operand | None = None, stream=None):
     """x [R, C] (rows may lie apart) -> (operand [R, C] | None, operand [C, R]
     of x^T | None).  NVFP4 takes the tensor's amax from ``amax`` (one fp32
-    device value) or finds it first."""
+    device value) or finds it first.  ``q`` and ``q_t`` are storage for the
+    orientations asked for by ``rows`` and ``cols``, which share one tensor
+    scale; one that is not asked for is not touched."""
     p, ld = _rows(x)
     R, C = x.shape
     if kind not in (MXFP4, NVFP4):
         raise ValueError("a 4-bit operand is MXFP4 or NVFP4")
-    g = None
+    q, q_t, g = (q if rows else None), (q_t if cols else None), None
     if kind == NVFP4:
         amax = amax if amax is not None else fp4_amax(x, stream=stream)
         given = q if q is not None else q_t
@@ -771,7 +773,7 @@ def fp4_quantize(x: torch.Tensor, kind: int, rows=True, cols=False,
         p, _in_dtype(x), R, C, ld, kind, _one(amax, "amax") if kind == NVFP4 else None,
         a.data if rows else None, a.scales if rows else None, b.data if cols else None,
         b.scales if cols else None, _addr(g), _raw_stream(stream)), "fp4_quantize")
-    return (q if rows else None), (q_t if cols else None)
+    return q, q_t
 
 
 def fp4_dequantize(op: Fp4Operand, out_dtype=torch.bfloat16, out=None, stream=None):
