@@ -63,7 +63,7 @@ __device__ __forceinline__ void activation(float u, float &f, float &df) {
     f = u * p;
     if (GRAD) {
       const float q = p * (1.0f - p);
-      df = p + (q == 0.0f ? 0.0f : u * q * (1.5957691f + 0.21406671f * uu));
+      df = p + (q == 0.0f ? 0.0f : u * q * (1.5957691f + 0.21406445f * uu));
     }
   }
 }
