@@ -44,6 +44,26 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
+// The normal distribution below -v, v >= 0, from e = e^(-v^2/2): e t P(t) with
+// t = 1 / (1 + v / sqrt 8), the form of C. Hastings (Approximations for Digital
+// Computers, 1955).  P, of degree 8, was fitted for this file to erfcx(v / sqrt
+// 2) / (2 t) with least largest relative error (4.3e-8 for v up to 13.5, where e
+// underflows; 3.2e-7 in fp32).  (1 + erf) / 2 instead would lose every digit
+// below -5.5; erfcf took 299 us where this takes 180 and erff took 206 (forward,
+// gated bf16 8192 x 16384).
+__device__ __forceinline__ float normal_tail(float v, float e) {
+  const float t = rcp_fast(fmaf(v, 0.353553391f, 1.0f));
+  float q = fmaf(t, -0.0294656865f, 0.141950533f);
+  q = fmaf(t, q, -0.242899209f);
+  q = fmaf(t, q, 0.13822794f);
+  q = fmaf(t, q, -0.0127546927f);
+  q = fmaf(t, q, 0.101105742f);
+  q = fmaf(t, q, 0.121612407f);
+  q = fmaf(t, q, 0.141179264f);
+  q = fmaf(t, q, 0.141043693f);
+  return q * (t * e);
+}
+
 // f(u), and f'(u) where it is wanted.  Large |u| stay finite: e^-u may
 // overflow to infinity, whose reciprocal is 0.
 template <int ACT, bool GRAD>
@@ -53,9 +73,10 @@ __device__ __forceinline__ void activation(float u, float &f, float &df) {
     f = u * s;
     if (GRAD) df = s * (1.0f + u * (1.0f - s));
   } else if (ACT == FP8Q_ACT_GELU) {
-    const float p = 0.5f + 0.5f * erff(u * 0.70710678f);
+    const float e = exp2_fast(-0.72134752f * u * u), q = normal_tail(fabsf(u), e);
+    const float p = u < 0.0f ? q : 1.0f - q;
     f = u * p;
-    if (GRAD) df = p + u * (0.39894228f * exp2_fast(-0.72134752f * u * u));
+    if (GRAD) df = p + u * (0.39894228f * e);
   } else {
     // (1 + tanh z) / 2 = 1 / (1 + e^-2z), 2 z log2(e) = u (2.302208 + 0.1029432 u^2)
     const float uu = u * u;

@@ -14,7 +14,7 @@ import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
-ACTS = ["silu", "gelu_tanh"]
+ACTS = ["silu", "gelu", "gelu_tanh"]
 LOWEST = {"silu": -87.0, "gelu": -13.5, "gelu_tanh": -9.5}
 ULP, TINY = 2.0 ** -23, 2e-36
 _erfc = np.vectorize(math.erfc)
@@ -84,3 +84,8 @@ def test_backward_keeps_its_digits(fq, name, dtype):
     lost = 0.0 if name == "gelu" else 2 * ULP * np.abs(x) * p * (slope / (p * r))
     near(du, df * w, (rel * (p + np.abs(x) * slope) + lost) * w + 2 * ULP * np.abs(df * w), name + " du")
 
+
+def test_gelu_below_minus_5_5_is_not_zero(fq):
+    u = torch.tensor([[-5.6], [-6.0], [-8.0], [-10.0]], device="cuda")
+    a, _ = fq.fp8_act_forward(fq.ACT_GELU, u)
+    assert (a < 0).all()
