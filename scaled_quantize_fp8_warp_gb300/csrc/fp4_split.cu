@@ -402,44 +402,59 @@ bool set_up(Kernel kernel) {
                               cudaSharedmemCarveoutMaxShared) == cudaSuccess;
 }
 
-// Clusters of 1 .. kMaxSplit CTAs that run at once on the current device: a
-// cluster keeps to one of the GPU's partitions, so fewer CTAs fit as sixes or
-// sevens than alone.  Every instantiation has the same block, shared memory
-// and residence, so one kernel answers for all.  The query counts one CTA an
-// SM here whatever the shared memory; two run (start and end times of 304 CTAs
-// overlap in pairs on an SM), hence twice its answer.  Null on failure.
-const int *clusters_at_once() {
-  static int fit[64][kMaxSplit];
+// Clusters of 1 .. kMaxSplit CTAs that run on the current device with every CTA
+// alone on its SM, and that run at once: a cluster keeps to one of the GPU's
+// partitions, so fewer CTAs fit as sixes or sevens than singly.  Every
+// instantiation has the same block, shared memory and residence, so one kernel
+// answers for all.  The query counts one CTA an SM here whatever the shared
+// memory; two run, hence twice its answer, and a cluster of seven or eight fits
+// on four SMs: as many as fours alone.  Counted, and found by the time's jump as
+// tiles are added (1 .. 8): 304, 152, 92, 72, 56, 46, 36, 36 and 304, 152, 97, 74,
+// 58, 46, 38, 36.
+struct Fit {
+  int alone[kMaxSplit], at_once[kMaxSplit];
+};
+
+// Null on failure.
+const Fit *clusters_at_once() {
+  static Fit fits[64];
   static PerDeviceOnce setup;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   const int ok = setup.get([&] {
+    Fit &fit = fits[dev];
     auto kernel = split_kernel<FP4Q_MXFP4, void, false>;
     if (!set_up(kernel)) return 0;
     for (int s = 1; s <= kMaxSplit; ++s) {
       Launch q(s, 1, kThreads, kSmemBytes, nullptr, s);
       q.cfg.numAttrs = 2;   // the query wants the cluster size, one included
-      if (cudaOccupancyMaxActiveClusters(&fit[dev][s - 1], kernel, &q.cfg) != cudaSuccess ||
-          fit[dev][s - 1] < 1)
+      if (cudaOccupancyMaxActiveClusters(&fit.alone[s - 1], kernel, &q.cfg) != cudaSuccess ||
+          fit.alone[s - 1] < 1)
         return 0;
-      fit[dev][s - 1] *= 2;
+      fit.at_once[s - 1] = 2 * fit.alone[s - 1];
+      if (s >= 7) fit.at_once[s - 1] = std::max(fit.at_once[s - 1], fit.alone[3]);
     }
     return 1;
   });
-  return ok == 1 ? fit[dev] : nullptr;
+  return ok == 1 ? &fits[dev] : nullptr;
 }
 
 int rows_per_tile(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
 
-// CTAs a tile: the most of which all tiles run at once, at most one per K
-// block.  With eight or more K blocks each, a few tiles too many (7%) may wait
-// for a free place: 13 x 4096 x 16384 NVFP4, 32 tiles of which 30 run at once
-// as eights, takes 11.7 us so and 13.6 us as sixes; with fewer K blocks the
-// second turn costs more than it saves (1 x 4096 x 4096: 6.2 us as eights, 5.7
-// as fours).
-int split_of(const int *fit, int64_t tiles, int64_t k_blocks) {
+// CTAs a tile: the most of which all tiles run at once.  A tile that has to
+// wait for a place costs a whole turn: one row, K 8192, 46 tiles as sixes take
+// 7.3 us and 47 take 11.9 (as fives 7.5).  Each CTA has a K block at least;
+// where CTAs share an SM, four, and eight if a tile has 128 rows, since joining
+// the sums of two CTAs an SM costs as much: 16 x 4480 x 2048, 35 tiles, 5.9 us as
+// eights and 4.9 as fours, 128 x 4096 x 4096, 32 tiles, 9.9 as eights and 7.9 as
+// fours.  Over 890 sizes (M 1-512, N 512-16384, K 1024-16384) the choice is 1.0%
+// from the best split on average; farthest where threes are counted low: 16 x
+// 12288 x 16384, 96 tiles, 31.8 us as twos and 24.2 as threes.
+int split_of(const Fit &fit, int64_t tiles, int64_t k_blocks, int nb) {
+  const int64_t least = nb == kMaxRows ? 8 : 4;
   int s = (int)std::min<int64_t>(kMaxSplit, k_blocks);
-  while (s > 1 && fit[s - 1] < tiles && !(k_blocks >= 8 * s && fit[s - 1] * 107 >= tiles * 100)) --s;
+  while (s > 1 && (fit.at_once[s - 1] < tiles || (fit.alone[s - 1] < tiles && k_blocks < least * s)))
+    --s;
   return s;
 }
 
@@ -461,11 +476,12 @@ template <bool GROUPED>
 int fill_group(Group<GROUPED> &group, int kind, const Product *prod, int n, bool quantized,
                int out_dtype) {
   unsigned int *err = device_error_word();
-  const int *fit = clusters_at_once();
+  const Fit *fit = clusters_at_once();
   if (err == nullptr || fit == nullptr) return FP8Q_ERR_CUDA;
   const int atoms = kind == FP4Q_MXFP4 ? 2 : 4, sf_cols = 8 * atoms;
   group.n = n;
   int64_t tiles = 0, k_blocks = 1;
+  int nb = 0;
   for (int i = 0; i < n; ++i) {
     const Product &d = prod[i];
     Args &a = group.prob[i];
@@ -490,6 +506,7 @@ int fill_group(Group<GROUPED> &group, int kind, const Product *prod, int n, bool
     if (tiles > INT32_MAX / kMaxSplit) return FP8Q_ERR_INVALID_ARG;
     group.tile_end[i] = (int)tiles;
     k_blocks = std::max<int64_t>(k_blocks, a.num_k_blocks);
+    nb = std::max(nb, a.nb);
     Maps &m = group.maps[i];
     if (!make_tmap(&m.w, d.B.data, d.N, d.K, 128) ||
         !make_scale_tmap(&m.sfw, d.B.scales, d.N, a.atoms_k, (uint32_t)atoms))
@@ -502,7 +519,7 @@ int fill_group(Group<GROUPED> &group, int kind, const Product *prod, int n, bool
       return FP8Q_ERR_CUDA;
     }
   }
-  const int split = split_of(fit, tiles, k_blocks);
+  const int split = split_of(*fit, tiles, k_blocks, nb);
   for (int i = 0; i < n; ++i) {
     group.prob[i].split = split;
     if (log_enabled())
@@ -528,13 +545,14 @@ int start_split(int kind, const Product *prod, int n, int out_dtype, cudaStream_
 }  // namespace
 
 double split_cost(int64_t M, int64_t N, int64_t K) {
-  const int *fit = clusters_at_once();
+  const Fit *fit = clusters_at_once();
   if (fit == nullptr) return 0.0;
-  const int64_t nb = rows_per_tile(M), kb = (K + kBK - 1) / kBK;
+  const int nb = rows_per_tile(M);
+  const int64_t kb = (K + kBK - 1) / kBK;
   const int64_t tiles = (N + 127) / 128 * ((M + nb - 1) / nb);
-  const int s = split_of(fit, tiles, kb);
-  const int64_t waves = (tiles + fit[s - 1] - 1) / fit[s - 1];
-  return (double)waves * (0.45 * (double)((kb + s - 1) / s) + (tiles * s > sm_count() ? 2.0 : 0.3));
+  const int s = split_of(*fit, tiles, kb, nb);
+  const int64_t waves = (tiles + fit->at_once[s - 1] - 1) / fit->at_once[s - 1];
+  return (double)waves * (0.45 * (double)((kb + s - 1) / s) + (fit->alone[s - 1] < tiles ? 2.0 : 0.3));
 }
 
 int launch_split(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream) {
