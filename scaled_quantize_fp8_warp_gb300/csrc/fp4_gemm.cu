@@ -564,9 +564,10 @@ double split_saves(const Product &d) {
   return 0.33 * (double)waves * (double)((d.K + kBK - 1) / kBK) - split_cost(d.M, d.N, d.K);
 }
 
-// What one launch more costs: products of a call that differ by less than this
-// go together (333 x 650 x 1031, all three of a training step: 13.1 us the
-// third alone after 10.3 us the other two, 12 us in one).
+// What one launch more costs: where those of a call's products that pairs suit
+// better lose less than this together, they join the others' split launch (333
+// x 650 x 1031, all three of a training step: 13.1 us the third alone after 10.3
+// us the other two, 12 us in one).
 constexpr double kLaunchCost = 3.0;
 
 }  // namespace
@@ -595,9 +596,8 @@ bool product_fits(int kind, int64_t M, int64_t N, int64_t K) {
 
 int launch_products(int kind, const Product *prod, int n, int out_dtype, cudaStream_t stream) {
   Product todo[kGroupMax];
-  double saves[kGroupMax];
+  double saves[kGroupMax], loss = 0.0;   // of those that pairs suit better
   int count = 0;
-  bool some = false;   // of them split
   for (int i = 0; i < n; ++i) {
     const Product &d = prod[i];
     if (d.M == 0 || d.N == 0) continue;
@@ -609,17 +609,17 @@ int launch_products(int kind, const Product *prod, int n, int out_dtype, cudaStr
     }
     todo[count] = d;
     saves[count] = split_saves(d);
-    some = some || saves[count] > 0.0;
+    if (saves[count] <= 0.0) loss -= saves[count];
     ++count;
   }
   // those of the split kernel first
   int split = 0;
   for (int i = 0; i < count; ++i)
-    if (saves[i] > (some ? -kLaunchCost : 0.0)) {
+    if (saves[i] > 0.0) {
       std::swap(todo[split], todo[i]);
-      std::swap(saves[split], saves[i]);
       ++split;
     }
+  if (split > 0 && loss < kLaunchCost) split = count;
   if (split > 0) {
     const int rc = launch_split(kind, todo, split, out_dtype, stream);
     if (rc != FP8Q_OK) return rc;

@@ -56,3 +56,20 @@ for N in range(256, 12289, 256):
     order = [max(split[N]) for N in sorted(split)]
     assert order == sorted(order, reverse=True)
     assert order[0] == 8 and order[-1] > 1
+
+
+def test_a_training_step_shares_a_launch_only_where_one_is_saved():
+    """By the times the choice goes by: three products that differ little go
+    together; where one or both of the others belong on CTA pairs by more than
+    a launch in all, none of the others is moved."""
+    log = logged(r"""
+for M, N, K in ((128, 128, 4096), (128, 1024, 16384), (200, 200, 16384)):
+    x, w, g = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((M, K), (N, K), (M, N)))
+    mark(M, N, K)
+    fq.fp4_linear_train(x, w, g, fq.MXFP4)
+""")
+    kernels = {k: [("split" if "split_kernel" in s else "pair", "grouped" in s) for s in lines if "launch fp4" in s
+                   and ("split_kernel" in s or "gemm_pair_kernel" in s)] for k, lines in log.items()}
+    assert kernels["128 128 4096"] == [("split", True)] * 3
+    for k in ("128 1024 16384", "200 200 16384"):
+        assert kernels[k] == [("split", False), ("pair", True), ("pair", True)], kernels[k]
