@@ -3,7 +3,6 @@
 // check, workspace layout and dispatch.  No call allocates or synchronises.
 #include <cuda_runtime.h>
 #include <stdint.h>
-#include <stdio.h>
 
 #include "fp4_common.cuh"
 #include "fp4_internal.h"
@@ -135,9 +134,8 @@ int fp4_quantize(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_
       !aligned(amax, 4) || !aligned(global_scale, 4))
     return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
-  if (log_enabled())
-    fprintf(stderr, "[fp8q] fp4_quantize %lldx%lld kind=%d q=%d qt=%d\n", (long long)rows,
-            (long long)cols, kind, q != nullptr, qt != nullptr);
+  log_line("fp4_quantize %lldx%lld kind=%d q=%d qt=%d", (long long)rows, (long long)cols, kind,
+           q != nullptr, qt != nullptr);
   if (empty)
     return kind == FP4Q_NVFP4 ? from_cuda(fp4::launch_global(amax, global_scale, stream)) : FP8Q_OK;
   const fp4q_operand a{q, q_scales, nullptr, kind, 0}, b{qt, qt_scales, nullptr, kind, 0};
@@ -154,6 +152,7 @@ int fp4_amax(const void *x, int in_dtype, int64_t rows, int64_t cols, int64_t ld
   if (rc != FP8Q_OK) return rc;
   if (!aligned(amax, 4)) return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
+  log_line("fp4_amax %lldx%lld", (long long)rows, (long long)cols);
   return from_cuda(fp4::launch_amax_ld(x, in_dtype, rows, cols, ld, amax, stream));
 }
 
@@ -165,6 +164,7 @@ int fp4_dequantize(const fp4q_operand *op, int64_t rows, int64_t K, void *y, int
   if ((rc = check_matrix(y, rows, K, K, 16)) != FP8Q_OK) return rc;
   if ((rc = check_device()) != FP8Q_OK) return rc;
   if (rows == 0 || K == 0) return FP8Q_OK;
+  log_line("fp4_dequantize %lldx%lld kind=%d", (long long)rows, (long long)K, op->kind);
   return from_cuda(fp4::launch_dequantize(op->kind, *op, rows, K, out_dtype, y, stream));
 }
 
@@ -177,6 +177,8 @@ int fp4_gemm(const fp4q_operand *A, const fp4q_operand *B, void *C, int out_dtyp
   if (A->kind != B->kind || !fp4::product_fits(A->kind, M, N, K)) return FP8Q_ERR_INVALID_ARG;
   if ((rc = check_matrix(C, M, N, N, 16)) != FP8Q_OK) return rc;
   if ((rc = check_device()) != FP8Q_OK) return rc;
+  log_line("fp4_gemm M=%lld N=%lld K=%lld kind=%d out=%d", (long long)M, (long long)N, (long long)K,
+           A->kind, out_dtype);
   const fp4::Product d{*A, *B, C, M, N, K};
   return fp4::launch_products(A->kind, &d, 1, out_dtype, stream);
 }
@@ -209,6 +211,8 @@ int fp4_linear(const void *x, int in_dtype, int64_t ldx, const fp4q_operand *w, 
   if (!aligned(workspace, 256)) return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
   if (M == 0 || N == 0) return FP8Q_OK;
+  log_line("fp4_linear M=%lld N=%lld K=%lld kind=%d out=%d amax=%d", (long long)M, (long long)N,
+           (long long)K, w->kind, out_dtype, x_amax != nullptr);
   Pieces ws{static_cast<uint8_t *>(workspace)};
   float *words = reinterpret_cast<float *>(ws.take(8));
   fp4q_operand q{};
@@ -264,6 +268,8 @@ int fp4_linear_train(const void *x, const void *w, const void *g, int in_dtype, 
     return FP8Q_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
+  log_line("fp4_linear_train M=%lld N=%lld K=%lld kind=%d out=%d", (long long)M, (long long)N,
+           (long long)K, kind, out_dtype);
   Pieces ws{static_cast<uint8_t *>(workspace)};
   float *amax = reinterpret_cast<float *>(ws.take(3 * sizeof(float)));
   Both bx, bw, bg;
@@ -317,9 +323,7 @@ int fp8_act_forward(int act, int dtype, int64_t T, int64_t F, const void *u, int
   if (!aligned(v_scales, 4)) return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
   if (T == 0 || F == 0) return FP8Q_OK;
-  if (log_enabled())
-    fprintf(stderr, "[fp8q] fp8_act_forward act=%d %lldx%lld gated=%d\n", act, (long long)T,
-            (long long)F, gated);
+  log_line("fp8_act_forward act=%d %lldx%lld gated=%d", act, (long long)T, (long long)F, gated);
   act::ForwardArgs p{};
   p.T = T;
   p.F = F;
@@ -356,9 +360,8 @@ int fp8_act_backward(int act, int dtype, int64_t T, int64_t F, const uint8_t *u8
   if (!aligned(v_scales, 4)) return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
   if (T == 0 || F == 0) return FP8Q_OK;
-  if (log_enabled())
-    fprintf(stderr, "[fp8q] fp8_act_backward act=%d %lldx%lld gated=%d a=%d\n", act, (long long)T,
-            (long long)F, gated, a != nullptr);
+  log_line("fp8_act_backward act=%d %lldx%lld gated=%d a=%d", act, (long long)T, (long long)F,
+           gated, a != nullptr);
   act::BackwardArgs p{};
   p.T = T;
   p.F = F;

@@ -27,7 +27,6 @@
 // one thread for the whole loop (351 for 347).
 #include <cuda.h>
 #include <stdint.h>
-#include <stdio.h>
 
 #include <algorithm>
 #include <cmath>
@@ -438,6 +437,7 @@ int run_pair(const PairGroup<GROUPED> &grp, cudaStream_t stream) {
   });
   if (pairs < 1) return FP8Q_ERR_CUDA;
   const int units = grp.unit_end[grp.n - 1];
+  log_line("  %d products, %d tiles, grid %d in pairs", grp.n, units, 2 * std::min(units, pairs));
   return Launch(2 * std::min(units, pairs), 1, L::kThreads, L::kSmemBytes, stream, 2)
                      .run(kernel, grp) == cudaSuccess
              ? FP8Q_OK
@@ -527,11 +527,10 @@ int launch_pairs(int kind, const Product *prod, int n, int out_dtype, cudaStream
   // the last wave is a whole one
   for (int w = 0; w < 2; ++w) cost[w] *= std::ceil(waves[w]) / waves[w];
   const bool wide = bf16 && width == 32 && cost[1] < cost[0];
-  if (log_enabled())
-    for (int i = 0; i < n; ++i)
-      fprintf(stderr, "[fp8q] launch fp4 gemm_pair_kernel %lldx%lldx%lld kind %d tile 256x%d out %d%s\n",
-              (long long)prod[i].M, (long long)prod[i].N, (long long)prod[i].K, kind,
-              wide ? 384 : 256, out_dtype, n > 1 ? " grouped" : "");
+  for (int i = 0; i < n; ++i)
+    log_line("launch fp4 gemm_pair_kernel %lldx%lldx%lld kind %d tile 256x%d out %d%s", (long long)prod[i].M,
+             (long long)prod[i].N, (long long)prod[i].K, kind, wide ? 384 : 256, out_dtype,
+             n > 1 ? " grouped" : "");
   if (kind == FP4Q_MXFP4) {
     if (n > 1)
       return bf16 ? launch_pair<FP4Q_MXFP4, __nv_bfloat16, true>(prod, n, width, wide, stream)

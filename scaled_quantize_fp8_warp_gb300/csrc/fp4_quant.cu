@@ -18,7 +18,6 @@
 // 32.2 us where three take 28.8, four 30.6 (MXFP4: 29.8, 26.0, 26.0).
 #include <cuda.h>
 #include <stdint.h>
-#include <stdio.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -518,6 +517,9 @@ cudaError_t start_quantize(const QuantArgs *a, int n, cudaStream_t stream) {
     group.tile_end[i] = (unsigned)tiles;
     group.prob[i] = a[i];
   }
+  log_line("launch fp4 quantize_kernel kind %d %s input%s, %d matrices, tiles of 128x128, grid %lld",
+           KIND, sizeof(T) == 2 ? "bf16" : "fp32", VEC ? "" : " element by element", n,
+           (long long)tiles);
   return Launch((unsigned)tiles, 1, kThreads, smem, stream).run(kernel, group);
 }
 
@@ -545,6 +547,7 @@ cudaError_t launch_quantize(int kind, int in_dtype, const QuantArgs *a, int n, c
 }
 
 cudaError_t launch_global(const float *amax, float *global_scale, cudaStream_t stream) {
+  log_line("launch fp4 global_kernel grid 1");
   return Launch(1, 1, 1, 0, stream).run(global_kernel, amax, global_scale);
 }
 
@@ -556,6 +559,8 @@ static cudaError_t start_amax(const void *x, int64_t rows, int64_t cols, int64_t
   const int64_t per_cta = kThreads * (vec ? 8 * 4 : 8);
   const int64_t gx = std::min<int64_t>((cols + per_cta - 1) / per_cta, 8 * sm_count());
   const unsigned gy = (unsigned)std::min<int64_t>(rows, 8 * sm_count() / gx + 1);
+  log_line("launch fp4 amax_rows_kernel %s input, %lldx%lld, grid %lldx%u",
+           sizeof(T) == 2 ? "bf16" : "fp32", (long long)rows, (long long)cols, (long long)gx, gy);
   return Launch((unsigned)gx, gy, kThreads, 0, stream)
       .run(vec ? amax_rows_kernel<T, true> : amax_rows_kernel<T, false>, static_cast<const T *>(x), rows, cols,
            ld, amax);
@@ -584,6 +589,7 @@ static cudaError_t start_amax_group(const AmaxGroup &group, int n, unsigned int 
   }
   const int64_t per_cta = kThreads * (vec ? 8 * 4 : 8);
   const unsigned gx = (unsigned)std::min<int64_t>((most + per_cta - 1) / per_cta, 8 * sm_count() / n);
+  log_line("launch fp4 amax_group_kernel %s input, grid %ux%d", sizeof(T) == 2 ? "bf16" : "fp32", gx, n);
   return Launch(gx, (unsigned)n, kThreads, 0, stream)
       .run(vec ? amax_group_kernel<T, true> : amax_group_kernel<T, false>, group, amax);
 }
@@ -604,7 +610,10 @@ static cudaError_t run_dequantize(const fp4q_operand &op, int64_t rows, int64_t 
                                   cudaStream_t stream) {
   const int64_t gx = (K + 8 * kThreads - 1) / (8 * kThreads);
   if (gx > INT32_MAX) return cudaErrorInvalidValue;
-  return Launch((unsigned)gx, (unsigned)std::min<int64_t>((rows + 3) / 4, 65535), kThreads, 0, stream)
+  const unsigned gy = (unsigned)std::min<int64_t>((rows + 3) / 4, 65535);
+  log_line("launch fp4 dequantize_kernel kind %d %s output, four rows of 2048 columns a CTA, grid %lldx%u",
+           KIND, sizeof(T) == 2 ? "bf16" : "fp32", (long long)gx, gy);
+  return Launch((unsigned)gx, gy, kThreads, 0, stream)
       .run(K % 16 == 0 ? dequantize_kernel<KIND, T, true> : dequantize_kernel<KIND, T, false>, op,
            rows, K, static_cast<T *>(y));
 }

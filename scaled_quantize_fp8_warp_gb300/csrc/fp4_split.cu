@@ -25,7 +25,6 @@
 // launch less on the host, some 3 us, is what speaks for casting it here.
 #include <cuda.h>
 #include <stdint.h>
-#include <stdio.h>
 
 #include <algorithm>
 
@@ -464,6 +463,7 @@ int run_split(const Group<GROUPED> &group, cudaStream_t stream) {
   static PerDeviceOnce setup;  // per instantiation
   if (setup.get([&] { return set_up(kernel) ? 1 : 0; }) != 1) return FP8Q_ERR_CUDA;
   const int split = group.prob[0].split;
+  log_line("  %d products, grid %d in clusters of %d", group.n, group.tile_end[group.n - 1] * split, split);
   return Launch((unsigned)(group.tile_end[group.n - 1] * split), 1, kThreads, kSmemBytes, stream,
                 split)
                      .run(kernel, group) == cudaSuccess
@@ -522,13 +522,10 @@ int fill_group(Group<GROUPED> &group, int kind, const Product *prod, int n, bool
   const int split = split_of(*fit, tiles, k_blocks, nb);
   for (int i = 0; i < n; ++i) {
     group.prob[i].split = split;
-    if (log_enabled())
-      fprintf(stderr,
-              "[fp8q] launch fp4 split_kernel %lldx%lldx%lld kind %d rows %d tiles %lld split %d "
-              "stages %d%s%s\n",
-              (long long)prod[i].M, (long long)prod[i].N, (long long)prod[i].K, kind,
-              group.prob[i].nb, (long long)tiles, split, group.prob[i].stages,
-              quantized ? "" : " quantising x", n > 1 ? " grouped" : "");
+    log_line("launch fp4 split_kernel %lldx%lldx%lld kind %d rows %d tiles %lld split %d stages %d%s%s",
+             (long long)prod[i].M, (long long)prod[i].N, (long long)prod[i].K, kind,
+             group.prob[i].nb, (long long)tiles, split, group.prob[i].stages,
+             quantized ? "" : " quantising x", n > 1 ? " grouped" : "");
   }
   return FP8Q_OK;
 }

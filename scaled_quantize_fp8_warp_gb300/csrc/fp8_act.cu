@@ -14,7 +14,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
-#include <stdio.h>
 
 #include <algorithm>
 
@@ -505,6 +504,8 @@ cudaError_t run_forward(const ForwardArgs &a, cudaStream_t stream) {
   struct Tag {};   // a set-up of its own for every kernel of this signature
   const int grid = grid_for<Tag>(kernel, smem, a.T, a.F);
   if (grid < 1) return cudaErrorInvalidValue;
+  log_line("launch act forward_kernel act %d %s%s%s, two rows of 256 columns a warp, grid %d", ACT,
+           sizeof(T) == 2 ? "bf16" : "fp32", GATED ? " gated" : "", VEC ? "" : " element by element", grid);
   return Launch((unsigned)grid, 1, kThreads, smem, stream).run(kernel, a);
 }
 
@@ -515,6 +516,8 @@ cudaError_t run_backward(const BackwardArgs &a, cudaStream_t stream) {
   struct Tag {};
   const int grid = grid_for<Tag>(kernel, smem, a.T, a.F);
   if (grid < 1) return cudaErrorInvalidValue;
+  log_line("launch act backward_kernel act %d %s%s%s, two rows of 256 columns a warp, grid %d", ACT,
+           sizeof(T) == 2 ? "bf16" : "fp32", GATED ? " gated" : "", VEC ? "" : " element by element", grid);
   return Launch((unsigned)grid, 1, kThreads, smem, stream).run(kernel, a);
 }
 

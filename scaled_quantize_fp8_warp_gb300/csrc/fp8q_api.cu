@@ -3,6 +3,7 @@
 // point allocates device memory; none synchronises except the diagnostics
 // and fp8q_history_init.
 #include <cuda_runtime.h>
+#include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -205,6 +206,16 @@ bool log_enabled() {
   return on;
 }
 
+void log_line(const char *format, ...) {
+  if (!log_enabled()) return;
+  char text[512];
+  va_list args;
+  va_start(args, format);
+  vsnprintf(text, sizeof text, format, args);
+  va_end(args);
+  fprintf(stderr, "[fp8q] %s\n", text);
+}
+
 }  // namespace fp8q
 
 using namespace fp8q;
@@ -249,6 +260,7 @@ int fp8q_selftest_barrier_timeout(cudaStream_t stream) {
   if (rc != FP8Q_OK) return rc;
   unsigned int *err = device_error_word();
   if (err == nullptr) return FP8Q_ERR_CUDA;
+  log_line("launch selftest_timeout_kernel grid 1");
   selftest_timeout_kernel<<<1, 32, 0, stream>>>(err);
   return from_cuda(cudaGetLastError());
 }
@@ -261,6 +273,7 @@ int fp8_amax(const void *x, int in_dtype, int64_t n, float *amax, cudaStream_t s
   if ((reinterpret_cast<uintptr_t>(amax) & 3u) != 0) return FP8Q_ERR_MISALIGNED;
   int rc = check_device();
   if (rc != FP8Q_OK) return rc;
+  log_line("amax of %lld elements", (long long)n);
   return from_cuda(launch_amax(x, in_dtype, n, amax, stream));
 }
 
@@ -302,6 +315,8 @@ int fp8_quantize_tensor_current(const void *x, int in_dtype, int64_t rows, int64
   if (rows > 0 && cols > 0 && q == nullptr && q_t == nullptr) return FP8Q_ERR_INVALID_ARG;
   if ((rc = check_ptr(q, false)) != FP8Q_OK || (rc = check_ptr(q_t, false)) != FP8Q_OK) return rc;
   if ((rc = check_device()) != FP8Q_OK) return rc;
+  log_line("quantize_tensor_current %lldx%lld fmt=%d q=%d q_t=%d", (long long)rows,
+           (long long)cols, format, q != nullptr, q_t != nullptr);
   const int64_t bytes = rows * cols * (in_dtype == FP8Q_DT_BF16 ? 2 : 4);
   const int slot = stream_slot(stream);   // of the grid barrier's counters
   if (rows == 0 || cols == 0 || bytes > kFusedTensorMaxBytes || slot < 0) {
@@ -345,6 +360,8 @@ int fp8_quantize_delayed(const void *x, int in_dtype, int64_t rows, int64_t cols
   p.format = format;
   p.saturate = saturate;
   p.mode = kModeTensorDelayed;
+  log_line("quantize_delayed %lldx%lld fmt=%d q=%d q_t=%d", (long long)rows, (long long)cols,
+           format, q != nullptr, q_t != nullptr);
   p.err = device_error_word();
   p.hist = hist;
   p.scale_out = scale_out;
@@ -421,6 +438,8 @@ int fp8_quantize_rowwise(const void *x, int in_dtype, int64_t rows, int64_t cols
     return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
   if (rows == 0 || cols == 0) return FP8Q_OK;
+  log_line("quantize_rowwise %lldx%lld fmt=%d rows=%d cols=%d", (long long)rows, (long long)cols,
+           format, want_row, want_col);
   // pass 1 gathers the amaxes in the scale arrays, so they start at zero
   if (want_row && cudaMemsetAsync(q_scales, 0, sizeof(float) * (size_t)rows, stream) != cudaSuccess)
     return FP8Q_ERR_CUDA;
@@ -509,6 +528,8 @@ int fp8_quantize_block128x128(const void *x, int in_dtype, int64_t rows, int64_t
   p.format = format;
   p.saturate = saturate;
   p.mode = kModeBlock;
+  log_line("quantize_block128x128 %lldx%lld fmt=%d q=%d q_t=%d", (long long)rows, (long long)cols,
+           format, q != nullptr, q_t != nullptr);
   p.err = device_error_word();
   p.q = q;
   p.q_t = q_t;
@@ -604,6 +625,7 @@ int fp8_gemm_grouped(const fp8q_gemm_desc *descs, int count, int out_dtype,
   if (count == 0) return FP8Q_OK;
   int rc;
   if ((rc = check_device()) != FP8Q_OK) return rc;
+  log_line("gemm_grouped of %d", count);
   return launch_gemm_group(A, B, C, M, N, K, count, out_dtype, stream);
 }
 
@@ -654,6 +676,8 @@ int fp8_linear_autocast(const void *x, const void *w, int in_dtype, int64_t M, i
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FP8Q_ERR_MISALIGNED;
   int rc = check_device();
   if (rc != FP8Q_OK) return rc;
+  log_line("linear_autocast M=%lld N=%lld K=%lld recipe=%d", (long long)M, (long long)N,
+           (long long)K, recipe);
 
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   uint8_t *qx = ws;
@@ -947,6 +971,8 @@ int fp8_linear_train(const void *x, const void *w, const void *g, int in_dtype, 
     return FP8Q_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FP8Q_ERR_MISALIGNED;
   if ((rc = check_device()) != FP8Q_OK) return rc;
+  log_line("linear_train M=%lld N=%lld K=%lld recipe=%d", (long long)M, (long long)N, (long long)K,
+           recipe);
   return train_impl(x, w, g, in_dtype, M, N, K, recipe, hist_x, hist_w, hist_g, y, dx, dw,
                     out_dtype, static_cast<uint8_t *>(workspace), stream, nullptr, nullptr,
                     nullptr);
@@ -978,6 +1004,8 @@ int fp8_linear_train_host(const void *x_h, const void *w_h, const void *g_h, int
               dx_h == nullptr || dw_h == nullptr))
     return FP8Q_ERR_INVALID_ARG;
   if ((rc = check_device()) != FP8Q_OK) return rc;
+  log_line("linear_train_host M=%lld N=%lld K=%lld recipe=%d", (long long)M, (long long)N,
+           (long long)K, recipe);
   HostStepRes *r = host_step_res();
   if (r == nullptr) return FP8Q_ERR_CUDA;
   const size_t ib = in_dtype == FP8Q_DT_BF16 ? 2 : 4, ob = out_dtype == FP8Q_DT_BF16 ? 2 : 4;

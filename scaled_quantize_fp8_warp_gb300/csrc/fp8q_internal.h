@@ -54,6 +54,9 @@ int stream_slot(cudaStream_t stream);
 // point and every kernel launch then prints one line to stderr naming what
 // it runs, so a caller can see which kernel served each call.
 bool log_enabled();
+// One such line (printf form, without the prefix and the line's end); nothing
+// where it is off.
+void log_line(const char *format, ...) __attribute__((format(printf, 1, 2)));
 
 // True when M, N, K are non-negative and M*K, N*K (and the byte sums of a
 // linear layer's workspace) fit in int64.  Defined in fp8q_api.cu.

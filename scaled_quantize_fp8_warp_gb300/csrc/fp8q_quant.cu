@@ -1257,6 +1257,8 @@ __global__ void __launch_bounds__(256) amax_to_scale_kernel(float *s, int64_t n,
 cudaError_t launch_amax_to_scale(float *s, int64_t n, int format, cudaStream_t stream) {
   if (n <= 0) return cudaSuccess;
   const float fm = format == FP8Q_E4M3 ? 448.0f : 57344.0f;
+  log_line("launch amax_to_scale_kernel %lld scales, grid %lld", (long long)n,
+           (long long)((n + 255) / 256));
   amax_to_scale_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(s, n, fm);
   return cudaGetLastError();
 }
