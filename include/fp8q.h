@@ -597,7 +597,7 @@ size_t fp4q_scale_bytes(int kind, int64_t rows, int64_t K);
  *   qt, qt_scales: the operand [cols, rows], i.e. x^T, blocks down each
  *                  column of x (what Dgrad and Wgrad contract over)
  * Each pair is both-or-neither; at least one.  Rows that start on 16-byte
- * boundaries (base and ld) are read 16 bytes at a time.
+ * boundaries (base and ld) with cols % 8 == 0 are read 16 bytes at a time.
  *   amax          NVFP4: device float, the tensor's amax as the caller knows
  *                 it (a calibrated value may be smaller than max|x|: elements
  *                 then saturate).  MXFP4: ignored, may be NULL.

@@ -15,7 +15,9 @@
 //
 // What bounds it: the copies into shared memory, then the MMAs.  8192 cube with
 // 256-wide tiles: 183 us NVFP4 and 176 MXFP4, 157 and 144 with the loads taken
-// out.  A fit over sizes gives a 384-wide tile 0.49 us per 256 of K (48 KB a CTA
+// out: 7.6 PFLOP/s, four times the measured bf16 rate, is what MMAs of K = 64
+// reach (the dense 4-bit rate the chip is sold at, six times bf16's, has an
+// MMA of K = 96, which is not used here).  A fit over sizes gives a 384-wide tile 0.49 us per 256 of K (48 KB a CTA
 // for NVFP4, so 15 TB/s over all SMs) and 1.65 us at its end.  Long loops meet
 // the board's power limit: 256-wide 398 us at 1.83-1.90 GHz, with operands of
 // zeros 369 at 2.07.  In several runs, NVFP4 15872 x 16384 x 4096: 340-344

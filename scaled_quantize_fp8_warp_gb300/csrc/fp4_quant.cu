@@ -10,8 +10,11 @@
 // and stored 16 bytes at a time, as are the transposed codes (64 bytes a
 // column).
 //
-// What bounds it: instructions rather than HBM (20.7 an element for NVFP4 in
-// both orientations; 66% of issue slots and 59% of the integer pipe are used).
+// What bounds it: neither HBM (31% busy) nor the issue slots (66% used, 20.7
+// instructions an element for NVFP4 in both orientations) alone, but the three
+// turns of a CTA: it loads its tile, casts all of it, then stores, with nothing
+// of another tile under way, and a third of the warps an SM could hold to fill
+// in.  With the encoding taken out 25.0 of 28.8 us are left.
 // 8192 x 4096 bf16, both orientations: NVFP4 28.8 us (3.6 TB/s), MXFP4 26.0 us
 // (4.0); 15872 x 4096, rows only: 33.7 us (4.9) and 31.2 us (5.3), of which 28.5
 // and 27.4 us are left with the encoding taken out.  Three CTAs an SM: two take

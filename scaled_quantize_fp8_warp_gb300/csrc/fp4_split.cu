@@ -17,12 +17,15 @@
 // never waits for a CTA that waits for this one's cluster.)
 //
 // What bounds it: latency for one row, then the casting of x, which every tile
-// repeats.  In a graph, w in L2, one row and 16 rows: MXFP4 1024 x 4096 4.2 and
-// 4.9 us, 12288 x 4096 7.3 and 10.1, 4096 x 16384 8.0 and 10.7; NVFP4 4.9 and 5.5,
-// 8.1 and 11.5, 8.7 and 12.0.  Casting x in a launch of its own: one row 1.2-2.5
-// us more; 16 rows 0.9-1.2 us more at 1024 x 4096, level at 4096 x 16384, but
-// 1.6-1.7 us less at 12288 x 4096, where nine rows are about level.  There a
-// launch less on the host, some 3 us, is what speaks for casting it here.
+// repeats.  In a graph, one row and 16 rows, each call with another w so that all
+// come from HBM: MXFP4 1024 x 4096 4.2 and 4.7 us, 12288 x 4096 8.4 and 11.1, 4096 x
+// 16384 10.1 and 12.3; NVFP4 4.8 and 5.3, 9.1 and 11.7, 10.8 and 13.0 (bytes at the
+// measured copy rate: 0.3, 4 and 5.3).  With w in L2: MXFP4 4.0 and 4.7, 7.3 and
+// 10.2, 8.2 and 11.0; NVFP4 4.7 and 5.3, 8.1 and 11.5, 8.8 and 12.2.  Casting x in a
+// launch of its own takes from HBM 1.3-3.1 us more for one row and 1.0-1.5 us
+// more for 16, but for 12288 x 4096, where 16 rows are level in NVFP4 and 0.65 us
+// less in MXFP4; with w in L2 12288 x 4096 takes 1.6 us less apart at 16 rows and
+// is level at nine, 4096 x 16384 is level at 13.
 #include <cuda.h>
 #include <stdint.h>
 
