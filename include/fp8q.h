@@ -720,6 +720,149 @@ int fp8_act_backward(int act, int dtype, int64_t T, int64_t F,
                      int64_t ldda, void *du, int64_t lddu, void *dv,
                      int64_t lddv, void *a, int64_t lda, cudaStream_t stream);
 
+/* ------------------------------------- RMS norm with an 8-bit output */
+
+/* The norm in front of a linear layer, the residual's addition before it and
+ * the cast after it in one pass over the rows:
+ *   h = round(x + residual)            (h = x without a residual)
+ *   rstd[t] = 1 / sqrt(sum_c h[t,c]^2 / C + eps)
+ *   y = (h rstd) weight
+ *   q = RNE_e4m3(y / s),  s = max(fl32(amax / 448), 1e-12)
+ * h is rounded to `dtype` first and everything after is computed from it as it
+ * is stored, in fp32 (squares above fp32's range make rstd 0); y is rounded
+ * once where it is stored, and q is cast from y in fp32, not from a stored y.
+ * The scales s are those of a GEMM operand [T, C]: per 1x128 tile
+ * (FP8Q_SCALE_TILE_1x128, q_scales [ceil(C/128), T]) or per row
+ * (FP8Q_SCALE_ROW, q_scales [T]); partial tiles are allowed.  A NaN or an
+ * infinity in a row makes its NaNs; a tile or row with a NaN has a NaN scale,
+ * one without but with an infinity an infinite scale, as in
+ * fp8_quantize_tile1x128.
+ *   x, residual, h, y
+ *             device [T, C] of `dtype`, rows ldx, ldr, ldh, ldy elements apart,
+ *             aligned to their type.  residual and h come together or are both
+ *             NULL; y may be NULL.  Outputs do not overlap inputs, except that
+ *             h may be exactly x or residual, with its ld.
+ *   weight    device [C] of w_dtype, aligned to its type
+ *   eps       HOST: one value, >= 0 and finite, read before the call returns
+ *   q         device bytes [T, C] dense, with q_scales; both or neither
+ *   scaling   ignored without q
+ *   rstd      device [T] or NULL
+ * T and C are at most INT32_MAX / 4; T or C == 0: nothing is done.  Rows that
+ * start on 16-byte boundaries with C % 8 == 0 are moved in vectors.
+ * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
+int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                int dtype, const void *weight, int w_dtype, const float *eps,
+                int64_t T, int64_t C, void *h, int64_t ldh, void *y,
+                int64_t ldy, int scaling, uint8_t *q, float *q_scales,
+                float *rstd, cudaStream_t stream);
+
+/* Bytes of device workspace fp8_rmsnorm_backward needs (the partial sums of
+ * dweight); 0 for invalid sizes. */
+size_t fp8q_rmsnorm_backward_workspace_size(int64_t T, int64_t C);
+
+/* The backward pass from what the forward pass kept, h and rstd: with dy the
+ * gradient of y, n = h rstd and g = dy weight,
+ *   dx[t,c]    = rstd[t] (g - n sum_c(g n) / C) + dresidual[t,c]
+ *   dweight[c] = sum_t dy[t,c] n[t,c]
+ * in fp32, each rounded once.  dx is the gradient of x and of the residual
+ * alike; dresidual, the gradient that reaches h by its other use (the residual
+ * of the next layer), may be NULL (0).  The rows of dweight's sum are added in
+ * an order that depends on T, C and the device alone: results repeat.
+ *   dy, h, dresidual, dx  device [T, C] of `dtype`, rows lddy, ldh, lddr, lddx
+ *                         elements apart; dx may be exactly dy or dresidual,
+ *                         with its ld
+ *   dweight   device [C] of w_dtype; NULL where it is not wanted (then no
+ *             workspace is needed)
+ *   workspace device, >= fp8q_rmsnorm_backward_workspace_size, 256-byte aligned
+ * T == 0: dweight is zero.  C == 0: nothing is done.
+ * Errors: INVALID_ARG, MISALIGNED, WORKSPACE, ARCH, CUDA. */
+int fp8_rmsnorm_backward(const void *dy, int64_t lddy, const void *h,
+                         int64_t ldh, int dtype, const void *weight,
+                         int w_dtype, const float *rstd, const void *dresidual,
+                         int64_t lddr, int64_t T, int64_t C, void *dx,
+                         int64_t lddx, void *dweight, void *workspace,
+                         size_t ws_bytes, cudaStream_t stream);
+
+/* --------------------------------- a linear layer per expert, in MXFP8 */
+
+/* Rows in groups.  A layer of experts multiplies row r of x by the weight of
+ * the expert that a router chose for it.  Rows of one expert lie together:
+ * group e of E holds rows offsets[e] to offsets[e+1] of a matrix [S, C], with
+ * offsets (device int32 [E+1], 4-byte aligned) non-decreasing from 0 to at
+ * most S.  The sizes of the groups are known on the device only; the calls
+ * never wait for them.  Rows from offsets[E] on belong to nobody: they are not
+ * read as data and what lies there in a result is left as it was.  Offsets
+ * outside [0, S] are taken as 0 or S, a group that ends before it begins as
+ * empty.  offsets NULL: E equal groups of S / E rows (S % E == 0), as the rows
+ * of E weights have.
+ *
+ * fp8q_experts, an MXFP8 operand [S, C] in groups: E4M3 or E5M2 bytes and E8M0
+ * scales as fp8_quantize_mxfp8 defines them, in either or both orientations.
+ * Group e's scales, and its transposed bytes, start at the boundary of a block
+ * of 128 rows: block
+ *   first(e) = offsets[e] / 128 + e        (rounded down; room for any group
+ *                                           before the next one's first block)
+ *   first(e) = e * ceil(S / E / 128)       (equal groups)
+ * of NB = fp8q_experts_blocks(S, E, offsets != NULL) blocks.
+ *   q          bytes [S, C] dense, blocks of 32 along each row
+ *   q_scales   atoms as in fp8_quantize_mxfp8: that of group e's rows 128 i on
+ *              and columns 128 j on is atom (first(e) + i) * ceil(C/128) + j
+ *   q_t        bytes [C, 128 NB]: row r of group e is column 128 first(e) + r
+ *              - offsets[e]; blocks of 32 down each column of a group, from the
+ *              group's first row; zeros behind a group in its last block
+ *   qt_scales  that of columns 128 j on and group e's rows 128 i on is atom j
+ *              * NB + first(e) + i
+ * q_scales and qt_scales take fp8q_experts_scale_bytes; in a group's last
+ * block the scales of rows behind the group have code 0.  All pointers 16-byte
+ * aligned.  C % 16 == 0.  E is at most FP8Q_EXPERTS_MAX; S, C and 128 NB are at
+ * most INT32_MAX - 1024, and there are at most INT32_MAX scale atoms. */
+#define FP8Q_EXPERTS_MAX 1024
+typedef struct fp8q_experts {
+  const uint8_t *q, *q_scales;    /* either pair may be NULL */
+  const uint8_t *q_t, *qt_scales;
+  const int32_t *offsets;         /* NULL: equal groups */
+  int64_t rows, cols;             /* S, C */
+  int32_t groups;                 /* E */
+  int32_t format;                 /* fp8q_format */
+} fp8q_experts;
+
+/* NB: S / 128 + E (ragged) or E * ceil(S / E / 128); 0 for invalid sizes. */
+int64_t fp8q_experts_blocks(int64_t rows, int groups, int ragged);
+
+/* NB * ceil(C/128) * 512; 0 for invalid sizes. */
+size_t fp8q_experts_scale_bytes(int64_t rows, int64_t cols, int groups,
+                                int ragged);
+
+/* Casts rows of x [T, cols] (device, in_dtype, rows ld elements apart, aligned
+ * to its type) into the pairs of `out` that are not NULL, from one read: row r
+ * of the operand is row index[r] of x (device int32 [out->rows]; one token
+ * goes to several experts), or row r where index is NULL (T == out->rows).  An
+ * index outside [0, T) stands for a row of zeros.  Indexes of rows that belong
+ * to nobody are not read.
+ * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
+int fp8_quantize_experts(const void *x, int in_dtype, int64_t T, int64_t ld,
+                         const int32_t *index, const fp8q_experts *out,
+                         cudaStream_t stream);
+
+/* The three products of the layer y_r = x_r w_e^T, r in group e, with w_e
+ * [N, K] the rows of w [E N, K] (equal groups), on the tensor cores' own block
+ * scaling with fp32 accumulation:
+ *   fprop: y  [S, N]    = x w_e^T        x by rows, w by rows
+ *   dgrad: dx [S, K]    = g w_e          g [S, N] by rows, w transposed
+ *   wgrad: dw [E, N, K] = g_e^T x_e      g and x transposed (one pair of
+ *                                        offsets: x->offsets are used)
+ * Results are dense, of out_dtype, 16-byte aligned.  Rows of y and dx behind the
+ * last group are left as they were; dw of an empty group is zero.  Any S; N %
+ * 16 == 0, K % 16 == 0.  The groups of x (g) may be equal ones.
+ * Errors: INVALID_ARG (also operands whose sizes or groups do not fit, or
+ * without the orientation that is needed), MISALIGNED, ARCH, CUDA. */
+int fp8_experts_fprop(const fp8q_experts *x, const fp8q_experts *w, void *y,
+                      int out_dtype, cudaStream_t stream);
+int fp8_experts_dgrad(const fp8q_experts *g, const fp8q_experts *w, void *dx,
+                      int out_dtype, cudaStream_t stream);
+int fp8_experts_wgrad(const fp8q_experts *g, const fp8q_experts *x, void *dw,
+                      int out_dtype, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

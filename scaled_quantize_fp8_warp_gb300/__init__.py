@@ -11,14 +11,17 @@ The names follow the C ABI: ``fp8_amax``, ``fp8_quantize_tensor``,
 ``fp8_quantize_block128x128``, ``fp8_gemm`` and the role wrappers
 ``fp8_gemm_fprop`` / ``fp8_gemm_dgrad`` / ``fp8_gemm_wgrad``, and
 ``fp8_linear_autocast``; the 4-bit ``fp4_quantize``, ``fp4_dequantize``,
-``fp4_gemm``, ``fp4_linear`` and ``fp4_linear_train``; and ``fp8_act_forward`` /
-``fp8_act_backward``, activation functions with 8-bit checkpoints.
+``fp4_gemm``, ``fp4_linear`` and ``fp4_linear_train``; ``fp8_act_forward`` /
+``fp8_act_backward``, activation functions with 8-bit checkpoints; ``fp8_rmsnorm`` /
+``fp8_rmsnorm_backward``; and ``fp8_quantize_experts`` with ``fp8_experts_fprop`` /
+``fp8_experts_dgrad`` / ``fp8_experts_wgrad``, a linear layer per expert in MXFP8.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -68,6 +71,9 @@ EXPORTS = (
     "fp4q_linear_workspace_size", "fp4_linear",
     "fp4q_linear_train_workspace_size", "fp4_linear_train",
     "fp8_act_forward", "fp8_act_backward",
+    "fp8_rmsnorm", "fp8q_rmsnorm_backward_workspace_size", "fp8_rmsnorm_backward",
+    "fp8q_experts_blocks", "fp8q_experts_scale_bytes", "fp8_quantize_experts",
+    "fp8_experts_fprop", "fp8_experts_dgrad", "fp8_experts_wgrad",
 )
 
 
@@ -133,6 +139,17 @@ def signatures() -> dict:
         "fp8_act_forward": (I32, [I32, I32, I64, I64, P, I64, P, I64, P, I64, P, P, P, P, P]),
         "fp8_act_backward": (I32, [I32, I32, I64, I64, P, P, P, P, P, I64, P, I64, P, I64, P,
                                    I64, P]),
+        "fp8_rmsnorm": (I32, [P, I64, P, I64, I32, P, I32, P, I64, I64, P, I64, P, I64, I32, P, P,
+                              P, P]),
+        "fp8q_rmsnorm_backward_workspace_size": (SZ, [I64, I64]),
+        "fp8_rmsnorm_backward": (I32, [P, I64, P, I64, I32, P, I32, P, P, I64, I64, I64, P, I64, P,
+                                       P, SZ, P]),
+        "fp8q_experts_blocks": (I64, [I64, I32, I32]),
+        "fp8q_experts_scale_bytes": (SZ, [I64, I64, I32, I32]),
+        "fp8_quantize_experts": (I32, [P, I32, I64, I64, P, P, P]),
+        "fp8_experts_fprop": (I32, [P, P, P, I32, P]),
+        "fp8_experts_dgrad": (I32, [P, P, P, I32, P]),
+        "fp8_experts_wgrad": (I32, [P, P, P, I32, P]),
     }
 
 
@@ -922,6 +939,227 @@ def fp8_act_backward(act: int, ckpt: ActCheckpoint, da: torch.Tensor, want_a=Fal
         _addr(ckpt.v_scales), pd, ldd, pu, ldu, pv, ldv, pa, lda, _raw_stream(stream)),
         "fp8_act_backward")
     return du, dv, a
+
+
+# ------------------------------------------- RMS norm with an 8-bit output
+
+class NormOutput(NamedTuple):
+    """What fp8_rmsnorm gives.  ``h`` [T, C]: x + residual as it is stored (x
+    itself without a residual).  ``y`` [T, C] or None.  ``q`` [T, C] E4M3 bytes
+    (uint8) with ``scales`` ([ceil(C/128), T] per tile, [T] per row), or None:
+    an operand for GemmOperand.tile or GemmOperand.row.  ``rstd`` [T] fp32."""
+    h: torch.Tensor
+    y: torch.Tensor | None
+    q: torch.Tensor | None
+    scales: torch.Tensor | None
+    rstd: torch.Tensor
+
+
+def _norm_weight(weight: torch.Tensor, C: int):
+    """(pointer, dtype code) of a norm's weight."""
+    if weight.shape != (C,):
+        raise ValueError(f"weight must have shape ({C},), got {tuple(weight.shape)}")
+    return _addr(weight), _in_dtype(weight)
+
+
+def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                eps: float = 1e-6, scaling: int | None = SCALE_TILE_1x128, want_y=True, h=None,
+                y=None, q=None, scales=None, rstd=None, stream=None) -> NormOutput:
+    """h = x + residual, y = weight h / sqrt(mean(h^2) + eps), and y in E4M3 under
+    1x128 tile scales or row scales (``scaling`` None: no 8-bit output).  x,
+    residual, h and y are [T, C] of one type and their rows may lie apart;
+    weight is bf16 or fp32.  ``want_y`` (or a given ``y``) asks for y beside
+    its 8-bit form.  h may be x or residual itself."""
+    px, ldx = _rows(x)
+    T, C = shape = x.shape
+    dtype, device = x.dtype, x.device
+    pw, w_dtype = _norm_weight(weight, C)
+    pr, ldr, ph, ldh, py, ldy, pq, ps = None, 0, None, 0, None, 0, None, None
+    if residual is not None:
+        pr, ldr = _rows(_like(residual, shape, dtype, "residual"))
+        h, ph, ldh = _out_rows(h, shape, dtype, device, stream, "h")
+    elif h is not None:
+        raise ValueError("without a residual h is x")
+    if want_y or y is not None:
+        y, py, ldy = _out_rows(y, shape, dtype, device, stream, "y")
+    if scaling is not None:
+        s_shape = ((C + 127) // 128, T) if scaling == SCALE_TILE_1x128 else (T,)
+        if q is None:
+            q = _new(shape, torch.uint8, device, stream)
+        if scales is None:
+            scales = _new(s_shape, torch.float32, device, stream)
+        pq = _addr(_like(q, shape, torch.uint8, "q"))
+        ps = _addr(_like(scales, s_shape, torch.float32, "scales"))
+    elif q is not None or scales is not None:
+        raise ValueError("an 8-bit output needs a scaling")
+    if rstd is None:
+        rstd = _new((T,), torch.float32, device, stream)
+    _check(lib().fp8_rmsnorm(
+        px, ldx, pr, ldr, _in_dtype(x), pw, w_dtype, ctypes.byref(ctypes.c_float(eps)), T, C, ph,
+        ldh, py, ldy, 0 if scaling is None else scaling, pq, ps,
+        _addr(_like(rstd, (T,), torch.float32, "rstd")), _raw_stream(stream)), "fp8_rmsnorm")
+    return NormOutput(x if h is None else h, y, q, scales, rstd)
+
+
+def fp8_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                         rstd: torch.Tensor, dresidual: torch.Tensor | None = None,
+                         want_dweight=True, dx=None, dweight=None, workspace=None, stream=None):
+    """(dx, dweight | None) of fp8_rmsnorm from the gradient dy of y and the h
+    and rstd that it gave; dx includes ``dresidual``, the gradient that reaches
+    h by its other use."""
+    pd, ldd = _rows(dy)
+    T, C = shape = dy.shape
+    dtype, device = dy.dtype, dy.device
+    ph, ldh = _rows(_like(h, shape, dtype, "h"))
+    pw, w_dtype = _norm_weight(weight, C)
+    ps = _addr(_like(rstd, (T,), torch.float32, "rstd"))
+    pr, ldr, pdw = None, 0, None
+    if dresidual is not None:
+        pr, ldr = _rows(_like(dresidual, shape, dtype, "dresidual"))
+    dx, px, ldx = _out_rows(dx, shape, dtype, device, stream, "dx")
+    if want_dweight or dweight is not None:
+        if dweight is None:
+            dweight = _new((C,), weight.dtype, device, stream)
+        pdw = _addr(_like(dweight, (C,), weight.dtype, "dweight"))
+        if workspace is None:
+            workspace = _new((int(lib().fp8q_rmsnorm_backward_workspace_size(T, C)),), torch.uint8,
+                             device, stream)
+    _check(lib().fp8_rmsnorm_backward(
+        pd, ldd, ph, ldh, _in_dtype(dy), pw, w_dtype, ps, pr, ldr, T, C, px, ldx, pdw,
+        _addr(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(stream)),
+        "fp8_rmsnorm_backward")
+    return dx, dweight
+
+
+# --------------------------------------- a linear layer per expert, in MXFP8
+
+class _ExpertsStruct(ctypes.Structure):
+    """fp8q_experts."""
+    _fields_ = [("q", ctypes.c_void_p), ("q_scales", ctypes.c_void_p), ("q_t", ctypes.c_void_p),
+                ("qt_scales", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("groups", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
+
+
+#: most groups of an operand (FP8Q_EXPERTS_MAX)
+EXPERTS_MAX = 1024
+
+
+def experts_blocks(rows: int, groups: int, ragged: bool) -> int:
+    """128-row blocks that the groups of an operand take."""
+    return rows // 128 + groups if ragged else groups * ((rows // groups + 127) // 128)
+
+
+class ExpertsOperand:
+    """An MXFP8 operand [rows, cols] whose rows lie in groups, one per expert:
+    group e has rows offsets[e] to offsets[e + 1] (``offsets``: int32 device
+    tensor [groups + 1]), or rows / groups each where ``offsets`` is None (the
+    weights of all experts, one below the other).  By rows: ``q`` uint8 [rows,
+    cols] and ``q_scales``; transposed: ``q_t`` uint8 [cols, 128 blocks] and
+    ``qt_scales``; scales are uint8, 512 * blocks * ceil(cols/128) of them.  See
+    fp8q_experts in include/fp8q.h for where things lie."""
+    __slots__ = ("rows", "cols", "groups", "fmt", "offsets", "q", "q_scales", "q_t", "qt_scales",
+                 "struct")
+
+    def __init__(self, rows: int, cols: int, groups: int, fmt: int = E4M3,
+                 offsets: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                 q_scales: torch.Tensor | None = None, q_t: torch.Tensor | None = None,
+                 qt_scales: torch.Tensor | None = None):
+        if not 1 <= groups <= EXPERTS_MAX:
+            raise ValueError(f"an operand has 1 to {EXPERTS_MAX} groups")
+        if offsets is None:
+            if rows % groups:
+                raise ValueError("equal groups need rows that divide by their number")
+        elif offsets.dtype != torch.int32 or offsets.shape != (groups + 1,):
+            raise ValueError(f"offsets must be int32 of shape ({groups + 1},)")
+        if (q is None) != (q_scales is None) or (q_t is None) != (qt_scales is None):
+            raise ValueError("bytes and scales come together")
+        blocks = experts_blocks(rows, groups, offsets is not None)
+        for data, scales, shape in ((q, q_scales, (rows, cols)), (q_t, qt_scales, (cols, 128 * blocks))):
+            if data is not None:
+                _like(data, shape, torch.uint8, "bytes")
+                if scales.dtype != torch.uint8 or scales.numel() != 512 * blocks * ((cols + 127) // 128):
+                    raise ValueError(f"scales must be {512 * blocks * ((cols + 127) // 128)} uint8 values")
+        self.rows, self.cols, self.groups, self.fmt, self.offsets = rows, cols, groups, fmt, offsets
+        self.q, self.q_scales, self.q_t, self.qt_scales = q, q_scales, q_t, qt_scales
+        self.struct = _ExpertsStruct(_addr(q), _addr(q_scales), _addr(q_t), _addr(qt_scales),
+                                     _addr(offsets), rows, cols, groups, fmt)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, groups: int, device, fmt: int = E4M3, offsets=None,
+              by_rows=True, transposed=False, stream=None):
+        """Uninitialised storage for an operand."""
+        if not 1 <= groups <= EXPERTS_MAX:
+            raise ValueError(f"an operand has 1 to {EXPERTS_MAX} groups")
+        blocks = experts_blocks(rows, groups, offsets is not None)
+        n = 512 * blocks * ((cols + 127) // 128)
+        new = lambda *shape: _new(shape, torch.uint8, device, stream)
+        return cls(rows, cols, groups, fmt, offsets, *((new(rows, cols), new(n)) if by_rows else (None, None)),
+                   *((new(cols, 128 * blocks), new(n)) if transposed else (None, None)))
+
+
+def fp8_quantize_experts(x: torch.Tensor, groups: int, offsets: torch.Tensor | None = None,
+                         index: torch.Tensor | None = None, rows=True, cols=False, fmt: int = E4M3,
+                         out: ExpertsOperand | None = None, stream=None) -> ExpertsOperand:
+    """x [T, C] (rows may lie apart) -> MXFP8 operand in groups, by rows, by
+    columns (transposed) or both.  ``index`` (int32 device tensor): row r of the
+    operand is row index[r] of x, a row of zeros where that is no row of x;
+    without it row r is row r.  ``out``: storage, of which the orientations
+    asked for are written."""
+    p, ld = _rows(x)
+    T, C = x.shape
+    if index is not None and (index.dtype != torch.int32 or index.dim() != 1):
+        raise ValueError("index must be int32, one for each row")
+    S = T if index is None else index.shape[0]
+    if not rows and not cols:
+        raise ValueError("an orientation is needed: rows, cols or both")
+    if out is None:
+        out = ExpertsOperand.empty(S, C, groups, x.device, fmt, offsets, rows, cols, stream)
+    elif (out.rows, out.cols, out.groups, out.fmt) != (S, C, groups, fmt) or out.offsets is not offsets:
+        raise ValueError("an operand of these rows, columns, groups, offsets and format is needed")
+    st = out.struct
+    if (rows and out.q is None) or (cols and out.q_t is None):
+        raise ValueError("the operand has no storage for an orientation asked for")
+    if (out.q is not None and not rows) or (out.q_t is not None and not cols):
+        st = _ExpertsStruct(st.q if rows else None, st.q_scales if rows else None,
+                            st.q_t if cols else None, st.qt_scales if cols else None, st.offsets,
+                            S, C, groups, fmt)
+    _check(lib().fp8_quantize_experts(p, _in_dtype(x), T, ld, _addr(index), ctypes.byref(st),
+                                      _raw_stream(stream)), "fp8_quantize_experts")
+    return out
+
+
+def _experts_rows(name, x, w, shape, out_dtype, out, stream):
+    held = x.q if x.q is not None else x.q_t
+    if held is None:
+        raise ValueError("an operand without bytes")
+    device = held.device
+    out, po, dt = _out(out, shape, out_dtype, device, stream)
+    _check(getattr(lib(), name)(ctypes.byref(x.struct), ctypes.byref(w.struct), po, dt,
+                                _raw_stream(stream)), name)
+    return out
+
+
+def fp8_experts_fprop(x: ExpertsOperand, w: ExpertsOperand, out_dtype=torch.bfloat16, out=None,
+                      stream=None):
+    """y [S, N], y_r = x_r w_e^T for rows r of group e, from x [S, K] by rows and
+    the weights w [E N, K] by rows.  Rows of ``out`` behind the last group are
+    left as they were (uninitialised in a new one)."""
+    return _experts_rows("fp8_experts_fprop", x, w, (x.rows, w.rows // w.groups), out_dtype, out, stream)
+
+
+def fp8_experts_dgrad(g: ExpertsOperand, w: ExpertsOperand, out_dtype=torch.bfloat16, out=None,
+                      stream=None):
+    """dx [S, K], dx_r = g_r w_e, from g [S, N] by rows and the weights w [E N, K]
+    transposed.  Rows behind the last group as in fp8_experts_fprop."""
+    return _experts_rows("fp8_experts_dgrad", g, w, (g.rows, w.cols), out_dtype, out, stream)
+
+
+def fp8_experts_wgrad(g: ExpertsOperand, x: ExpertsOperand, out_dtype=torch.bfloat16, out=None,
+                      stream=None):
+    """dw [E, N, K], dw_e = g_e^T x_e, from g [S, N] and x [S, K] transposed;
+    zero for an expert without rows."""
+    return _experts_rows("fp8_experts_wgrad", g, x, (x.groups, g.cols, x.cols), out_dtype, out, stream)
 
 
 # ------------------------------------------------------------- diagnostics

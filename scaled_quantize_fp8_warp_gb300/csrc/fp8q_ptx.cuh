@@ -253,6 +253,21 @@ __device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc, ui
       : "memory");
 }
 
+// The same for a CTA pair (cta_group::2), issued by one thread of the even
+// CTA: M = 256, each CTA holding 128 rows of A, half of B's rows, the scales
+// of its own rows of A and those of all of B.
+__device__ __forceinline__ void mma_mxf8f6f4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                  uint32_t idesc, uint32_t sfa_tmem,
+                                                  uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+      " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
 // Copy 32 rows x 16 bytes of shared memory (descriptor `sdesc`) into tensor
 // memory at `taddr`, replicated into each of the four 32-lane quarters: row r
 // lands in lane r of every quarter, its bytes in columns taddr .. taddr + 3.
