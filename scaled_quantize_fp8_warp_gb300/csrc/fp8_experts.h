@@ -39,8 +39,9 @@ struct CastArgs {
   uint8_t *q, *q_scales, *q_t, *qt_scales;   // either pair null
 };
 
-// C_e [rows of B, rows of A] = B_e . A_e^T for every group: A's rows are the
-// columns of the result.
+// A product per group.  by_rows: C [rows of B, rows of A] = B . A_e^T, group e
+// owning rows of B and of C.  Otherwise C_e [rows of A, rows of B] = A_e . B_e^T,
+// group e owning a stretch of the contraction.
 struct Side {
   const uint8_t *data, *scales;
   int64_t rows, row_bytes;  // the whole matrix of bytes
@@ -48,11 +49,11 @@ struct Side {
 };
 struct ProductArgs {
   Groups groups;            // of the rows of B (by_rows) or of the contraction
-  int by_rows;              // 1: group e owns rows of B and of the result; 0: a stretch of K
+  int by_rows;
   Side a, b;
   int a_row, a_k, a_block;  // by_rows: group e's part of A starts at row a_row * e,
                             // K block a_k * e, 128-row block a_block * e
-  int a_rows;               // rows of A in a group: columns of the result
+  int a_rows;               // rows of A in a group
   int b_rows;               // not by_rows: rows of B
   int k;                    // by_rows: the contraction
   int a_format, b_format;

@@ -300,14 +300,14 @@ int fp8_experts_wgrad(const fp8q_experts *g, const fp8q_experts *x, void *dw, in
   experts::ProductArgs a{};
   a.groups = groups_of(*x);
   a.by_rows = 0;
-  a.a = transposed(*x);
-  a.b = transposed(*g);
-  a.a_rows = (int)K;
-  a.b_rows = (int)N;
-  a.a_format = x->format;
-  a.b_format = g->format;
+  a.a = transposed(*g);
+  a.b = transposed(*x);
+  a.a_rows = (int)N;
+  a.b_rows = (int)K;
+  a.a_format = g->format;
+  a.b_format = x->format;
   a.C = dw;
-  return run(a, out_dtype, *x, *g, stream);
+  return run(a, out_dtype, *g, *x, stream);
 }
 
 }  // extern "C"

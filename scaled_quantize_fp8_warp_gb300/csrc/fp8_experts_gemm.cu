@@ -30,107 +30,184 @@ namespace {
 using namespace ptx;
 
 constexpr int kBK = 128;          // bytes = elements of K per stage
-constexpr int kMaxN = 256;        // rows of B per tile
-constexpr int kBoxRows = 16;      // rows of B per load of a tile that is not full
 constexpr int kRaster = 8;        // tiles of B visited together
+constexpr int kTilesAhead = 8;    // tiles that are found ahead of their results
 constexpr int kMostTiles = INT32_MAX / 2;   // of a launch
 
 struct PairMaps {
-  CUtensorMap a, b, b16, sfa, sfb;   // b16: boxes of 16 rows
+  CUtensorMap a, b[4], sfa, sfb;   // b: boxes of 128, 64, 32 and 16 rows
+  CUtensorMap c;                   // wgrad: the results
 };
-
-struct Layout {
-  static constexpr int kABytes = 128 * kBK, kBBytes = kMaxN / 2 * kBK;
-  static constexpr int kSfaOff = kABytes + kBBytes, kSfbOff = kSfaOff + 512;
-  static constexpr int kStageBytes = (kSfbOff + 2 * 512 + 1023) / 1024 * 1024;
-  static constexpr int kStages = 6;
-  static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kBarBytes = 8 * (2 * kStages + 3);
-  static constexpr int kTileBytes = (FP8Q_EXPERTS_MAX + 1) * 4;   // first tile of every group
-  static constexpr int kSmemBytes = kRingBytes + kBarBytes + 16 + kTileBytes + 1024;
-  static constexpr uint32_t kTmemCols = 512, kSfCols = 16;
-  static_assert(kSmemBytes <= 227 * 1024, "the ring fits in shared memory");
-  static_assert(kMaxN + kSfCols * kStages <= kTmemCols, "scale slots fit in tensor memory");
-};
-constexpr int kEpilogueWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpilogueWarps);
 
 // One tile: what of A, B and K it takes, and where its result goes.
-struct Tile {
+struct __align__(16) Tile {
   int a_row, b_row;        // first rows of A and of B
   int k_block, num_k;      // K blocks
-  int64_t a_atom, b_atom;  // scale atom of the first rows and the first K block
+  int a_block, b_block;    // 128-row blocks of the scales of the first rows
   int n, valid;            // rows of B: as the MMA takes them (a multiple of 32), and those that count
-  int col;                 // first column of C
-  int64_t c_row;           // first row of C
+  int across, along;       // first rows of the tile in the group's parts of A and B
+  int64_t c_row;           // ROWS: row of C of the first row of B; else the group
+  int turn;                // tiles of this CTA before it that have a contraction
 };
 
-// Tiles of a group of so many rows.
-__device__ __forceinline__ long long tiles_of(const ProductArgs &p, int rows) {
-  const int b = p.by_rows ? rows : p.b_rows;
-  return (long long)((b + kMaxN - 1) / kMaxN) * ((p.a_rows + 255) / 256);
+// ROWS: groups own rows of C, which are B's rows and lie across the lanes
+// (fprop, dgrad); otherwise C's rows are A's and lie along the lanes (wgrad).
+// WIDE: rows of B per tile, 256 or 128.
+template <typename T, bool ROWS, int WIDE>
+struct Layout {
+  static constexpr int kRowBlocks = WIDE / 128;
+  static constexpr int kABytes = 128 * kBK, kBBytes = WIDE / 2 * kBK;
+  static constexpr int kSfaOff = kABytes + kBBytes, kSfbOff = kSfaOff + 512;
+  static constexpr int kStageBytes = (kSfbOff + kRowBlocks * 512 + 1023) / 1024 * 1024;
+  // Tensor memory: accumulators, then a slot of scales per stage.  256 columns
+  // leave no room for a second accumulator.
+  static constexpr uint32_t kTmemCols = 512, kSfCols = 4 * (1 + kRowBlocks);
+  static constexpr int kAcc = WIDE == 256 ? 1 : 3;
+  // Epilogue warps: teams take tiles in turn, so that one team's stores go out
+  // while the other waits for its tile.  In a team a warp has 32 lanes and
+  // kChunks chunks of 32 rows of B; a lone accumulator is taken into registers
+  // at once and released (bf16 only: fp32 results would not fit).
+  static constexpr int kTeams = kAcc > 1 ? 2 : 1;
+  static constexpr int kColumnGroups = kAcc > 1 ? 1 : 2;
+  static_assert(kAcc > 1 || sizeof(T) == 2, "a tile's results fit in registers");
+  static constexpr int kTeamWarps = 4 * kColumnGroups;
+  static constexpr int kEpilogueWarps = kTeams * kTeamWarps;
+  static constexpr int kChunks = WIDE / 32 / kColumnGroups;
+  static constexpr int kThreads = 32 * (3 + kEpilogueWarps);
+  // Results along the lanes leave through shared memory, 32 rows x 128 bytes a
+  // warp at a time.
+  static constexpr int kOutBytes = ROWS ? 0 : kEpilogueWarps * 4096;
+  static constexpr int kStages = (208 * 1024 - kOutBytes) / kStageBytes;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kBarBytes = 8 * (2 * kStages + 2 * kAcc + 2 * kTilesAhead + 2) / 16 * 16;
+  static constexpr int kFirstBytes = (FP8Q_EXPERTS_MAX + 1) * 4;   // first tile of every group
+  static constexpr int kSmemBytes =
+      kRingBytes + kOutBytes + kBarBytes + 16 + kTilesAhead * (int)sizeof(Tile) + kFirstBytes + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "the ring fits in shared memory");
+  static_assert(WIDE * kAcc + kSfCols * kStages <= kTmemCols, "scale slots fit in tensor memory");
+};
+
+// Tiles along B for so many of its rows, and across A.
+template <int WIDE>
+__device__ __forceinline__ int tiles_along(int rows) { return (rows + WIDE - 1) / WIDE; }
+__device__ __forceinline__ int tiles_across(const ProductArgs &p) { return (p.a_rows + 255) / 256; }
+
+// Where every group's tiles start in the numbering of all, by one warp.
+template <bool ROWS, int WIDE>
+__device__ __forceinline__ void number_tiles(const ProductArgs &p, int *first) {
+  const int lane = threadIdx.x & 31, E = p.groups.count;
+  long long done = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    long long n = 0;
+    if (e0 + lane < E)
+      n = (long long)tiles_along<WIDE>(ROWS ? group_rows(p.groups, e0 + lane).y : p.b_rows) * tiles_across(p);
+    long long sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long other = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += other;
+    }
+    if (e0 + lane < E) first[e0 + lane] = (int)min(done + sum - n, (long long)kMostTiles);
+    done += __shfl_sync(0xFFFFFFFFu, sum, 31);
+  }
+  // more than the host allows for come from offsets that are no offsets: nothing is done
+  if (lane == 0) first[E] = done <= kMostTiles ? (int)done : 0;
 }
 
-__device__ __forceinline__ Tile find_tile(const ProductArgs &p, const int *first, int u) {
-  int lo = 0, hi = p.groups.count;   // first[lo] <= u < first[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (first[mid] <= u)
-      lo = mid;
-    else
-      hi = mid;
+// The tiles of one CTA pair, in their order: every `step`-th of all, group after
+// group; next() is false behind the last.
+template <bool ROWS, int WIDE>
+struct Tiles {
+  const ProductArgs &p;
+  const int *first;
+  int u, step;
+  int e = -1, row, rows;       // the group, its first row and its rows
+  int block, along, each, more;
+  __device__ __forceinline__ Tiles(const ProductArgs &args, const int *first_tiles, int pair, int pairs)
+      : p(args), first(first_tiles), u(pair), step(pairs) {}
+  __device__ __forceinline__ bool next(Tile &t) {
+    if (u >= first[p.groups.count]) return false;
+    if (e < 0 || u >= first[e + 1]) {
+      int lo = e + 1, hi = p.groups.count;   // first[lo] <= u < first[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (first[mid] <= u)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      e = lo;
+      const int2 group = group_rows(p.groups, e);
+      row = group.x;
+      rows = group.y;
+      block = first_block(p.groups, e, row);
+      const int n = ROWS ? rows : p.b_rows, blocks = (n + 127) / 128;
+      along = tiles_along<WIDE>(n);
+      each = blocks / along;   // whole 128-row blocks, as evenly as they go
+      more = blocks - each * along;
+    }
+    int bt, at;
+    gemm::tile_coords(u - first[e], along, tiles_across(p), bt, at, kRaster, 0);
+    const int b0 = bt * each + min(bt, more), b1 = b0 + each + (bt < more);
+    t.across = at * 256;
+    t.along = b0 * 128;
+    t.valid = min(b1 * 128, ROWS ? rows : p.b_rows) - t.along;
+    t.n = (t.valid + 31) / 32 * 32;
+    if (ROWS) {
+      t.a_row = p.a_row * e + t.across;
+      t.b_row = row + t.along;
+      t.k_block = p.a_k * e;
+      t.num_k = (p.k + kBK - 1) / kBK;
+      t.a_block = p.a_block * e + 2 * at;
+      t.b_block = block + b0;
+      t.c_row = row + t.along;
+    } else {
+      t.a_row = t.across;
+      t.b_row = t.along;
+      t.k_block = block;
+      t.num_k = (rows + kBK - 1) / kBK;
+      t.a_block = 2 * at;
+      t.b_block = b0;
+      t.c_row = e;
+    }
+    u += step;
+    return true;
   }
-  const int e = lo;
-  const int2 group = group_rows(p.groups, e);
-  const int block = first_block(p.groups, e, group.x);
-  const int rows = p.by_rows ? group.y : p.b_rows;
-  int bt, at;
-  gemm::tile_coords(u - first[e], (rows + kMaxN - 1) / kMaxN, (p.a_rows + 255) / 256, bt, at,
-                    kRaster, 0);
-  Tile t;
-  t.col = at * 256;
-  t.valid = min(kMaxN, rows - bt * kMaxN);
-  t.n = (t.valid + 31) / 32 * 32;
-  if (p.by_rows) {
-    t.a_row = p.a_row * e + t.col;
-    t.b_row = group.x + bt * kMaxN;
-    t.k_block = p.a_k * e;
-    t.num_k = (p.k + kBK - 1) / kBK;
-    t.a_atom = (int64_t)(p.a_block * e + 2 * at) * p.a.atoms_k + t.k_block;
-    t.b_atom = (int64_t)(block + 2 * bt) * p.b.atoms_k;
-    t.c_row = group.x + bt * kMaxN;
-  } else {
-    t.a_row = t.col;
-    t.b_row = bt * kMaxN;
-    t.k_block = block;
-    t.num_k = (group.y + kBK - 1) / kBK;
-    t.a_atom = (int64_t)(2 * at) * p.a.atoms_k + block;
-    t.b_atom = (int64_t)(2 * bt) * p.b.atoms_k + block;
-    t.c_row = (int64_t)e * p.b_rows + bt * kMaxN;
-  }
-  return t;
-}
+};
 
 // One K block in the ring slot at `sa`, by one elected thread: scales into
 // tensor memory at sf, then four MMAs of K = 32.
-__device__ __forceinline__ void issue_block(uint32_t sa, uint32_t d_tmem, uint32_t sf,
-                                            uint32_t idesc, bool second, bool first) {
-  const uint64_t atom = sdesc_plain(sa + Layout::kSfaOff, 128);   // + 32 per atom
+template <typename L>
+__device__ __forceinline__ void issue_block(uint32_t sa, uint32_t d_tmem, uint32_t sf, uint32_t idesc,
+                                            bool second, bool first) {
+  const uint64_t atom = sdesc_plain(sa + L::kSfaOff, 128);   // + 32 per atom
   tmem_cp_32x128b_x4_pair(sf, atom);
   tmem_cp_32x128b_x4_pair(sf + 4, atom + 32);
-  if (second) tmem_cp_32x128b_x4_pair(sf + 8, atom + 64);
+  if (L::kRowBlocks > 1 && second) tmem_cp_32x128b_x4_pair(sf + 8, atom + 64);
   const uint64_t ad = sdesc_k(sa, gemm::kSwzSBO, gemm::kSwzMode);
-  const uint64_t bd = sdesc_k(sa + Layout::kABytes, gemm::kSwzSBO, gemm::kSwzMode);
+  const uint64_t bd = sdesc_k(sa + L::kABytes, gemm::kSwzSBO, gemm::kSwzMode);
 #pragma unroll
   for (int k = 0; k < 4; ++k)   // step k uses byte k of each scale word
     mma_mxf8f6f4_pair(d_tmem, ad + 2 * k, bd + 2 * k, idesc | ((uint32_t)k << 29) | ((uint32_t)k << 4),
                       sf, sf + 4, (!first || k > 0) ? 1u : 0u);
 }
 
-// 32 rows of B in one column of C, as they are kept for storing: bf16 results
-// two rows to a register.
+// `rows` rows of B from `row` on, a multiple of 16, in as few boxes as there are.
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap (&maps)[4], int k, int row,
+                                          int rows, uint32_t full) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (rows & (128 >> i)) {
+      tma_load_2d_pair(dst, &maps[i], k, row, full);
+      dst += (128 >> i) * kBK;
+      row += 128 >> i;
+    }
+}
+
+// Results of one row of A and 32 rows of B, as they are kept for storing:
+// bf16 ones two to a register.
 template <typename T>
-struct Column {
+struct Chunk {
   static constexpr int kRegs = 8 * sizeof(T);
   uint32_t r[kRegs];
   __device__ __forceinline__ void take(const uint32_t (&v)[32]) {
@@ -143,9 +220,17 @@ struct Column {
 #pragma unroll
     for (int j = 0; j < kRegs; ++j) r[j] = 0u;
   }
-  // Column m of C from row c_row on, `count` rows of it; lanes hold
+  // Into 128 bytes of this lane's row at `row`, a multiple of 128, from chunk
+  // of 16 bytes c0 on, as 128-byte swizzling has them.
+  __device__ __forceinline__ void stage(uint32_t row, int c0) const {
+#pragma unroll
+    for (int c = 0; c < kRegs / 4; ++c)
+      st_shared_16(row + (((uint32_t)(c0 + c) << 4) ^ (row >> 3 & 0x70u)), r[4 * c], r[4 * c + 1],
+                   r[4 * c + 2], r[4 * c + 3]);
+  }
+  // Into column m of C from row c_row on, `count` rows of it; lanes hold
   // neighbouring columns.
-  __device__ __forceinline__ void store(T *C, int64_t ld, int64_t c_row, int m, int columns,
+  __device__ __forceinline__ void store_column(T *C, int64_t ld, int64_t c_row, int m, int columns,
                                         int count) const {
     if constexpr (sizeof(T) == 4) {
       if (m >= columns) return;
@@ -168,23 +253,26 @@ struct Column {
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, bool ROWS, int WIDE>
+__global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
     product_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ ProductArgs p,
                    unsigned int *err) {
-  using L = Layout;
+  using L = Layout<T, ROWS, WIDE>;
   constexpr int kStages = L::kStages;
   constexpr uint16_t kBoth = 3;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
-  const uint32_t bars = ring + L::kRingBytes;
+  const uint32_t bars = ring + L::kRingBytes + L::kOutBytes;
   const uint32_t full0 = bars, empty0 = bars + 8 * kStages;
-  const uint32_t accf = bars + 8 * (2 * kStages), acce = accf + 8, drain = acce + 8;
+  const uint32_t accf0 = bars + 8 * (2 * kStages), acce0 = accf0 + 8 * L::kAcc;
+  const uint32_t tilef0 = acce0 + 8 * L::kAcc, tilee0 = tilef0 + 8 * kTilesAhead;
+  const uint32_t drain = tilee0 + 8 * kTilesAhead;
   const uint32_t slot = bars + L::kBarBytes;
   uint8_t *slot_ptr = smem_raw + (slot - raw);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(slot_ptr + 4);
-  int *first = reinterpret_cast<int *>(slot_ptr + 16);
+  Tile *tile_ring = reinterpret_cast<Tile *>(slot_ptr + 16);
+  int *first = reinterpret_cast<int *>(tile_ring + kTilesAhead);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();   // 0: issues the pair's MMAs
@@ -193,15 +281,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
-    mbar_init(accf, 1);
-    mbar_init(acce, 2 * kEpilogueWarps);
+    for (int i = 0; i < L::kAcc; ++i) {
+      mbar_init(accf0 + 8 * i, 1);
+      mbar_init(acce0 + 8 * i, 2 * L::kTeamWarps);
+    }
+    for (int i = 0; i < kTilesAhead; ++i) {   // read by the loading warp, in the even CTA the
+      mbar_init(tilef0 + 8 * i, 1);           // issuing one, and a team of the epilogue
+      mbar_init(tilee0 + 8 * i, (rank == 0 ? 2 : 1) + L::kTeamWarps);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
     prefetch_tmap(&maps.a);
-    prefetch_tmap(&maps.b);
-    prefetch_tmap(&maps.b16);
+    for (int i = 0; i < 4; ++i) prefetch_tmap(&maps.b[i]);
     prefetch_tmap(&maps.sfa);
     prefetch_tmap(&maps.sfb);
   }
@@ -211,26 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   follow_previous();
   allow_next();
-  if (warp == 2) {   // where every group's tiles start: a lane has a run of groups
-    const int E = p.groups.count, per = (E + 31) / 32;
-    const int e0 = min(lane * per, E), e1 = min(e0 + per, E);
-    long long sum = 0;
-    for (int e = e0; e < e1; ++e) sum += tiles_of(p, group_rows(p.groups, e).y);
-    long long upto = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long other = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += other;
-    }
-    // more than the host allows for come from offsets that are no offsets: nothing is done
-    const bool fits = __shfl_sync(0xFFFFFFFFu, upto, 31) <= kMostTiles;
-    long long at = fits ? upto - sum : 0;
-    for (int e = e0; e < e1; ++e) {
-      first[e] = (int)at;
-      if (fits) at += tiles_of(p, group_rows(p.groups, e).y);
-    }
-    if (lane == 31) first[E] = fits ? (int)upto : 0;
-  }
+  if (warp == 2) number_tiles<ROWS, WIDE>(p, first);
   tc_fence_before();
   __syncthreads();
   cluster_sync_any();
@@ -241,21 +315,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool paired = ld_shared_cluster_u32(mapa_shared(slot, rank ^ 1u)) == tmem_base;
   if (!paired && threadIdx.x == 0) atomicOr(err, 4u);
 
-  const int total = first[p.groups.count];
-  const int unit0 = blockIdx.x / 2, unit_step = gridDim.x / 2;
+  // Tile j of this CTA, by one thread that arrives for its warp, or by a
+  // converged warp; false where there is none or the CTA aborts.
+  const auto take_tile = [&](int j, bool warp_wide, Tile &t) {
+    const int i = j % kTilesAhead;
+    const uint32_t phase = (uint32_t)(j / kTilesAhead) & 1u;
+    const bool ok = warp_wide ? wait_bounded_all(tilef0 + 8 * i, phase, abort_flag, err)
+                              : wait_bounded(tilef0 + 8 * i, phase, abort_flag, err);
+    if (!ok) return false;
+    t = tile_ring[i];
+    if (warp_wide) __syncwarp();
+    if (!warp_wide || lane == 0) mbar_arrive(tilee0 + 8 * i);
+    return t.valid > 0;
+  };
 
   if (!paired) {
   } else if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
       const int a_blocks = (p.a_rows + 127) / 128;   // 128-row blocks of a group's A
-      for (int u = unit0; u < total && ok; u += unit_step) {
-        const Tile t = find_tile(p, first, u);
+      Tile t;
+      for (int j = 0; ok && take_tile(j, false, t); ++j) {
         // past the last block of A (odd count): the even CTA's scales again, nothing is stored
-        const int64_t sfa = t.a_atom + (t.col / 128 + (int)rank < a_blocks ? (int)rank : 0) * (int64_t)p.a.atoms_k;
-        const int half = t.n / 2, second = t.n > 128;
-        const uint32_t bytes = L::kABytes + (uint32_t)half * kBK + 512u * (2u + second);
+        const int a_block = t.a_block + (t.across / 128 + (int)rank < a_blocks ? (int)rank : 0);
+        const int half = t.n / 2, b_row = t.b_row + (int)rank * half;   // this CTA's half of B's rows
+        const uint32_t bytes = L::kABytes + (uint32_t)half * kBK + 512u * (1 + L::kRowBlocks);
         for (int kb = 0; kb < t.num_k; ++kb, ++it) {
           const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
           if (!wait_bounded(empty0 + 8 * s, ph ^ 1u, abort_flag, err)) {
@@ -265,23 +350,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sa = ring + s * L::kStageBytes;
           const uint32_t full_even = mapa_shared(full0 + 8 * s, 0);
           if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
-          tma_load_2d_pair(sa, &maps.a, (t.k_block + kb) * kBK, t.a_row + (int)rank * 128, full_even);
-          // B's K blocks are numbered as A's where both hold a stretch of K
-          const int b_k = (p.by_rows ? kb : t.k_block + kb) * kBK, b_row = t.b_row + (int)rank * half;
-          if (half == kMaxN / 2) {
-            tma_load_2d_pair(sa + L::kABytes, &maps.b, b_k, b_row, full_even);
-          } else {
-            for (int i = 0; i < half; i += kBoxRows)
-              tma_load_2d_pair(sa + L::kABytes + i * kBK, &maps.b16, b_k, b_row + i, full_even);
-          }
-          tma_load_2d_pair(sa + L::kSfaOff, &maps.sfa, 0, (int)(sfa + kb), full_even);
-          tma_load_2d_pair(sa + L::kSfbOff, &maps.sfb, 0, (int)(t.b_atom + kb), full_even);
-          if (second)
-            tma_load_2d_pair(sa + L::kSfbOff + 512, &maps.sfb, 0, (int)(t.b_atom + p.b.atoms_k + kb),
-                             full_even);
+          // ROWS: B's contraction is its own, A's may be a stretch of a longer one
+          const int a_k = t.k_block + kb, b_k = ROWS ? kb : a_k;
+          tma_load_2d_pair(sa, &maps.a, a_k * kBK, t.a_row + (int)rank * 128, full_even);
+          load_rows(sa + L::kABytes, maps.b, b_k * kBK, b_row, half, full_even);
+          tma_load_2d_pair(sa + L::kSfaOff, &maps.sfa, a_k * 128, a_block, full_even);
+          // blocks past the group's are another's or zeros; no MMA reads them
+          tma_load_2d_pair(sa + L::kSfbOff, &maps.sfb, b_k * 128, t.b_block, full_even);
         }
       }
       // every slot's last release (the even CTA's commits) has arrived here
+      ok = ok && !*abort_flag;
       for (uint32_t j = 0, jt = it; ok && j < (uint32_t)kStages; ++j, ++jt)
         ok = wait_bounded(empty0 + 8 * (jt % kStages), ((jt / kStages) & 1u) ^ 1u, abort_flag, err);
       if (!ok) {
@@ -294,14 +373,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
-    uint32_t it = 0, acc_it = 0;
+    uint32_t it = 0;
     bool ok = true;
-    for (int u = unit0; u < total && ok; u += unit_step) {
-      const Tile t = find_tile(p, first, u);
+    Tile t;
+    for (int j = 0; ok && take_tile(j, true, t); ++j) {
       if (t.num_k == 0) continue;   // zeros, which the epilogue writes
       const uint32_t idesc = idesc_mxf8f6f4((uint32_t)p.a_format, (uint32_t)p.b_format, 256,
                                             (uint32_t)t.n, 0, 0);
-      if (!wait_bounded_all(acce, (acc_it & 1u) ^ 1u, abort_flag, err)) break;
+      const uint32_t acc = (uint32_t)t.turn % L::kAcc, turn = ((uint32_t)t.turn / L::kAcc) & 1u;
+      if (!wait_bounded_all(acce0 + 8 * acc, turn ^ 1u, abort_flag, err)) break;
       tc_fence_after();
       for (int kb = 0; kb < t.num_k; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
@@ -311,14 +391,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (elect_one()) {
-          issue_block(ring + s * L::kStageBytes, tmem_base, tmem_base + kMaxN + L::kSfCols * s, idesc,
-                      t.n > 128, kb == 0);
+          issue_block<L>(ring + s * L::kStageBytes, tmem_base + WIDE * acc,
+                         tmem_base + WIDE * L::kAcc + L::kSfCols * s, idesc, t.n > 128, kb == 0);
           mma_commit_pair_multicast(empty0 + 8 * s, kBoth);
-          if (kb == t.num_k - 1) mma_commit_pair_multicast(accf, kBoth);
+          if (kb == t.num_k - 1) mma_commit_pair_multicast(accf0 + 8 * acc, kBoth);
         }
         __syncwarp();
       }
-      ++acc_it;
     }
     if (elect_one()) {
       mma_commit_pair(drain);
@@ -328,47 +407,114 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
+  } else if (warp == 2 + L::kEpilogueWarps) {
+    // Finds the tiles ahead of the others: in the loading warp alone it took
+    // some 750 cycles of each tile.
+    Tiles<ROWS, WIDE> tiles(p, first, blockIdx.x / 2, gridDim.x / 2);
+    int turn = 0;
+    for (int j = 0, ends = 0; ends < L::kTeams; ++j) {
+      Tile t;
+      if (ends == 0 && tiles.next(t)) {
+        t.turn = turn;
+        turn += t.num_k > 0;
+      } else {
+        t.valid = 0;   // behind the last tile: one for each team
+        ++ends;
+      }
+      const int i = j % kTilesAhead;
+      if (!wait_bounded_all(tilee0 + 8 * i, ((uint32_t)(j / kTilesAhead) & 1u) ^ 1u, abort_flag, err)) break;
+      if (lane == 0) {
+        tile_ring[i] = t;
+        mbar_arrive(tilef0 + 8 * i);
+      }
+      __syncwarp();
+    }
   } else {
-    // Warp w drains TMEM lane quarter w % 4 and rows of B [128 h, 128 h + 128)
-    // with h = (w - 2) / 4, 32 at a time.
-    const int quarter = warp & 3, h = (warp - 2) >> 2;
-    const uint32_t acce_even = mapa_shared(acce, 0);
-    uint32_t acc_it = 0;
-    for (int u = unit0; u < total; u += unit_step) {
-      const Tile t = find_tile(p, first, u);
-      Column<T> r[4];
+    // A warp of a team drains TMEM lane quarter w % 4 and the kChunks chunks of
+    // 32 rows of B that are its.
+    const int team = (warp - 2) / L::kTeamWarps;
+    const int quarter = warp & 3, h = (warp - 2) % L::kTeamWarps >> 2;
+    const uint32_t acce_even = mapa_shared(acce0, 0);
+    const uint32_t out = ring + L::kRingBytes + (warp - 2) * 4096;
+    // chunks alternate between warps (ROWS: few rows are shared by all) or follow one another
+    const auto chunk_at = [&](int c) { return 32 * (ROWS ? L::kColumnGroups * c + h : L::kChunks * h + c); };
+    Tile t;
+    for (int j = team; take_tile(j, true, t); j += L::kTeams) {
+      const uint32_t acc = (uint32_t)t.turn % L::kAcc;
+      const uint32_t from = tmem_base + ((uint32_t)(quarter * 32) << 16) + WIDE * acc;
       if (t.num_k > 0) {
-        if (!wait_bounded_warp(accf, acc_it & 1u, abort_flag, err)) break;
+        if (!wait_bounded_warp(accf0 + 8 * acc, ((uint32_t)t.turn / L::kAcc) & 1u, abort_flag, err)) break;
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (128 * h + 32 * c < t.valid) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + 128 * h + 32 * c, v);
-            tmem_ld_wait();
-            r[c].take(v);
-          }
+      }
+      const auto release = [&] {   // the accumulator is free for another tile
+        if (t.num_k == 0) return;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {   // the accumulator is free for the next tile
+        if (lane == 0) {
           if (rank == 0)
-            mbar_arrive(acce);
+            mbar_arrive(acce0 + 8 * acc);
           else
-            mbar_arrive_cluster(acce_even);
+            mbar_arrive_peer(acce_even + 8 * acc);
         }
-        ++acc_it;
+      };
+      const int m = t.across + (int)rank * 128 + quarter * 32;   // first row of the group's A
+      // kPiece chunks: ROWS: as many as are loaded at once; else 128 bytes of a row
+      constexpr int kPiece = ROWS ? 2 : 4 / (int)sizeof(T);
+      Chunk<T> r[L::kAcc > 1 ? kPiece : L::kChunks];
+      const auto load = [&](Chunk<T> *to, int c) {
+        uint32_t x[kPiece][32];
+        if (t.num_k > 0) {
+#pragma unroll
+          for (int k = 0; k < kPiece; ++k)
+            if (chunk_at(c + k) < t.valid) tmem_ld_32x32b_x32(from + chunk_at(c + k), x[k]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < kPiece; ++k) to[k].take(x[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPiece; ++k) to[k].clear();
+        }
+      };
+      const auto store = [&](const Chunk<T> *of, int c) {
+        if constexpr (ROWS) {
+#pragma unroll
+          for (int k = 0; k < kPiece; ++k) {
+            const int n0 = chunk_at(c + k);
+            if (n0 < t.valid)
+              of[k].store_column(static_cast<T *>(p.C), p.a_rows, t.c_row + n0, m + lane, p.a_rows,
+                                 t.valid - n0);
+          }
+        } else {
+          const int n0 = chunk_at(c);
+          if (n0 >= t.valid || m >= p.a_rows) return;
+          if (lane == 0) bulk_wait_read();   // the piece before has left
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < kPiece; ++k) of[k].stage(out + lane * 128, k * 8 / kPiece);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {   // rows and columns past the weight are not written
+            tma_store_3d(&maps.c, out, t.along + n0, m, (int)t.c_row);
+            bulk_commit();
+          }
+        }
+      };
+      if constexpr (L::kAcc > 1) {
+#pragma unroll
+        for (int c = 0; c < L::kChunks; c += kPiece) {
+          load(r, c);
+          if (c + kPiece >= L::kChunks) release();
+          store(r, c);
+        }
       } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) r[c].clear();
-      }
-      const int m = t.col + (int)rank * 128 + quarter * 32 + lane;
+        for (int c = 0; c < L::kChunks; c += kPiece) load(r + c, c);
+        release();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int n0 = 128 * h + 32 * c;
-        if (n0 < t.valid)
-          r[c].store(static_cast<T *>(p.C), p.a_rows, t.c_row + n0, m, p.a_rows, t.valid - n0);
+        for (int c = 0; c < L::kChunks; c += kPiece) store(r + c, c);
       }
     }
+    if (!ROWS && lane == 0) bulk_wait();
   }
 
   __syncwarp();
@@ -386,27 +532,45 @@ bool data_map(CUtensorMap *m, const Side &s, uint32_t box_rows) {
                       CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// The scale atoms as a matrix with an atom a row.
-bool scale_map(CUtensorMap *m, const Side &s, int64_t atoms) {
-  return make_tmap_2d(m, s.scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 128, (uint64_t)atoms, 512, 128, 1,
+// The scale atoms of a 128-row block as a row.
+bool scale_map(CUtensorMap *m, const Side &s, int64_t atoms, uint32_t box_blocks) {
+  return make_tmap_2d(m, s.scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 128 * (uint64_t)s.atoms_k,
+                      (uint64_t)(atoms / s.atoms_k), 512 * (uint64_t)s.atoms_k, 128, box_blocks,
                       CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <typename T>
-int run_product(const PairMaps &maps, const ProductArgs &a, int64_t most, cudaStream_t stream) {
-  auto kernel = product_kernel<T>;
+template <typename T, bool ROWS, int WIDE>
+int run_product(const ProductArgs &a, int64_t a_atoms, int64_t b_atoms, cudaStream_t stream) {
+  using L = Layout<T, ROWS, WIDE>;
+  PairMaps maps;
+  bool ok = data_map(&maps.a, a.a, 128) && scale_map(&maps.sfa, a.a, a_atoms, 1) &&
+            scale_map(&maps.sfb, a.b, b_atoms, L::kRowBlocks);
+  for (int i = 0; i < 4; ++i) ok = ok && data_map(&maps.b[i], a.b, 128u >> i);
+  const uint64_t size = sizeof(T);
+  if (!ROWS)
+    ok = ok && make_tmap_3d(&maps.c, a.C, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                            (uint64_t)a.b_rows, (uint64_t)a.a_rows, (uint64_t)a.groups.count, a.b_rows * size,
+                            a.a_rows * (a.b_rows * size), 128 / sizeof(T), 32, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!ok) return FP8Q_ERR_CUDA;
+  // the most tiles that the groups can make
+  const int64_t along = ROWS ? std::min<int64_t>(a.groups.rows, a.groups.rows / WIDE + a.groups.count)
+                             : (int64_t)a.groups.count * ((a.b_rows + WIDE - 1) / WIDE);
+  const int64_t most = along * ((a.a_rows + 255) / 256);
+  if (most > kMostTiles) return FP8Q_ERR_INVALID_ARG;
+  auto kernel = product_kernel<T, ROWS, WIDE>;
   static PerDeviceOnce setup;  // per instantiation: the pairs that fit at once, 0 on failure
   const int pairs = setup.get([&] {
-    if (gemm::set_smem(kernel, Layout::kSmemBytes) != cudaSuccess) return 0;
-    Launch q(2 * (sm_count() / 2), 1, kThreads, Layout::kSmemBytes, stream, 2);
+    if (gemm::set_smem(kernel, L::kSmemBytes) != cudaSuccess) return 0;
+    Launch q(2 * (sm_count() / 2), 1, L::kThreads, L::kSmemBytes, stream, 2);
     int n = 0;
     return cudaOccupancyMaxActiveClusters(&n, kernel, &q.cfg) == cudaSuccess ? n : 0;
   });
   unsigned int *err = device_error_word();
   if (pairs < 1 || err == nullptr) return FP8Q_ERR_CUDA;
   const int grid = 2 * (int)std::min<int64_t>(most, pairs);
-  log_line("launch experts product_kernel, %d groups, tile 256x256, grid %d in pairs", a.groups.count, grid);
-  return Launch((unsigned)grid, 1, kThreads, Layout::kSmemBytes, stream, 2)
+  log_line("launch experts product_kernel, %d groups, tile 256x%d, grid %d in pairs", a.groups.count,
+           WIDE, grid);
+  return Launch((unsigned)grid, 1, L::kThreads, L::kSmemBytes, stream, 2)
                      .run(kernel, maps, a, err) == cudaSuccess
              ? FP8Q_OK
              : FP8Q_ERR_CUDA;
@@ -416,19 +580,15 @@ int run_product(const PairMaps &maps, const ProductArgs &a, int64_t most, cudaSt
 
 int launch_product(const ProductArgs &a, int out_dtype, int64_t a_atoms, int64_t b_atoms,
                    cudaStream_t stream) {
-  PairMaps maps;
-  if (!data_map(&maps.a, a.a, 128) || !data_map(&maps.b, a.b, kMaxN / 2) ||
-      !data_map(&maps.b16, a.b, kBoxRows) || !scale_map(&maps.sfa, a.a, a_atoms) ||
-      !scale_map(&maps.sfb, a.b, b_atoms))
-    return FP8Q_ERR_CUDA;
-  // the most tiles that the groups can make
-  const int64_t across = (a.a_rows + 255) / 256;
-  const int64_t most =
-      across * (a.by_rows ? std::min<int64_t>(a.groups.rows, a.groups.rows / kMaxN + a.groups.count)
-                          : (int64_t)a.groups.count * ((a.b_rows + kMaxN - 1) / kMaxN));
-  if (most > kMostTiles) return FP8Q_ERR_INVALID_ARG;
-  return out_dtype == FP8Q_DT_BF16 ? run_product<__nv_bfloat16>(maps, a, most, stream)
-                                   : run_product<float>(maps, a, most, stream);
+  const bool bf16 = out_dtype == FP8Q_DT_BF16;
+  if (!a.by_rows)
+    return bf16 ? run_product<__nv_bfloat16, false, 256>(a, a_atoms, b_atoms, stream)
+                : run_product<float, false, 128>(a, a_atoms, b_atoms, stream);
+  // few rows a group on average: a deeper ring of narrower tiles
+  if (bf16 && a.groups.rows > 32 * (int64_t)a.groups.count)
+    return run_product<__nv_bfloat16, true, 256>(a, a_atoms, b_atoms, stream);
+  return bf16 ? run_product<__nv_bfloat16, true, 128>(a, a_atoms, b_atoms, stream)
+              : run_product<float, true, 128>(a, a_atoms, b_atoms, stream);
 }
 
 }  // namespace experts

@@ -597,6 +597,21 @@ bool make_tmap_2d(CUtensorMap *m, const void *base, CUtensorMapDataType dtype, u
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dtype, uint64_t inner,
+                  uint64_t rows, uint64_t slices, uint64_t row_stride_bytes,
+                  uint64_t slice_stride_bytes, uint32_t box_inner, uint32_t box_rows,
+                  CUtensorMapSwizzle swizzle) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t gdim[3] = {inner, rows, slices};
+  cuuint64_t gstride[2] = {row_stride_bytes, slice_stride_bytes};
+  cuuint32_t box[3] = {box_inner, box_rows, 1};
+  cuuint32_t estride[3] = {1, 1, 1};
+  return fn(m, dtype, 3, const_cast<void *>(base), gdim, gstride, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The launch arguments every kernel family shares.
 static void fill_args(GemmArgs &a, const GemmOperandDev &A, const GemmOperandDev &B, void *C,
                       int64_t M, int64_t N, int64_t K, int BN, float *amax_out) {

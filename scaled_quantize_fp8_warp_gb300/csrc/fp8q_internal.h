@@ -69,6 +69,13 @@ bool make_tmap_2d(CUtensorMap *m, const void *base, CUtensorMapDataType dtype, u
                   uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
                   uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
+// 3D tiled tensor map over `slices` such matrices, slice_stride_bytes apart,
+// with boxes of one slice.
+bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dtype, uint64_t inner,
+                  uint64_t rows, uint64_t slices, uint64_t row_stride_bytes,
+                  uint64_t slice_stride_bytes, uint32_t box_inner, uint32_t box_rows,
+                  CUtensorMapSwizzle swizzle);
+
 enum QuantMode : int {
   kModeTensorCurrent = 0,  // s from a device amax
   kModeTensorDelayed = 1,  // s from a device amax history, amax(x) pushed
