@@ -29,7 +29,6 @@ namespace norm {
 namespace {
 
 using pack8::Pack8;
-using pack8::store;
 using tilecast::cast8_any;
 using tilecast::store_bytes;
 using tilecast::tile_scale;
@@ -42,26 +41,88 @@ struct Shape {
   static constexpr int kThreads = RT < 256 ? 256 : RT;
   static constexpr int kRows = kThreads / RT;    // rows of a block at once
   static constexpr int kColumns = 8 * RT * CHUNKS;
+  // blocks an SM has to hold: 80 registers a thread forward, 128 backward
+  static constexpr int kForwardBlocks = CHUNKS > 2 ? 1 : (768 / kThreads > 0 ? 768 / kThreads : 1);
+  static constexpr int kBackwardBlocks = kThreads > 512 ? 1 : (CHUNKS == 1 ? 768 : 512) / kThreads;
+  // Backward, the next row's loads are under way while one is worked on.  1024
+  // threads have no registers for that, nor for the weight's.
+  static constexpr bool kAhead = kThreads <= 512;
 };
 
-__device__ __forceinline__ int columns_in(int64_t col, int64_t C) {
-  return (int)max((int64_t)0, min((int64_t)8, C - col));
+// The eight columns of a thread's chunk (number k of the row's 8-column chunks)
+// and how many of them exist.  VEC: neighbours, moved 16 bytes at a time;
+// otherwise every 16th of the tile that 16 lanes share, so that lanes move
+// neighbouring elements.
+template <bool VEC>
+struct Columns {
+  int64_t first;
+  int valid;
+  __device__ __forceinline__ Columns(int64_t k, int64_t C) {
+    first = VEC ? 8 * k : (k >> 4) * 128 + (k & 15);
+    const int64_t left = C - first;
+    valid = (int)max((int64_t)0, min((int64_t)8, VEC ? left : (left + 15) >> 4));
+    if (valid == 0) first = 0;   // nothing is addressed where nothing is valid
+  }
+};
+
+// A chunk of a row of T, as pairs of values; zeros past the row.
+template <typename T>
+struct Raw {
+  Pack8<T> x;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const T *row, const Columns<VEC> &c) {
+    const T *p = row + c.first;
+    if (VEC) {
+      pack8::load<true>(x, p, c.valid);
+    } else if constexpr (sizeof(T) == 2) {
+      const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x.w[k] = (2 * k < c.valid ? (uint32_t)q[32 * k] : 0u) |
+                 (2 * k + 1 < c.valid ? (uint32_t)q[32 * k + 16] << 16 : 0u);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x.v[j] = j < c.valid ? p[16 * j] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ float2 pair(int k) const { return x.pair(k); }
+};
+
+template <bool VEC, bool STREAM = false, typename T>
+__device__ __forceinline__ void store8(T *row, const Columns<VEC> &c, const float (&v)[8]) {
+  if (VEC) {
+    pack8::store<true, STREAM>(row + c.first, c.valid, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < c.valid) row[c.first + 16 * j] = (T)v[j];
+  }
 }
 
-// Eight weights from column c on; zeros past the row.
 template <bool VEC>
-__device__ __forceinline__ void load_weight(const void *w, int w_bf16, int64_t c, int valid,
-                                            float (&out)[8]) {
-  if (w_bf16) {
-    Pack8<__nv_bfloat16> p;
-    pack8::load<VEC>(p, static_cast<const __nv_bfloat16 *>(w) + (valid > 0 ? c : 0), valid);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = p.at(j);
+__device__ __forceinline__ void store8_bytes(uint8_t *row, const Columns<VEC> &c, uint2 w) {
+  if (VEC) {
+    store_bytes<true>(row + c.first, c.valid, w);
   } else {
-    Pack8<float> p;
-    pack8::load<VEC>(p, static_cast<const float *>(w) + (valid > 0 ? c : 0), valid);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = p.at(j);
+    for (int j = 0; j < 8; ++j)
+      if (j < c.valid) row[c.first + 16 * j] = (uint8_t)((j < 4 ? w.x >> (8 * j) : w.y >> (8 * (j - 4))) & 0xFFu);
+  }
+}
+
+// A chunk of the weight.
+template <bool VEC>
+__device__ __forceinline__ void load_weight(const void *w, int w_bf16, const Columns<VEC> &c, float2 (&out)[4]) {
+  if (w_bf16) {
+    Raw<__nv_bfloat16> r;
+    r.load(static_cast<const __nv_bfloat16 *>(w), c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = r.pair(k);
+  } else {
+    Raw<float> r;
+    r.load(static_cast<const float *>(w), c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = r.pair(k);
   }
 }
 
@@ -71,19 +132,26 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum and maximum over a row's threads, the same in each; the block's warps
-// meet in a slot of shared memory that the next but one call uses again.
+// Sum and maximum over a row's threads, the same in each; a row's warps meet in
+// a slot of shared memory that the next but one call uses again, at a barrier of
+// their own.
 template <int RT>
 struct Reduce {
   float (*slot)[RT / 32];
   int turn = 0;
+  __device__ __forceinline__ void meet() const {
+    if (RT >= 256)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / RT), "n"(RT) : "memory");
+  }
   __device__ __forceinline__ float sum(float v) {
     v = warp_sum(v);
     if constexpr (RT == 32) return v;
     float *s = slot[turn];
     turn ^= 1;
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[(threadIdx.x % RT) >> 5] = v;
+    meet();
     v = 0.0f;
 #pragma unroll
     for (int k = 0; k < RT / 32; ++k) v += s[k];
@@ -94,8 +162,8 @@ struct Reduce {
     if constexpr (RT == 32) return v;
     float *s = slot[turn];
     turn ^= 1;
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = __uint_as_float(v);
-    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[(threadIdx.x % RT) >> 5] = __uint_as_float(v);
+    meet();
     v = 0u;
 #pragma unroll
     for (int k = 0; k < RT / 32; ++k) v = max(v, __float_as_uint(s[k]));
@@ -105,11 +173,26 @@ struct Reduce {
 
 // The rounded sum x + r, as the values that are stored.
 template <typename T>
-__device__ __forceinline__ void add_rounded(const Pack8<T> &x, const Pack8<T> &r, float (&h)[8]) {
+__device__ __forceinline__ void add_rounded(const Raw<T> &x, const Raw<T> &r, float2 (&h)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    h[j] = __fadd_rn(x.at(j), r.at(j));
-    if constexpr (sizeof(T) == 2) h[j] = __bfloat162float(__float2bfloat16_rn(h[j]));
+  for (int k = 0; k < 4; ++k) {
+    h[k] = __fadd2_rn(x.pair(k), r.pair(k));
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w = pack8::bf16x2(h[k].x, h[k].y);
+      h[k] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+  }
+}
+__device__ __forceinline__ void spread(const float2 (&v)[4], float (&out)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) out[2 * k] = v[k].x, out[2 * k + 1] = v[k].y;
+}
+// y = (v rstd) w.
+__device__ __forceinline__ void normed(const float2 (&v)[4], float rstd, const float2 (&w)[4], Pack8<float> &y) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = __fmul2_rn(__fmul2_rn(v[k], make_float2(rstd, rstd)), w[k]);
+    y.v[2 * k] = t.x, y.v[2 * k + 1] = t.y;
   }
 }
 
@@ -125,63 +208,57 @@ __device__ __forceinline__ uint32_t tile_max(uint32_t m) {
 }
 
 template <typename T, int RT, int CHUNKS, bool VEC>
-__global__ void __launch_bounds__(Shape<RT, CHUNKS>::kThreads) forward_kernel(const ForwardArgs p) {
+__global__ void __launch_bounds__(Shape<RT, CHUNKS>::kThreads, Shape<RT, CHUNKS>::kForwardBlocks)
+    forward_kernel(const ForwardArgs p) {
   using S = Shape<RT, CHUNKS>;
-  __shared__ float slots[2][RT / 32];
-  Reduce<RT> reduce{slots};
+  __shared__ float slots[S::kRows][2][RT / 32];
+  Reduce<RT> reduce{slots[threadIdx.x / RT]};
   const int t = threadIdx.x % RT;
   const int64_t step = (int64_t)gridDim.x * S::kRows;
   int64_t row = (int64_t)blockIdx.x * S::kRows + threadIdx.x / RT;
   follow_previous();
   allow_next();
-  float w[CHUNKS][8];
-  int valid[CHUNKS];
+  float2 w[CHUNKS][4];
+  const auto at = [&](int i) { return Columns<VEC>(i * RT + t, p.C); };
 #pragma unroll
-  for (int i = 0; i < CHUNKS; ++i) {
-    const int64_t c = 8 * (int64_t)(i * RT + t);
-    valid[i] = columns_in(c, p.C);
-    load_weight<VEC>(p.weight, p.w_bf16, c, valid[i], w[i]);
-  }
+  for (int i = 0; i < CHUNKS; ++i) load_weight(p.weight, p.w_bf16, at(i), w[i]);
   const T *x = static_cast<const T *>(p.x), *res = static_cast<const T *>(p.residual);
-  Pack8<T> a[CHUNKS], b[CHUNKS];
+  Raw<T> a[CHUNKS], b[CHUNKS];
   const auto fetch = [&](int64_t r) {
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int64_t c = valid[i] > 0 ? 8 * (int64_t)(i * RT + t) : 0;
-      pack8::load<VEC>(a[i], x + r * p.ldx + c, valid[i]);
-      if (res != nullptr) pack8::load<VEC>(b[i], res + r * p.ldr + c, valid[i]);
+      a[i].load(x + r * p.ldx, at(i));
+      if (res != nullptr) b[i].load(res + r * p.ldr, at(i));
     }
   };
   if (row < p.T) fetch(row);
   for (; row < p.T; row += step) {
-    float v[CHUNKS][8];
-    float sum = 0.0f;
+    float2 v[CHUNKS][4], sum = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int64_t c = 8 * (int64_t)(i * RT + t);
       if (res != nullptr) {
         add_rounded<T>(a[i], b[i], v[i]);
-        store<VEC>(static_cast<T *>(p.h) + row * p.ldh + c, valid[i], v[i]);
+        float h[8];
+        spread(v[i], h);
+        store8(static_cast<T *>(p.h) + row * p.ldh, at(i), h);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = a[i].at(j);
+        for (int k = 0; k < 4; ++k) v[i][k] = a[i].pair(k);
       }
     }
+    if (row + step < p.T) fetch(row + step);
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
-    if (row + step < p.T) fetch(row + step);
-    const float rstd = rstd_of(reduce.sum(sum), p);
+      for (int k = 0; k < 4; ++k) sum = __ffma2_rn(v[i][k], v[i][k], sum);
+    const float rstd = rstd_of(reduce.sum(sum.x + sum.y), p);
     if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
     uint32_t m[CHUNKS], all = 0u;
     Pack8<float> y[CHUNKS];
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[i].v[j] = __fmul_rn(__fmul_rn(v[i][j], rstd), w[i][j]);
-      if (p.y != nullptr)
-        store<VEC>(static_cast<T *>(p.y) + row * p.ldy + 8 * (int64_t)(i * RT + t), valid[i], y[i].v);
+      normed(v[i], rstd, w[i], y[i]);
+      if (p.y != nullptr) store8<VEC, true>(static_cast<T *>(p.y) + row * p.ldy, at(i), y[i].v);
       m[i] = y[i].amax_bits();
       all = max(all, m[i]);
     }
@@ -193,12 +270,12 @@ __global__ void __launch_bounds__(Shape<RT, CHUNKS>::kThreads) forward_kernel(co
     }
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int64_t c = 8 * (int64_t)(i * RT + t);
       if (!p.row_scale) {
         s = tile_scale(tile_max(m[i]));
-        if ((t & 15) == 0 && valid[i] > 0) p.q_scales[(c >> 7) * p.T + row] = s;
+        const int64_t tile = (i * RT + t) >> 4;
+        if ((t & 15) == 0 && 128 * tile < p.C) p.q_scales[tile * p.T + row] = s;
       }
-      store_bytes<VEC>(p.q + row * p.C + c, valid[i], cast8_any(y[i], s, __frcp_rn(s)));
+      store8_bytes(p.q + row * p.C, at(i), cast8_any(y[i], s, __frcp_rn(s)));
     }
   }
 }
@@ -213,83 +290,100 @@ __global__ void __launch_bounds__(512) forward_long_kernel(const ForwardArgs p) 
   follow_previous();
   allow_next();
   const T *x = static_cast<const T *>(p.x), *res = static_cast<const T *>(p.residual);
+  const int64_t chunks = (p.C + 127) / 128 * 16;   // whole tiles
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    float sum = 0.0f;
-    for (int64_t c = 8 * t; c < p.C; c += 8 * RT) {
-      const int valid = columns_in(c, p.C);
-      Pack8<T> a, b;
-      float v[8];
-      pack8::load<VEC>(a, x + row * p.ldx + c, valid);
+    float2 sum = make_float2(0.0f, 0.0f);
+    for (int64_t k = t; k < chunks; k += RT) {
+      const Columns<VEC> at(k, p.C);
+      Raw<T> a, b;
+      float2 v[4];
+      a.load(x + row * p.ldx, at);
       if (res != nullptr) {
-        pack8::load<VEC>(b, res + row * p.ldr + c, valid);
+        b.load(res + row * p.ldr, at);
         add_rounded<T>(a, b, v);
-        store<VEC>(static_cast<T *>(p.h) + row * p.ldh + c, valid, v);
+        float h[8];
+        spread(v, h);
+        store8(static_cast<T *>(p.h) + row * p.ldh, at, h);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = a.at(j);
+        for (int j = 0; j < 4; ++j) v[j] = a.pair(j);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+      for (int j = 0; j < 4; ++j) sum = __ffma2_rn(v[j], v[j], sum);
     }
-    const float rstd = rstd_of(reduce.sum(sum), p);
+    const float rstd = rstd_of(reduce.sum(sum.x + sum.y), p);
     if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
     // what this thread stored as h, or x where there is no residual
     const T *h = res != nullptr ? static_cast<const T *>(p.h) + row * p.ldh : x + row * p.ldx;
-    const auto normed = [&](int64_t c, int valid, Pack8<float> &y) {
-      Pack8<T> a;
-      float w[8];
-      pack8::load<VEC>(a, h + (valid > 0 ? c : 0), valid);
-      load_weight<VEC>(p.weight, p.w_bf16, c, valid, w);
+    const auto read = [&](const Columns<VEC> &at, Pack8<float> &y) {
+      Raw<T> a;
+      float2 v[4], w[4];
+      a.load(h, at);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y.v[j] = __fmul_rn(__fmul_rn(a.at(j), rstd), w[j]);
+      for (int j = 0; j < 4; ++j) v[j] = a.pair(j);
+      load_weight(p.weight, p.w_bf16, at, w);
+      normed(v, rstd, w, y);
     };
     uint32_t all = 0u;
     const bool cast = p.q != nullptr && !p.row_scale;
-    for (int64_t c0 = 0; c0 < p.C; c0 += 8 * RT) {   // whole warps, for the tiles' maxima
-      const int64_t c = c0 + 8 * t;
-      const int valid = columns_in(c, p.C);
+    for (int64_t k0 = 0; k0 < chunks; k0 += RT) {   // whole warps, for the tiles' maxima
+      const Columns<VEC> at(k0 + t, p.C);
       Pack8<float> y;
-      normed(c, valid, y);
-      if (p.y != nullptr) store<VEC>(static_cast<T *>(p.y) + row * p.ldy + c, valid, y.v);
+      read(at, y);
+      if (p.y != nullptr) store8<VEC, true>(static_cast<T *>(p.y) + row * p.ldy, at, y.v);
       const uint32_t m = y.amax_bits();
       all = max(all, m);
       if (!cast) continue;
       const float s = tile_scale(tile_max(m));
-      if ((t & 15) == 0 && valid > 0) p.q_scales[(c >> 7) * p.T + row] = s;
-      store_bytes<VEC>(p.q + row * p.C + c, valid, cast8_any(y, s, __frcp_rn(s)));
+      if ((t & 15) == 0 && 8 * (k0 + t) < p.C) p.q_scales[((k0 + t) >> 4) * p.T + row] = s;
+      store8_bytes(p.q + row * p.C, at, cast8_any(y, s, __frcp_rn(s)));
     }
     if (p.q == nullptr || cast) continue;
     const float s = tile_scale(reduce.max_bits(all)), r = __frcp_rn(s);
     if (t == 0) p.q_scales[row] = s;
-    for (int64_t c = 8 * t; c < p.C; c += 8 * RT) {
-      const int valid = columns_in(c, p.C);
+    for (int64_t k = t; k < chunks; k += RT) {
+      const Columns<VEC> at(k, p.C);
       Pack8<float> y;
-      normed(c, valid, y);
-      store_bytes<VEC>(p.q + row * p.C + c, valid, cast8_any(y, s, r));
+      read(at, y);
+      store8_bytes(p.q + row * p.C, at, cast8_any(y, s, r));
     }
   }
 }
 
-// dx of one chunk.
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_dx(const BackwardArgs &p, int64_t row, int64_t c, int valid,
-                                         const float (&g)[8], const float (&n)[8], float mean,
-                                         float rstd, const Pack8<T> &add) {
-  float dx[8];
+// n = h rstd and g = dy w of one chunk.
+template <typename T>
+__device__ __forceinline__ void terms(const Raw<T> &dy, const Raw<T> &h, float rstd, const float2 (&w)[4],
+                                      float2 (&g)[4], float2 (&n)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    dx[j] = __fmul_rn(rstd, fmaf(-n[j], mean, g[j]));
-    if (p.dresidual != nullptr) dx[j] = __fadd_rn(dx[j], add.at(j));
+  for (int k = 0; k < 4; ++k) {
+    n[k] = __fmul2_rn(h.pair(k), make_float2(rstd, rstd));
+    g[k] = __fmul2_rn(dy.pair(k), w[k]);
   }
-  store<VEC>(static_cast<T *>(p.dx) + row * p.lddx + c, valid, dx);
+}
+
+// dx = rstd (g - n mean) + dresidual of one chunk.
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_dx(const BackwardArgs &p, int64_t row, const Columns<VEC> &at,
+                                         const float2 (&g)[4], const float2 (&n)[4], float mean, float rstd,
+                                         const Raw<T> &add) {
+  float2 dx[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    dx[k] = __fmul2_rn(make_float2(rstd, rstd), __ffma2_rn(n[k], make_float2(-mean, -mean), g[k]));
+    if (p.dresidual != nullptr) dx[k] = __fadd2_rn(dx[k], add.pair(k));
+  }
+  float out[8];
+  spread(dx, out);
+  store8<VEC, true>(static_cast<T *>(p.dx) + row * p.lddx, at, out);
 }
 
 template <typename T, int RT, int CHUNKS, bool VEC>
-__global__ void __launch_bounds__(Shape<RT, CHUNKS>::kThreads) backward_kernel(const BackwardArgs p) {
+__global__ void __launch_bounds__(Shape<RT, CHUNKS>::kThreads, Shape<RT, CHUNKS>::kBackwardBlocks)
+    backward_kernel(const BackwardArgs p) {
   using S = Shape<RT, CHUNKS>;
-  __shared__ float slots[2][RT / 32];
+  __shared__ float slots[S::kRows][2][RT / 32];
   __shared__ float join[S::kRows > 1 ? S::kRows : 1][S::kRows > 1 ? S::kColumns : 1];
-  Reduce<RT> reduce{slots};
+  Reduce<RT> reduce{slots[threadIdx.x / RT]};
   const int t = threadIdx.x % RT, mine = threadIdx.x / RT;
   const int64_t step = (int64_t)gridDim.x * S::kRows;
   int64_t row = (int64_t)blockIdx.x * S::kRows + mine;
@@ -297,59 +391,68 @@ __global__ void __launch_bounds__(Shape<RT, CHUNKS>::kThreads) backward_kernel(c
   allow_next();
   const T *dy = static_cast<const T *>(p.dy), *h = static_cast<const T *>(p.h);
   const T *res = static_cast<const T *>(p.dresidual);
-  int valid[CHUNKS];
-  float dw[CHUNKS][8];
+  const auto at = [&](int i) { return Columns<VEC>(i * RT + t, p.C); };
+  float2 dw[CHUNKS][4], w[CHUNKS][4];
 #pragma unroll
   for (int i = 0; i < CHUNKS; ++i) {
-    valid[i] = columns_in(8 * (int64_t)(i * RT + t), p.C);
+    if (S::kAhead) load_weight(p.weight, p.w_bf16, at(i), w[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    for (int k = 0; k < 4; ++k) dw[i][k] = make_float2(0.0f, 0.0f);
   }
-  Pack8<T> a[CHUNKS], b[CHUNKS];
+  Raw<T> a[CHUNKS], b[CHUNKS], add[CHUNKS];   // dy, h, dresidual of the next row
   float rstd = 0.0f;
   const auto fetch = [&](int64_t r) {
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int64_t c = valid[i] > 0 ? 8 * (int64_t)(i * RT + t) : 0;
-      pack8::load<VEC>(a[i], dy + r * p.lddy + c, valid[i]);
-      pack8::load<VEC>(b[i], h + r * p.ldh + c, valid[i]);
+      a[i].load(dy + r * p.lddy, at(i));
+      b[i].load(h + r * p.ldh, at(i));
+      if (S::kAhead && res != nullptr) add[i].load(res + r * p.lddr, at(i));
     }
     rstd = p.rstd[r];
   };
-  if (row < p.T) fetch(row);
+  if (S::kAhead && row < p.T) fetch(row);
   for (; row < p.T; row += step) {
-    float g[CHUNKS][8], n[CHUNKS][8];
-    Pack8<T> add[CHUNKS];
+    // this row stays as it was read, half the registers of bf16's values: n and
+    // g are found twice
+    if (!S::kAhead) fetch(row);
+    Raw<T> d[CHUNKS], x[CHUNKS], plus[CHUNKS];
     const float scale = rstd;
-    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) d[i] = a[i], x[i] = b[i], plus[i] = add[i];
+    if (S::kAhead && row + step < p.T) fetch(row + step);
+    float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int64_t c = 8 * (int64_t)(i * RT + t);
-      float w[8];
-      load_weight<VEC>(p.weight, p.w_bf16, c, valid[i], w);
-      if (res != nullptr) pack8::load<VEC>(add[i], res + row * p.lddr + (valid[i] > 0 ? c : 0), valid[i]);
+      float2 g[4], n[4];
+      if (!S::kAhead) load_weight(p.weight, p.w_bf16, at(i), w[i]);
+      terms(d[i], x[i], scale, w[i], g, n);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = a[i].at(j);
-        n[i][j] = __fmul_rn(b[i].at(j), scale);
-        g[i][j] = __fmul_rn(d, w[j]);
-        dw[i][j] = fmaf(d, n[i][j], dw[i][j]);
-        sum = fmaf(g[i][j], n[i][j], sum);
+      for (int k = 0; k < 4; ++k) {
+        dw[i][k] = __ffma2_rn(d[i].pair(k), n[k], dw[i][k]);
+        sum = __ffma2_rn(g[k], n[k], sum);
       }
     }
-    if (row + step < p.T) fetch(row + step);
-    const float mean = __fdiv_rn(reduce.sum(sum), (float)p.C);
+    const float mean = __fdiv_rn(reduce.sum(sum.x + sum.y), (float)p.C);
 #pragma unroll
-    for (int i = 0; i < CHUNKS; ++i)
-      store_dx<T, VEC>(p, row, 8 * (int64_t)(i * RT + t), valid[i], g[i], n[i], mean, scale, add[i]);
+    for (int i = 0; i < CHUNKS; ++i) {
+      float2 g[4], n[4];
+      if (!S::kAhead) {
+        load_weight(p.weight, p.w_bf16, at(i), w[i]);
+        if (res != nullptr) plus[i].load(res + row * p.lddr, at(i));
+      }
+      terms(d[i], x[i], scale, w[i], g, n);
+      store_dx(p, row, at(i), g, n, mean, scale, plus[i]);
+    }
   }
   if (p.dweight == nullptr) return;
   float *out = p.partial + (int64_t)blockIdx.x * p.C;
   if constexpr (S::kRows > 1) {   // the warps' sums, added in their order
 #pragma unroll
-    for (int i = 0; i < CHUNKS; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) join[mine][8 * (i * RT + t) + j] = dw[i][j];
+    for (int i = 0; i < CHUNKS; ++i) {
+      float v[8];
+      spread(dw[i], v);
+      store8(join[mine], at(i), v);
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < (int)p.C; c += S::kThreads) {
       float s = 0.0f;
@@ -359,10 +462,11 @@ __global__ void __launch_bounds__(Shape<RT, CHUNKS>::kThreads) backward_kernel(c
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < CHUNKS; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < valid[i]) out[8 * (int64_t)(i * RT + t) + j] = dw[i][j];
+    for (int i = 0; i < CHUNKS; ++i) {
+      float v[8];
+      spread(dw[i], v);
+      store8(out, at(i), v);
+    }
   }
 }
 
@@ -371,38 +475,32 @@ __global__ void __launch_bounds__(512) backward_long_kernel(const BackwardArgs p
   constexpr int RT = 512;
   __shared__ float slots[2][RT / 32];
   Reduce<RT> reduce{slots};
-  const int t = threadIdx.x;
+  const int64_t t = threadIdx.x, chunks = (p.C + 127) / 128 * 16;
   follow_previous();
   allow_next();
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
     const float rstd = p.rstd[row];
-    float g[8], n[8];
-    const auto read = [&](int64_t c, int valid) {
-      Pack8<T> a, b;
-      float w[8];
-      pack8::load<VEC>(a, static_cast<const T *>(p.dy) + row * p.lddy + c, valid);
-      pack8::load<VEC>(b, static_cast<const T *>(p.h) + row * p.ldh + c, valid);
-      load_weight<VEC>(p.weight, p.w_bf16, c, valid, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        n[j] = __fmul_rn(b.at(j), rstd);
-        g[j] = __fmul_rn(a.at(j), w[j]);
-      }
+    float2 g[4], n[4], sum = make_float2(0.0f, 0.0f);
+    const auto read = [&](const Columns<VEC> &at) {
+      Raw<T> a, b;
+      float2 w[4];
+      a.load(static_cast<const T *>(p.dy) + row * p.lddy, at);
+      b.load(static_cast<const T *>(p.h) + row * p.ldh, at);
+      load_weight(p.weight, p.w_bf16, at, w);
+      terms(a, b, rstd, w, g, n);
     };
-    float sum = 0.0f;
-    for (int64_t c = 8 * t; c < p.C; c += 8 * RT) {
-      read(c, columns_in(c, p.C));
+    for (int64_t k = t; k < chunks; k += RT) {
+      read(Columns<VEC>(k, p.C));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(g[j], n[j], sum);
+      for (int j = 0; j < 4; ++j) sum = __ffma2_rn(g[j], n[j], sum);
     }
-    const float mean = __fdiv_rn(reduce.sum(sum), (float)p.C);
-    for (int64_t c = 8 * t; c < p.C; c += 8 * RT) {
-      const int valid = columns_in(c, p.C);
-      read(c, valid);
-      Pack8<T> add;
-      if (p.dresidual != nullptr)
-        pack8::load<VEC>(add, static_cast<const T *>(p.dresidual) + row * p.lddr + c, valid);
-      store_dx<T, VEC>(p, row, c, valid, g, n, mean, rstd, add);
+    const float mean = __fdiv_rn(reduce.sum(sum.x + sum.y), (float)p.C);
+    for (int64_t k = t; k < chunks; k += RT) {
+      const Columns<VEC> at(k, p.C);
+      read(at);
+      Raw<T> add;
+      if (p.dresidual != nullptr) add.load(static_cast<const T *>(p.dresidual) + row * p.lddr, at);
+      store_dx(p, row, at, g, n, mean, rstd, add);
     }
   }
 }
@@ -423,26 +521,27 @@ __global__ void __launch_bounds__(256) columns_kernel(const BackwardArgs p) {
   p.partial[(int64_t)blockIdx.y * p.C + c] = sum;
 }
 
-// dweight from `count` rows of partial sums: 32 columns a block, whose eight
-// warps take the rows in turns and are added in their order.
-__global__ void __launch_bounds__(256) join_kernel(const float *partial, int count, int64_t C,
-                                                   void *dweight, int w_bf16) {
-  __shared__ float sums[8][33];
+// dweight from `count` rows of partial sums: 32 columns a block, whose warps
+// take the rows in turns and are added in their order.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const float *partial, int count, int64_t C,
+                                                               void *dweight, int w_bf16) {
+  __shared__ float sums[kJoinWarps][33];
   follow_previous();
   allow_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (c < C) {
-#pragma unroll 8
-    for (int k = warp; k < count; k += 8) s += partial[k * C + c];
+#pragma unroll 10
+    for (int k = warp; k < count; k += kJoinWarps) s += partial[k * C + c];
   }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || c >= C) return;
   s = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s += sums[k][lane];
+  for (int k = 0; k < kJoinWarps; ++k) s += sums[k][lane];
   if (w_bf16)
     static_cast<__nv_bfloat16 *>(dweight)[c] = __float2bfloat16_rn(s);
   else
@@ -476,10 +575,10 @@ cudaError_t run_forward(const ForwardArgs &a, cudaStream_t stream) {
 template <typename T, bool VEC>
 cudaError_t forward(const ForwardArgs &a, cudaStream_t stream) {
   if (a.C <= 256) return run_forward<T, 32, 1, VEC>(a, stream);
-  if (a.C <= 1024) return run_forward<T, 32, 4, VEC>(a, stream);
+  if (a.C <= 1024) return run_forward<T, 128, 1, VEC>(a, stream);
   if (a.C <= 2048) return run_forward<T, 256, 1, VEC>(a, stream);
   if (a.C <= 4096) return run_forward<T, 256, 2, VEC>(a, stream);
-  if (a.C <= 8192) return run_forward<T, 256, 4, VEC>(a, stream);
+  if (a.C <= 8192) return run_forward<T, 512, 2, VEC>(a, stream);
   if (a.C <= 16384) return run_forward<T, 512, 4, VEC>(a, stream);
   auto kernel = forward_long_kernel<T, VEC>;
   struct Tag {};
@@ -507,11 +606,11 @@ cudaError_t run_backward(const BackwardArgs &a, int &partials, cudaStream_t stre
 template <typename T, bool VEC>
 cudaError_t backward(const BackwardArgs &a, int &partials, cudaStream_t stream) {
   if (a.C <= 256) return run_backward<T, 32, 1, VEC>(a, partials, stream);
-  if (a.C <= 1024) return run_backward<T, 32, 4, VEC>(a, partials, stream);
+  if (a.C <= 1024) return run_backward<T, 128, 1, VEC>(a, partials, stream);
   if (a.C <= 2048) return run_backward<T, 256, 1, VEC>(a, partials, stream);
   if (a.C <= 4096) return run_backward<T, 256, 2, VEC>(a, partials, stream);
   if (a.C <= 8192) return run_backward<T, 512, 2, VEC>(a, partials, stream);
-  if (a.C <= 16384) return run_backward<T, 512, 4, VEC>(a, partials, stream);
+  if (a.C <= 16384) return run_backward<T, 1024, 2, VEC>(a, partials, stream);
   // dw first: dx may overwrite dy
   if (a.dweight != nullptr) {
     const int64_t columns = (a.C + 255) / 256;
@@ -566,7 +665,7 @@ cudaError_t launch_backward(int dtype, const BackwardArgs &a, cudaStream_t strea
   if (a.dweight == nullptr) return cudaSuccess;
   const int64_t blocks = (a.C + 31) / 32;
   log_line("launch norm join_kernel, %d partial sums, grid %lld", partials, (long long)blocks);
-  return Launch((unsigned)blocks, 1, 256, 0, stream)
+  return Launch((unsigned)blocks, 1, 32 * kJoinWarps, 0, stream)
       .run(join_kernel, static_cast<const float *>(a.partial), partials, a.C, a.dweight, a.w_bf16);
 }
 

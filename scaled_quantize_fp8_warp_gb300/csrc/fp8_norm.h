@@ -35,8 +35,8 @@ struct BackwardArgs {
 };
 
 // Partial sums of dweight, one row of C for each CTA of the backward kernel:
-// two CTAs on each of 152 SMs.
-constexpr int kPartials = 2 * kNumSMsHint;
+// three CTAs at most on each of 152 SMs.
+constexpr int kPartials = 3 * kNumSMsHint;
 
 cudaError_t launch_forward(int dtype, const ForwardArgs &a, cudaStream_t stream);
 cudaError_t launch_backward(int dtype, const BackwardArgs &a, cudaStream_t stream);
