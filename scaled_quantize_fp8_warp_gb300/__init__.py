@@ -709,6 +709,15 @@ def _out_rows(out, shape, dtype, device, stream, what):
     return _like(out, shape, dtype, what), *_rows(out)
 
 
+def _given(t, shape, dtype, device, stream, what):
+    """(tensor, its address) of a dense result of one type: the caller's,
+    checked, or a new one."""
+    if t is None:
+        t = _new(shape, dtype, device, stream)
+        return t, t.data_ptr()
+    return t, _addr(_like(t, shape, dtype, what))
+
+
 def fp4_scale_bytes(kind: int, rows: int, K: int) -> int:
     """Bytes of the scale atoms of an [rows, K] 4-bit operand."""
     return (rows + 127) // 128 * ((K + 127) // 128 if kind == MXFP4 else (K + 63) // 64) * 512
@@ -974,7 +983,8 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
     T, C = shape = x.shape
     dtype, device = x.dtype, x.device
     pw, w_dtype = _norm_weight(weight, C)
-    pr, ldr, ph, ldh, py, ldy, pq, ps = None, 0, None, 0, None, 0, None, None
+    pr = ph = py = pq = ps = None
+    ldr = ldh = ldy = 0
     if residual is not None:
         pr, ldr = _rows(_like(residual, shape, dtype, "residual"))
         h, ph, ldh = _out_rows(h, shape, dtype, device, stream, "h")
@@ -984,20 +994,15 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
         y, py, ldy = _out_rows(y, shape, dtype, device, stream, "y")
     if scaling is not None:
         s_shape = ((C + 127) // 128, T) if scaling == SCALE_TILE_1x128 else (T,)
-        if q is None:
-            q = _new(shape, torch.uint8, device, stream)
-        if scales is None:
-            scales = _new(s_shape, torch.float32, device, stream)
-        pq = _addr(_like(q, shape, torch.uint8, "q"))
-        ps = _addr(_like(scales, s_shape, torch.float32, "scales"))
+        q, pq = _given(q, shape, torch.uint8, device, stream, "q")
+        scales, ps = _given(scales, s_shape, torch.float32, device, stream, "scales")
     elif q is not None or scales is not None:
         raise ValueError("an 8-bit output needs a scaling")
-    if rstd is None:
-        rstd = _new((T,), torch.float32, device, stream)
+    rstd, pd = _given(rstd, (T,), torch.float32, device, stream, "rstd")
     _check(lib().fp8_rmsnorm(
         px, ldx, pr, ldr, _in_dtype(x), pw, w_dtype, ctypes.byref(ctypes.c_float(eps)), T, C, ph,
-        ldh, py, ldy, 0 if scaling is None else scaling, pq, ps,
-        _addr(_like(rstd, (T,), torch.float32, "rstd")), _raw_stream(stream)), "fp8_rmsnorm")
+        ldh, py, ldy, 0 if scaling is None else scaling, pq, ps, pd, _raw_stream(stream)),
+        "fp8_rmsnorm")
     return NormOutput(x if h is None else h, y, q, scales, rstd)
 
 
@@ -1018,12 +1023,10 @@ def fp8_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
         pr, ldr = _rows(_like(dresidual, shape, dtype, "dresidual"))
     dx, px, ldx = _out_rows(dx, shape, dtype, device, stream, "dx")
     if want_dweight or dweight is not None:
-        if dweight is None:
-            dweight = _new((C,), weight.dtype, device, stream)
-        pdw = _addr(_like(dweight, (C,), weight.dtype, "dweight"))
+        dweight, pdw = _given(dweight, (C,), weight.dtype, device, stream, "dweight")
         if workspace is None:
-            workspace = _new((int(lib().fp8q_rmsnorm_backward_workspace_size(T, C)),), torch.uint8,
-                             device, stream)
+            workspace = _new((lib().fp8q_rmsnorm_backward_workspace_size(T, C),), torch.uint8, device,
+                             stream)
     _check(lib().fp8_rmsnorm_backward(
         pd, ldd, ph, ldh, _in_dtype(dy), pw, w_dtype, ps, pr, ldr, T, C, px, ldx, pdw,
         _addr(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(stream)),
@@ -1092,10 +1095,13 @@ class ExpertsOperand:
         if not 1 <= groups <= EXPERTS_MAX:
             raise ValueError(f"an operand has 1 to {EXPERTS_MAX} groups")
         blocks = experts_blocks(rows, groups, offsets is not None)
-        n = 512 * blocks * ((cols + 127) // 128)
-        new = lambda *shape: _new(shape, torch.uint8, device, stream)
-        return cls(rows, cols, groups, fmt, offsets, *((new(rows, cols), new(n)) if by_rows else (None, None)),
-                   *((new(cols, 128 * blocks), new(n)) if transposed else (None, None)))
+        n = (512 * blocks * ((cols + 127) // 128),)
+        q = qs = qt = qts = None
+        if by_rows:
+            q, qs = (_new(s, torch.uint8, device, stream) for s in ((rows, cols), n))
+        if transposed:
+            qt, qts = (_new(s, torch.uint8, device, stream) for s in ((cols, 128 * blocks), n))
+        return cls(rows, cols, groups, fmt, offsets, q, qs, qt, qts)
 
 
 def fp8_quantize_experts(x: torch.Tensor, groups: int, offsets: torch.Tensor | None = None,

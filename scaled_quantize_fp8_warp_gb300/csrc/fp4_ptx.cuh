@@ -128,6 +128,16 @@ __device__ __forceinline__ bool wait_counter_all(uint32_t addr, int value,
   }
 }
 
+// The two halves of a barrier over the cluster where no memory is passed on,
+// only that all CTAs have come this far: a release would wait for stores to
+// global memory (a CTA that had just stored a tile waited 2 to 4 us).
+__device__ __forceinline__ void cluster_arrive_any() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_any() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Every thread of every CTA in the cluster: release this CTA's prior writes,
 // wait for all the others.  Not the .aligned form, whose warps must be
 // converged: threads come here from loops of different lengths, and an arrival
@@ -136,6 +146,11 @@ __device__ __forceinline__ void cluster_sync_any() {
   asm volatile(
       "barrier.cluster.arrive.release;\n\t"
       "barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// One word into a CTA of the cluster, at a shared::cluster address.
+__device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {

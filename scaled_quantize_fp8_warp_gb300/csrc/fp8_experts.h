@@ -18,11 +18,12 @@ struct Groups {
 #ifdef __CUDACC__
 // First row and number of rows of group e.  Offsets are read as they are and
 // brought into [0, rows]: whatever they hold, rows stay inside the operand.
-__device__ __forceinline__ int2 group_rows(const Groups &g, int e) {
+__device__ __forceinline__ int2 group_rows(const Groups &g, const int32_t *offsets, int e) {
   if (g.offsets == nullptr) return make_int2(e * g.each, g.each);
-  const int a = min(max(g.offsets[e], 0), g.rows), z = min(max(g.offsets[e + 1], 0), g.rows);
+  const int a = min(max(offsets[e], 0), g.rows), z = min(max(offsets[e + 1], 0), g.rows);
   return make_int2(a, max(z - a, 0));
 }
+__device__ __forceinline__ int2 group_rows(const Groups &g, int e) { return group_rows(g, g.offsets, e); }
 
 // First 128-row block of a group whose first row is `row`.
 __device__ __forceinline__ int first_block(const Groups &g, int e, int row) {
@@ -64,6 +65,13 @@ cudaError_t launch_cast(int in_dtype, int format, const CastArgs &a, cudaStream_
 // a_atoms, b_atoms: scale atoms of each side in all.
 int launch_product(const ProductArgs &a, int out_dtype, int64_t a_atoms, int64_t b_atoms,
                    cudaStream_t stream);
+
+// The same for few rows (by_rows): the contraction split over a cluster.
+// split_for: CTAs that a tile's contraction is split over, 0 where this kernel
+// does not serve the product.
+int split_for(const ProductArgs &a);
+int launch_split(const ProductArgs &a, int split, int out_dtype, int64_t a_atoms, int64_t b_atoms,
+                 cudaStream_t stream);
 
 }  // namespace experts
 }  // namespace fp8q

@@ -106,7 +106,8 @@ int rows_product(const fp8q_experts *x, const fp8q_experts *w, bool dgrad, void 
   if (w->offsets != nullptr || w->groups != x->groups) return FP8Q_ERR_INVALID_ARG;
   const int64_t N = w->rows / w->groups, K = w->cols, S = x->rows;
   const int64_t contract = dgrad ? N : K, result = dgrad ? K : N;
-  if (N % 16 != 0 || x->cols != contract) return FP8Q_ERR_INVALID_ARG;
+  if (N % 16 != 0 || x->cols != contract || (contract == 0 && S > 0 && result > 0))
+    return FP8Q_ERR_INVALID_ARG;
   if (S > 0 && result > 0) {
     if (y == nullptr || result > INT64_MAX / 8 / S) return FP8Q_ERR_INVALID_ARG;
     if (!aligned(y, 16)) return FP8Q_ERR_MISALIGNED;

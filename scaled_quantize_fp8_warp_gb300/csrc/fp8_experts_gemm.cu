@@ -20,6 +20,7 @@
 #include "fp4_launch.cuh"
 #include "fp4_ptx.cuh"
 #include "fp8_experts.h"
+#include "fp8_experts_maps.h"
 #include "fp8_pack8.cuh"
 #include "fp8q_gemm_common.cuh"
 
@@ -29,7 +30,6 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kBK = 128;          // bytes = elements of K per stage
 constexpr int kRaster = 8;        // tiles of B visited together
 constexpr int kTilesAhead = 8;    // tiles that are found ahead of their results
 constexpr int kMostTiles = INT32_MAX / 2;   // of a launch
@@ -80,9 +80,10 @@ struct Layout {
   static constexpr int kStages = (208 * 1024 - kOutBytes) / kStageBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kBarBytes = 8 * (2 * kStages + 2 * kAcc + 2 * kTilesAhead + 2) / 16 * 16;
-  static constexpr int kFirstBytes = (FP8Q_EXPERTS_MAX + 1) * 4;   // first tile of every group
+  // the groups' offsets, and the first tile of each
+  static constexpr int kGroupBytes = 2 * (FP8Q_EXPERTS_MAX + 1) * 4;
   static constexpr int kSmemBytes =
-      kRingBytes + kOutBytes + kBarBytes + 16 + kTilesAhead * (int)sizeof(Tile) + kFirstBytes + 1024;
+      kRingBytes + kOutBytes + kBarBytes + 16 + kTilesAhead * (int)sizeof(Tile) + kGroupBytes + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "the ring fits in shared memory");
   static_assert(WIDE * kAcc + kSfCols * kStages <= kTmemCols, "scale slots fit in tensor memory");
 };
@@ -94,13 +95,13 @@ __device__ __forceinline__ int tiles_across(const ProductArgs &p) { return (p.a_
 
 // Where every group's tiles start in the numbering of all, by one warp.
 template <bool ROWS, int WIDE>
-__device__ __forceinline__ void number_tiles(const ProductArgs &p, int *first) {
+__device__ __forceinline__ void number_tiles(const ProductArgs &p, const int32_t *offsets, int *first) {
   const int lane = threadIdx.x & 31, E = p.groups.count;
   long long done = 0;
   for (int e0 = 0; e0 < E; e0 += 32) {
     long long n = 0;
     if (e0 + lane < E)
-      n = (long long)tiles_along<WIDE>(ROWS ? group_rows(p.groups, e0 + lane).y : p.b_rows) * tiles_across(p);
+      n = (long long)tiles_along<WIDE>(ROWS ? group_rows(p.groups, offsets, e0 + lane).y : p.b_rows) * tiles_across(p);
     long long sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -119,12 +120,14 @@ __device__ __forceinline__ void number_tiles(const ProductArgs &p, int *first) {
 template <bool ROWS, int WIDE>
 struct Tiles {
   const ProductArgs &p;
+  const int32_t *offsets;
   const int *first;
   int u, step;
   int e = -1, row, rows;       // the group, its first row and its rows
   int block, along, each, more;
-  __device__ __forceinline__ Tiles(const ProductArgs &args, const int *first_tiles, int pair, int pairs)
-      : p(args), first(first_tiles), u(pair), step(pairs) {}
+  __device__ __forceinline__ Tiles(const ProductArgs &args, const int32_t *group_offsets,
+                                   const int *first_tiles, int pair, int pairs)
+      : p(args), offsets(group_offsets), first(first_tiles), u(pair), step(pairs) {}
   __device__ __forceinline__ bool next(Tile &t) {
     if (u >= first[p.groups.count]) return false;
     if (e < 0 || u >= first[e + 1]) {
@@ -137,7 +140,7 @@ struct Tiles {
           hi = mid;
       }
       e = lo;
-      const int2 group = group_rows(p.groups, e);
+      const int2 group = group_rows(p.groups, offsets, e);
       row = group.x;
       rows = group.y;
       block = first_block(p.groups, e, row);
@@ -272,10 +275,12 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
   uint8_t *slot_ptr = smem_raw + (slot - raw);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(slot_ptr + 4);
   Tile *tile_ring = reinterpret_cast<Tile *>(slot_ptr + 16);
-  int *first = reinterpret_cast<int *>(tile_ring + kTilesAhead);
+  int32_t *offsets = reinterpret_cast<int32_t *>(tile_ring + kTilesAhead);
+  int *first = offsets + FP8Q_EXPERTS_MAX + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();   // 0: issues the pair's MMAs
+  cluster_arrive_any();
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full0 + 8 * s, 1);
@@ -304,15 +309,23 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
   }
   follow_previous();
   allow_next();
-  if (warp == 2) number_tiles<ROWS, WIDE>(p, first);
+  if (warp >= 2) {   // the epilogue's warps fetch the offsets
+    if (p.groups.offsets != nullptr)
+      for (int e = threadIdx.x - 64; e <= p.groups.count; e += 32 * L::kEpilogueWarps)
+        if (warp < 2 + L::kEpilogueWarps) offsets[e] = p.groups.offsets[e];
+  }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_any();
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(slot_ptr);
+  cluster_wait_any();   // the peer runs: its shared memory may be written
+  if (warp == 1 && lane == 0) st_shared_cluster_u32(mapa_shared(slot + 8, rank ^ 1u), tmem_base);
+  if (warp == 2) number_tiles<ROWS, WIDE>(p, offsets, first);
+  __syncthreads();
+  cluster_sync_any();
   // One allocation serves the pair: both CTAs must hold the same address.
   // Otherwise neither does any work (a symmetric decision, no waiting).
-  const bool paired = ld_shared_cluster_u32(mapa_shared(slot, rank ^ 1u)) == tmem_base;
+  const bool paired = *reinterpret_cast<volatile uint32_t *>(slot_ptr + 8) == tmem_base;
   if (!paired && threadIdx.x == 0) atomicOr(err, 4u);
 
   // Tile j of this CTA, by one thread that arrives for its warp, or by a
@@ -410,7 +423,7 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
   } else if (warp == 2 + L::kEpilogueWarps) {
     // Finds the tiles ahead of the others: in the loading warp alone it took
     // some 750 cycles of each tile.
-    Tiles<ROWS, WIDE> tiles(p, first, blockIdx.x / 2, gridDim.x / 2);
+    Tiles<ROWS, WIDE> tiles(p, offsets, first, blockIdx.x / 2, gridDim.x / 2);
     int turn = 0;
     for (int j = 0, ends = 0; ends < L::kTeams; ++j) {
       Tile t;
@@ -520,23 +533,11 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_any();  // neither CTA leaves while the other may still signal it
+  cluster_arrive_any();
+  cluster_wait_any();  // neither CTA leaves while the other may still signal it
   tc_fence_after();
   __syncwarp();
   if (warp == 1) tmem_dealloc_pair(tmem_base, L::kTmemCols);
-}
-
-bool data_map(CUtensorMap *m, const Side &s, uint32_t box_rows) {
-  return make_tmap_2d(m, s.data, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)s.row_bytes,
-                      (uint64_t)s.rows, (uint64_t)s.row_bytes, kBK, box_rows,
-                      CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-// The scale atoms of a 128-row block as a row.
-bool scale_map(CUtensorMap *m, const Side &s, int64_t atoms, uint32_t box_blocks) {
-  return make_tmap_2d(m, s.scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 128 * (uint64_t)s.atoms_k,
-                      (uint64_t)(atoms / s.atoms_k), 512 * (uint64_t)s.atoms_k, 128, box_blocks,
-                      CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename T, bool ROWS, int WIDE>
@@ -584,8 +585,13 @@ int launch_product(const ProductArgs &a, int out_dtype, int64_t a_atoms, int64_t
   if (!a.by_rows)
     return bf16 ? run_product<__nv_bfloat16, false, 256>(a, a_atoms, b_atoms, stream)
                 : run_product<float, false, 128>(a, a_atoms, b_atoms, stream);
-  // few rows a group on average: a deeper ring of narrower tiles
-  if (bf16 && a.groups.rows > 32 * (int64_t)a.groups.count)
+  const int split = split_for(a);
+  if (split > 0) return launch_split(a, split, out_dtype, a_atoms, b_atoms, stream);
+  // Tiles 128 wide, which have a deeper ring and three accumulators, up to 96 rows
+  // a group on average: 64 equal groups, 1024 x 4096, 1024 rows 49.6 us and 52.4 with
+  // 256-wide tiles; groups of unlike sizes, 4000 rows in 50, 2048 x 1024, 25.2 and
+  // 26.2, but 8192 in 64, 1024 x 4096, 56.5 and 54.6.
+  if (bf16 && a.groups.rows > 96 * (int64_t)a.groups.count)
     return run_product<__nv_bfloat16, true, 256>(a, a_atoms, b_atoms, stream);
   return bf16 ? run_product<__nv_bfloat16, true, 128>(a, a_atoms, b_atoms, stream)
               : run_product<float, true, 128>(a, a_atoms, b_atoms, stream);

@@ -237,6 +237,18 @@ def test_long_contractions_and_many_tiles(fq, K):
     check_rows_product(fq, [3, 600, 0, 257, 31], 0, 1040, K, BF16, False)
 
 
+@pytest.mark.parametrize("sizes,spare", [([1], 0), ([0, 2, 0, 1], 0), ([100], 27), ([17, 0, 31], 60), ([1] * 9, 1),
+                                         ([127], 0), ([0, 0], 9)])
+@pytest.mark.parametrize("N,K", [(144, 2048), (272, 4112), (1040, 4096)])
+@pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("dgrad", [False, True])
+def test_few_rows(fq, sizes, spare, N, K, out, dgrad):
+    """Fewer than 128 rows, whose contraction (4096 or so) is split over a cluster."""
+    if dgrad:
+        N, K = 16 * (K // 16), N
+    check_rows_product(fq, sizes, spare, N, K, out, dgrad)
+
+
 def test_many_experts(fq):
     g = np.random.default_rng(13)
     check_rows_product(fq, g.integers(0, 6, 1024).tolist(), 10, 48, 64, BF16, False)
