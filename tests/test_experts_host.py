@@ -136,6 +136,46 @@ def test_products_refuse(fq):
     assert call(f, g(qt=None, qts=None), x()) == INVALID and call(f, g(), x(qt=None, qts=None)) == INVALID
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="valid arguments would reach a kernel on placeholder pointers")
+def test_random_arguments_get_a_status_not_a_crash(fq):
+    """Seeded random arguments to every new entry point: a documented status each,
+    before any device work (no device here: ARCH 3 or CUDA 6 past the checks)."""
+    import random
+    rng = random.Random(77)
+    pick = rng.choice
+    sizes = [-1, 0, 1, 15, 16, 48, 128, 130, 4096, 1 << 30, 2 ** 31 - 1, 1 << 40, (1 << 62) + 16]
+    small = [0, 16, 32, 48, 128, 256]
+    ptrs = [None, P(0x10000), P(0x10000), P(0x10008), P(0x10001)]
+    addr = lambda: getattr(pick(ptrs), "value", None)
+    lib = fq.lib()
+
+    def operand():
+        s = sizes if rng.random() < 0.3 else small
+        return fq._ExpertsStruct(addr(), addr(), addr(), addr(), addr(), pick(s), pick(s), pick([-1, 0, 1, 2, 4, 1024, 1025]),
+                                 pick([0, 1, 0, 1, 2, -1]))
+    seen = set()
+    for _ in range(20000):
+        s = sizes if rng.random() < 0.3 else small
+        kind = rng.randrange(4)
+        if kind == 0:
+            eps = pick([None, ctypes.byref(ctypes.c_float(1e-6)), ctypes.byref(ctypes.c_float(-1.0))])
+            rc = lib.fp8_rmsnorm(pick(ptrs), pick(s), pick(ptrs), pick(s), pick([0, 1, 2]), pick(ptrs), pick([0, 1, 3]), eps,
+                                 pick(s), pick(s), pick(ptrs), pick(s), pick(ptrs), pick(s), pick([0, 1, 3, 7]), pick(ptrs),
+                                 pick(ptrs), pick(ptrs), None)
+        elif kind == 1:
+            rc = lib.fp8_rmsnorm_backward(pick(ptrs), pick(s), pick(ptrs), pick(s), pick([0, 1, 2]), pick(ptrs), pick([0, 1, 3]),
+                                          pick(ptrs), pick(ptrs), pick(s), pick(s), pick(s), pick(ptrs), pick(s), pick(ptrs),
+                                          pick(ptrs), pick([0, 1 << 30, 1 << 40]), None)
+        elif kind == 2:
+            rc = lib.fp8_quantize_experts(pick(ptrs), pick([0, 1, 2]), pick(s), pick(s), pick(ptrs), ctypes.byref(operand()), None)
+        else:
+            f = pick([lib.fp8_experts_fprop, lib.fp8_experts_dgrad, lib.fp8_experts_wgrad])
+            rc = f(ctypes.byref(operand()), ctypes.byref(operand()), pick(ptrs), pick([0, 1, 2]), None)
+        assert rc in (0, 1, 2, 3, 4, 6), (kind, rc)
+        seen.add((kind, rc))
+    assert {(k, 6) for k in range(3)} <= seen   # some passed every check
+
+
 def test_struct_layout_matches_header(fq, tmp_path):
     import os
     import subprocess

@@ -120,6 +120,57 @@ def test_h_in_place(fq, C):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("row", [False, True])
+def test_output_is_an_operand(fq, row):
+    """The 8-bit output multiplied by a weight is what the cast of an fp32 y gives."""
+    x, w = normal((200, 512), 50).cuda(), (1 + 0.2 * normal((512,), 51, 1.0, FP32)).cuda()
+    weight = normal((256, 512), 52, 0.05).cuda()
+    y = fq.fp8_rmsnorm(x.float(), w, eps=EPS, scaling=None).y
+    G = fq.GemmOperand
+    if row:
+        q, s, _, _ = fq.fp8_quantize_rowwise(y, fq.E4M3)
+        wq, ws, _, _ = fq.fp8_quantize_rowwise(weight, fq.E4M3)
+        n = fq.fp8_rmsnorm(x, w, eps=EPS, scaling=fq.SCALE_ROW)
+        a, b, c = G.row(q, fq.E4M3, s), G.row(n.q, fq.E4M3, n.scales), G.row(wq, fq.E4M3, ws)
+    else:
+        q, s, _, _ = fq.fp8_quantize_tile1x128(y, fq.E4M3)
+        wq, _, ws = fq.fp8_quantize_block128x128(weight, fq.E4M3)
+        n = fq.fp8_rmsnorm(x, w, eps=EPS)
+        a, b, c = G.tile(q, fq.E4M3, s), G.tile(n.q, fq.E4M3, n.scales), G.block(wq, fq.E4M3, ws)
+    assert torch.equal(fq.fp8_gemm_fprop(a, c), fq.fp8_gemm_fprop(b, c))
+
+
+def test_another_stream_and_a_graph(fq):
+    x, r, w = normal((90, 640), 53).cuda(), normal((90, 640), 54).cuda(), normal((640,), 55).cuda()
+
+    def step(stream=None):
+        n = fq.fp8_rmsnorm(x, w, r, EPS, stream=stream)
+        return (*n, *fq.fp8_rmsnorm_backward(n.y, n.h, w, n.rstd, dresidual=x, stream=stream))
+    want = step()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = step(s)
+    s.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    graphs = []
+    for _ in range(2):   # two at once, each with storage of its own
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, step()))
+    x.copy_(normal((90, 640), 56))
+    for k, (g, _) in enumerate(graphs):
+        with torch.cuda.stream(s if k else torch.cuda.current_stream()):
+            if k:
+                s.wait_stream(torch.cuda.default_stream())
+            g.replay()
+    torch.cuda.synchronize()
+    want = step()
+    for _, got in graphs:
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_zero_and_special_rows(fq):
     C = 300
     x = normal((7, C), 14, 1.0, FP32)
