@@ -851,10 +851,11 @@ int fp8_quantize_experts(const void *x, int in_dtype, int64_t T, int64_t ld,
  *   dgrad: dx [S, K]    = g w_e          g [S, N] by rows, w transposed
  *   wgrad: dw [E, N, K] = g_e^T x_e      g and x transposed (one pair of
  *                                        offsets: x->offsets are used)
- * Results are dense, of out_dtype, 16-byte aligned.  Rows of y and dx behind the
- * last group are left as they were; dw of an empty group is zero.  Any S; N %
- * 16 == 0, K % 16 == 0, and what fprop and dgrad contract over is not empty.
- * The groups of x (g) may be equal ones.
+ * Results are dense, of out_dtype, 16-byte aligned, and overlap no operand.  Rows
+ * of y and dx behind the last group are left as they were; dw of an empty group
+ * is zero.  Any S; N % 16 == 0, K % 16 == 0; what is contracted over (K, N and
+ * S) is at most 2^27 long and, in fprop and dgrad, not empty.  The groups of x
+ * (g) may be equal ones.
  * Errors: INVALID_ARG (also operands whose sizes or groups do not fit, or
  * without the orientation that is needed), MISALIGNED, ARCH, CUDA. */
 int fp8_experts_fprop(const fp8q_experts *x, const fp8q_experts *w, void *y,

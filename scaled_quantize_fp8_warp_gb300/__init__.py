@@ -713,7 +713,8 @@ def _given(t, shape, dtype, device, stream, what):
     """(tensor, its address) of a dense result of one type: the caller's,
     checked, or a new one."""
     if t is None:
-        t = _new(shape, dtype, device, stream)
+        t = torch.empty(shape, dtype=dtype, device=device) if stream is None else _new(
+            shape, dtype, device, stream)
         return t, t.data_ptr()
     return t, _addr(_like(t, shape, dtype, what))
 
@@ -987,22 +988,30 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
     ldr = ldh = ldy = 0
     if residual is not None:
         pr, ldr = _rows(_like(residual, shape, dtype, "residual"))
-        h, ph, ldh = _out_rows(h, shape, dtype, device, stream, "h")
+        if h is None:
+            h, ph = _given(None, shape, dtype, device, stream, "h")
+            ldh = C
+        else:
+            ph, ldh = _rows(_like(h, shape, dtype, "h"))
     elif h is not None:
         raise ValueError("without a residual h is x")
-    if want_y or y is not None:
-        y, py, ldy = _out_rows(y, shape, dtype, device, stream, "y")
+    if y is not None:
+        py, ldy = _rows(_like(y, shape, dtype, "y"))
+    elif want_y:
+        y, py = _given(None, shape, dtype, device, stream, "y")
+        ldy = C
     if scaling is not None:
-        s_shape = ((C + 127) // 128, T) if scaling == SCALE_TILE_1x128 else (T,)
         q, pq = _given(q, shape, torch.uint8, device, stream, "q")
-        scales, ps = _given(scales, s_shape, torch.float32, device, stream, "scales")
+        scales, ps = _given(scales, ((C + 127) // 128, T) if scaling == SCALE_TILE_1x128 else (T,),
+                            torch.float32, device, stream, "scales")
     elif q is not None or scales is not None:
         raise ValueError("an 8-bit output needs a scaling")
     rstd, pd = _given(rstd, (T,), torch.float32, device, stream, "rstd")
-    _check(lib().fp8_rmsnorm(
+    status = lib().fp8_rmsnorm(
         px, ldx, pr, ldr, _in_dtype(x), pw, w_dtype, ctypes.byref(ctypes.c_float(eps)), T, C, ph,
-        ldh, py, ldy, 0 if scaling is None else scaling, pq, ps, pd, _raw_stream(stream)),
-        "fp8_rmsnorm")
+        ldh, py, ldy, scaling or 0, pq, ps, pd, _raw_stream(stream))
+    if status != OK:
+        raise Fp8qError(status, "fp8_rmsnorm")
     return NormOutput(x if h is None else h, y, q, scales, rstd)
 
 

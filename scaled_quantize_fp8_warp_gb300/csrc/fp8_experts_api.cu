@@ -34,6 +34,9 @@ int check_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t 
 }
 
 constexpr int64_t kMostRows = INT32_MAX - 1024;
+// Longest contraction of a product: a tile of it takes some 0.4 s, a fifth of
+// what a kernel waits for anything.
+constexpr int64_t kMostContract = 1 << 27;
 
 // Blocks of 128 rows; -1 for sizes that are refused.
 int64_t blocks_of(int64_t rows, int64_t groups, bool ragged) {
@@ -106,7 +109,8 @@ int rows_product(const fp8q_experts *x, const fp8q_experts *w, bool dgrad, void 
   if (w->offsets != nullptr || w->groups != x->groups) return FP8Q_ERR_INVALID_ARG;
   const int64_t N = w->rows / w->groups, K = w->cols, S = x->rows;
   const int64_t contract = dgrad ? N : K, result = dgrad ? K : N;
-  if (N % 16 != 0 || x->cols != contract || (contract == 0 && S > 0 && result > 0))
+  if (N % 16 != 0 || x->cols != contract || contract > kMostContract ||
+      (contract == 0 && S > 0 && result > 0))
     return FP8Q_ERR_INVALID_ARG;
   if (S > 0 && result > 0) {
     if (y == nullptr || result > INT64_MAX / 8 / S) return FP8Q_ERR_INVALID_ARG;
@@ -285,7 +289,7 @@ int fp8_experts_wgrad(const fp8q_experts *g, const fp8q_experts *x, void *dw, in
   int rc = check_operand(g, 2);
   if (rc != FP8Q_OK) return rc;
   if ((rc = check_operand(x, 2)) != FP8Q_OK) return rc;
-  if (g->rows != x->rows || g->groups != x->groups || (g->offsets == nullptr) != (x->offsets == nullptr))
+  if (x->rows > kMostContract || g->rows != x->rows || g->groups != x->groups || (g->offsets == nullptr) != (x->offsets == nullptr))
     return FP8Q_ERR_INVALID_ARG;
   const int64_t N = g->cols, K = x->cols, E = x->groups;
   if (N > 0 && K > 0) {

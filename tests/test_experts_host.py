@@ -126,6 +126,10 @@ def test_products_refuse(fq):
         assert call(name, a(), w(rows=4 * 24)) == INVALID                    # N % 16
         assert call(name, a(fmt=9), w()) == INVALID and call(name, a(), w(fmt=-1)) == INVALID
         assert call(name, a(qs=0x10008), w()) == MISALIGNED
+    long = 1 << 28
+    assert call("fp8_experts_fprop", x(rows=16, cols=long, groups=1), w(rows=16, cols=long, groups=1)) == INVALID
+    assert call("fp8_experts_wgrad", g(rows=long, groups=1), x(rows=long, groups=1)) == INVALID
+    assert call("fp8_experts_fprop", x(cols=0), w(cols=0)) == INVALID         # nothing to contract over
     assert call("fp8_experts_fprop", x(), w(q=None, qs=None)) == INVALID
     assert call("fp8_experts_dgrad", g(), w(qt=None, qts=None)) == INVALID
     f = "fp8_experts_wgrad"
