@@ -2,11 +2,20 @@
 // E8M0 scale 2^(floor(log2 amax) - emax), along rows and down the columns of a
 // group, from one read (include/fp8q.h, fp8_quantize_experts).
 //
-// A block of 256 threads casts 128 rows of one group x 128 columns.  A warp
-// has a 32 x 32 piece at a time, four rows x eight columns a thread, so both
-// kinds of blocks of 32 lie inside a warp: maxima along a row are two shuffles
-// away, down a column three.  The transposed bytes and the scales pass through
-// shared memory, to leave as whole lines and atoms.
+// A block of 256 threads casts 128 rows of one group x 128 columns at a time.  A
+// warp has a 32 x 32 piece, four rows x eight columns a thread, so both kinds of
+// blocks of 32 lie inside a warp: maxima along a row are two shuffles away, down
+// a column three.  The transposed bytes and the scales pass through shared
+// memory, to leave as whole lines and atoms.
+//
+// What bounds it: its instructions (950 a warp and 32 x 64 elements in bf16, both
+// orientations; the integer pipe is busy 53% of the time and a third of the warps
+// an SM could hold are there, for want of registers), then HBM.  16384 routed rows
+// of 8192 tokens x 4096 bf16 in 32 groups: 55.8 us both ways (205 MB with each token
+// read once, 272 as the gather reads them: 4.9 TB/s), 35.4 by rows alone; 16384 rows
+// in one group 53.0; fp32 in 128 groups 91.  70 us before the groups were found 32 at a
+// time, the transposed bytes left as lines and the scales were found two at a
+// time.  The next tile's loads ahead of this one's arithmetic: no gain.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
@@ -348,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) cast_kernel(
 template <int FMT, typename T>
 cudaError_t run_cast(const CastArgs &a, bool vec, cudaStream_t stream) {
   // Two tiles a CTA where that leaves the SMs work for some turns: finding the
-  // group and the rows costs every CTA once (16384 rows x 4096 in 32 groups: 54 us,
-  // 56 with one tile, 55 with four; 4096 rows in 64: 25, 26 and 30).
+  // group and the rows costs every CTA once (16384 rows x 4096 in 32 groups, one, two
+  // and four tiles: 56.4, 54.0 and 54.6 us; 4096 rows in 64 groups: 25.6, 25.0 and 30.2).
   const int64_t tiles = (a.cols + 127) / 128;
   const int run = (int)std::min<int64_t>(2, std::max<int64_t>(1, a.blocks * tiles / (4 * sm_count())));
   const int64_t grid = a.blocks * ((tiles + run - 1) / run);

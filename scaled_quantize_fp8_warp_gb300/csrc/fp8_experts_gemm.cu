@@ -1,17 +1,40 @@
-// The products of a layer of experts in MXFP8, C_e = B_e . A_e^T for every
-// group e, on the tensor cores' own block scaling (tcgen05.mma
-// kind::mxf8f6f4): scales go from shared into tensor memory ahead of each K
-// block's MMAs, the whole contraction accumulates in fp32 in tensor memory.
+// The products of a layer of experts in MXFP8, per group e, on the tensor cores'
+// own block scaling (tcgen05.mma kind::mxf8f6f4): scales go from shared into
+// tensor memory ahead of each K block's MMAs, the whole contraction accumulates
+// in fp32 in tensor memory.
 //
-// The side whose row count is known on the host (a weight's output rows, or
-// x's columns for the weights' gradient) is the MMA's M: 256 rows a tile, 128
-// in each CTA of a pair (cta_group::2).  The side whose count the router
-// decided is its N, up to 256 rows a tile and as few as 32: a group of a few
-// rows costs MMAs and loads of 32 rows and not of 256.  The result comes out
-// with a column of C in every lane, so a warp stores 32 neighbouring columns.
+// fprop, dgrad (C = B . A_e^T): a weight's rows are the MMA's M, 256 a tile, 128 in
+// each CTA of a pair (cta_group::2); the group's rows, whose number the router
+// decided, are its N, up to 256 and as few as 32.  So a group of a few rows costs
+// MMAs and loads of 32 rows and not of 256, and groups may start anywhere.  A
+// column of C comes out in every lane; a warp stores 32 neighbouring columns.
+// wgrad (C_e = A_e . B_e^T): both sides are known on the host, the contraction is
+// the group's.  A row of C comes out in every lane and leaves through shared
+// memory by TMA, clipped at the weight's edges.
 //
-// Persistent: each CTA finds from the offsets where every group's tiles start
-// in the numbering of all tiles, and works on every grid-th one.
+// Roles: one warp loads, one (of the even CTA) issues the MMAs, one finds the
+// tiles ahead of both from the offsets, the others take the results out.  A tile's
+// coordinates pass through a ring in shared memory: found by each role for
+// itself they cost some 750 cycles of every tile.  Persistent, every grid-th tile,
+// group after group, so that neighbours read the same weight.
+//
+// What bounds it: shared memory.  A K block of 128 moves 16 KB of A and n / 2 rows of
+// B into each CTA and reads them once in MMAs of 2 n cycles, 256 + n cycles at 128
+// bytes a cycle: 512 for n = 256, where the MMAs take 512 too, 384 for n = 128, where
+// they take 256.  16384 rows in one group, 2048 x 4096: 79 us (3.5 PFLOP/s; MMAs alone
+// 69); in 32 groups of unlike sizes 106 (2.6; loads alone 86, tensor pipe busy 67% of
+// an SM's time there, and 12% of the time is before the first or behind the last
+// tile of an SM); 16384 rows in 128 groups, 1024 x 4096: 98 (its 537 MB of weights at
+// the copy rate: 82).  wgrad of those 32 groups: 147 us, 537 MB of results; with no more
+// than a K block a tile 98 (5.5 TB/s, past what a memset of them takes, 136).
+//
+// Tried: tiles 384 wide (two MMAs a step, five stages): 118 us where 256 take 112, and
+// one token 24.5 for 18.3: fewer bytes of the weight are under way.  A's blocks called
+// into L2 ahead: no gain.  Groups sorted by what a tile of theirs costs: 1% here,
+// more lost elsewhere.  Scales copied a block ahead of their MMAs: 110 for 107.
+// wgrad by places of C_e instead of group by group: 229 for 219, DRAM reads 291 MB
+// for 126.  Arriving at the even CTA's barrier with cluster-scope release: wgrad
+// 219 us for 146.
 #include <cuda.h>
 #include <stdint.h>
 
@@ -421,8 +444,7 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
   } else if (warp == 2 + L::kEpilogueWarps) {
-    // Finds the tiles ahead of the others: in the loading warp alone it took
-    // some 750 cycles of each tile.
+    // finds the tiles ahead of the others
     Tiles<ROWS, WIDE> tiles(p, offsets, first, blockIdx.x / 2, gridDim.x / 2);
     int turn = 0;
     for (int j = 0, ends = 0; ends < L::kTeams; ++j) {

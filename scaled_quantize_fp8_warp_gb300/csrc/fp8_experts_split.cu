@@ -12,6 +12,11 @@
 // third one fits their 112 KB of shared memory, nor any other kernel of this
 // library that allocates tensor memory: an allocation never waits for a CTA
 // that waits for this one's cluster.)
+//
+// What bounds it: latency.  In a graph, each call with other weights so that they
+// come from HBM: 1 row, 1024 x 4096 5.8 us and 4096 x 4096 6.8 (bytes at the measured
+// copy rate 0.6 and 2.5), 32 rows, 2048 x 4096 7.2; the kernel on pairs takes 10.8, 10.6
+// and 10.7.
 #include <cuda.h>
 #include <stdint.h>
 
