@@ -70,7 +70,6 @@ struct __align__(16) Tile {
   int n, valid;            // rows of B: as the MMA takes them (a multiple of 32), and those that count
   int across, along;       // first rows of the tile in the group's parts of A and B
   int64_t c_row;           // ROWS: row of C of the first row of B; else the group
-  int turn;                // tiles of this CTA before it that have a contraction
 };
 
 // ROWS: groups own rows of C, which are B's rows and lie across the lanes
@@ -92,6 +91,11 @@ struct Layout {
   // at once and released (bf16 only: fp32 results would not fit).
   static constexpr int kTeams = kAcc > 1 ? 2 : 1;
   static constexpr int kColumnGroups = kAcc > 1 ? 1 : 2;
+  // Tile j takes accumulator j % kAcc and is announced on barrier j % kFull.  A
+  // barrier is one team's alone and the team waits for each of its phases: a wait
+  // names a phase by its parity, so one that is two phases early passes.
+  static constexpr int kFull = kAcc * kTeams;
+  static_assert(kFull % kTeams == 0 && kTilesAhead % kTeams == 0, "a barrier serves one team");
   static_assert(kAcc > 1 || sizeof(T) == 2, "a tile's results fit in registers");
   static constexpr int kTeamWarps = 4 * kColumnGroups;
   static constexpr int kEpilogueWarps = kTeams * kTeamWarps;
@@ -102,7 +106,7 @@ struct Layout {
   static constexpr int kOutBytes = ROWS ? 0 : kEpilogueWarps * 4096;
   static constexpr int kStages = (208 * 1024 - kOutBytes) / kStageBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kBarBytes = 8 * (2 * kStages + 2 * kAcc + 2 * kTilesAhead + 2) / 16 * 16;
+  static constexpr int kBarBytes = 8 * (2 * kStages + kFull + kAcc + 2 * kTilesAhead + 2) / 16 * 16;
   // the groups' offsets, and the first tile of each
   static constexpr int kGroupBytes = 2 * (FP8Q_EXPERTS_MAX + 1) * 4;
   static constexpr int kSmemBytes =
@@ -291,7 +295,7 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
   const uint32_t ring = (raw + 1023u) & ~1023u;
   const uint32_t bars = ring + L::kRingBytes + L::kOutBytes;
   const uint32_t full0 = bars, empty0 = bars + 8 * kStages;
-  const uint32_t accf0 = bars + 8 * (2 * kStages), acce0 = accf0 + 8 * L::kAcc;
+  const uint32_t accf0 = bars + 8 * (2 * kStages), acce0 = accf0 + 8 * L::kFull;
   const uint32_t tilef0 = acce0 + 8 * L::kAcc, tilee0 = tilef0 + 8 * kTilesAhead;
   const uint32_t drain = tilee0 + 8 * kTilesAhead;
   const uint32_t slot = bars + L::kBarBytes;
@@ -309,10 +313,8 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
-    for (int i = 0; i < L::kAcc; ++i) {
-      mbar_init(accf0 + 8 * i, 1);
-      mbar_init(acce0 + 8 * i, 2 * L::kTeamWarps);
-    }
+    for (int i = 0; i < L::kFull; ++i) mbar_init(accf0 + 8 * i, 1);
+    for (int i = 0; i < L::kAcc; ++i) mbar_init(acce0 + 8 * i, 2 * L::kTeamWarps);
     for (int i = 0; i < kTilesAhead; ++i) {   // read by the loading warp, in the even CTA the
       mbar_init(tilef0 + 8 * i, 1);           // issuing one, and a team of the epilogue
       mbar_init(tilee0 + 8 * i, (rank == 0 ? 2 : 1) + L::kTeamWarps);
@@ -413,12 +415,17 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
     bool ok = true;
     Tile t;
     for (int j = 0; ok && take_tile(j, true, t); ++j) {
-      if (t.num_k == 0) continue;   // zeros, which the epilogue writes
       const uint32_t idesc = idesc_mxf8f6f4((uint32_t)p.a_format, (uint32_t)p.b_format, 256,
                                             (uint32_t)t.n, 0, 0);
-      const uint32_t acc = (uint32_t)t.turn % L::kAcc, turn = ((uint32_t)t.turn / L::kAcc) & 1u;
+      const uint32_t acc = (uint32_t)j % L::kAcc, turn = ((uint32_t)j / L::kAcc) & 1u;
+      const uint32_t accf = accf0 + 8 * ((uint32_t)j % L::kFull);
       if (!wait_bounded_all(acce0 + 8 * acc, turn ^ 1u, abort_flag, err)) break;
       tc_fence_after();
+      // an empty group's tile takes its turn too; the epilogue writes zeros
+      if (t.num_k == 0) {
+        if (elect_one()) mma_commit_pair_multicast(accf, kBoth);
+        __syncwarp();
+      }
       for (int kb = 0; kb < t.num_k; ++kb, ++it) {
         const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
         if (!wait_bounded_all(full0 + 8 * s, ph, abort_flag, err)) {
@@ -430,7 +437,7 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
           issue_block<L>(ring + s * L::kStageBytes, tmem_base + WIDE * acc,
                          tmem_base + WIDE * L::kAcc + L::kSfCols * s, idesc, t.n > 128, kb == 0);
           mma_commit_pair_multicast(empty0 + 8 * s, kBoth);
-          if (kb == t.num_k - 1) mma_commit_pair_multicast(accf0 + 8 * acc, kBoth);
+          if (kb == t.num_k - 1) mma_commit_pair_multicast(accf, kBoth);
         }
         __syncwarp();
       }
@@ -446,13 +453,9 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
   } else if (warp == 2 + L::kEpilogueWarps) {
     // finds the tiles ahead of the others
     Tiles<ROWS, WIDE> tiles(p, offsets, first, blockIdx.x / 2, gridDim.x / 2);
-    int turn = 0;
     for (int j = 0, ends = 0; ends < L::kTeams; ++j) {
       Tile t;
-      if (ends == 0 && tiles.next(t)) {
-        t.turn = turn;
-        turn += t.num_k > 0;
-      } else {
+      if (ends > 0 || !tiles.next(t)) {
         t.valid = 0;   // behind the last tile: one for each team
         ++ends;
       }
@@ -475,14 +478,13 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
     const auto chunk_at = [&](int c) { return 32 * (ROWS ? L::kColumnGroups * c + h : L::kChunks * h + c); };
     Tile t;
     for (int j = team; take_tile(j, true, t); j += L::kTeams) {
-      const uint32_t acc = (uint32_t)t.turn % L::kAcc;
+      const uint32_t acc = (uint32_t)j % L::kAcc;
       const uint32_t from = tmem_base + ((uint32_t)(quarter * 32) << 16) + WIDE * acc;
-      if (t.num_k > 0) {
-        if (!wait_bounded_warp(accf0 + 8 * acc, ((uint32_t)t.turn / L::kAcc) & 1u, abort_flag, err)) break;
-        tc_fence_after();
-      }
+      if (!wait_bounded_warp(accf0 + 8 * ((uint32_t)j % L::kFull), ((uint32_t)j / L::kFull) & 1u,
+                             abort_flag, err))
+        break;
+      tc_fence_after();
       const auto release = [&] {   // the accumulator is free for another tile
-        if (t.num_k == 0) return;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -499,6 +501,9 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
       const auto load = [&](Chunk<T> *to, int c) {
         uint32_t x[kPiece][32];
         if (t.num_k > 0) {
+          // a store before this one left lanes behind (those past the columns, the
+          // one that issues TMA stores), and tcgen05.ld is the whole warp's
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < kPiece; ++k)
             if (chunk_at(c + k) < t.valid) tmem_ld_32x32b_x32(from + chunk_at(c + k), x[k]);

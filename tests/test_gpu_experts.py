@@ -270,6 +270,62 @@ def test_wgrad(fq, sizes, spare, N, K, out):
             assert (dw[e] == 0).all()
 
 
+EMPTY = ["1010011010", "0101", "1000001000001", "111000", "1" + "0" * 30 + "11", "01" * 16, "0011" * 8, "100" * 11]
+
+
+@pytest.mark.parametrize("present", EMPTY)
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_wgrad_with_empty_groups_between(fq, present, out):
+    """As many tiles a group as CTA pairs run at once: every pair meets every
+    group, those with no rows in any order with the others, time after time."""
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    N, K = 16, (128 if out == FP32 else 256) * pairs
+    sizes = [int(c) * (1 + 37 * i % 150) for i, c in enumerate(present)]
+    g, x = normal((sum(sizes), N), 40, 0.1), normal((sum(sizes), K), 41)
+    gop, groups = operand(fq, g, sizes, 3, 1, by_rows=False)
+    xop, _ = operand(fq, x, sizes, 3, 0, by_rows=False)
+    dw = torch.full((len(sizes), N, K), 5.0, dtype=out, device="cuda")
+    first = fq.fp8_experts_wgrad(gop, xop, out=dw).clone()
+    torch.cuda.synchronize()
+    assert fq.device_status() == fq.OK
+    for (e, a, z, _), gv, xv in zip(groups, ref.group_cols(arrays(gop), groups, 1),
+                                    ref.group_cols(arrays(xop), groups, 0)):
+        if z > a:
+            near(first[e], gv, xv, e)
+        else:
+            assert (first[e] == 0).all()
+    for _ in range(20):
+        dw.fill_(5.0)
+        assert torch.equal(fq.fp8_experts_wgrad(gop, xop, out=dw), first)
+
+
+@pytest.mark.parametrize("E,N,K,seed", [(1024, 16, 48, 42), (128, 112, 1600, 43), (83, 272, 528, 44),
+                                        (31, 1040, 272, 45)])
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_wgrad_of_many_groups_many_empty(fq, E, N, K, seed, out):
+    r = np.random.default_rng(seed)
+    sizes = (r.integers(0, 2, E) * r.integers(1, 40, E)).tolist()
+    g, x = normal((sum(sizes), N), seed, 0.1), normal((sum(sizes), K), seed + 100)
+    gop, groups = operand(fq, g, sizes, 0, 1, by_rows=False)
+    xop, _ = operand(fq, x, sizes, 0, 0, by_rows=False)
+    dw = fq.fp8_experts_wgrad(gop, xop, out=torch.full((E, N, K), 5.0, dtype=out, device="cuda"))
+    torch.cuda.synchronize()
+    assert fq.device_status() == fq.OK
+    for (e, a, z, _), gv, xv in zip(groups, ref.group_cols(arrays(gop), groups, 1),
+                                    ref.group_cols(arrays(xop), groups, 0)):
+        if z > a:
+            near(dw[e], gv, xv, e)
+        else:
+            assert (dw[e] == 0).all()
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("sizes", [[130, 0, 300, 5, 0, 60], [20] * 6])
+def test_rows_products_of_many_tiles(fq, sizes, out):
+    """Five tiles and more for every CTA pair, tiles of 128 and 256 rows."""
+    check_rows_product(fq, sizes, 2, 16384, 48, out, False)
+
+
 def test_equal_groups_of_tokens(fq):
     """x in equal groups, as experts of fixed capacity have: the same as offsets that say so."""
     x, w, g = normal((3 * 70, 96), 16), normal((3 * 64, 96), 17), normal((3 * 70, 64), 18)
