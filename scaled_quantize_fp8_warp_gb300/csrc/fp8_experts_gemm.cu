@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
       if (!wait_bounded_all(acce0 + 8 * acc, turn ^ 1u, abort_flag, err)) break;
       tc_fence_after();
       // an empty group's tile takes its turn too; the epilogue writes zeros
-      if (t.num_k == 0) {
+      if (!ROWS && t.num_k == 0) {
         if (elect_one()) mma_commit_pair_multicast(accf, kBoth);
         __syncwarp();
       }
@@ -500,10 +500,10 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
       Chunk<T> r[L::kAcc > 1 ? kPiece : L::kChunks];
       const auto load = [&](Chunk<T> *to, int c) {
         uint32_t x[kPiece][32];
-        if (t.num_k > 0) {
-          // a store before this one left lanes behind (those past the columns, the
-          // one that issues TMA stores), and tcgen05.ld is the whole warp's
-          __syncwarp();
+        if (ROWS || t.num_k > 0) {
+          // a piece's store leaves lanes behind (those past the columns, the one that
+          // issues TMA stores), and tcgen05.ld is the whole warp's
+          if (L::kAcc > 1) __syncwarp();
 #pragma unroll
           for (int k = 0; k < kPiece; ++k)
             if (chunk_at(c + k) < t.valid) tmem_ld_32x32b_x32(from + chunk_at(c + k), x[k]);
