@@ -719,6 +719,15 @@ def _given(t, shape, dtype, device, stream, what):
     return t, _addr(_like(t, shape, dtype, what))
 
 
+def _here(*tensors):
+    """Refuses tensors of another device than the current one, on which a call
+    runs (CUDA tensors or None)."""
+    device = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("fp8q needs tensors on the current device")
+
+
 def fp4_scale_bytes(kind: int, rows: int, K: int) -> int:
     """Bytes of the scale atoms of an [rows, K] 4-bit operand."""
     return (rows + 127) // 128 * ((K + 127) // 128 if kind == MXFP4 else (K + 63) // 64) * 512
@@ -979,7 +988,8 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
     1x128 tile scales or row scales (``scaling`` None: no 8-bit output).  x,
     residual, h and y are [T, C] of one type and their rows may lie apart;
     weight is bf16 or fp32.  ``want_y`` (or a given ``y``) asks for y beside
-    its 8-bit form.  h may be x or residual itself."""
+    its 8-bit form.  h may be x or residual itself; no other result overlaps an
+    input."""
     px, ldx = _rows(x)
     T, C = shape = x.shape
     dtype, device = x.dtype, x.device
@@ -1007,6 +1017,7 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
     elif q is not None or scales is not None:
         raise ValueError("an 8-bit output needs a scaling")
     rstd, pd = _given(rstd, (T,), torch.float32, device, stream, "rstd")
+    _here(x, weight, residual, h, y, q, scales, rstd)
     status = lib().fp8_rmsnorm(
         px, ldx, pr, ldr, _in_dtype(x), pw, w_dtype, ctypes.byref(ctypes.c_float(eps)), T, C, ph,
         ldh, py, ldy, scaling or 0, pq, ps, pd, _raw_stream(stream))
@@ -1036,6 +1047,7 @@ def fp8_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
         if workspace is None:
             workspace = _new((lib().fp8q_rmsnorm_backward_workspace_size(T, C),), torch.uint8, device,
                              stream)
+    _here(dy, h, weight, rstd, dresidual, dx, dweight, workspace)
     _check(lib().fp8_rmsnorm_backward(
         pd, ldd, ph, ldh, _in_dtype(dy), pw, w_dtype, ps, pr, ldr, T, C, px, ldx, pdw,
         _addr(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(stream)),
@@ -1097,6 +1109,10 @@ class ExpertsOperand:
         self.struct = _ExpertsStruct(_addr(q), _addr(q_scales), _addr(q_t), _addr(qt_scales),
                                      _addr(offsets), rows, cols, groups, fmt)
 
+    def tensors(self):
+        """What the operand holds, None for what it lacks."""
+        return self.q, self.q_scales, self.q_t, self.qt_scales, self.offsets
+
     @classmethod
     def empty(cls, rows: int, cols: int, groups: int, device, fmt: int = E4M3, offsets=None,
               by_rows=True, transposed=False, stream=None):
@@ -1139,6 +1155,7 @@ def fp8_quantize_experts(x: torch.Tensor, groups: int, offsets: torch.Tensor | N
         st = _ExpertsStruct(st.q if rows else None, st.q_scales if rows else None,
                             st.q_t if cols else None, st.qt_scales if cols else None, st.offsets,
                             S, C, groups, fmt)
+    _here(x, index, *out.tensors())
     _check(lib().fp8_quantize_experts(p, _in_dtype(x), T, ld, _addr(index), ctypes.byref(st),
                                       _raw_stream(stream)), "fp8_quantize_experts")
     return out
@@ -1150,6 +1167,7 @@ def _experts_rows(name, x, w, shape, out_dtype, out, stream):
         raise ValueError("an operand without bytes")
     device = held.device
     out, po, dt = _out(out, shape, out_dtype, device, stream)
+    _here(out, *x.tensors(), *w.tensors())
     _check(getattr(lib(), name)(ctypes.byref(x.struct), ctypes.byref(w.struct), po, dt,
                                 _raw_stream(stream)), name)
     return out

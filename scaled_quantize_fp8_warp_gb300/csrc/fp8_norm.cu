@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(Shape<RT, CHUNKS>::kThreads, Shape<RT, CHUNKS>
     backward_kernel(const BackwardArgs p) {
   using S = Shape<RT, CHUNKS>;
   __shared__ float slots[S::kRows][2][RT / 32];
-  __shared__ float join[S::kRows > 1 ? S::kRows : 1][S::kRows > 1 ? S::kColumns : 1];
+  __shared__ __align__(16) float join[S::kRows > 1 ? S::kRows : 1][S::kRows > 1 ? S::kColumns : 1];
   Reduce<RT> reduce{slots[threadIdx.x / RT]};
   const int t = threadIdx.x % RT, mine = threadIdx.x / RT;
   const int64_t step = (int64_t)gridDim.x * S::kRows;

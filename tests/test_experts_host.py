@@ -180,6 +180,20 @@ def test_random_arguments_get_a_status_not_a_crash(fq):
     assert {(k, 6) for k in range(3)} <= seen   # some passed every check
 
 
+def test_only_the_current_device_serves(fq, monkeypatch):
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 2, raising=False)
+    fq._here(On(2), None, On(2))
+    for bad in ((On(0),), (On(2), None, On(1))):
+        with pytest.raises(ValueError):
+            fq._here(*bad)
+
+
 def test_struct_layout_matches_header(fq, tmp_path):
     import os
     import subprocess

@@ -83,3 +83,21 @@ def test_a_captured_step_follows_its_inputs(ex):
         kept = [t.clone() for t in got]
         for a, b in zip(kept, step()):
             assert torch.equal(a, b)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """With another device current, as the calls see it, nothing is launched."""
+    import scaled_quantize_fp8_warp_gb300 as fq
+    x, w = torch.randn(64, 64, device="cuda").bfloat16(), torch.ones(64, device="cuda")
+    op, wop = (fq.fp8_quantize_experts(x, 2, rows=True, cols=True) for _ in range(2))
+    rstd = fq.fp8_rmsnorm(x, w).rstd
+    out, y, narrow = (torch.full(s, 7.0, device="cuda") for s in ((2, 64, 64), (64, 64), (64, 32)))
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for f in (lambda: fq.fp8_rmsnorm(x, w, y=y.bfloat16()), lambda: fq.fp8_rmsnorm_backward(x, x, w, rstd),
+              lambda: fq.fp8_quantize_experts(x, 2, cols=True), lambda: fq.fp8_experts_fprop(op, wop, out=narrow),
+              lambda: fq.fp8_experts_dgrad(op, wop, out=y), lambda: fq.fp8_experts_wgrad(op, op, out=out)):
+        with pytest.raises(ValueError, match="current device"):
+            f()
+    monkeypatch.undo()
+    assert all((t == 7.0).all() for t in (out, y, narrow)) and fq.device_status() == fq.OK
