@@ -101,16 +101,19 @@ struct Layout {
   static constexpr int kEpilogueWarps = kTeams * kTeamWarps;
   static constexpr int kChunks = WIDE / 32 / kColumnGroups;
   static constexpr int kThreads = 32 * (3 + kEpilogueWarps);
-  // Results along the lanes leave through shared memory, 32 rows x 128 bytes a
-  // warp at a time.
-  static constexpr int kOutBytes = ROWS ? 0 : kEpilogueWarps * 4096;
-  static constexpr int kStages = (208 * 1024 - kOutBytes) / kStageBytes;
+  // Results along the lanes leave through shared memory, a chunk of 32 x 32 a warp
+  // at a time: what staging takes, the ring lacks (wgrad.  Bf16, six stages as here:
+  // 64 groups of 64 rows, 1024 x 2048 53.3 us, 16384 rows in 8, 2048 x 4096 93.4; 32 x 64
+  // a warp and five stages 58.7 and 95.8; two places a warp and four 58.0 and 101.6).
+  static constexpr int kPieceBytes = 1024 * (int)sizeof(T);
+  static constexpr int kOutBytes = ROWS ? 0 : kEpilogueWarps * kPieceBytes;
+  // the groups' offsets, and the first tile of each where it depends on them
+  static constexpr int kGroupBytes = (ROWS ? 2 : 1) * (FP8Q_EXPERTS_MAX + 1) * 4;
+  static constexpr int kOtherBytes = 16 + kTilesAhead * (int)sizeof(Tile) + kGroupBytes + 1024;
+  static constexpr int kStages = (227 * 1024 - 512 - kOtherBytes - kOutBytes) / kStageBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kBarBytes = 8 * (2 * kStages + kFull + kAcc + 2 * kTilesAhead + 2) / 16 * 16;
-  // the groups' offsets, and the first tile of each
-  static constexpr int kGroupBytes = 2 * (FP8Q_EXPERTS_MAX + 1) * 4;
-  static constexpr int kSmemBytes =
-      kRingBytes + kOutBytes + kBarBytes + 16 + kTilesAhead * (int)sizeof(Tile) + kGroupBytes + 1024;
+  static constexpr int kSmemBytes = kRingBytes + kOutBytes + kBarBytes + kOtherBytes;
   static_assert(kSmemBytes <= 227 * 1024, "the ring fits in shared memory");
   static_assert(WIDE * kAcc + kSfCols * kStages <= kTmemCols, "scale slots fit in tensor memory");
 };
@@ -120,15 +123,15 @@ template <int WIDE>
 __device__ __forceinline__ int tiles_along(int rows) { return (rows + WIDE - 1) / WIDE; }
 __device__ __forceinline__ int tiles_across(const ProductArgs &p) { return (p.a_rows + 255) / 256; }
 
-// Where every group's tiles start in the numbering of all, by one warp.
-template <bool ROWS, int WIDE>
+// Where every group's tiles start in the numbering of all, by one warp (ROWS).
+template <int WIDE>
 __device__ __forceinline__ void number_tiles(const ProductArgs &p, const int32_t *offsets, int *first) {
   const int lane = threadIdx.x & 31, E = p.groups.count;
   long long done = 0;
   for (int e0 = 0; e0 < E; e0 += 32) {
     long long n = 0;
     if (e0 + lane < E)
-      n = (long long)tiles_along<WIDE>(ROWS ? group_rows(p.groups, offsets, e0 + lane).y : p.b_rows) * tiles_across(p);
+      n = (long long)tiles_along<WIDE>(group_rows(p.groups, offsets, e0 + lane).y) * tiles_across(p);
     long long sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -155,18 +158,25 @@ struct Tiles {
   __device__ __forceinline__ Tiles(const ProductArgs &args, const int32_t *group_offsets,
                                    const int *first_tiles, int pair, int pairs)
       : p(args), offsets(group_offsets), first(first_tiles), u(pair), step(pairs) {}
+  __device__ __forceinline__ int first_of(int group) const {
+    return ROWS ? first[group] : group * (tiles_along<WIDE>(p.b_rows) * tiles_across(p));
+  }
   __device__ __forceinline__ bool next(Tile &t) {
-    if (u >= first[p.groups.count]) return false;
-    if (e < 0 || u >= first[e + 1]) {
-      int lo = e + 1, hi = p.groups.count;   // first[lo] <= u < first[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (first[mid] <= u)
-          lo = mid;
-        else
-          hi = mid;
+    if (u >= first_of(p.groups.count)) return false;
+    if (e < 0 || u >= first_of(e + 1)) {
+      if (ROWS) {
+        int lo = e + 1, hi = p.groups.count;   // first[lo] <= u < first[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (first[mid] <= u)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        e = lo;
+      } else {
+        e = u / first_of(1);
       }
-      e = lo;
       const int2 group = group_rows(p.groups, offsets, e);
       row = group.x;
       rows = group.y;
@@ -177,7 +187,7 @@ struct Tiles {
       more = blocks - each * along;
     }
     int bt, at;
-    gemm::tile_coords(u - first[e], along, tiles_across(p), bt, at, kRaster, 0);
+    gemm::tile_coords(u - first_of(e), along, tiles_across(p), bt, at, kRaster, 0);
     const int b0 = bt * each + min(bt, more), b1 = b0 + each + (bt < more);
     t.across = at * 256;
     t.along = b0 * 128;
@@ -250,12 +260,11 @@ struct Chunk {
 #pragma unroll
     for (int j = 0; j < kRegs; ++j) r[j] = 0u;
   }
-  // Into 128 bytes of this lane's row at `row`, a multiple of 128, from chunk
-  // of 16 bytes c0 on, as 128-byte swizzling has them.
-  __device__ __forceinline__ void stage(uint32_t row, int c0) const {
+  // Into this lane's row of 64 or 128 bytes, as swizzling of that width has them.
+  __device__ __forceinline__ void stage(uint32_t row) const {
 #pragma unroll
     for (int c = 0; c < kRegs / 4; ++c)
-      st_shared_16(row + (((uint32_t)(c0 + c) << 4) ^ (row >> 3 & 0x70u)), r[4 * c], r[4 * c + 1],
+      st_shared_16(row + (((uint32_t)c << 4) ^ (row >> 3 & 4u * kRegs - 16u)), r[4 * c], r[4 * c + 1],
                    r[4 * c + 2], r[4 * c + 3]);
   }
   // Into column m of C from row c_row on, `count` rows of it; lanes hold
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(slot_ptr);
   cluster_wait_any();   // the peer runs: its shared memory may be written
   if (warp == 1 && lane == 0) st_shared_cluster_u32(mapa_shared(slot + 8, rank ^ 1u), tmem_base);
-  if (warp == 2) number_tiles<ROWS, WIDE>(p, offsets, first);
+  if (ROWS && warp == 2) number_tiles<WIDE>(p, offsets, first);
   __syncthreads();
   cluster_sync_any();
   // One allocation serves the pair: both CTAs must hold the same address.
@@ -473,7 +482,7 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
     const int team = (warp - 2) / L::kTeamWarps;
     const int quarter = warp & 3, h = (warp - 2) % L::kTeamWarps >> 2;
     const uint32_t acce_even = mapa_shared(acce0, 0);
-    const uint32_t out = ring + L::kRingBytes + (warp - 2) * 4096;
+    const uint32_t out = ring + L::kRingBytes + (warp - 2) * L::kPieceBytes;
     // chunks alternate between warps (ROWS: few rows are shared by all) or follow one another
     const auto chunk_at = [&](int c) { return 32 * (ROWS ? L::kColumnGroups * c + h : L::kChunks * h + c); };
     Tile t;
@@ -495,7 +504,7 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
         }
       };
       const int m = t.across + (int)rank * 128 + quarter * 32;   // first row of the group's A
-      // kPiece chunks: ROWS: as many as are loaded at once; else 128 bytes of a row
+      // kPiece chunks are loaded at once
       constexpr int kPiece = ROWS ? 2 : 4 / (int)sizeof(T);
       Chunk<T> r[L::kAcc > 1 ? kPiece : L::kChunks];
       const auto load = [&](Chunk<T> *to, int c) {
@@ -525,17 +534,19 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
                                  t.valid - n0);
           }
         } else {
-          const int n0 = chunk_at(c);
-          if (n0 >= t.valid || m >= p.a_rows) return;
-          if (lane == 0) bulk_wait_read();   // the piece before has left
-          __syncwarp();
 #pragma unroll
-          for (int k = 0; k < kPiece; ++k) of[k].stage(out + lane * 128, k * 8 / kPiece);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {   // rows and columns past the weight are not written
-            tma_store_3d(&maps.c, out, t.along + n0, m, (int)t.c_row);
-            bulk_commit();
+          for (int k = 0; k < kPiece; ++k) {
+            const int n0 = chunk_at(c + k);
+            if (n0 >= t.valid || m >= p.a_rows) return;
+            if (lane == 0) bulk_wait_read();   // the piece before has left
+            __syncwarp();
+            of[k].stage(out + lane * (32 * sizeof(T)));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {   // rows and columns past the weight are not written
+              tma_store_3d(&maps.c, out, t.along + n0, m, (int)t.c_row);
+              bulk_commit();
+            }
           }
         }
       };
@@ -578,7 +589,7 @@ int run_product(const ProductArgs &a, int64_t a_atoms, int64_t b_atoms, cudaStre
   if (!ROWS)
     ok = ok && make_tmap_3d(&maps.c, a.C, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                             (uint64_t)a.b_rows, (uint64_t)a.a_rows, (uint64_t)a.groups.count, a.b_rows * size,
-                            a.a_rows * (a.b_rows * size), 128 / sizeof(T), 32, CU_TENSOR_MAP_SWIZZLE_128B);
+                            a.a_rows * (a.b_rows * size), 32, 32, sizeof(T) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return FP8Q_ERR_CUDA;
   // the most tiles that the groups can make
   const int64_t along = ROWS ? std::min<int64_t>(a.groups.rows, a.groups.rows / WIDE + a.groups.count)
