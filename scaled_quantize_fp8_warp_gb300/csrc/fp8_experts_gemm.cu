@@ -25,7 +25,7 @@
 // 69); in 32 groups of unlike sizes 106 (2.6; loads alone 86, tensor pipe busy 67% of
 // an SM's time there, and 12% of the time is before the first or behind the last
 // tile of an SM); 16384 rows in 128 groups, 1024 x 4096: 98 (its 537 MB of weights at
-// the copy rate: 82).  wgrad of those 32 groups: 147 us, 537 MB of results; with no more
+// the copy rate: 82).  wgrad of those 32 groups: 148 us, 537 MB of results; with no more
 // than a K block a tile 98 (5.5 TB/s, past what a memset of them takes, 136).
 //
 // Tried: tiles 384 wide (two MMAs a step, five stages): 118 us where 256 take 112, and
@@ -33,7 +33,8 @@
 // into L2 ahead: no gain.  Groups sorted by what a tile of theirs costs: 1% here,
 // more lost elsewhere.  Scales copied a block ahead of their MMAs: 110 for 107.
 // wgrad by places of C_e instead of group by group: 229 for 219, DRAM reads 291 MB
-// for 126.  Arriving at the even CTA's barrier with cluster-scope release: wgrad
+// for 126.  Tiles of wgrad 128 wide with three accumulators: 161.  kRaster of 4 or
+// 16: level.  Arriving at the even CTA's barrier with cluster-scope release: wgrad
 // 219 us for 146.
 #include <cuda.h>
 #include <stdint.h>
