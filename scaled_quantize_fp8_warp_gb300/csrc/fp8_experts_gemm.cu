@@ -45,6 +45,7 @@
 #include "fp4_ptx.cuh"
 #include "fp8_experts.h"
 #include "fp8_experts_maps.h"
+#include "fp8_experts_turns.h"
 #include "fp8_pack8.cuh"
 #include "fp8q_gemm_common.cuh"
 
@@ -424,12 +425,14 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     Tile t;
-    for (int j = 0; ok && take_tile(j, true, t); ++j) {
+    int j = 0;
+    for (; ok && take_tile(j, true, t); ++j) {
       const uint32_t idesc = idesc_mxf8f6f4((uint32_t)p.a_format, (uint32_t)p.b_format, 256,
                                             (uint32_t)t.n, 0, 0);
-      const uint32_t acc = (uint32_t)j % L::kAcc, turn = ((uint32_t)j / L::kAcc) & 1u;
+      const uint32_t acc = accumulator_of<L::kAcc>(j), turn = turn_of<L::kAcc>(j);
       const uint32_t accf = accf0 + 8 * ((uint32_t)j % L::kFull);
-      if (!wait_bounded_all(acce0 + 8 * acc, turn ^ 1u, abort_flag, err)) break;
+      ok = wait_bounded_all(acce0 + 8 * acc, (turn & 1u) ^ 1u, abort_flag, err);
+      if (!ok) break;
       tc_fence_after();
       // an empty group's tile takes its turn too; the epilogue writes zeros
       if (!ROWS && t.num_k == 0) {
@@ -452,6 +455,13 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
         __syncwarp();
       }
     }
+    // The odd CTA's last releases land in this CTA's shared memory, and the barrier
+    // at the end orders none of them: they are waited for here.  They were sent
+    // before the last results' stores, so this waits for no store.
+    if (ok)
+      settle<L::kAcc>((uint32_t)j, [&](uint32_t a, uint32_t turn) {
+        return wait_bounded_all(acce0 + 8 * a, turn & 1u, abort_flag, err);
+      });
     if (elect_one()) {
       mma_commit_pair(drain);
       const uint64_t t0 = globaltimer_ns();
@@ -488,7 +498,7 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
     const auto chunk_at = [&](int c) { return 32 * (ROWS ? L::kColumnGroups * c + h : L::kChunks * h + c); };
     Tile t;
     for (int j = team; take_tile(j, true, t); j += L::kTeams) {
-      const uint32_t acc = (uint32_t)j % L::kAcc;
+      const uint32_t acc = accumulator_of<L::kAcc>(j);
       const uint32_t from = tmem_base + ((uint32_t)(quarter * 32) << 16) + WIDE * acc;
       if (!wait_bounded_warp(accf0 + 8 * ((uint32_t)j % L::kFull), ((uint32_t)j / L::kFull) & 1u,
                              abort_flag, err))
@@ -573,7 +583,10 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_arrive_any();
-  cluster_wait_any();  // neither CTA leaves while the other may still signal it
+  // Neither CTA leaves while the other may still signal it: what was sent has been
+  // waited for on its barrier (copies and commits by the loading warp and the
+  // epilogue, releases by the issuing warp), this one counts CTAs only.
+  cluster_wait_any();
   tc_fence_after();
   __syncwarp();
   if (warp == 1) tmem_dealloc_pair(tmem_base, L::kTmemCols);

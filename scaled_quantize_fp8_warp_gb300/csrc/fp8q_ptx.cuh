@@ -157,7 +157,9 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 // The same where the arrival passes no memory on, only the end of this
 // thread's reads of tensor memory (ordered by tc_fence_before): release at
 // cluster scope waits for the thread's stores to global memory, some 2400
-// cycles in an epilogue that had just stored a tile.
+// cycles in an epilogue that had just stored a tile.  Nor does a relaxed barrier
+// of the cluster wait for the arrival: the CTA that owns `addr` has to see its
+// phase end before it may leave.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
