@@ -818,7 +818,8 @@ int fp8_rmsnorm_backward(const void *dy, int64_t lddy, const void *h,
  * most INT32_MAX - 1024, and there are at most INT32_MAX scale atoms. */
 #define FP8Q_EXPERTS_MAX 1024
 typedef struct fp8q_experts {
-  const uint8_t *q, *q_scales;    /* either pair may be NULL */
+  const uint8_t *q, *q_scales;    /* either pair may be NULL; without rows or
+                                   * columns any of the four */
   const uint8_t *q_t, *qt_scales;
   const int32_t *offsets;         /* NULL: equal groups */
   int64_t rows, cols;             /* S, C */
@@ -836,9 +837,10 @@ size_t fp8q_experts_scale_bytes(int64_t rows, int64_t cols, int groups,
 /* Casts rows of x [T, cols] (device, in_dtype, rows ld elements apart, aligned
  * to its type) into the pairs of `out` that are not NULL, from one read: row r
  * of the operand is row index[r] of x (device int32 [out->rows]; one token
- * goes to several experts), or row r where index is NULL (T == out->rows).  An
- * index outside [0, T) stands for a row of zeros.  Indexes of rows that belong
- * to nobody are not read.
+ * goes to several experts), or row r where index is NULL (T == out->rows; for an
+ * operand without rows an index may be NULL whatever T).  An index outside
+ * [0, T) stands for a row of zeros.  Indexes of rows that belong to nobody are
+ * not read.
  * Errors: INVALID_ARG, MISALIGNED, ARCH, CUDA. */
 int fp8_quantize_experts(const void *x, int in_dtype, int64_t T, int64_t ld,
                          const int32_t *index, const fp8q_experts *out,

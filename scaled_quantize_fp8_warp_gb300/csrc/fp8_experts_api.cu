@@ -59,10 +59,11 @@ int check_operand(const fp8q_experts *op, int need) {
   if (op == nullptr || (op->format != FP8Q_E4M3 && op->format != FP8Q_E5M2)) return FP8Q_ERR_INVALID_ARG;
   const int64_t atoms = atoms_of(op->rows, op->cols, op->groups, op->offsets != nullptr);
   if (atoms < 0) return FP8Q_ERR_INVALID_ARG;
-  if ((op->q == nullptr) != (op->q_scales == nullptr) || (op->q_t == nullptr) != (op->qt_scales == nullptr))
-    return FP8Q_ERR_INVALID_ARG;
+  // without rows or columns nothing is read or written through a pointer, and what
+  // holds nothing may have any address: q of no rows is null beside scales that are not
   if (op->rows > 0 && op->cols > 0 &&
-      (((need & 1) && op->q == nullptr) || ((need & 2) && op->q_t == nullptr)))
+      ((op->q == nullptr) != (op->q_scales == nullptr) || (op->q_t == nullptr) != (op->qt_scales == nullptr) ||
+       ((need & 1) && op->q == nullptr) || ((need & 2) && op->q_t == nullptr)))
     return FP8Q_ERR_INVALID_ARG;
   if (!aligned(op->offsets, 4) || !aligned(op->q, 16) || !aligned(op->q_scales, 16) ||
       !aligned(op->q_t, 16) || !aligned(op->qt_scales, 16))
@@ -250,7 +251,9 @@ int fp8_quantize_experts(const void *x, int in_dtype, int64_t T, int64_t ld, con
   int rc = check_operand(out, 0);
   if (rc != FP8Q_OK) return rc;
   const bool empty = out->rows == 0 || out->cols == 0;
-  if ((!empty && out->q == nullptr && out->q_t == nullptr) || (index == nullptr && T != out->rows))
+  // an index of no rows may be null
+  if ((!empty && out->q == nullptr && out->q_t == nullptr) ||
+      (index == nullptr && out->rows > 0 && T != out->rows))
     return FP8Q_ERR_INVALID_ARG;
   if ((rc = check_matrix(x, T, out->cols, ld, dtype_size(in_dtype))) != FP8Q_OK) return rc;
   if (!aligned(index, 4)) return FP8Q_ERR_MISALIGNED;

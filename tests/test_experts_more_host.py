@@ -1,0 +1,51 @@
+"""Arguments of the norm's and the experts' entry points at their edges, without a
+GPU: what holds nothing may have any address."""
+import ctypes
+
+import pytest
+import torch
+
+from test_experts_host import A, INVALID, fq, struct  # noqa: F401
+
+PASSED = (0, 3, 6)   # done, or stopped for want of a device behind every check
+
+
+def operand(fq, **k):
+    return ctypes.byref(struct(fq, **dict(dict(rows=0), **k)))
+
+
+def weights(fq, **k):
+    return ctypes.byref(struct(fq, **dict(dict(off=None, rows=4 * 32), **k)))
+
+
+@pytest.mark.parametrize("given", [dict(q=None), dict(q=None, qt=None), dict(qs=None), dict(qts=None), {},
+                                   dict(q=None, qs=None, qt=None, qts=None)])
+def test_operands_of_no_rows_are_served(fq, given):
+    lib = fq.lib()
+    for index, T, x in ((None, 0, None), (None, 100, A), (A, 100, A)):
+        assert lib.fp8_quantize_experts(x, fq.DT_BF16, T, 64, index, operand(fq, **given), None) in PASSED
+    # N = 32, K = 64; the result of no rows is null too
+    for y in (None, A):
+        assert lib.fp8_experts_fprop(operand(fq, **given), weights(fq), y, fq.DT_BF16, None) in PASSED
+        assert lib.fp8_experts_dgrad(operand(fq, cols=32, **given), weights(fq), y, fq.DT_F32, None) in PASSED
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would clear a result at a placeholder pointer")
+def test_gradient_of_no_rows_is_served(fq):
+    for given in (dict(q=None), dict(q=None, qs=None), {}):
+        assert fq.lib().fp8_experts_wgrad(operand(fq, cols=32, **given), operand(fq, **given), A, fq.DT_BF16,
+                                          None) in PASSED
+    assert fq.lib().fp8_experts_wgrad(operand(fq, cols=32), operand(fq), None, fq.DT_BF16, None) == INVALID
+
+
+def test_operands_of_no_columns_are_served(fq):
+    none = dict(rows=256, cols=0, q=None, qs=None, qt=None, qts=None)
+    for k in ({}, dict(q=0x10000), dict(qts=0x40000)):
+        assert fq.lib().fp8_quantize_experts(None, fq.DT_BF16, 256, 0, None, operand(fq, **dict(none, **k)), None) in PASSED
+
+
+def test_half_a_pair_is_still_refused(fq):
+    for k in ("q", "qs", "qt", "qts"):
+        assert fq.lib().fp8_quantize_experts(A, fq.DT_BF16, 256, 64, None, operand(fq, rows=256, **{k: None}),
+                                             None) == INVALID
+    assert fq.lib().fp8_quantize_experts(A, fq.DT_BF16, 255, 64, None, operand(fq, rows=256), None) == INVALID

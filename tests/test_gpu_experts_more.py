@@ -40,3 +40,56 @@ def test_products_back_to_back(fq):
         for i in picked:
             assert torch.equal(jobs[i][3], want[i])
     assert fq.device_status() == fq.OK
+
+
+@pytest.mark.parametrize("ragged", [True, False])
+@pytest.mark.parametrize("T", [0, 70])
+def test_no_rows(fq, ragged, T):
+    """A rank whose experts got no token: every call serves, dw is zero."""
+    E, N, K = 4, 48, 80
+    off = offsets_of([0] * (E + 1)) if ragged else None
+    index = torch.empty(0, dtype=torch.int32, device="cuda")
+    w, _ = weights(fq, normal((E * N, K), 90), E)
+    for out in (BF16, FP32):
+        x = fq.fp8_quantize_experts(normal((T, K), 91).cuda(), E, off, index, cols=True)
+        g = fq.fp8_quantize_experts(normal((T, N), 92).cuda(), E, off, index, rows=True, cols=True, fmt=fq.E5M2)
+        assert x.q.shape == (0, K)
+        assert fq.fp8_experts_fprop(x, w, out_dtype=out).shape == (0, N)
+        assert fq.fp8_experts_dgrad(g, w, out_dtype=out).shape == (0, K)
+        dw = torch.full((E, N, K), 5.0, dtype=out, device="cuda")
+        assert (fq.fp8_experts_wgrad(g, x, out=dw) == 0).all()
+    if T == 0:   # without an index the operand's rows are x's
+        x = fq.fp8_quantize_experts(torch.empty(0, K, device="cuda"), E, off, cols=True)
+        assert fq.fp8_experts_fprop(x, w).shape == (0, N)
+
+
+def test_no_rows_in_a_graph(fq):
+    E, N, K = 3, 32, 64
+    off = offsets_of([0] * (E + 1))
+    x = fq.fp8_quantize_experts(torch.empty(0, K, device="cuda"), E, off, cols=True)
+    g = fq.fp8_quantize_experts(torch.empty(0, N, device="cuda"), E, off, cols=True)
+    dw = torch.full((E, N, K), 5.0, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fq.fp8_quantize_experts(torch.empty(0, K, device="cuda"), E, off, cols=True, out=x)
+        fq.fp8_experts_wgrad(g, x, out=dw)
+    graph.replay()
+    assert (dw == 0).all()
+
+
+def test_a_block_of_no_tokens():
+    import importlib.util
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("experts_mxfp8", os.path.join(root, "examples", "experts_mxfp8.py"))
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    block = ex.ExpertsBlock(128, 64, 8, 2)
+    x = torch.empty(0, 128, dtype=BF16, device="cuda")
+    out, saved = block.forward(x, x.clone())
+    assert out.shape == x.shape
+    dx, *grads = block.backward(out, saved)
+    assert dx.shape == x.shape
+    for d, w in zip(grads, (block.norm, block.router, block.up, block.down)):
+        assert d.shape == w.shape and (d == 0).all()
