@@ -150,7 +150,8 @@ int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, i
                 float *rstd, cudaStream_t stream) {
   if (!valid_dtype(dtype) || !valid_dtype(w_dtype) || !norm_dims_ok(T, C)) return FP8Q_ERR_INVALID_ARG;
   if (eps == nullptr || !(*eps >= 0.0f) || *eps > 3.4028235e38f) return FP8Q_ERR_INVALID_ARG;
-  if ((residual == nullptr) != (h == nullptr) || (q == nullptr) != (q_scales == nullptr))
+  // results of no elements may have any address: row scales of [T, 0] are not null beside a q that is
+  if (T > 0 && C > 0 && ((residual == nullptr) != (h == nullptr) || (q == nullptr) != (q_scales == nullptr)))
     return FP8Q_ERR_INVALID_ARG;
   if (q != nullptr && scaling != FP8Q_SCALE_TILE_1x128 && scaling != FP8Q_SCALE_ROW)
     return FP8Q_ERR_INVALID_ARG;

@@ -49,3 +49,15 @@ def test_half_a_pair_is_still_refused(fq):
         assert fq.lib().fp8_quantize_experts(A, fq.DT_BF16, 256, 64, None, operand(fq, rows=256, **{k: None}),
                                              None) == INVALID
     assert fq.lib().fp8_quantize_experts(A, fq.DT_BF16, 255, 64, None, operand(fq, rows=256), None) == INVALID
+
+
+@pytest.mark.parametrize("T,C", [(5, 0), (0, 64), (0, 0)])
+def test_norm_of_nothing_is_served(fq, T, C):
+    eps = ctypes.byref(ctypes.c_float(1e-6))
+    for scaling in (fq.SCALE_ROW, fq.SCALE_TILE_1x128):
+        for q, s in ((None, A), (A, None), (None, None)):
+            for r, h in ((None, None), (None, A), (A, None)):
+                assert fq.lib().fp8_rmsnorm(None, C, r, C, fq.DT_BF16, None, fq.DT_F32, eps, T, C, h, C, None, C,
+                                            scaling, q, s, A, None) in PASSED
+    assert fq.lib().fp8_rmsnorm(None, C, None, C, fq.DT_BF16, None, fq.DT_F32, eps, T, C, None, C, None, C,
+                                fq.SCALE_TENSOR, A, A, A, None) == INVALID
