@@ -851,11 +851,12 @@ int fp8_quantize_experts(const void *x, int in_dtype, int64_t T, int64_t ld,
  * scaling with fp32 accumulation:
  *   fprop: y  [S, N]    = x w_e^T        x by rows, w by rows
  *   dgrad: dx [S, K]    = g w_e          g [S, N] by rows, w transposed
- *   wgrad: dw [E, N, K] = g_e^T x_e      g and x transposed (one pair of
- *                                        offsets: x->offsets are used)
+ *   wgrad: dw [E, N, K] = g_e^T x_e      g and x transposed, in the same
+ *                                        groups
  * Results are dense, of out_dtype, 16-byte aligned, and overlap no operand.  Rows
  * of y and dx behind the last group are left as they were; dw of an empty group
- * is zero.  Any S; N % 16 == 0, K % 16 == 0; what is contracted over (K, N and
+ * is zero.  Where g and x hold their offsets at different addresses, dw of a group
+ * that does not begin and end at the same rows in both is NaN.  Any S; N % 16 == 0, K % 16 == 0; what is contracted over (K, N and
  * S) is at most 2^27 long and, in fprop and dgrad, not empty.  The groups of x
  * (g) may be equal ones.
  * Errors: INVALID_ARG (also operands whose sizes or groups do not fit, or

@@ -1190,8 +1190,9 @@ def fp8_experts_dgrad(g: ExpertsOperand, w: ExpertsOperand, out_dtype=torch.bflo
 
 def fp8_experts_wgrad(g: ExpertsOperand, x: ExpertsOperand, out_dtype=torch.bfloat16, out=None,
                       stream=None):
-    """dw [E, N, K], dw_e = g_e^T x_e, from g [S, N] and x [S, K] transposed;
-    zero for an expert without rows."""
+    """dw [E, N, K], dw_e = g_e^T x_e, from g [S, N] and x [S, K] transposed, cast in
+    the same groups; zero for an expert without rows.  Where the offsets of g and x are
+    different tensors, dw_e is NaN for a group that is not the same rows in both."""
     return _experts_rows("fp8_experts_wgrad", g, x, (x.groups, g.cols, x.cols), out_dtype, out, stream)
 
 

@@ -16,11 +16,12 @@ struct Groups {
 };
 
 #ifdef __CUDACC__
-// First row and number of rows of group e.  Offsets are read as they are and
-// brought into [0, rows]: whatever they hold, rows stay inside the operand.
+// An offset is brought into [0, rows]: whatever it holds, rows stay inside the operand.
+__device__ __forceinline__ int row_of(const Groups &g, int32_t offset) { return min(max(offset, 0), g.rows); }
+// First row and number of rows of group e.
 __device__ __forceinline__ int2 group_rows(const Groups &g, const int32_t *offsets, int e) {
   if (g.offsets == nullptr) return make_int2(e * g.each, g.each);
-  const int a = min(max(offsets[e], 0), g.rows), z = min(max(offsets[e + 1], 0), g.rows);
+  const int a = row_of(g, offsets[e]), z = row_of(g, offsets[e + 1]);
   return make_int2(a, max(z - a, 0));
 }
 __device__ __forceinline__ int2 group_rows(const Groups &g, int e) { return group_rows(g, g.offsets, e); }
@@ -50,6 +51,7 @@ struct Side {
 };
 struct ProductArgs {
   Groups groups;            // of the rows of B (by_rows) or of the contraction
+  const int32_t *a_offsets; // not by_rows: those of A's rows, where they lie elsewhere; null: B's
   int by_rows;
   Side a, b;
   int a_row, a_k, a_block;  // by_rows: group e's part of A starts at row a_row * e,

@@ -308,6 +308,7 @@ int fp8_experts_wgrad(const fp8q_experts *g, const fp8q_experts *x, void *dw, in
     return from_cuda(cudaMemsetAsync(dw, 0, (size_t)(E * N * K * dtype_size(out_dtype)), stream));
   experts::ProductArgs a{};
   a.groups = groups_of(*x);
+  a.a_offsets = g->offsets != x->offsets ? g->offsets : nullptr;
   a.by_rows = 0;
   a.a = transposed(*g);
   a.b = transposed(*x);

@@ -58,6 +58,7 @@ using namespace ptx;
 constexpr int kRaster = 8;        // tiles of B visited together
 constexpr int kTilesAhead = 8;    // tiles that are found ahead of their results
 constexpr int kMostTiles = INT32_MAX / 2;   // of a launch
+constexpr int kApart = INT32_MIN;   // in place of an offset that A and B do not share
 
 struct PairMaps {
   CUtensorMap a, b[4], sfa, sfb;   // b: boxes of 128, 64, 32 and 16 rows
@@ -67,7 +68,7 @@ struct PairMaps {
 // One tile: what of A, B and K it takes, and where its result goes.
 struct __align__(16) Tile {
   int a_row, b_row;        // first rows of A and of B
-  int k_block, num_k;      // K blocks
+  int k_block, num_k;      // K blocks; num_k < 0: A and B have other groups, the result is NaN
   int a_block, b_block;    // 128-row blocks of the scales of the first rows
   int n, valid;            // rows of B: as the MMA takes them (a multiple of 32), and those that count
   int across, along;       // first rows of the tile in the group's parts of A and B
@@ -157,6 +158,7 @@ struct Tiles {
   int u, step;
   int e = -1, row, rows;       // the group, its first row and its rows
   int block, along, each, more;
+  bool apart = false;          // the group begins or ends elsewhere in A
   __device__ __forceinline__ Tiles(const ProductArgs &args, const int32_t *group_offsets,
                                    const int *first_tiles, int pair, int pairs)
       : p(args), offsets(group_offsets), first(first_tiles), u(pair), step(pairs) {}
@@ -180,6 +182,7 @@ struct Tiles {
         e = u / first_of(1);
       }
       const int2 group = group_rows(p.groups, offsets, e);
+      if (!ROWS && p.a_offsets != nullptr) apart = offsets[e] == kApart || offsets[e + 1] == kApart;
       row = group.x;
       rows = group.y;
       block = first_block(p.groups, e, row);
@@ -207,7 +210,7 @@ struct Tiles {
       t.a_row = t.across;
       t.b_row = t.along;
       t.k_block = block;
-      t.num_k = (rows + kBK - 1) / kBK;
+      t.num_k = apart ? -1 : (rows + kBK - 1) / kBK;
       t.a_block = 2 * at;
       t.b_block = b0;
       t.c_row = e;
@@ -261,6 +264,10 @@ struct Chunk {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int j = 0; j < kRegs; ++j) r[j] = 0u;
+  }
+  __device__ __forceinline__ void poison() {
+#pragma unroll
+    for (int j = 0; j < kRegs; ++j) r[j] = sizeof(T) == 4 ? 0x7FC00000u : 0x7FC07FC0u;
   }
   // Into this lane's row of 64 or 128 bytes, as swizzling of that width has them.
   __device__ __forceinline__ void stage(uint32_t row) const {
@@ -348,7 +355,10 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
   if (warp >= 2) {   // the epilogue's warps fetch the offsets
     if (p.groups.offsets != nullptr)
       for (int e = threadIdx.x - 64; e <= p.groups.count; e += 32 * L::kEpilogueWarps)
-        if (warp < 2 + L::kEpilogueWarps) offsets[e] = p.groups.offsets[e];
+        if (warp < 2 + L::kEpilogueWarps) {
+          const int32_t at = row_of(p.groups, p.groups.offsets[e]);
+          offsets[e] = !ROWS && p.a_offsets != nullptr && row_of(p.groups, p.a_offsets[e]) != at ? kApart : at;
+        }
   }
   tc_fence_before();
   __syncthreads();
@@ -434,8 +444,8 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
       ok = wait_bounded_all(acce0 + 8 * acc, (turn & 1u) ^ 1u, abort_flag, err);
       if (!ok) break;
       tc_fence_after();
-      // an empty group's tile takes its turn too; the epilogue writes zeros
-      if (!ROWS && t.num_k == 0) {
+      // an empty group's tile takes its turn too; the epilogue writes zeros (or NaN)
+      if (!ROWS && t.num_k <= 0) {
         if (elect_one()) mma_commit_pair_multicast(accf, kBoth);
         __syncwarp();
       }
@@ -533,6 +543,11 @@ __global__ void __launch_bounds__(Layout<T, ROWS, WIDE>::kThreads, 1)
         } else {
 #pragma unroll
           for (int k = 0; k < kPiece; ++k) to[k].clear();
+          if (t.num_k < 0) {
+            __syncwarp();   // a branch: as selects it costs every tile (151 us for 148)
+#pragma unroll
+            for (int k = 0; k < kPiece; ++k) to[k].poison();
+          }
         }
       };
       const auto store = [&](const Chunk<T> *of, int c) {

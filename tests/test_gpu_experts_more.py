@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import experts_reference as ref
-from test_gpu_experts import BF16, FP32, MARK, arrays, ends_of, f64, fq, near, normal, offsets_of, operand, weights  # noqa: F401
+from test_gpu_experts import BF16, FP32, MARK, arrays, ends_of, f64, fq, marked, near, normal, offsets_of, operand, weights  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,29 @@ def test_a_block_of_no_tokens():
     assert dx.shape == x.shape
     for d, w in zip(grads, (block.norm, block.router, block.up, block.down)):
         assert d.shape == w.shape and (d == 0).all()
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_gradient_of_operands_in_other_groups(fq, out):
+    """g cast under another route's offsets: NaN where a group is not the same rows
+    in both, in every order with groups that are, and empty ones; never another's sum."""
+    S, N, K = 400, 272, 528
+    ends = [0, 100, 130, 130, 130, 260, 261, 400]
+    others = [[0, 100, 130, 130, 130, 260, 261, 400], [0, 100, 129, 130, 130, 260, 261, 400], [0, 0, 130, 130, 131, 260, 261, 390],
+              [1, 100, 130, 130, 130, 260, 261, 400], [0] * 8, [-5, 100, 130, 130, 130, 260, 261, 400]]
+    E, off = len(ends) - 1, offsets_of(ends)
+    g, x = normal((S, N), 93, 0.1).cuda(), normal((S, K), 94).cuda()
+    xo = fq.fp8_quantize_experts(x, E, off, rows=False, cols=True)
+    want = fq.fp8_experts_wgrad(fq.fp8_quantize_experts(g, E, off, rows=False, cols=True, fmt=1), xo, out_dtype=out)
+    for other in others:
+        go = marked(fq, S, N, E, 1, offsets_of(other), by_rows=False)
+        fq.fp8_quantize_experts(g, E, go.offsets, rows=False, cols=True, fmt=1, out=go)
+        dw = torch.full((E, N, K), 5.0, dtype=out, device="cuda")
+        fq.fp8_experts_wgrad(go, xo, out=dw)
+        for e in range(E):
+            if ends[e:e + 2] == [max(0, o) for o in other[e:e + 2]]:   # below 0 is 0
+                assert torch.equal(dw[e], want[e]), (other, e)
+            else:
+                assert dw[e].isnan().all(), (other, e)
+    torch.cuda.synchronize()
+    assert fq.device_status() == fq.OK
