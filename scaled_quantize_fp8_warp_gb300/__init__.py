@@ -1129,6 +1129,13 @@ class ExpertsOperand:
         return cls(rows, cols, groups, fmt, offsets, q, qs, qt, qts)
 
 
+def _same_offsets(a: torch.Tensor | None, b: torch.Tensor | None) -> bool:
+    """Whether two sets of offsets are the same memory (or both equal groups)."""
+    if a is None or b is None:
+        return a is b
+    return a is b or (a.data_ptr(), a.dtype, a.shape, a.stride()) == (b.data_ptr(), b.dtype, b.shape, b.stride())
+
+
 def fp8_quantize_experts(x: torch.Tensor, groups: int, offsets: torch.Tensor | None = None,
                          index: torch.Tensor | None = None, rows=True, cols=False, fmt: int = E4M3,
                          out: ExpertsOperand | None = None, stream=None) -> ExpertsOperand:
@@ -1146,7 +1153,8 @@ def fp8_quantize_experts(x: torch.Tensor, groups: int, offsets: torch.Tensor | N
         raise ValueError("an orientation is needed: rows, cols or both")
     if out is None:
         out = ExpertsOperand.empty(S, C, groups, x.device, fmt, offsets, rows, cols, stream)
-    elif (out.rows, out.cols, out.groups, out.fmt) != (S, C, groups, fmt) or out.offsets is not offsets:
+    elif (out.rows, out.cols, out.groups, out.fmt) != (S, C, groups, fmt) or not _same_offsets(
+            out.offsets, offsets):
         raise ValueError("an operand of these rows, columns, groups, offsets and format is needed")
     st = out.struct
     if (rows and out.q is None) or (cols and out.q_t is None):

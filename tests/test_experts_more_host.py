@@ -61,3 +61,12 @@ def test_norm_of_nothing_is_served(fq, T, C):
                                             scaling, q, s, A, None) in PASSED
     assert fq.lib().fp8_rmsnorm(None, C, None, C, fq.DT_BF16, None, fq.DT_F32, eps, T, C, None, C, None, C,
                                 fq.SCALE_TENSOR, A, A, A, None) == INVALID
+
+
+def test_offsets_are_the_same_by_their_memory(fq):
+    a = torch.tensor([0, 3, 5, 9, 9, 12], dtype=torch.int32)
+    assert fq._same_offsets(a, a) and fq._same_offsets(None, None)
+    assert fq._same_offsets(a, a[:]) and fq._same_offsets(a.view(-1), a)
+    for other in (None, a.clone(), a[:5], a[1:], a.view(torch.float32), a[::1].view(2, 3), a[::2]):
+        assert not fq._same_offsets(a, other) and not fq._same_offsets(other, a)
+    assert not fq._same_offsets(a[::2], a[:3])

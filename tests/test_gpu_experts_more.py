@@ -119,3 +119,14 @@ def test_gradient_of_operands_in_other_groups(fq, out):
                 assert dw[e].isnan().all(), (other, e)
     torch.cuda.synchronize()
     assert fq.device_status() == fq.OK
+
+
+def test_storage_under_a_view_of_its_offsets(fq):
+    x, off = normal((60, 64), 95).cuda(), offsets_of([0, 20, 60])
+    want = fq.fp8_quantize_experts(x, 2, off, cols=True)
+    op = marked(fq, 60, 64, 2, 0, off)
+    fq.fp8_quantize_experts(x, 2, off[:], cols=True, out=op)
+    assert torch.equal(op.q, want.q)
+    for other in (off.clone(), None):
+        with pytest.raises(ValueError):
+            fq.fp8_quantize_experts(x, 2, other, cols=True, out=op)
