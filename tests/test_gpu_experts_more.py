@@ -130,3 +130,73 @@ def test_storage_under_a_view_of_its_offsets(fq):
     for other in (off.clone(), None):
         with pytest.raises(ValueError):
             fq.fp8_quantize_experts(x, 2, other, cols=True, out=op)
+
+
+NONE = [[0, 50, 20, 70], [-5, 10, 90, 4000], [0, 70, 70, 2 ** 31 - 1], [60, 10, 0, 0], [-(2 ** 31), -1, 0, 12], [70, 70, 70, 70],
+        [2 ** 31 - 1, 0, 2 ** 31 - 1, 0]]
+
+
+@pytest.mark.parametrize("bad", NONE)
+@pytest.mark.parametrize("scale,N,K", [(1, 272, 4112), (1, 4096, 272), (1, 272, 144), (10, 272, 144)])
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_offsets_that_are_none_in_every_kernel(fq, bad, scale, N, K, out):
+    """Few rows, whose contraction (4112 of fprop, 4096 of dgrad) is split over a
+    cluster, and tiles 256 and 128 wide: nothing is written beside the result, and offsets that are brought into
+    [0, S] serve as those they become."""
+    S, E = 70 * scale, 3
+    off = offsets_of([max(-(2 ** 31), min(2 ** 31 - 1, b * scale)) for b in bad])
+    inside = off.clamp(0, S)
+    w, _ = weights(fq, normal((E * N, K), 96, 0.05), E)
+    for f, cols, wide in ((fq.fp8_experts_fprop, K, N), (fq.fp8_experts_dgrad, N, K)):
+        x = normal((S, cols), 97).cuda()
+        got = []
+        for o in (off, inside):
+            op = marked(fq, S, cols, E, 0, o, transposed=False)
+            fq.fp8_quantize_experts(x, E, o, out=op)
+            result = torch.full((3, S, wide), 7.0, dtype=out, device="cuda")
+            f(op, w, out=result[1])
+            assert (result[0] == 7.0).all() and (result[2] == 7.0).all()
+            got.append(result[1])
+        ends = inside.tolist()
+        if ends == sorted(ends):
+            assert torch.equal(*got)
+            assert (got[0][ends[-1]:] == 7.0).all() and (got[0][:ends[0]] == 7.0).all()
+            assert (got[0][ends[0]:ends[-1]] != 7.0).any(dim=1).all()
+    torch.cuda.synchronize()
+    assert fq.device_status() == fq.OK
+
+
+def test_large_input_gradient(fq):
+    """More results than 32 bits count, checked in a few rows."""
+    S, N, K, E, T = 600_000, 128, 4096, 3, 500
+    g = normal((T, N), 98)
+    index = (torch.arange(S, dtype=torch.int32) * 7) % T
+    ends = [0, 1000, 1000, S - 5]
+    op = fq.fp8_quantize_experts(g.cuda(), E, offsets_of(ends), index.cuda(), fmt=fq.E5M2)
+    w, groups = weights(fq, normal((E * N, K), 99, 0.05), E, by_rows=False)
+    dx = torch.full((S, K), 3.0, dtype=BF16, device="cuda")
+    fq.fp8_experts_dgrad(op, w, out=dx)
+    some = [0, 999, 1000, 524_287, 524_288, 524_289, S - 6]
+    values = ref.mx_values(*ref.mx_rows(f64(g[index[some].long()]), 1), 1)
+    wv = list(ref.group_cols(arrays(w), groups, 0))
+    for i, r in enumerate(some):
+        near(dx[r:r + 1], values[i:i + 1], wv[0 if r < 1000 else 2], r)
+    assert (dx[S - 5:] == 3.0).all()
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_large_weight_gradient(fq, out):
+    """More results than 32 bits count, checked in a few groups."""
+    E, N, K = 256, 2048, 4128
+    sizes = [i % 3 for i in range(E)]
+    g, x = normal((sum(sizes), N), 100, 0.1), normal((sum(sizes), K), 101)
+    go, groups = operand(fq, g, sizes, 2, 1, by_rows=False)
+    xo, _ = operand(fq, x, sizes, 2, 0, by_rows=False)
+    dw = torch.full((E, N, K), 5.0, dtype=out, device="cuda")
+    assert dw.numel() > 2 ** 31
+    fq.fp8_experts_wgrad(go, xo, out=dw)
+    gv, xv = list(ref.group_cols(arrays(go), groups, 1)), list(ref.group_cols(arrays(xo), groups, 0))
+    for e in (1, 127, 253, 254):
+        near(dw[e], gv[e], xv[e], e)
+    empty = torch.tensor([e for e in range(E) if sizes[e] == 0], device="cuda")
+    assert all((dw[e] == 0).all() for e in empty.tolist())
