@@ -19,6 +19,7 @@ The names follow the C ABI: ``fp8_amax``, ``fp8_quantize_tensor``,
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from typing import NamedTuple
@@ -1081,9 +1082,13 @@ class ExpertsOperand:
     weights of all experts, one below the other).  By rows: ``q`` uint8 [rows,
     cols] and ``q_scales``; transposed: ``q_t`` uint8 [cols, 128 blocks] and
     ``qt_scales``; scales are uint8, 512 * blocks * ceil(cols/128) of them.  See
-    fp8q_experts in include/fp8q.h for where things lie."""
-    __slots__ = ("rows", "cols", "groups", "fmt", "offsets", "q", "q_scales", "q_t", "qt_scales",
-                 "struct")
+    fp8q_experts in include/fp8q.h for where things lie.  An operand keeps the
+    tensors it was made of: the calls use their addresses, found once; for other
+    tensors (a step's new offsets over the same storage) make another operand."""
+    __slots__ = ("_rows", "_cols", "_groups", "_fmt", "_offsets", "_q", "_q_scales", "_q_t",
+                 "_qt_scales", "struct")
+    rows, cols, groups, fmt, offsets, q, q_scales, q_t, qt_scales = (
+        property(operator.attrgetter(name)) for name in __slots__[:-1])
 
     def __init__(self, rows: int, cols: int, groups: int, fmt: int = E4M3,
                  offsets: torch.Tensor | None = None, q: torch.Tensor | None = None,
@@ -1104,14 +1109,14 @@ class ExpertsOperand:
                 _like(data, shape, torch.uint8, "bytes")
                 if scales.dtype != torch.uint8 or scales.numel() != 512 * blocks * ((cols + 127) // 128):
                     raise ValueError(f"scales must be {512 * blocks * ((cols + 127) // 128)} uint8 values")
-        self.rows, self.cols, self.groups, self.fmt, self.offsets = rows, cols, groups, fmt, offsets
-        self.q, self.q_scales, self.q_t, self.qt_scales = q, q_scales, q_t, qt_scales
+        self._rows, self._cols, self._groups, self._fmt, self._offsets = rows, cols, groups, fmt, offsets
+        self._q, self._q_scales, self._q_t, self._qt_scales = q, q_scales, q_t, qt_scales
         self.struct = _ExpertsStruct(_addr(q), _addr(q_scales), _addr(q_t), _addr(qt_scales),
                                      _addr(offsets), rows, cols, groups, fmt)
 
     def tensors(self):
         """What the operand holds, None for what it lacks."""
-        return self.q, self.q_scales, self.q_t, self.qt_scales, self.offsets
+        return self._q, self._q_scales, self._q_t, self._qt_scales, self._offsets
 
     @classmethod
     def empty(cls, rows: int, cols: int, groups: int, device, fmt: int = E4M3, offsets=None,

@@ -70,3 +70,16 @@ def test_offsets_are_the_same_by_their_memory(fq):
     for other in (None, a.clone(), a[:5], a[1:], a.view(torch.float32), a[::1].view(2, 3), a[::2]):
         assert not fq._same_offsets(a, other) and not fq._same_offsets(other, a)
     assert not fq._same_offsets(a[::2], a[:3])
+
+
+def test_an_operand_keeps_what_it_was_made_of(fq):
+    """The calls use addresses found once: an attribute that could be set would be
+    read by none of them."""
+    op = fq.ExpertsOperand(64, 32, 2, fq.E5M2)
+    assert (op.rows, op.cols, op.groups, op.fmt) == (64, 32, 2, fq.E5M2)
+    assert op.tensors() == (None,) * 5 and op.offsets is None and op.q is None and op.qt_scales is None
+    for name in ("rows", "cols", "groups", "fmt", "offsets", "q", "q_scales", "q_t", "qt_scales"):
+        with pytest.raises(AttributeError):
+            setattr(op, name, torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(AttributeError):
+        op.another = 1
