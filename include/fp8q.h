@@ -729,7 +729,7 @@ int fp8_act_backward(int act, int dtype, int64_t T, int64_t F,
  *   y = (h rstd) weight
  *   q = RNE_e4m3(y / s),  s = max(fl32(amax / 448), 1e-12)
  * h is rounded to `dtype` first and everything after is computed from it as it
- * is stored, in fp32 (squares above fp32's range make rstd 0); y is rounded
+ * is stored, in fp32 (a sum of squares above its range makes rstd 0); y is rounded
  * once where it is stored, and q is cast from y in fp32, not from a stored y.
  * The scales s are those of a GEMM operand [T, C]: per 1x128 tile
  * (FP8Q_SCALE_TILE_1x128, q_scales [ceil(C/128), T]) or per row
@@ -767,7 +767,8 @@ size_t fp8q_rmsnorm_backward_workspace_size(int64_t T, int64_t C);
  * in fp32, each rounded once.  dx is the gradient of x and of the residual
  * alike; dresidual, the gradient that reaches h by its other use (the residual
  * of the next layer), may be NULL (0).  The rows of dweight's sum are added in
- * an order that depends on T, C and the device alone: results repeat.
+ * an order that depends on the sizes, the types, whether rows start on 16-byte
+ * boundaries, and the device: a call's results repeat.
  *   dy, h, dresidual, dx  device [T, C] of `dtype`, rows lddy, ldh, lddr, lddx
  *                         elements apart; dx may be exactly dy or dresidual,
  *                         with its ld

@@ -13,7 +13,11 @@
 // an SM could hold are there, for want of registers), then HBM.  16384 routed rows
 // of 8192 tokens x 4096 bf16 in 32 groups: 55.8 us both ways (205 MB with each token
 // read once, 272 as the gather reads them: 4.9 TB/s), 35.4 by rows alone; 16384 rows
-// in one group 53.0; fp32 in 128 groups 91.  70 us before the groups were found 32 at a
+// in one group 53.0; fp32 in 32 groups 73, in 128 groups 91 (128 rows
+// a group on average, most in a block that is not full or in two).  Without an index, where each row is read once, 65536 x 4096 of
+// weights in 32 groups: fp32 188 by rows and 250 both ways (7.2 and 6.5 TB/s), bf16 122
+// and 189 (6.6, 5.8).  In bf16 8 bytes (rows alone) or 16 (both ways) a thread spill at
+// three blocks an SM, in rows that start anywhere up to 148.  70 us before the groups were found 32 at a
 // time, the transposed bytes left as lines and the scales were found two at a
 // time.  The next tile's loads ahead of this one's arithmetic: no gain.
 #include <cuda_bf16.h>

@@ -21,21 +21,24 @@
 // What bounds it: shared memory.  A K block of 128 moves 16 KB of A and n / 2 rows of
 // B into each CTA and reads them once in MMAs of 2 n cycles, 256 + n cycles at 128
 // bytes a cycle: 512 for n = 256, where the MMAs take 512 too, 384 for n = 128, where
-// they take 256.  16384 rows in one group, 2048 x 4096: 79 us (3.5 PFLOP/s; MMAs alone
-// 69); in 32 groups of unlike sizes 106 (2.6; loads alone 86, tensor pipe busy 67% of
-// an SM's time there, and 12% of the time is before the first or behind the last
-// tile of an SM); 16384 rows in 128 groups, 1024 x 4096: 98 (its 537 MB of weights at
-// the copy rate: 82).  wgrad of those 32 groups: 148 us, 537 MB of results; with no more
-// than a K block a tile 98 (5.5 TB/s, past what a memset of them takes, 136).
+// they take 256.  Captured, on a GPU that was idle: 16384 rows in one group, 2048 x
+// 4096 83 us (3.3 PFLOP/s; MMAs alone 69); in 32 groups of unlike sizes 106 (2.6;
+// loads alone 86, tensor pipe busy 67% of an SM's time there, and 12% of the time is
+// before the first or behind the last tile of an SM), dgrad of them 115, to fp32 148;
+// in 128 groups, 1024 x 4096 90 (its 537 MB of weights at the copy rate: 82).  wgrad of
+// the 32 groups 148 us, 537 MB of results, to fp32 247; with 64 rows a group 90.
+// After a second of them the power limit lowers the clock from 2070 to 1600 - 1950
+// MHz: fprop 120, dgrad 126, wgrad 156.
 //
-// Tried: tiles 384 wide (two MMAs a step, five stages): 118 us where 256 take 112, and
-// one token 24.5 for 18.3: fewer bytes of the weight are under way.  A's blocks called
-// into L2 ahead: no gain.  Groups sorted by what a tile of theirs costs: 1% here,
-// more lost elsewhere.  Scales copied a block ahead of their MMAs: 110 for 107.
-// wgrad by places of C_e instead of group by group: 229 for 219, DRAM reads 291 MB
-// for 126.  Tiles of wgrad 128 wide with three accumulators: 161.  kRaster of 4 or
-// 16: level.  Arriving at the even CTA's barrier with cluster-scope release: wgrad
-// 219 us for 146.
+// Tried, each against the kernel of its day (fprop of the 32 groups went from 116 to
+// 112, 110 and 107 us, wgrad from 219 to 146 and 148): tiles 384 wide (two MMAs a step,
+// five stages) 118 us where 256 took 112, and one token 24.5 for 18.3: fewer bytes of
+// the weight are under way.  A's blocks called into L2 ahead: no gain.  Groups sorted
+// by what a tile of theirs costs: 1% here, more lost elsewhere.  Scales copied a
+// block ahead of their MMAs: 110 for 107.  wgrad by places of C_e instead of group by
+// group: 229 for 219, DRAM reads 291 MB for 126.  Tiles of wgrad 128 wide with three
+// accumulators: 161.  kRaster of 4 or 16: level.  Arriving at the even CTA's barrier
+// with cluster-scope release: wgrad 219 us for 146.
 #include <cuda.h>
 #include <stdint.h>
 
@@ -655,7 +658,8 @@ int launch_product(const ProductArgs &a, int out_dtype, int64_t a_atoms, int64_t
   const int split = split_for(a);
   if (split > 0) return launch_split(a, split, out_dtype, a_atoms, b_atoms, stream);
   // Tiles 128 wide, which have a deeper ring and three accumulators, up to 96 rows
-  // a group on average: 64 equal groups, 1024 x 4096, 1024 rows 49.6 us and 52.4 with
+  // a group on average, as far as the host knows (rows behind the last group count):
+  // 64 equal groups, 1024 x 4096, 1024 rows 49.6 us and 52.4 with
   // 256-wide tiles; groups of unlike sizes, 4000 rows in 50, 2048 x 1024, 25.2 and
   // 26.2, but 8192 in 64, 1024 x 4096, 56.5 and 54.6.
   if (bf16 && a.groups.rows > 96 * (int64_t)a.groups.count)

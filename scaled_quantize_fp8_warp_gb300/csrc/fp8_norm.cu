@@ -20,7 +20,11 @@
 // 1024 92.6, 4096 x 16384 (row scales) 92.8; fp32 8192 x 4096 104 (5.5).  Backward with
 // dresidual, 8 bytes: 8192 x 4096 48.5 us (5.5), of which 2 for adding the blocks'
 // sums, 8192 x 8192 88 (6.1), 32768 x 1024 49, 4096 x 16384 126 (4.3: a row's loads wait
-// for the row before).  The same rows on other numbers of threads, 15872 x 4096
+// for the row before); fp32 8192 x 4096 98 (5.5), 4096 x 8192 113, 2048 x 16384 111 (4.8).
+// Rows that are read again: forward 2048 x 20480 bf16 73 with tile scales and 76 with
+// row scales (5.2, 5.0), fp32 1024 x 20480 71; backward 140 both (2.4: dy and h three
+// times).  Rows that start anywhere, element by element: 1003 x 2570 fp32 12.6 (1.8),
+// 15872 x 4094 bf16 231 (2.6), backward 8192 x 4094 103 (2.6).  The same rows on other numbers of threads, 15872 x 4096
 // forward and 8192 x 4096 backward: 512 threads of one chunk 120 and 86, 128 of four
 // 112 and 77.  Arithmetic two values at a time (f32x2) took the backward pass from
 // 64 to 48.5 us.  One row of 4096: 2.6 us in a graph.
@@ -52,7 +56,9 @@ struct Shape {
   static constexpr int kThreads = RT < 256 ? 256 : RT;
   static constexpr int kRows = kThreads / RT;    // rows of a block at once
   static constexpr int kColumns = 8 * RT * CHUNKS;
-  // blocks an SM has to hold: 80 registers a thread forward, 128 backward
+  // Blocks an SM has to hold: 80 registers a thread forward, 128 backward (80 with one
+  // chunk).  Backward in fp32 that is not enough, its rows take twice bf16's registers:
+  // 32 to 160 bytes a thread spill, and 96 (bf16) to 180 with 1024 threads.
   static constexpr int kForwardBlocks = CHUNKS > 2 ? 1 : (768 / kThreads > 0 ? 768 / kThreads : 1);
   static constexpr int kBackwardBlocks = kThreads > 512 ? 1 : (CHUNKS == 1 ? 768 : 512) / kThreads;
   // Backward, the next row's loads are under way while one is worked on.  1024
